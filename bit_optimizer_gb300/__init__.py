@@ -10,6 +10,8 @@ from ._lib import (BF16, E4M3, E5M2, EXPORTS, F16, F32, KERNELS, Fp8OptError,
 from .api import (AdamWPlan, CastPlan, CastStepPlan, Fp8AdamW, ReducePlan,
                   StepState, arena_views, fp8_adamw_step, fp8_cast_scaled,
                   fp8_reduce_scaled)
+from .ops import (act_load, act_save, gelu, gelu_backward, layer_norm,
+                  layer_norm_backward)
 
 load()
 
@@ -18,4 +20,5 @@ __all__ = ["fp8_cast_scaled", "fp8_adamw_step", "fp8_reduce_scaled",
            "Fp8AdamW", "arena_views", "E4M3", "E5M2", "F32", "BF16", "F16",
            "Fp8OptError", "strerror", "release", "release_stream", "load",
            "LIB_PATH", "EXPORTS",
-           "KERNELS", "timing_enable", "timing_read"]
+           "KERNELS", "timing_enable", "timing_read", "act_save", "act_load",
+           "gelu", "gelu_backward", "layer_norm", "layer_norm_backward"]

@@ -15,6 +15,7 @@
 
 #include "../../include/fp8opt.h"
 #include "fp8opt_internal.cuh"
+#include "ops_internal.cuh"
 
 namespace fp8opt {
 
@@ -185,6 +186,7 @@ struct Workspace {
   DevBuf saved_scales;       // n floats: m_scale before the step
   DevBuf norm_buf;           // gradient norm: 2n sum words, norm, clip
   DevBuf dev_scalars;        // the *_dev calls' DevScalars
+  DevBuf op_scratch;         // the training operators' scratch
   // cast tables
   std::vector<fp8opt_cast_item> cast_key;
   DevBuf cast_descs, cast_chunks;
@@ -208,9 +210,9 @@ struct Workspace {
 
   void freeze() {
     frozen = true;
-    for (DevBuf* b : {&slots, &saved_scales, &norm_buf, &dev_scalars, &cast_descs,
-                      &cast_chunks, &step_descs, &step_chunks, &reduce_descs,
-                      &reduce_chunks})
+    for (DevBuf* b : {&slots, &saved_scales, &norm_buf, &dev_scalars, &op_scratch,
+                      &cast_descs, &cast_chunks, &step_descs, &step_chunks,
+                      &reduce_descs, &reduce_chunks})
       b->frozen = true;
   }
 
@@ -219,6 +221,7 @@ struct Workspace {
     saved_scales.release();
     norm_buf.release();
     dev_scalars.release();
+    op_scratch.release();
     cast_descs.release();
     cast_chunks.release();
     step_descs.release();
@@ -332,7 +335,8 @@ cudaError_t prepare_slots(Workspace* ws, size_t words, cudaStream_t stream,
 const char* const kKernelNames[kNumKernels] = {
     "cast_amax", "cast_encode", "step_amax", "step_update", "step_w8",
     "cast_step_amax", "reduce_amax", "reduce_encode", "grad_norm",
-    "grad_norm_terms", "clip_coef", "found"};
+    "grad_norm_terms", "clip_coef", "found", "act_save", "act_load", "gelu",
+    "gelu_backward", "layer_norm", "layer_norm_backward", "layer_norm_params"};
 
 struct Timing {
   bool on = false;
@@ -489,6 +493,35 @@ int current_device_and_info(int* dev, DeviceInfo** info) {
 // Records the detail fp8opt_last_error() returns, for entry points defined
 // in other translation units.
 int record_error(int status, const char* what) { return fail(status, what); }
+
+// The call scope of the training operators.  The scratch follows the other
+// workspace buffers' rules: it only grows, not while the stream captures a
+// CUDA graph, and not after one was captured with it.
+OpCall::OpCall() : lock_(g_mu) {}
+
+int OpCall::open(const char* fn, cudaStream_t stream, size_t scratch_bytes) {
+  int dev = 0;
+  DeviceInfo* info = nullptr;
+  const int st = current_device_and_info(&dev, &info);
+  if (st != FP8OPT_OK) return st;
+  sms = info->sms;
+  mark = launch_mark();
+  if (scratch_bytes == 0) return FP8OPT_OK;
+  Workspace* ws = workspace(dev, stream);
+  const bool graph = capturing(stream);
+  cudaError_t e = cudaSuccess;
+  if (graph && scratch_bytes > ws->op_scratch.cap) e = cudaErrorStreamCaptureUnsupported;
+  if (e == cudaSuccess) e = ws->op_scratch.reserve(scratch_bytes);
+  if (e != cudaSuccess) return cuda_fail(e, (std::string(fn) + ": workspace").c_str());
+  if (graph) ws->freeze();
+  scratch = static_cast<char*>(ws->op_scratch.ptr);
+  return FP8OPT_OK;
+}
+
+int OpCall::done(const char* fn, cudaError_t e) {
+  return e == cudaSuccess ? FP8OPT_OK
+                          : cuda_fail(e, (std::string(fn) + ": launch").c_str());
+}
 
 }  // namespace fp8opt
 

@@ -126,6 +126,8 @@ enum ReducePhase { kReduceAmaxPass = 1, kReduceEncodePass = 2,
 enum KernelId { kCastAmaxK = 0, kCastEncodeK, kStepAmaxK, kStepUpdateK,
                 kStepW8K, kCastStepAmaxK, kReduceAmaxK, kReduceEncodeK,
                 kGradNormK, kGradNormTermsK, kClipCoefK, kFoundK,
+                kActSaveK, kActLoadK, kGeluK, kGeluBackwardK, kLayerNormK,
+                kLayerNormBackwardK, kLayerNormParamsK,
                 kNumKernels };
 
 // Called before (end = 0) and after (end = 1) each kernel launch when timing

@@ -1,0 +1,115 @@
+// Shared by the training operators (activation checkpoints, layer norm, the
+// vocabulary's cross entropy): their call scope, launch records and element
+// helpers.
+#pragma once
+
+#include <mutex>
+
+#include "fp8opt_internal.cuh"
+
+namespace fp8opt {
+
+// Elements that share one scale of an activation checkpoint.
+constexpr int kActGroup = 128;
+
+enum ActKind { kActSave = 0, kActGelu = 1, kActGeluTanh = 2 };
+
+// One call of the activation kernels: forward reads x and writes codes_out,
+// scales_out and (GELU) out; backward reads codes, scales and (GELU) x, the
+// output's gradient, and writes out.
+struct ActArgs {
+  const void* x;
+  int64_t n;
+  int dtype;
+  bool vec_ok;              // every buffer aligned for 16-byte accesses
+  void* out;
+  uint8_t* codes_out;
+  float* scales_out;
+  const uint8_t* codes;
+  const float* scales;
+};
+
+cudaError_t launch_act(int act, bool fwd, const ActArgs& a, int sms,
+                       cudaStream_t stream, LaunchMark mark);
+
+// Longest row that a CTA keeps in registers.
+constexpr int64_t kLnMaxRegCols = 16384, kLnMaxRegColsBackward = 8192;
+
+// Layer norm over rows of `cols` elements; x, y, dy and dx of type dtype, the
+// parameters and their gradients of type wdtype.  codes and scales (one per
+// row) hold xhat in 8 bits; without them mean and x are kept instead.
+struct LnForward {
+  const void* x;
+  const void* weight;
+  const void* bias;          // may be NULL
+  void* y;
+  float* mean;               // NULL with codes
+  float* rstd;
+  uint8_t* codes;
+  float* scales;
+  int64_t rows, cols;
+  int dtype, wdtype;
+  bool vec_ok;               // cols and every buffer allow 16-byte accesses
+  float eps;
+};
+
+struct LnBackward {
+  const void* dy;
+  const void* x;
+  const void* weight;
+  const float* mean;
+  const float* rstd;
+  const uint8_t* codes;
+  const float* scales;
+  void* dx;
+  void* dw;
+  void* db;                  // may be NULL
+  int64_t rows, cols;
+  int dtype, wdtype;
+  bool vec_ok;
+};
+
+cudaError_t launch_ln_forward(const LnForward& a, int sms, cudaStream_t stream,
+                              LaunchMark mark);
+size_t ln_backward_scratch(const LnBackward& a, int sms);
+cudaError_t launch_ln_backward(const LnBackward& a, void* scratch, int sms,
+                               cudaStream_t stream, LaunchMark mark);
+
+// Holds the library lock for one operator call, with the current device's SM
+// count, the launch marks, and `scratch_bytes` of the stream's workspace
+// (contents undefined; the call's own until its work on the stream ends).
+// open() returns a status and records the error's text.
+class OpCall {
+ public:
+  OpCall();
+  int open(const char* fn, cudaStream_t stream, size_t scratch_bytes);
+  int done(const char* fn, cudaError_t e);   // the call's status
+  char* scratch = nullptr;
+  int sms = 0;
+  LaunchMark mark = nullptr;
+
+ private:
+  std::unique_lock<std::mutex> lock_;
+};
+
+int record_error(int status, const char* what);
+
+// --------------------------------------------------------- element helpers
+
+// Two fp32 values rounded to nearest even to a pair of DT (kBF16 or kF16),
+// the first in the low half.
+template <int DT>
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+  if (DT == kF16) return f2_to_h2(make_float2(a, b));
+  uint32_t d;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(b), "f"(a));
+  return d;
+}
+
+template <int DT>
+__device__ __forceinline__ void store1(void* p, int64_t i, float x) {
+  if (DT == kF32) static_cast<float*>(p)[i] = x;
+  else static_cast<uint16_t*>(p)[i] = (uint16_t)pack2<DT>(x, 0.0f);
+}
+
+}  // namespace fp8opt

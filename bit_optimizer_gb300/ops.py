@@ -1,0 +1,208 @@
+"""The training operators around the optimizer: 8-bit activation checkpoints,
+GELU, layer norm and the cross entropy of a linear layer over a large
+vocabulary, forward and backward, as functions of CUDA tensors.
+
+Like the rest of the package this is argument checking and marshalling: every
+step runs in the library's kernels (include/fp8opt.h describes the arithmetic).
+Tensors must be contiguous and on one device; outputs are allocated on
+``stream`` (the current stream unless given), where the work runs too, and the
+caller orders other streams' use of the inputs and outputs against it, as for
+any CUDA work.  No function waits for the GPU.
+
+``bit_optimizer_gb300.nn`` wraps these functions for autograd.
+"""
+from __future__ import annotations
+
+import torch
+
+from . import _lib
+from ._lib import BF16, F16, F32, check, load
+
+__all__ = ["act_save", "act_load", "gelu", "gelu_backward", "layer_norm",
+           "layer_norm_backward", "ACT_GROUP"]
+
+ACT_GROUP = _lib.ACT_GROUP
+_DT = {torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16}
+_FORMS = {"none": _lib.GELU_ERF, "tanh": _lib.GELU_TANH}
+
+
+def _dtype(t: torch.Tensor, name: str) -> int:
+    try:
+        return _DT[t.dtype]
+    except KeyError:
+        raise TypeError(f"{name}: unsupported dtype {t.dtype}") from None
+
+
+def _check(t, name: str, dev: int, dtype=None, shape=None) -> int:
+    """The address of a contiguous CUDA tensor on device ``dev`` (any device
+    when dev < 0) with the given dtype and shape, where given."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if dev >= 0 and t.get_device() != dev:
+        raise ValueError(f"{name} is on another device")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+    return t.data_ptr()
+
+
+class _On:
+    """Makes a tensor's device, and a stream given for it, current."""
+
+    def __init__(self, dev: int, stream):
+        self._ctx = (torch.cuda.stream(stream) if stream is not None else
+                     torch.cuda.device(dev) if dev != torch.cuda.current_device()
+                     else None)
+        if stream is not None and stream.device_index != dev:
+            raise ValueError("stream is on another device than the tensors")
+        self._dev = dev
+
+    def __enter__(self) -> int:
+        if self._ctx is not None:
+            self._ctx.__enter__()
+        return torch.cuda.current_stream(self._dev).cuda_stream
+
+    def __exit__(self, *exc):
+        if self._ctx is not None:
+            self._ctx.__exit__(*exc)
+
+
+def _form(approximate: str) -> int:
+    try:
+        return _FORMS[approximate]
+    except (KeyError, TypeError):
+        raise ValueError(f"approximate must be 'none' or 'tanh', not {approximate!r}") from None
+
+
+def _groups(numel: int) -> int:
+    return -(-numel // ACT_GROUP)
+
+
+# ------------------------------------------------- activation checkpoints
+
+def act_save(x: torch.Tensor, stream=None):
+    """The 8-bit checkpoint of x: (codes, scales), E4M3 codes in x's shape
+    (uint8) and one float32 scale per ACT_GROUP consecutive elements."""
+    px, dt, dev = _check(x, "x", -1), _dtype(x, "x"), x.get_device()
+    with _On(dev, stream) as s:
+        codes = torch.empty_like(x, dtype=torch.uint8)
+        scales = torch.empty(_groups(x.numel()), dtype=torch.float32, device=x.device)
+        check(load().fp8_act_save(px, x.numel(), dt, codes.data_ptr(),
+                                  scales.data_ptr(), s))
+    return codes, scales
+
+
+def _checkpoint(codes, scales, dev: int, shape=None):
+    pc = _check(codes, "codes", dev, torch.uint8, shape)
+    return pc, _check(scales, "scales", codes.get_device(), torch.float32,
+                      (_groups(codes.numel()),))
+
+
+def act_load(codes: torch.Tensor, scales: torch.Tensor, dtype=torch.float16,
+             stream=None) -> torch.Tensor:
+    """The activation of an ``act_save`` checkpoint, in ``dtype``."""
+    pc, ps = _checkpoint(codes, scales, -1)
+    if dtype not in _DT:
+        raise TypeError(f"unsupported dtype {dtype}")
+    with _On(codes.get_device(), stream) as s:
+        x = torch.empty_like(codes, dtype=dtype)
+        check(load().fp8_act_load(pc, ps, codes.numel(), _DT[dtype], x.data_ptr(), s))
+    return x
+
+
+def gelu(x: torch.Tensor, approximate: str = "none", stream=None):
+    """(y, codes, scales): y = gelu(x) and the 8-bit checkpoint of x, in one
+    pass.  approximate: "none" (x Phi(x)) or "tanh", as torch's."""
+    px, dt, dev, form = _check(x, "x", -1), _dtype(x, "x"), x.get_device(), _form(approximate)
+    with _On(dev, stream) as s:
+        y = torch.empty_like(x)
+        codes = torch.empty_like(x, dtype=torch.uint8)
+        scales = torch.empty(_groups(x.numel()), dtype=torch.float32, device=x.device)
+        check(load().fp8_gelu(px, x.numel(), dt, form, y.data_ptr(), codes.data_ptr(),
+                              scales.data_ptr(), s))
+    return y, codes, scales
+
+
+def gelu_backward(dy: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor,
+                  approximate: str = "none", stream=None) -> torch.Tensor:
+    """dx = dy * gelu'(x), with x read from its 8-bit checkpoint."""
+    pd, dt, dev, form = _check(dy, "dy", -1), _dtype(dy, "dy"), dy.get_device(), _form(approximate)
+    pc, ps = _checkpoint(codes, scales, dev, dy.shape)
+    with _On(dev, stream) as s:
+        dx = torch.empty_like(dy)
+        check(load().fp8_gelu_backward(pd, pc, ps, dy.numel(), dt, form, dx.data_ptr(), s))
+    return dx
+
+
+# -------------------------------------------------------------- layer norm
+
+def _rows_cols(t: torch.Tensor, name: str):
+    if t.dim() < 1 or t.shape[-1] < 1:
+        raise ValueError(f"{name} needs a last dimension of at least 1")
+    cols = t.shape[-1]
+    return t.numel() // cols, cols
+
+
+def layer_norm(x: torch.Tensor, weight: torch.Tensor, bias=None, eps: float = 1e-5,
+               save: str = "x", stream=None):
+    """Layer norm over the last dimension.
+
+    save="x": returns (y, mean, rstd); the backward pass takes x again.
+    save="fp8": returns (y, codes, scales, rstd): the normalised x in E4M3
+    (uint8, x's shape) with one float32 scale per row, instead of x.
+    mean, rstd and scales have x's shape without its last dimension.
+    """
+    if save not in ("x", "fp8"):
+        raise ValueError(f"save must be 'x' or 'fp8', not {save!r}")
+    px, dt, dev = _check(x, "x", -1), _dtype(x, "x"), x.get_device()
+    rows, cols = _rows_cols(x, "x")
+    pw, wdt = _check(weight, "weight", dev, None, (cols,)), _dtype(weight, "weight")
+    pb = None if bias is None else _check(bias, "bias", dev, weight.dtype, (cols,))
+    lead = x.shape[:-1]
+    with _On(dev, stream) as s:
+        y = torch.empty_like(x)
+        rstd = torch.empty(lead, dtype=torch.float32, device=x.device)
+        if save == "x":
+            mean = torch.empty_like(rstd)
+            check(load().fp8_layer_norm(px, pw, pb, rows, cols, dt, wdt, eps,
+                                        y.data_ptr(), mean.data_ptr(), rstd.data_ptr(),
+                                        None, None, s))
+            return y, mean, rstd
+        codes = torch.empty_like(x, dtype=torch.uint8)
+        scales = torch.empty_like(rstd)
+        check(load().fp8_layer_norm(px, pw, pb, rows, cols, dt, wdt, eps, y.data_ptr(),
+                                    None, rstd.data_ptr(), codes.data_ptr(),
+                                    scales.data_ptr(), s))
+        return y, codes, scales, rstd
+
+
+def layer_norm_backward(dy: torch.Tensor, weight: torch.Tensor, rstd: torch.Tensor,
+                        x=None, mean=None, codes=None, scales=None,
+                        need_bias: bool = True, stream=None):
+    """(dx, dweight, dbias) of ``layer_norm``, from x and mean (save="x") or
+    from codes and scales (save="fp8"); dbias is None without need_bias."""
+    pd, dt, dev = _check(dy, "dy", -1), _dtype(dy, "dy"), dy.get_device()
+    rows, cols = _rows_cols(dy, "dy")
+    lead = dy.shape[:-1]
+    pw, wdt = _check(weight, "weight", dev, None, (cols,)), _dtype(weight, "weight")
+    pr = _check(rstd, "rstd", dev, torch.float32, lead)
+    px = pm = pc = ps = None
+    if codes is not None and scales is not None and x is None and mean is None:
+        pc = _check(codes, "codes", dev, torch.uint8, dy.shape)
+        ps = _check(scales, "scales", dev, torch.float32, lead)
+    elif x is not None and mean is not None and codes is None and scales is None:
+        px = _check(x, "x", dev, dy.dtype, dy.shape)
+        pm = _check(mean, "mean", dev, torch.float32, lead)
+    else:
+        raise ValueError("give x and mean, or codes and scales")
+    with _On(dev, stream) as s:
+        dx = torch.empty_like(dy)
+        dw = torch.empty_like(weight)
+        db = torch.empty_like(weight) if need_bias else None
+        check(load().fp8_layer_norm_backward(
+            pd, px, pm, pc, ps, pr, pw, rows, cols, dt, wdt, dx.data_ptr(), dw.data_ptr(),
+            db.data_ptr() if need_bias else None, s))
+    return dx, dw, db

@@ -587,6 +587,84 @@ FP8OPT_API int fp8_norm_terms_from_limbs(const int64_t *limbs_dev,
                                          int fmt, float inv_loss_scale,
                                          double *terms_dev, void *stream);
 
+/*
+ * Training operators around the optimizer: 8-bit activation checkpoints,
+ * GELU, layer norm and the cross entropy of a linear layer over a large
+ * vocabulary.  They keep what the backward pass needs in the same E4M3 codes
+ * and just-in-time scales as the optimizer state.  No counterpart in the
+ * MS-AMP pages, whose savings stop at gradients, weights and optimizer state.
+ *
+ * Common rules: tensors are contiguous; `dtype` is FP8OPT_F32, FP8OPT_BF16 or
+ * FP8OPT_F16; sums, statistics and exponentials are fp32, and a result is
+ * rounded to its type once.  16-byte-aligned buffers (and, for layer norm, a
+ * row length that is a multiple of 8) take the vector path, others an element
+ * path.  Outputs may not overlap inputs.  An empty tensor may have a NULL
+ * address.  No call waits for the stream.  Results do not depend on the
+ * schedule: repeated calls give the same bits.  Scratch (the backward passes
+ * and the cross entropy) comes from the stream's workspace, with its rules on
+ * growth and capture.
+ */
+
+/* Elements that share one scale of an activation checkpoint. */
+#define FP8OPT_ACT_GROUP 128
+
+/* Forms of GELU: x Phi(x), and its tanh approximation. */
+#define FP8OPT_GELU_ERF  0
+#define FP8OPT_GELU_TANH 1
+
+/*
+ * fp8_act_save: the 8-bit checkpoint of an activation, codes (numel) and
+ * scales (ceil(numel / FP8OPT_ACT_GROUP) fp32): fp8_cast_scaled's arithmetic
+ * on each group of FP8OPT_ACT_GROUP consecutive elements (amax, scale = 448 /
+ * amax with its guards, E4M3 code = encode(x * scale)).
+ * fp8_act_load: x = decode(code) * (1 / scale), one division per scale.
+ */
+FP8OPT_API int fp8_act_save(const void *x, int64_t numel, int dtype,
+                            uint8_t *codes, float *scales, void *stream);
+FP8OPT_API int fp8_act_load(const uint8_t *codes, const float *scales,
+                            int64_t numel, int dtype, void *x, void *stream);
+
+/*
+ * fp8_gelu: y = gelu(x), and fp8_act_save's checkpoint of x, in one pass.
+ * form: FP8OPT_GELU_ERF, x Phi(x) with Phi the normal distribution function,
+ * or FP8OPT_GELU_TANH, 0.5 x (1 + tanh(sqrt(2 / pi) (x + 0.044715 x^3))).
+ * fp8_gelu_backward: dx = dy * gelu'(x) with x read from the checkpoint.
+ */
+FP8OPT_API int fp8_gelu(const void *x, int64_t numel, int dtype, int form,
+                        void *y, uint8_t *codes, float *scales, void *stream);
+FP8OPT_API int fp8_gelu_backward(const void *dy, const uint8_t *codes,
+                                 const float *scales, int64_t numel, int dtype,
+                                 int form, void *dx, void *stream);
+
+/*
+ * fp8_layer_norm: over each of `rows` rows of `cols` elements,
+ *   mean = sum x / cols, rstd = 1 / sqrt(sum (x - mean)^2 / cols + eps),
+ *   xhat = (x - mean) * rstd, y = xhat * weight + bias.
+ * weight and bias (NULL: none) have `cols` elements of type wdtype.  rstd
+ * (rows fp32) is always written.  What else the backward pass needs is kept
+ * in one of two forms: codes and scales NULL, mean (rows fp32) given: the
+ * caller keeps x; codes (rows x cols) and scales (rows fp32) given, mean
+ * NULL: xhat in E4M3 with one scale 448 / max |xhat| per row, and x need not
+ * be kept.
+ *
+ * fp8_layer_norm_backward: with h = dy * weight,
+ *   dx = rstd * (h - sum h / cols - xhat * sum(h * xhat) / cols),
+ *   dweight = sum over rows of dy * xhat, dbias = sum over rows of dy (NULL:
+ * not wanted), of type wdtype.  xhat comes from x and mean (codes and scales
+ * NULL) or from codes and scales (x and mean NULL).  rows = 0 gives zero
+ * dweight and dbias.  cols >= 1, eps >= 0.
+ */
+FP8OPT_API int fp8_layer_norm(const void *x, const void *weight,
+                              const void *bias, int64_t rows, int64_t cols,
+                              int dtype, int wdtype, float eps, void *y,
+                              float *mean, float *rstd, uint8_t *codes,
+                              float *scales, void *stream);
+FP8OPT_API int fp8_layer_norm_backward(
+    const void *dy, const void *x, const float *mean, const uint8_t *codes,
+    const float *scales, const float *rstd, const void *weight, int64_t rows,
+    int64_t cols, int dtype, int wdtype, void *dx, void *dweight, void *dbias,
+    void *stream);
+
 /* Text of a status code (static storage). */
 FP8OPT_API const char *fp8opt_strerror(int status);
 
@@ -602,7 +680,8 @@ FP8OPT_API const char *fp8opt_last_error(void);
  * recorded events and returns, for one kernel name ("cast_amax",
  * "cast_encode", "step_amax", "step_update", "step_w8", "cast_step_amax",
  * "reduce_amax", "reduce_encode", "grad_norm", "grad_norm_terms", "clip_coef",
- * "found"), the launches
+ * "found", "act_save", "act_load", "gelu", "gelu_backward", "layer_norm",
+ * "layer_norm_backward", "layer_norm_params"), the launches
  * recorded since enabling and their summed duration in milliseconds.  Returns
  * FP8OPT_ERR_ARG for an unknown name or NULL outputs. */
 FP8OPT_API int fp8opt_timing_enable(int on);

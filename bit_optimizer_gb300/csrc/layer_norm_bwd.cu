@@ -17,69 +17,37 @@ namespace fp8opt {
 
 namespace {
 
-// The saved side of a row: x, or the codes of xhat.
-template <int DT, int VEC, bool FP8>
-struct LnSaved {
-  LnRaw<DT, VEC> x;
-};
-template <int DT>
-struct LnSaved<DT, 8, true> {
-  uint2 c;
-};
-template <int DT>
-struct LnSaved<DT, 1, true> {
-  uint8_t c[8];
-};
+// Threads of an SM (128 registers each), in one or two CTAs: each CTA writes
+// one pair of partial sums.
+constexpr int kBwdThreads = 512;
 
-template <int DT, int VEC, bool FP8, int TPR>
-__device__ __forceinline__ LnSaved<DT, VEC, FP8> ln_load_saved(const LnBackward& a, int64_t r,
-                                                              int v, int t, int cols) {
-  LnSaved<DT, VEC, FP8> s;
-  if constexpr (!FP8) {
-    s.x = ln_load<DT, VEC, TPR>(
-        static_cast<const char*>(a.x) + (size_t)r * a.cols * (DT == kF32 ? 4 : 2), v, t, cols);
-  } else if constexpr (VEC == 8) {
-    const int c = ln_col<TPR, 8>(v, 0, t);
-    s.c = make_uint2(0, 0);
-    if (c < cols) s.c = ld_once2(a.codes + r * a.cols + c);
-  } else {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const int c = ln_col<TPR, 1>(v, e, t);
-      s.c[e] = c < cols ? a.codes[r * a.cols + c] : 0;
-    }
-  }
-  return s;
-}
+// Bytes of a vector of eight elements: of dy (and x), and of the saved side.
+template <int DT>
+constexpr int kVecBytes = DT == kF32 ? 32 : 16;
+template <int DT, bool FP8>
+constexpr int kSavedBytes = FP8 ? 8 : kVecBytes<DT>;
+template <int DT>
+constexpr int kStages = DT == kF32 ? 3 : 4;
+
+template <int DT, int VPT, int NT, bool FP8>
+constexpr int kRingBytes = kStages<DT> * VPT * NT * (kVecBytes<DT> + kSavedBytes<DT, FP8>);
 
 // xhat of eight elements: (x - sub) * mul, with sub = mean and mul = rstd, or
-// sub = 0 and mul = 1 / scale.
-template <int DT, int VEC, bool FP8>
-__device__ __forceinline__ void ln_xhat(const LnSaved<DT, VEC, FP8>& s, float sub, float mul,
-                                        float* x) {
-  if constexpr (!FP8) {
-    ln_widen<DT, VEC>(s.x, x);
+// the code's value * mul with mul = 1 / scale.
+__device__ __forceinline__ void ln_xhat(const float* x, float sub, float mul, float2* out) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = (x[e] - sub) * mul;
-  } else {
-    if constexpr (VEC == 8) {
-      float d[8];
-      dec8<kE4M3>(s.c, d);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) x[e] = d[e] * mul;
-    } else {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) x[e] = dec2<kE4M3>(s.c[e]).x * mul;
-    }
-  }
+  for (int j = 0; j < 4; ++j)
+    out[j] = mul2(add2(make_float2(x[2 * j], x[2 * j + 1]), splat2(-sub)), splat2(mul));
 }
 
-template <int DT, int VEC, int TPR, int VPT, int NT, int CTAS, bool FP8>
-__global__ void __launch_bounds__(NT, CTAS)
+template <int DT, int VEC, int TPR, int VPT, int NT, bool FP8>
+__global__ void __launch_bounds__(NT, kBwdThreads / NT)
 ln_backward_kernel(const LnBackward a, float* __restrict__ partial) {
-  constexpr int RPC = NT / TPR;
+  constexpr int RPC = NT / TPR, ST = kStages<DT>, Q = DT == kF32 ? 2 : 1;
   __shared__ RowSums<TPR> sums[RPC];
-  extern __shared__ float merge[];   // [2][cols], used when RPC > 1
+  // the ring: dy [ST][VPT][Q][NT] of 16 bytes, then x alike or the codes
+  // [ST][VPT][NT] of 8; afterwards the row slots' sums [RPC][2][cols]
+  extern __shared__ uint4 ring[];
   const int slot = threadIdx.x / TPR, t = threadIdx.x % TPR;
   const int cols = (int)a.cols;
   const size_t es = DT == kF32 ? 4 : 2;
@@ -87,110 +55,182 @@ ln_backward_kernel(const LnBackward a, float* __restrict__ partial) {
   const int64_t step = (int64_t)gridDim.x * RPC;
   int turn = 0;
 
-  float aw[8 * VPT], ab[8 * VPT];
-#pragma unroll
-  for (int i = 0; i < 8 * VPT; ++i) aw[i] = ab[i] = 0.0f;
-
-  int64_t r = (int64_t)blockIdx.x * RPC + slot;
-  LnRaw<DT, VEC> dy[VPT];
-  LnSaved<DT, VEC, FP8> sv[VPT];
-  float mul = 0.0f, sub = 0.0f, rstd = 0.0f;
-  if (r < a.rows) {
-#pragma unroll
-    for (int v = 0; v < VPT; ++v) {
-      dy[v] = ln_load<DT, VEC, TPR>(static_cast<const char*>(a.dy) + (size_t)r * a.cols * es, v,
-                                    t, cols);
-      sv[v] = ln_load_saved<DT, VEC, FP8, TPR>(a, r, v, t, cols);
-    }
-    rstd = __ldg(a.rstd + r);
-    if (FP8) mul = __ldg(a.scales + r);
-    else sub = __ldg(a.mean + r);
-  }
-  while (r < a.rows) {
-    const int64_t rn = r + step;
-    LnRaw<DT, VEC> dyn[VPT];
-    LnSaved<DT, VEC, FP8> svn[VPT];
-    float muln = 0.0f, subn = 0.0f, rstdn = 0.0f;
-    if (rn < a.rows) {
+  const auto at_dy = [&](int stage, int v, int q) -> uint4* {
+    return ring + ((stage * VPT + v) * Q + q) * NT + threadIdx.x;
+  };
+  uint4* const ring2 = ring + ST * VPT * Q * NT;
+  const auto at_x = [&](int stage, int v, int q) -> uint4* {
+    return ring2 + ((stage * VPT + v) * Q + q) * NT + threadIdx.x;
+  };
+  const auto at_code = [&](int stage, int v) -> uint2* {
+    return reinterpret_cast<uint2*>(ring2) + (stage * VPT + v) * NT + threadIdx.x;
+  };
+  const auto fetch = [&](int stage, int64_t row) {
+    if (row < a.rows) {
+      const size_t at = (size_t)row * a.cols;
 #pragma unroll
       for (int v = 0; v < VPT; ++v) {
-        dyn[v] = ln_load<DT, VEC, TPR>(static_cast<const char*>(a.dy) + (size_t)rn * a.cols * es,
-                                       v, t, cols);
-        svn[v] = ln_load_saved<DT, VEC, FP8, TPR>(a, rn, v, t, cols);
-      }
-      rstdn = __ldg(a.rstd + rn);
-      if (FP8) muln = __ldg(a.scales + rn);
-      else subn = __ldg(a.mean + rn);
-    }
-    // The values are made twice, before and after the reduction, from the raw
-    // words: keeping them would take twice the registers.
-    const float k = FP8 ? __fdiv_rn(1.0f, mul) : rstd;
-    float s1 = 0.0f, s2 = 0.0f;
+        const int c = ln_col<TPR, 8>(v, 0, t);
+        if (c >= cols) continue;
 #pragma unroll
-    for (int v = 0; v < VPT; ++v) {
-      float g[8], x[8], w[8];
-      ln_widen<DT, VEC>(dy[v], g);
-      ln_xhat<DT, VEC, FP8>(sv[v], sub, k, x);
-      ln_param<VEC, TPR>(a.weight, a.wdtype, 0.0f, v, t, cols, w);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        if (!ln_in<TPR, VEC>(v, e, t, cols)) x[e] = 0.0f;   // g is 0 there
-        const float h = g[e] * w[e];
-        s1 += h;
-        s2 = __fmaf_rn(h, x[e], s2);
-        aw[8 * v + e] = __fmaf_rn(g[e], x[e], aw[8 * v + e]);
-        ab[8 * v + e] += g[e];
+        for (int q = 0; q < Q; ++q) {
+          copy_async<16>(at_dy(stage, v, q), static_cast<const char*>(a.dy) + (at + c) * es + 16 * q);
+          if (!FP8)
+            copy_async<16>(at_x(stage, v, q), static_cast<const char*>(a.x) + (at + c) * es + 16 * q);
+        }
+        if (FP8) copy_async<8>(at_code(stage, v), a.codes + at + c);
       }
     }
-    const float2 s = row_sum2<TPR>(s1, s2, sums[slot], turn, slot);
-    const float m1 = s.x * inv_c, m2 = s.y * inv_c;
+    copy_commit();
+  };
+
+  float2 w[4 * VPT], aw[4 * VPT], ab[4 * VPT];
 #pragma unroll
-    for (int v = 0; v < VPT; ++v) {
-      float g[8], x[8], w[8];
-      ln_widen<DT, VEC>(dy[v], g);
-      ln_xhat<DT, VEC, FP8>(sv[v], sub, k, x);
-      ln_param<VEC, TPR>(a.weight, a.wdtype, 0.0f, v, t, cols, w);
+  for (int v = 0; v < VPT; ++v) {
+    float p[8];
+    ln_param<VEC, TPR>(a.weight, a.wdtype, 0.0f, v, t, cols, p);
 #pragma unroll
-      for (int e = 0; e < 8; ++e)
-        g[e] = rstd * __fmaf_rn(-x[e], m2, __fmaf_rn(g[e], w[e], -m1));
-      ln_store<DT, VEC, TPR>(static_cast<char*>(a.dx) + (size_t)r * a.cols * es, v, t, cols, g);
+    for (int j = 0; j < 4; ++j) {
+      w[4 * v + j] = make_float2(p[2 * j], p[2 * j + 1]);
+      aw[4 * v + j] = ab[4 * v + j] = make_float2(0.0f, 0.0f);
     }
-#pragma unroll
-    for (int v = 0; v < VPT; ++v) {
-      dy[v] = dyn[v];
-      sv[v] = svn[v];
-    }
-    mul = muln;
-    sub = subn;
-    rstd = rstdn;
-    r = rn;
   }
 
-  float* out = partial + (size_t)blockIdx.x * 2 * cols;
-  for (int s = 0; s < RPC; ++s) {
-    if (slot == s) {
+  int64_t r = (int64_t)blockIdx.x * RPC + slot;
+  if constexpr (VEC == 8) {
+#pragma unroll
+    for (int i = 0; i < ST; ++i)   // what lies past the row's end stays zero
 #pragma unroll
       for (int v = 0; v < VPT; ++v)
+        if (ln_col<TPR, 8>(v, 0, t) >= cols) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const int c = ln_col<TPR, VEC>(v, e, t);
-          if (c >= cols) continue;
-          if (RPC == 1) {
-            out[c] = aw[8 * v + e];
-            out[cols + c] = ab[8 * v + e];
-          } else if (s == 0) {
-            merge[c] = aw[8 * v + e];
-            merge[cols + c] = ab[8 * v + e];
-          } else {
-            merge[c] += aw[8 * v + e];
-            merge[cols + c] += ab[8 * v + e];
+          for (int q = 0; q < Q; ++q) {
+            *at_dy(i, v, q) = make_uint4(0, 0, 0, 0);
+            if (!FP8) *at_x(i, v, q) = make_uint4(0, 0, 0, 0);
+          }
+          if (FP8) *at_code(i, v) = make_uint2(0, 0);
+        }
+#pragma unroll
+    for (int i = 0; i < ST - 1; ++i) fetch(i, r + i * step);
+  }
+  // a row's rstd, and its mean or scale, are read one row ahead
+  const float* const other = FP8 ? a.scales : a.mean;
+  float rstd_next = 0.0f, other_next = 1.0f;
+  if (r < a.rows) {
+    rstd_next = __ldg(a.rstd + r);
+    other_next = __ldg(other + r);
+  }
+  for (int stage = 0; r < a.rows; r += step, stage = stage + 1 == ST ? 0 : stage + 1) {
+    const float rstd = rstd_next;
+    const float sub = FP8 ? 0.0f : other_next;
+    const float mul = FP8 ? __fdiv_rn(1.0f, other_next) : rstd;
+    if (r + step < a.rows) {
+      rstd_next = __ldg(a.rstd + r + step);
+      other_next = __ldg(other + r + step);
+    }
+    if constexpr (VEC == 8) copy_wait<ST - 2>();
+    float2 g[4 * VPT], x[4 * VPT];
+    float2 s1 = make_float2(0.0f, 0.0f), s2 = s1;
+#pragma unroll
+    for (int v = 0; v < VPT; ++v) {
+      float d[8], e[8];
+      if constexpr (VEC == 8) {
+        LnRaw<DT, 8> raw;
+#pragma unroll
+        for (int q = 0; q < Q; ++q) raw.v[q] = *at_dy(stage, v, q);
+        ln_widen<DT, 8>(raw, d);
+        if constexpr (FP8) {
+          dec8<kE4M3>(*at_code(stage, v), e);
+        } else {
+#pragma unroll
+          for (int q = 0; q < Q; ++q) raw.v[q] = *at_x(stage, v, q);
+          ln_widen<DT, 8>(raw, e);
+        }
+      } else {
+        const size_t at = (size_t)r * a.cols;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const int c = ln_col<TPR, 1>(v, k, t);
+          d[k] = e[k] = 0.0f;
+          if (c < cols) {
+            d[k] = load1<DT>(a.dy, at + c);
+            e[k] = FP8 ? dec2<kE4M3>(a.codes[at + c]).x : load1<DT>(a.x, at + c);
           }
         }
+      }
+      ln_xhat(e, sub, mul, x + 4 * v);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int i = 4 * v + j;
+        g[i] = make_float2(d[2 * j], d[2 * j + 1]);
+        // past the row's end dy is 0, and xhat must not be a NaN there
+        if (!ln_in<TPR, VEC>(v, 2 * j, t, cols)) x[i].x = 0.0f;
+        if (!ln_in<TPR, VEC>(v, 2 * j + 1, t, cols)) x[i].y = 0.0f;
+        aw[i] = fma2(g[i], x[i], aw[i]);
+        ab[i] = add2(ab[i], g[i]);
+        g[i] = mul2(g[i], w[i]);
+        s1 = add2(s1, g[i]);
+        s2 = fma2(g[i], x[i], s2);
+      }
     }
-    if (RPC > 1) __syncthreads();
+    if constexpr (VEC == 8) fetch(stage == 0 ? ST - 1 : stage - 1, r + (ST - 1) * step);
+    const float2 s = row_sum2<TPR>(s1.x + s1.y, s2.x + s2.y, sums[slot], turn, slot);
+    const float2 m1 = splat2(-s.x * inv_c), m2 = splat2(-s.y * inv_c), k = splat2(rstd);
+#pragma unroll
+    for (int v = 0; v < VPT; ++v) {
+      float d[8];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float2 y = mul2(k, fma2(x[4 * v + j], m2, add2(g[4 * v + j], m1)));
+        d[2 * j] = y.x;
+        d[2 * j + 1] = y.y;
+      }
+      ln_store<DT, VEC, TPR>(static_cast<char*>(a.dx) + (size_t)r * a.cols * es, v, t, cols, d);
+    }
   }
-  if (RPC > 1)
-    for (int c = threadIdx.x; c < 2 * cols; c += NT) out[c] = merge[c];
+
+  // The CTA's sums: the row slots side by side in shared memory (the ring is
+  // drained first), then added in slot order.
+  float* const out = partial + (size_t)blockIdx.x * 2 * cols;
+  float* const merge = reinterpret_cast<float*>(ring);
+  if (RPC > 1) {
+    copy_wait<0>();
+    __syncthreads();
+  }
+  float* const mine = RPC > 1 ? merge + slot * 2 * cols : out;
+#pragma unroll
+  for (int v = 0; v < VPT; ++v) {
+    const float2* s[2] = {aw + 4 * v, ab + 4 * v};
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      float* p = mine + h * cols;
+      if constexpr (VEC == 8) {
+        const int c = ln_col<TPR, 8>(v, 0, t);
+        if (c < cols) {
+          float4* q = reinterpret_cast<float4*>(p + c);
+          q[0] = make_float4(s[h][0].x, s[h][0].y, s[h][1].x, s[h][1].y);
+          q[1] = make_float4(s[h][2].x, s[h][2].y, s[h][3].x, s[h][3].y);
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const int c = ln_col<TPR, 1>(v, j, t);
+          if (c < cols) p[c] = (j & 1) ? s[h][j / 2].y : s[h][j / 2].x;
+        }
+      }
+    }
+  }
+  if (RPC > 1) {
+    __syncthreads();
+    for (int c = threadIdx.x; c < 2 * cols; c += NT) {
+      float v = merge[c];
+#pragma unroll
+      for (int i = 1; i < RPC; ++i) v += merge[i * 2 * cols + c];
+      out[c] = v;
+    }
+  }
+  // the kernel that adds the CTAs' sums may be set up meanwhile
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
 // dw and db of 32 columns: the `parts` partial sums, 32 at a time, then the 32
@@ -202,6 +242,7 @@ ln_param_grad_kernel(const float* __restrict__ partial, int64_t parts, int64_t c
   const int64_t c = (int64_t)blockIdx.x * 32 + threadIdx.x;
   void* out = blockIdx.y == 0 ? dw : db;
   float s = 0.0f;
+  asm volatile("griddepcontrol.wait;" ::: "memory");   // for the partial sums
   if (c < cols)
     for (int64_t p = threadIdx.y; p < parts; p += 32)
       s += __ldcg(partial + (p * 2 + blockIdx.y) * cols + c);
@@ -282,51 +323,58 @@ ln_backward_long_cols_kernel(const LnBackward a, int64_t rows_per, float* __rest
 
 constexpr int kLongParts = 16;   // row ranges of the long rows' dw and db
 
-// Rows a CTA visits at a time, and how many CTAs run, for the kernel that
-// by_cols() picks.
-struct Shape {
-  int rpc, nt, ctas;
-};
-Shape shape_of(int64_t cols) {
-  if (cols <= 1024) return {8, 256, 2};
-  if (cols <= 2048) return {2, 256, 2};
-  if (cols <= 4096) return {1, 256, 2};
-  return {1, 512, 1};
+// Rows that a CTA of the kernel that by_cols() picks visits at a time.
+int rows_per_cta(int64_t cols) {
+  return cols <= 512 ? 16 : cols <= 1024 ? 8 : cols <= 2048 ? 4 : cols <= 4096 ? 2 : 1;
 }
 
 unsigned grid_of(const LnBackward& a, int sms) {
-  const Shape s = shape_of(a.cols);
-  const int64_t need = (a.rows + s.rpc - 1) / s.rpc, most = (int64_t)sms * s.ctas;
-  return (unsigned)(need < most ? need : most);
+  const int64_t rpc = rows_per_cta(a.cols);
+  const int64_t need = (a.rows + rpc - 1) / rpc;
+  return (unsigned)(need < sms ? need : sms);
 }
 
-template <int DT, int VEC, int TPR, int VPT, int NT, int CTAS>
-void go(const LnBackward& a, float* partial, unsigned grid, cudaStream_t stream) {
-  const size_t smem = NT / TPR > 1 ? 2 * sizeof(float) * (size_t)a.cols : 0;
-  if (a.codes != nullptr)
-    ln_backward_kernel<DT, VEC, TPR, VPT, NT, CTAS, true><<<grid, NT, smem, stream>>>(a, partial);
-  else
-    ln_backward_kernel<DT, VEC, TPR, VPT, NT, CTAS, false><<<grid, NT, smem, stream>>>(a, partial);
+template <int DT, int VEC, int TPR, int VPT, bool FP8>
+cudaError_t go_form(const LnBackward& a, float* partial, unsigned grid, cudaStream_t stream) {
+  constexpr int NT = kBwdThreads, RPC = NT / TPR;
+  auto kernel = ln_backward_kernel<DT, VEC, TPR, VPT, NT, FP8>;
+  const int ring = VEC == 8 ? kRingBytes<DT, VPT, NT, FP8> : 0;
+  const int merge = RPC > 1 ? RPC * 2 * (int)sizeof(float) * (int)a.cols : 0;
+  const int smem = ring > merge ? ring : merge;
+  if (smem > 48 * 1024) {
+    const cudaError_t e =
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+  }
+  kernel<<<grid, NT, smem, stream>>>(a, partial);
+  return cudaSuccess;
+}
+
+template <int DT, int VEC, int TPR, int VPT>
+cudaError_t go(const LnBackward& a, float* p, unsigned grid, cudaStream_t s) {
+  return a.codes != nullptr ? go_form<DT, VEC, TPR, VPT, true>(a, p, grid, s)
+                            : go_form<DT, VEC, TPR, VPT, false>(a, p, grid, s);
 }
 
 template <int DT, int VEC>
-void by_cols(const LnBackward& a, float* p, unsigned grid, cudaStream_t s) {
-  if (a.cols <= 256) go<DT, VEC, 32, 1, 256, 2>(a, p, grid, s);
-  else if (a.cols <= 512) go<DT, VEC, 32, 2, 256, 2>(a, p, grid, s);
-  else if (a.cols <= 1024) go<DT, VEC, 32, 4, 256, 2>(a, p, grid, s);
-  else if (a.cols <= 2048) go<DT, VEC, 128, 2, 256, 2>(a, p, grid, s);
-  else if (a.cols <= 4096) go<DT, VEC, 256, 2, 256, 2>(a, p, grid, s);
-  else go<DT, VEC, 512, 2, 512, 1>(a, p, grid, s);
+cudaError_t by_cols(const LnBackward& a, float* p, unsigned grid, cudaStream_t s) {
+  if (a.cols <= 256) return go<DT, VEC, 32, 1>(a, p, grid, s);
+  if (a.cols <= 512) return go<DT, VEC, 32, 2>(a, p, grid, s);
+  if (a.cols <= 1024) return go<DT, VEC, 64, 2>(a, p, grid, s);
+  if (a.cols <= 2048) return go<DT, VEC, 128, 2>(a, p, grid, s);
+  if (a.cols <= 4096) return go<DT, VEC, 256, 2>(a, p, grid, s);
+  return go<DT, VEC, 512, 2>(a, p, grid, s);
 }
 
 template <int DT>
-int64_t by_type(const LnBackward& a, float* p, int sms, cudaStream_t s) {
-  if (a.rows == 0) return 0;
-  if (a.cols > kLnMaxRegColsBackward) {
+cudaError_t by_type(const LnBackward& a, float* p, int sms, cudaStream_t s, int64_t* parts) {
+  *parts = 0;
+  if (a.rows == 0) return cudaSuccess;
+  if (a.cols > kLnMaxRegCols) {
     const unsigned grid = (unsigned)(a.rows < 2 * sms ? a.rows : 2 * sms);
-    const int64_t parts = a.rows < kLongParts ? a.rows : kLongParts;
-    const int64_t rows_per = (a.rows + parts - 1) / parts;
-    const dim3 cg((unsigned)((a.cols + 255) / 256), (unsigned)parts);
+    *parts = a.rows < kLongParts ? a.rows : kLongParts;
+    const int64_t rows_per = (a.rows + *parts - 1) / *parts;
+    const dim3 cg((unsigned)((a.cols + 255) / 256), (unsigned)*parts);
     if (a.codes != nullptr) {
       ln_backward_long_dx_kernel<DT, true><<<grid, 1024, 0, s>>>(a);
       ln_backward_long_cols_kernel<DT, true><<<cg, 256, 0, s>>>(a, rows_per, p);
@@ -334,19 +382,18 @@ int64_t by_type(const LnBackward& a, float* p, int sms, cudaStream_t s) {
       ln_backward_long_dx_kernel<DT, false><<<grid, 1024, 0, s>>>(a);
       ln_backward_long_cols_kernel<DT, false><<<cg, 256, 0, s>>>(a, rows_per, p);
     }
-    return parts;
+    return cudaSuccess;
   }
   const unsigned grid = grid_of(a, sms);
-  if (a.vec_ok) by_cols<DT, 8>(a, p, grid, s);
-  else by_cols<DT, 1>(a, p, grid, s);
-  return grid;
+  *parts = grid;
+  return a.vec_ok ? by_cols<DT, 8>(a, p, grid, s) : by_cols<DT, 1>(a, p, grid, s);
 }
 
 }  // namespace
 
 size_t ln_backward_scratch(const LnBackward& a, int sms) {
   if (a.rows == 0) return 0;
-  const size_t parts = a.cols > kLnMaxRegColsBackward ? kLongParts : grid_of(a, sms);
+  const size_t parts = a.cols > kLnMaxRegCols ? kLongParts : grid_of(a, sms);
   return parts * 2 * (size_t)a.cols * sizeof(float);
 }
 
@@ -355,17 +402,26 @@ cudaError_t launch_ln_backward(const LnBackward& a, void* scratch, int sms, cuda
   float* p = static_cast<float*>(scratch);
   if (mark) mark(kLayerNormBackwardK, 0, stream);
   int64_t parts = 0;
-  if (a.dtype == kF32) parts = by_type<kF32>(a, p, sms, stream);
-  else if (a.dtype == kBF16) parts = by_type<kBF16>(a, p, sms, stream);
-  else parts = by_type<kF16>(a, p, sms, stream);
+  cudaError_t e = a.dtype == kF32    ? by_type<kF32>(a, p, sms, stream, &parts)
+                  : a.dtype == kBF16 ? by_type<kBF16>(a, p, sms, stream, &parts)
+                                     : by_type<kF16>(a, p, sms, stream, &parts);
   if (mark) mark(kLayerNormBackwardK, 1, stream);
-  cudaError_t e = cudaGetLastError();
+  if (e == cudaSuccess) e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   if (mark) mark(kLayerNormParamsK, 0, stream);
-  ln_param_grad_kernel<<<dim3((unsigned)((a.cols + 31) / 32), a.db != nullptr ? 2 : 1),
-                         dim3(32, 32), 0, stream>>>(p, parts, a.cols, a.wdtype, a.dw, a.db);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)((a.cols + 31) / 32), a.db != nullptr ? 2 : 1);
+  cfg.blockDim = dim3(32, 32);
+  cfg.stream = stream;
+  cudaLaunchAttribute early;
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &early;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, ln_param_grad_kernel, (const float*)p, parts, a.cols, a.wdtype,
+                         a.dw, a.db);
   if (mark) mark(kLayerNormParamsK, 1, stream);
-  return cudaGetLastError();
+  return e;
 }
 
 }  // namespace fp8opt

@@ -12,42 +12,134 @@ namespace fp8opt {
 
 namespace {
 
-template <int DT, int VEC, int TPR, int VPT, int NT, bool FP8>
-__global__ void __launch_bounds__(NT)
+// Threads of a CTA, and CTAs of an SM (64 registers a thread).
+constexpr int kFwdThreads = 512, kFwdCtas = 2;
+
+// Rows in flight of a thread's ring, and the ring's bytes.
+template <int DT>
+constexpr int kStages = DT == kF32 ? 2 : 4;
+template <int DT, int VPT>
+constexpr int kRingBytes = kStages<DT> * VPT * (DT == kF32 ? 32 : 16) * kFwdThreads;
+
+// Sum of the elements as a tree of pairs, so that its rounding error grows
+// with the logarithm of their number.
+template <int N>
+__device__ __forceinline__ float tree_sum(const float2* x) {
+  float2 s[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) s[i] = x[i];
+#pragma unroll
+  for (int h = N / 2; h > 0; h /= 2)
+#pragma unroll
+    for (int i = 0; i < h; ++i) s[i] = add2(s[i], s[i + h]);
+  return s[0].x + s[0].y;
+}
+
+template <int DT, int VEC, int TPR, int VPT, bool FP8>
+__global__ void __launch_bounds__(kFwdThreads, kFwdCtas)
 ln_forward_kernel(const LnForward a) {
-  constexpr int RPC = NT / TPR;
+  constexpr int NT = kFwdThreads, RPC = NT / TPR, Q = DT == kF32 ? 2 : 1, ST = kStages<DT>;
   __shared__ RowSums<TPR> sums[RPC];
+  // Weight and bias as fp32, then the ring [ST][VPT][Q][NT].  VEC 8: [2]
+  // [VPT][2][TPR] quads, so that a warp's quads lie side by side; VEC 1:
+  // [2][TPR * 8 * VPT] elements.
+  extern __shared__ uint4 shared[];
   const int slot = threadIdx.x / TPR, t = threadIdx.x % TPR;
   const int cols = (int)a.cols;
   const size_t es = DT == kF32 ? 4 : 2;
+  const int64_t step = (int64_t)gridDim.x * RPC;
   int turn = 0;
-  for (int64_t r = (int64_t)blockIdx.x * RPC + slot; r < a.rows;
-       r += (int64_t)gridDim.x * RPC) {
-    const char* row = static_cast<const char*>(a.x) + (size_t)r * a.cols * es;
-    LnRaw<DT, VEC> raw[VPT];
+  int64_t r = (int64_t)blockIdx.x * RPC + slot;
+  float* const sw = reinterpret_cast<float*>(shared);
+  float* const sb = sw + TPR * 8 * VPT;
+  uint4* const ring = shared + TPR * 4 * VPT;
+  const auto at = [&](int stage, int v, int q) -> uint4* {
+    return ring + ((stage * VPT + v) * Q + q) * NT + threadIdx.x;
+  };
+  const auto fetch = [&](int stage, int64_t row) {
+    if (row < a.rows) {
+      const char* p = static_cast<const char*>(a.x) + (size_t)row * a.cols * es;
 #pragma unroll
-    for (int v = 0; v < VPT; ++v) raw[v] = ln_load<DT, VEC, TPR>(row, v, t, cols);
-    float x[8 * VPT];
-    float s = 0.0f;
+      for (int v = 0; v < VPT; ++v) {
+        const int c = ln_col<TPR, 8>(v, 0, t);
+        if (c < cols)
 #pragma unroll
-    for (int v = 0; v < VPT; ++v) {
-      ln_widen<DT, VEC>(raw[v], x + 8 * v);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) s += x[8 * v + e];   // zero past the row's end
+          for (int q = 0; q < Q; ++q) copy_async<16>(at(stage, v, q), p + c * es + 16 * q);
+      }
     }
-    const float mean = row_sum2<TPR>(s, 0.0f, sums[slot], turn, slot).x / (float)cols;
-    float q = 0.0f;
-    uint32_t m = 0;
+    copy_commit();
+  };
+  if constexpr (VEC == 8) {
 #pragma unroll
-    for (int v = 0; v < VPT; ++v)
+    for (int i = 0; i < ST - 1; ++i) fetch(i, r + i * step);
+#pragma unroll
+    for (int i = 0; i < ST; ++i)   // what lies past the row's end stays zero
+#pragma unroll
+      for (int v = 0; v < VPT; ++v)
+        if (ln_col<TPR, 8>(v, 0, t) >= cols)
+#pragma unroll
+          for (int q = 0; q < Q; ++q) *at(i, v, q) = make_uint4(0, 0, 0, 0);
+  }
+  for (int i = threadIdx.x; i < TPR * VPT; i += NT) {
+    float w[8], b[8];
+    ln_param<VEC, TPR>(a.weight, a.wdtype, 0.0f, i / TPR, i % TPR, cols, w);
+    ln_param<VEC, TPR>(a.bias, a.wdtype, 0.0f, i / TPR, i % TPR, cols, b);
+    if constexpr (VEC == 8) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int at4 = (i / TPR * 2 + h) * TPR + i % TPR;
+        reinterpret_cast<float4*>(sw)[at4] =
+            make_float4(w[4 * h], w[4 * h + 1], w[4 * h + 2], w[4 * h + 3]);
+        reinterpret_cast<float4*>(sb)[at4] =
+            make_float4(b[4 * h], b[4 * h + 1], b[4 * h + 2], b[4 * h + 3]);
+      }
+    } else {
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        float& c = x[8 * v + e];
-        c = ln_in<TPR, VEC>(v, e, t, cols) ? c - mean : 0.0f;
-        q = __fmaf_rn(c, c, q);
-        if (FP8) m = max(m, abs_bits(c));
+        sw[ln_col<TPR, 1>(i / TPR, e, i % TPR)] = w[e];
+        sb[ln_col<TPR, 1>(i / TPR, e, i % TPR)] = b[e];
       }
-    float2 sq = make_float2(0.0f, 0.0f);
+    }
+  }
+  __syncthreads();
+  for (int stage = 0; r < a.rows; r += step, stage = stage + 1 == ST ? 0 : stage + 1) {
+    float2 x[4 * VPT];
+    if constexpr (VEC == 8) {
+      copy_wait<ST - 2>();
+#pragma unroll
+      for (int v = 0; v < VPT; ++v) {
+        LnRaw<DT, 8> raw;
+        float f[8];
+#pragma unroll
+        for (int q = 0; q < Q; ++q) raw.v[q] = *at(stage, v, q);
+        ln_widen<DT, 8>(raw, f);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) x[4 * v + j] = make_float2(f[2 * j], f[2 * j + 1]);
+      }
+      fetch(stage == 0 ? ST - 1 : stage - 1, r + (ST - 1) * step);
+    } else {
+#pragma unroll
+      for (int v = 0; v < VPT; ++v) {
+        const LnRaw<DT, 1> raw = ln_load<DT, 1, TPR>(
+            static_cast<const char*>(a.x) + (size_t)r * a.cols * es, v, t, cols);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) x[4 * v + j] = make_float2(raw.f[2 * j], raw.f[2 * j + 1]);
+      }
+    }
+    // (what lies past the row's end is zero in both)
+    const float s = tree_sum<4 * VPT>(x);
+    const float mean = row_sum2<TPR>(s, 0.0f, sums[slot], turn, slot).x / (float)cols;
+    float2 sq[4 * VPT];
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 4 * VPT; ++i) {
+      x[i] = add2(x[i], splat2(-mean));
+      if (!ln_in<TPR, VEC>(i / 4, 2 * (i % 4), t, cols)) x[i].x = 0.0f;
+      if (!ln_in<TPR, VEC>(i / 4, 2 * (i % 4) + 1, t, cols)) x[i].y = 0.0f;
+      sq[i] = mul2(x[i], x[i]);
+      if (FP8) m = max(m, max(abs_bits(x[i].x), abs_bits(x[i].y)));
+    }
+    float q = tree_sum<4 * VPT>(sq);
     if constexpr (FP8) {
       // the row's max |x - mean| beside its sum of squares
       m = __reduce_max_sync(0xFFFFFFFFu, m);
@@ -65,11 +157,10 @@ ln_forward_kernel(const LnForward a) {
         }
         turn ^= 1;
       }
-      sq.x = q;
     } else {
-      sq = row_sum2<TPR>(q, 0.0f, sums[slot], turn, slot);
+      q = row_sum2<TPR>(q, 0.0f, sums[slot], turn, slot).x;
     }
-    const float rstd = __frsqrt_rn(sq.x / (float)cols + a.eps);
+    const float rstd = __frsqrt_rn(q / (float)cols + a.eps);
     if (t == 0) {
       a.rstd[r] = rstd;
       if (!FP8) a.mean[r] = mean;
@@ -85,20 +176,41 @@ ln_forward_kernel(const LnForward a) {
     }
 #pragma unroll
     for (int v = 0; v < VPT; ++v) {
-      float w[8], b[8], y[8];
-      ln_param<VEC, TPR>(a.weight, a.wdtype, 1.0f, v, t, cols, w);
-      ln_param<VEC, TPR>(a.bias, a.wdtype, 0.0f, v, t, cols, b);
+      float y[8], z[8];
+      float4 w4[2], b4[2];
+      if constexpr (VEC == 8) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        x[8 * v + e] *= rstd;
-        y[e] = __fmaf_rn(x[8 * v + e], w[e], b[e]);
+        for (int h = 0; h < 2; ++h) {
+          w4[h] = reinterpret_cast<const float4*>(sw)[(2 * v + h) * TPR + t];
+          b4[h] = reinterpret_cast<const float4*>(sb)[(2 * v + h) * TPR + t];
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float2 h = mul2(x[4 * v + j], splat2(rstd));
+        float2 w, b;
+        if constexpr (VEC == 8) {
+          w = (j & 1) ? make_float2(w4[j / 2].z, w4[j / 2].w)
+                      : make_float2(w4[j / 2].x, w4[j / 2].y);
+          b = (j & 1) ? make_float2(b4[j / 2].z, b4[j / 2].w)
+                      : make_float2(b4[j / 2].x, b4[j / 2].y);
+        } else {
+          const int c0 = ln_col<TPR, 1>(v, 2 * j, t), c1 = ln_col<TPR, 1>(v, 2 * j + 1, t);
+          w = make_float2(sw[c0], sw[c1]);
+          b = make_float2(sb[c0], sb[c1]);
+        }
+        const float2 p = fma2(h, w, b);
+        y[2 * j] = p.x;
+        y[2 * j + 1] = p.y;
+        if constexpr (FP8) {
+          const float2 c = mul2(h, splat2(scale));
+          z[2 * j] = c.x;
+          z[2 * j + 1] = c.y;
+        }
       }
       ln_store<DT, VEC, TPR>(static_cast<char*>(a.y) + (size_t)r * a.cols * es, v, t, cols, y);
       if constexpr (FP8) {
         uint8_t* codes = a.codes + (size_t)r * a.cols;
-        float z[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) z[e] = x[8 * v + e] * scale;
         if constexpr (VEC == 8) {
           const int c = ln_col<TPR, 8>(v, 0, t);
           if (c < cols)
@@ -169,39 +281,47 @@ ln_forward_long_kernel(const LnForward a) {
   }
 }
 
-template <int DT, int VEC, int TPR, int VPT, int NT>
-void go(const LnForward& a, int sms, cudaStream_t stream) {
-  const int64_t ctas = (a.rows + NT / TPR - 1) / (NT / TPR);
-  const int64_t most = (int64_t)sms * (2048 / NT);
-  const unsigned grid = (unsigned)(ctas < most ? ctas : most);
-  if (a.codes != nullptr)
-    ln_forward_kernel<DT, VEC, TPR, VPT, NT, true><<<grid, NT, 0, stream>>>(a);
-  else
-    ln_forward_kernel<DT, VEC, TPR, VPT, NT, false><<<grid, NT, 0, stream>>>(a);
+template <int DT, int VEC, int TPR, int VPT, bool FP8>
+cudaError_t go_form(const LnForward& a, int sms, cudaStream_t stream) {
+  constexpr int RPC = kFwdThreads / TPR;
+  auto kernel = ln_forward_kernel<DT, VEC, TPR, VPT, FP8>;
+  const int smem = (VEC == 8 ? kRingBytes<DT, VPT> : 0) + 2 * (int)sizeof(float) * TPR * 8 * VPT;
+  if (smem > 48 * 1024) {
+    const cudaError_t e =
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+  }
+  const int64_t ctas = (a.rows + RPC - 1) / RPC, most = (int64_t)sms * kFwdCtas;
+  kernel<<<(unsigned)(ctas < most ? ctas : most), kFwdThreads, smem, stream>>>(a);
+  return cudaSuccess;
+}
+
+template <int DT, int VEC, int TPR, int VPT>
+cudaError_t go(const LnForward& a, int sms, cudaStream_t stream) {
+  return a.codes != nullptr ? go_form<DT, VEC, TPR, VPT, true>(a, sms, stream)
+                            : go_form<DT, VEC, TPR, VPT, false>(a, sms, stream);
 }
 
 template <int DT, int VEC>
-void by_cols(const LnForward& a, int sms, cudaStream_t stream) {
-  if (a.cols <= 256) go<DT, VEC, 32, 1, 128>(a, sms, stream);
-  else if (a.cols <= 512) go<DT, VEC, 32, 2, 128>(a, sms, stream);
-  else if (a.cols <= 1024) go<DT, VEC, 32, 4, 128>(a, sms, stream);
-  else if (a.cols <= 2048) go<DT, VEC, 128, 2, 128>(a, sms, stream);
-  else if (a.cols <= 4096) go<DT, VEC, 128, 4, 128>(a, sms, stream);
-  else go<DT, VEC, 512, 4, 512>(a, sms, stream);
+cudaError_t by_cols(const LnForward& a, int sms, cudaStream_t stream) {
+  if (a.cols <= 256) return go<DT, VEC, 32, 1>(a, sms, stream);
+  if (a.cols <= 512) return go<DT, VEC, 32, 2>(a, sms, stream);
+  if (a.cols <= 1024) return go<DT, VEC, 64, 2>(a, sms, stream);
+  if (a.cols <= 2048) return go<DT, VEC, 128, 2>(a, sms, stream);
+  if (a.cols <= 4096) return go<DT, VEC, 256, 2>(a, sms, stream);
+  return go<DT, VEC, 512, 2>(a, sms, stream);
 }
 
 template <int DT>
-void by_type(const LnForward& a, int sms, cudaStream_t stream) {
+cudaError_t by_type(const LnForward& a, int sms, cudaStream_t stream) {
   if (a.cols > kLnMaxRegCols) {
     const int64_t most = (int64_t)sms * 2;
     const unsigned grid = (unsigned)(a.rows < most ? a.rows : most);
     if (a.codes != nullptr) ln_forward_long_kernel<DT, true><<<grid, 1024, 0, stream>>>(a);
     else ln_forward_long_kernel<DT, false><<<grid, 1024, 0, stream>>>(a);
-  } else if (a.vec_ok) {
-    by_cols<DT, 8>(a, sms, stream);
-  } else {
-    by_cols<DT, 1>(a, sms, stream);
+    return cudaSuccess;
   }
+  return a.vec_ok ? by_cols<DT, 8>(a, sms, stream) : by_cols<DT, 1>(a, sms, stream);
 }
 
 }  // namespace
@@ -209,11 +329,11 @@ void by_type(const LnForward& a, int sms, cudaStream_t stream) {
 cudaError_t launch_ln_forward(const LnForward& a, int sms, cudaStream_t stream,
                               LaunchMark mark) {
   if (mark) mark(kLayerNormK, 0, stream);
-  if (a.dtype == kF32) by_type<kF32>(a, sms, stream);
-  else if (a.dtype == kBF16) by_type<kBF16>(a, sms, stream);
-  else by_type<kF16>(a, sms, stream);
+  const cudaError_t e = a.dtype == kF32    ? by_type<kF32>(a, sms, stream)
+                        : a.dtype == kBF16 ? by_type<kBF16>(a, sms, stream)
+                                           : by_type<kF16>(a, sms, stream);
   if (mark) mark(kLayerNormK, 1, stream);
-  return cudaGetLastError();
+  return e == cudaSuccess ? cudaGetLastError() : e;
 }
 
 }  // namespace fp8opt

@@ -33,7 +33,7 @@ cudaError_t launch_act(int act, bool fwd, const ActArgs& a, int sms,
                        cudaStream_t stream, LaunchMark mark);
 
 // Longest row that a CTA keeps in registers.
-constexpr int64_t kLnMaxRegCols = 16384, kLnMaxRegColsBackward = 8192;
+constexpr int64_t kLnMaxRegCols = 8192;
 
 // Layer norm over rows of `cols` elements; x, y, dy and dx of type dtype, the
 // parameters and their gradients of type wdtype.  codes and scales (one per

@@ -21,7 +21,10 @@ from ._lib import BF16, F16, F32, check, load
 __all__ = ["act_save", "act_load", "gelu", "gelu_backward", "layer_norm",
            "layer_norm_backward", "ACT_GROUP"]
 
+_L = load()
 ACT_GROUP = _lib.ACT_GROUP
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch.cuda.current_device
 _DT = {torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16}
 _FORMS = {"none": _lib.GELU_ERF, "tanh": _lib.GELU_TANH}
 
@@ -44,30 +47,21 @@ def _check(t, name: str, dev: int, dtype=None, shape=None) -> int:
         raise ValueError(f"{name} is on another device")
     if dtype is not None and t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
     return t.data_ptr()
 
 
-class _On:
-    """Makes a tensor's device, and a stream given for it, current."""
-
-    def __init__(self, dev: int, stream):
-        self._ctx = (torch.cuda.stream(stream) if stream is not None else
-                     torch.cuda.device(dev) if dev != torch.cuda.current_device()
-                     else None)
-        if stream is not None and stream.device_index != dev:
-            raise ValueError("stream is on another device than the tensors")
-        self._dev = dev
-
-    def __enter__(self) -> int:
-        if self._ctx is not None:
-            self._ctx.__enter__()
-        return torch.cuda.current_stream(self._dev).cuda_stream
-
-    def __exit__(self, *exc):
-        if self._ctx is not None:
-            self._ctx.__exit__(*exc)
+def _run(call, dev: int, stream, *args):
+    """call(stream handle, *args) with the tensors' device, and the stream
+    given for them, current (the usual case, the current stream of the current
+    device, needs no context)."""
+    if stream is None and dev == _current_device():
+        return call(_raw_stream(dev), *args)
+    if stream is not None and stream.device_index != dev:
+        raise ValueError("stream is on another device than the tensors")
+    with torch.cuda.device(dev) if stream is None else torch.cuda.stream(stream):
+        return call(_raw_stream(dev), *args)
 
 
 def _form(approximate: str) -> int:
@@ -83,16 +77,9 @@ def _groups(numel: int) -> int:
 
 # ------------------------------------------------- activation checkpoints
 
-def act_save(x: torch.Tensor, stream=None):
-    """The 8-bit checkpoint of x: (codes, scales), E4M3 codes in x's shape
-    (uint8) and one float32 scale per ACT_GROUP consecutive elements."""
-    px, dt, dev = _check(x, "x", -1), _dtype(x, "x"), x.get_device()
-    with _On(dev, stream) as s:
-        codes = torch.empty_like(x, dtype=torch.uint8)
-        scales = torch.empty(_groups(x.numel()), dtype=torch.float32, device=x.device)
-        check(load().fp8_act_save(px, x.numel(), dt, codes.data_ptr(),
-                                  scales.data_ptr(), s))
-    return codes, scales
+def _new_checkpoint(x):
+    return (torch.empty_like(x, dtype=torch.uint8),
+            torch.empty(_groups(x.numel()), dtype=torch.float32, device=x.device))
 
 
 def _checkpoint(codes, scales, dev: int, shape=None):
@@ -101,29 +88,44 @@ def _checkpoint(codes, scales, dev: int, shape=None):
                       (_groups(codes.numel()),))
 
 
+def act_save(x: torch.Tensor, stream=None):
+    """The 8-bit checkpoint of x: (codes, scales), E4M3 codes in x's shape
+    (uint8) and one float32 scale per ACT_GROUP consecutive elements."""
+    px, dt = _check(x, "x", -1), _dtype(x, "x")
+
+    def call(s):
+        codes, scales = _new_checkpoint(x)
+        check(_L.fp8_act_save(px, x.numel(), dt, codes.data_ptr(), scales.data_ptr(), s))
+        return codes, scales
+    return _run(call, x.get_device(), stream)
+
+
 def act_load(codes: torch.Tensor, scales: torch.Tensor, dtype=torch.float16,
              stream=None) -> torch.Tensor:
     """The activation of an ``act_save`` checkpoint, in ``dtype``."""
     pc, ps = _checkpoint(codes, scales, -1)
     if dtype not in _DT:
         raise TypeError(f"unsupported dtype {dtype}")
-    with _On(codes.get_device(), stream) as s:
+
+    def call(s):
         x = torch.empty_like(codes, dtype=dtype)
-        check(load().fp8_act_load(pc, ps, codes.numel(), _DT[dtype], x.data_ptr(), s))
-    return x
+        check(_L.fp8_act_load(pc, ps, codes.numel(), _DT[dtype], x.data_ptr(), s))
+        return x
+    return _run(call, codes.get_device(), stream)
 
 
 def gelu(x: torch.Tensor, approximate: str = "none", stream=None):
     """(y, codes, scales): y = gelu(x) and the 8-bit checkpoint of x, in one
     pass.  approximate: "none" (x Phi(x)) or "tanh", as torch's."""
-    px, dt, dev, form = _check(x, "x", -1), _dtype(x, "x"), x.get_device(), _form(approximate)
-    with _On(dev, stream) as s:
+    px, dt, form = _check(x, "x", -1), _dtype(x, "x"), _form(approximate)
+
+    def call(s):
         y = torch.empty_like(x)
-        codes = torch.empty_like(x, dtype=torch.uint8)
-        scales = torch.empty(_groups(x.numel()), dtype=torch.float32, device=x.device)
-        check(load().fp8_gelu(px, x.numel(), dt, form, y.data_ptr(), codes.data_ptr(),
-                              scales.data_ptr(), s))
-    return y, codes, scales
+        codes, scales = _new_checkpoint(x)
+        check(_L.fp8_gelu(px, x.numel(), dt, form, y.data_ptr(), codes.data_ptr(),
+                          scales.data_ptr(), s))
+        return y, codes, scales
+    return _run(call, x.get_device(), stream)
 
 
 def gelu_backward(dy: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor,
@@ -131,10 +133,12 @@ def gelu_backward(dy: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor,
     """dx = dy * gelu'(x), with x read from its 8-bit checkpoint."""
     pd, dt, dev, form = _check(dy, "dy", -1), _dtype(dy, "dy"), dy.get_device(), _form(approximate)
     pc, ps = _checkpoint(codes, scales, dev, dy.shape)
-    with _On(dev, stream) as s:
+
+    def call(s):
         dx = torch.empty_like(dy)
-        check(load().fp8_gelu_backward(pd, pc, ps, dy.numel(), dt, form, dx.data_ptr(), s))
-    return dx
+        check(_L.fp8_gelu_backward(pd, pc, ps, dy.numel(), dt, form, dx.data_ptr(), s))
+        return dx
+    return _run(call, dev, stream)
 
 
 # -------------------------------------------------------------- layer norm
@@ -161,22 +165,21 @@ def layer_norm(x: torch.Tensor, weight: torch.Tensor, bias=None, eps: float = 1e
     rows, cols = _rows_cols(x, "x")
     pw, wdt = _check(weight, "weight", dev, None, (cols,)), _dtype(weight, "weight")
     pb = None if bias is None else _check(bias, "bias", dev, weight.dtype, (cols,))
-    lead = x.shape[:-1]
-    with _On(dev, stream) as s:
+
+    def call(s):
         y = torch.empty_like(x)
-        rstd = torch.empty(lead, dtype=torch.float32, device=x.device)
+        rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
         if save == "x":
             mean = torch.empty_like(rstd)
-            check(load().fp8_layer_norm(px, pw, pb, rows, cols, dt, wdt, eps,
-                                        y.data_ptr(), mean.data_ptr(), rstd.data_ptr(),
-                                        None, None, s))
+            check(_L.fp8_layer_norm(px, pw, pb, rows, cols, dt, wdt, eps, y.data_ptr(),
+                                    mean.data_ptr(), rstd.data_ptr(), None, None, s))
             return y, mean, rstd
         codes = torch.empty_like(x, dtype=torch.uint8)
         scales = torch.empty_like(rstd)
-        check(load().fp8_layer_norm(px, pw, pb, rows, cols, dt, wdt, eps, y.data_ptr(),
-                                    None, rstd.data_ptr(), codes.data_ptr(),
-                                    scales.data_ptr(), s))
+        check(_L.fp8_layer_norm(px, pw, pb, rows, cols, dt, wdt, eps, y.data_ptr(), None,
+                                rstd.data_ptr(), codes.data_ptr(), scales.data_ptr(), s))
         return y, codes, scales, rstd
+    return _run(call, dev, stream)
 
 
 def layer_norm_backward(dy: torch.Tensor, weight: torch.Tensor, rstd: torch.Tensor,
@@ -198,11 +201,13 @@ def layer_norm_backward(dy: torch.Tensor, weight: torch.Tensor, rstd: torch.Tens
         pm = _check(mean, "mean", dev, torch.float32, lead)
     else:
         raise ValueError("give x and mean, or codes and scales")
-    with _On(dev, stream) as s:
+
+    def call(s):
         dx = torch.empty_like(dy)
         dw = torch.empty_like(weight)
         db = torch.empty_like(weight) if need_bias else None
-        check(load().fp8_layer_norm_backward(
+        check(_L.fp8_layer_norm_backward(
             pd, px, pm, pc, ps, pr, pw, rows, cols, dt, wdt, dx.data_ptr(), dw.data_ptr(),
             db.data_ptr() if need_bias else None, s))
-    return dx, dw, db
+        return dx, dw, db
+    return _run(call, dev, stream)

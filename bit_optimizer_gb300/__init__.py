@@ -11,7 +11,8 @@ from .api import (AdamWPlan, CastPlan, CastStepPlan, Fp8AdamW, ReducePlan,
                   StepState, arena_views, fp8_adamw_step, fp8_cast_scaled,
                   fp8_reduce_scaled)
 from .ops import (act_load, act_save, gelu, gelu_backward, layer_norm,
-                  layer_norm_backward)
+                  layer_norm_backward, linear_cross_entropy,
+                  linear_cross_entropy_backward)
 
 load()
 
@@ -21,4 +22,5 @@ __all__ = ["fp8_cast_scaled", "fp8_adamw_step", "fp8_reduce_scaled",
            "Fp8OptError", "strerror", "release", "release_stream", "load",
            "LIB_PATH", "EXPORTS",
            "KERNELS", "timing_enable", "timing_read", "act_save", "act_load",
-           "gelu", "gelu_backward", "layer_norm", "layer_norm_backward"]
+           "gelu", "gelu_backward", "layer_norm", "layer_norm_backward",
+           "linear_cross_entropy", "linear_cross_entropy_backward"]

@@ -28,7 +28,8 @@ EXPORTS = ("fp8_cast_scaled", "fp8_adamw_step", "fp8_adam_step",
            "fp8_adam_step_copy", "fp8_reduce_scaled_begin",
            "fp8_reduce_scaled_finish", "fp8_norm_terms_from_limbs",
            "fp8_act_save", "fp8_act_load", "fp8_gelu", "fp8_gelu_backward",
-           "fp8_layer_norm", "fp8_layer_norm_backward",
+           "fp8_layer_norm", "fp8_layer_norm_backward", "fp8_linear_xent",
+           "fp8_linear_xent_backward",
            "fp8opt_strerror",
            "fp8opt_last_error", "fp8opt_timing_enable", "fp8opt_timing_read",
            "fp8opt_release", "fp8opt_release_stream")
@@ -36,7 +37,8 @@ KERNELS = ("cast_amax", "cast_encode", "step_amax", "step_update", "step_w8",
            "cast_step_amax", "reduce_amax", "reduce_encode", "grad_norm",
            "grad_norm_terms", "clip_coef", "found", "act_save", "act_load",
            "gelu", "gelu_backward", "layer_norm", "layer_norm_backward",
-           "layer_norm_params")
+           "layer_norm_params", "xent_logits", "xent_join", "xent_prepare",
+           "xent_probs", "xent_grads")
 MAX_SHARDS = 64
 ACT_GROUP = 128
 GELU_ERF, GELU_TANH = 0, 1
@@ -186,7 +188,10 @@ def load(path: str = LIB_PATH) -> C.CDLL:
             ("fp8_layer_norm", [p, p, p, i64, i64, i32, i32, C.c_float, p, p,
                                 p, p, p, p]),
             ("fp8_layer_norm_backward", [p, p, p, p, p, p, p, i64, i64, i32,
-                                         i32, p, p, p, p])):
+                                         i32, p, p, p, p]),
+            ("fp8_linear_xent", [p, p, p, i64, i64, i64, i32, i64, p, p, p]),
+            ("fp8_linear_xent_backward", [p, p, p, p, p, i64, i64, i64, i32,
+                                          i64, p, p, p])):
         fn = getattr(L, name)
         fn.restype, fn.argtypes = C.c_int, args
     L.fp8opt_strerror.restype = C.c_char_p

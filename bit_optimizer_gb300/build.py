@@ -20,8 +20,10 @@ OUT_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(OUT_DIR, "libfp8opt.so")
 SOURCES = ["api.cu", "cast_kernels.cu", "step_kernels.cu", "fused_kernels.cu",
            "noalloc.cu", "reduce_kernels.cu", "norm_kernels.cu", "train_api.cu",
-           "act_kernels.cu", "layer_norm_fwd.cu", "layer_norm_bwd.cu"]
-DEPS = ["fp8opt_internal.cuh", "ops_internal.cuh", "layer_norm.cuh", os.path.join("..", "..", "include", "fp8opt.h")]
+           "act_kernels.cu", "layer_norm_fwd.cu", "layer_norm_bwd.cu",
+           "linear_xent.cu"]
+DEPS = ["fp8opt_internal.cuh", "ops_internal.cuh", "layer_norm.cuh",
+        "tensor_core.cuh", os.path.join("..", "..", "include", "fp8opt.h")]
 
 NVCC = os.environ.get("NVCC", "nvcc")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

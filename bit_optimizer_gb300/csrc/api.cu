@@ -336,7 +336,8 @@ const char* const kKernelNames[kNumKernels] = {
     "cast_amax", "cast_encode", "step_amax", "step_update", "step_w8",
     "cast_step_amax", "reduce_amax", "reduce_encode", "grad_norm",
     "grad_norm_terms", "clip_coef", "found", "act_save", "act_load", "gelu",
-    "gelu_backward", "layer_norm", "layer_norm_backward", "layer_norm_params"};
+    "gelu_backward", "layer_norm", "layer_norm_backward", "layer_norm_params",
+    "xent_logits", "xent_join", "xent_prepare", "xent_probs", "xent_grads"};
 
 struct Timing {
   bool on = false;
@@ -515,6 +516,29 @@ int OpCall::open(const char* fn, cudaStream_t stream, size_t scratch_bytes) {
   if (e != cudaSuccess) return cuda_fail(e, (std::string(fn) + ": workspace").c_str());
   if (graph) ws->freeze();
   scratch = static_cast<char*>(ws->op_scratch.ptr);
+  return FP8OPT_OK;
+}
+
+int OpCall::error_word(const char* fn, int** device) {
+  static int* host = nullptr;   // guarded by the lock
+  if (host == nullptr) {
+    const cudaError_t e = cudaHostAlloc(reinterpret_cast<void**>(&host), sizeof(int),
+                                        cudaHostAllocPortable | cudaHostAllocMapped);
+    if (e != cudaSuccess) {
+      host = nullptr;
+      return cuda_fail(e, (std::string(fn) + ": workspace").c_str());
+    }
+    *host = 0;
+  }
+  if (*static_cast<volatile int*>(host) != 0) {
+    *static_cast<volatile int*>(host) = 0;
+    return fail(FP8OPT_ERR_CUDA, std::string(fn) + ": a wait inside a kernel of an earlier call "
+                                 "ran out; that call's results are not complete");
+  }
+  void* p = nullptr;
+  const cudaError_t e = cudaHostGetDevicePointer(&p, host, 0);
+  if (e != cudaSuccess) return cuda_fail(e, (std::string(fn) + ": workspace").c_str());
+  *device = static_cast<int*>(p);
   return FP8OPT_OK;
 }
 

@@ -127,7 +127,8 @@ enum KernelId { kCastAmaxK = 0, kCastEncodeK, kStepAmaxK, kStepUpdateK,
                 kStepW8K, kCastStepAmaxK, kReduceAmaxK, kReduceEncodeK,
                 kGradNormK, kGradNormTermsK, kClipCoefK, kFoundK,
                 kActSaveK, kActLoadK, kGeluK, kGeluBackwardK, kLayerNormK,
-                kLayerNormBackwardK, kLayerNormParamsK,
+                kLayerNormBackwardK, kLayerNormParamsK, kXentLogitsK,
+                kXentJoinK, kXentPrepareK, kXentProbsK, kXentGradsK,
                 kNumKernels };
 
 // Called before (end = 0) and after (end = 1) each kernel launch when timing

@@ -3,6 +3,7 @@
 // helpers.
 #pragma once
 
+#include <algorithm>
 #include <mutex>
 
 #include "fp8opt_internal.cuh"
@@ -75,6 +76,30 @@ size_t ln_backward_scratch(const LnBackward& a, int sms);
 cudaError_t launch_ln_backward(const LnBackward& a, void* scratch, int sms,
                                cudaStream_t stream, LaunchMark mark);
 
+// Cross entropy of the linear layer z = x w^T: x rows x dim, w vocab x dim, of
+// type dtype (kBF16 or kF16).
+struct XentArgs {
+  const void* x;
+  const void* w;
+  const int64_t* target;
+  int64_t rows, dim, vocab, ignore;
+  int dtype;
+  float* loss;               // forward
+  float* lse_out;
+  const float* dloss;        // backward
+  const float* lse;
+  void* dx;
+  void* dw;
+};
+
+size_t xent_forward_scratch(const XentArgs& a);
+size_t xent_backward_scratch(const XentArgs& a);
+// error: a device word set to 1 when a wait in a kernel ran out.
+cudaError_t launch_xent_forward(const XentArgs& a, char* scratch, int* error, int sms,
+                                cudaStream_t stream, LaunchMark mark);
+cudaError_t launch_xent_backward(const XentArgs& a, char* scratch, int* error, int sms,
+                                 cudaStream_t stream, LaunchMark mark);
+
 // Holds the library lock for one operator call, with the current device's SM
 // count, the launch marks, and `scratch_bytes` of the stream's workspace
 // (contents undefined; the call's own until its work on the stream ends).
@@ -84,6 +109,10 @@ class OpCall {
   OpCall();
   int open(const char* fn, cudaStream_t stream, size_t scratch_bytes);
   int done(const char* fn, cudaError_t e);   // the call's status
+  // The word in which kernels record that a wait of theirs ran out: pinned
+  // host memory, so that a later call sees it without waiting for the GPU and
+  // fails.
+  int error_word(const char* fn, int** device);
   char* scratch = nullptr;
   int sms = 0;
   LaunchMark mark = nullptr;

@@ -195,3 +195,86 @@ extern "C" int fp8_layer_norm_backward(const void* dy, const void* x, const floa
     return call.done(fn, launch_ln_backward(a, call.scratch, call.sms, stream, call.mark));
   });
 }
+
+namespace fp8opt {
+namespace {
+
+int check_xent(const char* fn, const XentArgs& a) {
+  constexpr int64_t kMost = (int64_t)1 << 31;
+  if (a.rows < 0 || a.rows >= kMost || a.dim < 1 || a.dim >= kMost || a.vocab < 1 ||
+      a.vocab >= kMost || a.rows > kMaxElems / a.dim || a.vocab > kMaxElems / a.dim)
+    return bad(fn, "rows < 0, dim < 1, vocab < 1, or a size above its maximum");
+  if (a.dtype != FP8OPT_BF16 && a.dtype != FP8OPT_F16)
+    return unsupported(fn, "dtype is neither BF16 nor FP16");
+  return FP8OPT_OK;
+}
+
+}  // namespace
+}  // namespace fp8opt
+
+extern "C" int fp8_linear_xent(const void* x, const void* w, const int64_t* target,
+                               int64_t rows, int64_t dim, int64_t vocab, int dtype,
+                               int64_t ignore_index, float* loss, float* lse,
+                               void* stream_ptr) {
+  return entry([&] {
+    const char* fn = "fp8_linear_xent";
+    XentArgs a = {};
+    a.x = x;
+    a.w = w;
+    a.target = target;
+    a.rows = rows;
+    a.dim = dim;
+    a.vocab = vocab;
+    a.ignore = ignore_index;
+    a.dtype = dtype;
+    a.loss = loss;
+    a.lse_out = lse;
+    int st = check_xent(fn, a);
+    if (st != FP8OPT_OK || rows == 0) return st;
+    if (!x || !w || !target || !loss || !lse) return bad(fn, "NULL pointer");
+    cudaStream_t stream = static_cast<cudaStream_t>(stream_ptr);
+    OpCall call;
+    int* error = nullptr;
+    if ((st = call.open(fn, stream, xent_forward_scratch(a))) != FP8OPT_OK ||
+        (st = call.error_word(fn, &error)) != FP8OPT_OK)
+      return st;
+    return call.done(fn, launch_xent_forward(a, call.scratch, error, call.sms, stream,
+                                             call.mark));
+  });
+}
+
+extern "C" int fp8_linear_xent_backward(const float* dloss, const void* x, const void* w,
+                                        const int64_t* target, const float* lse, int64_t rows,
+                                        int64_t dim, int64_t vocab, int dtype,
+                                        int64_t ignore_index, void* dx, void* dw,
+                                        void* stream_ptr) {
+  return entry([&] {
+    const char* fn = "fp8_linear_xent_backward";
+    XentArgs a = {};
+    a.x = x;
+    a.w = w;
+    a.target = target;
+    a.rows = rows;
+    a.dim = dim;
+    a.vocab = vocab;
+    a.ignore = ignore_index;
+    a.dtype = dtype;
+    a.dloss = dloss;
+    a.lse = lse;
+    a.dx = dx;
+    a.dw = dw;
+    int st = check_xent(fn, a);
+    if (st != FP8OPT_OK) return st;
+    if (!dw || (rows > 0 && (!dloss || !x || !w || !target || !lse || !dx)))
+      return bad(fn, "NULL pointer");
+    cudaStream_t stream = static_cast<cudaStream_t>(stream_ptr);
+    OpCall call;
+    int* error = nullptr;
+    const size_t bytes = rows > 0 ? xent_backward_scratch(a) : 0;
+    if ((st = call.open(fn, stream, bytes)) != FP8OPT_OK ||
+        (st = call.error_word(fn, &error)) != FP8OPT_OK)
+      return st;
+    return call.done(fn, launch_xent_backward(a, call.scratch, error, call.sms, stream,
+                                              call.mark));
+  });
+}

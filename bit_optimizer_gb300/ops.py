@@ -19,7 +19,8 @@ from . import _lib
 from ._lib import BF16, F16, F32, check, load
 
 __all__ = ["act_save", "act_load", "gelu", "gelu_backward", "layer_norm",
-           "layer_norm_backward", "ACT_GROUP"]
+           "layer_norm_backward", "linear_cross_entropy",
+           "linear_cross_entropy_backward", "ACT_GROUP"]
 
 _L = load()
 ACT_GROUP = _lib.ACT_GROUP
@@ -210,4 +211,55 @@ def layer_norm_backward(dy: torch.Tensor, weight: torch.Tensor, rstd: torch.Tens
             pd, px, pm, pc, ps, pr, pw, rows, cols, dt, wdt, dx.data_ptr(), dw.data_ptr(),
             db.data_ptr() if need_bias else None, s))
         return dx, dw, db
+    return _run(call, dev, stream)
+
+
+# ----------------------------------------------- vocabulary cross entropy
+
+def _linear(x, w, target):
+    """Addresses and sizes of a linear layer's input, weight and targets."""
+    px, dt, dev = _check(x, "x", -1), _dtype(x, "x"), x.get_device()
+    if dt == F32:
+        raise TypeError("x must be bfloat16 or float16")
+    if x.dim() != 2 or x.shape[1] < 1:
+        raise ValueError("x must have shape (tokens, dim)")
+    pw = _check(w, "w", dev, x.dtype)
+    if w.dim() != 2 or w.shape[0] < 1 or w.shape[1] != x.shape[1]:
+        raise ValueError(f"w must have shape (vocabulary, {x.shape[1]}), not {tuple(w.shape)}")
+    pt = _check(target, "target", dev, torch.int64, x.shape[:1])
+    return px, pw, pt, x.shape[0], x.shape[1], w.shape[0], dt, dev
+
+
+def linear_cross_entropy(x: torch.Tensor, w: torch.Tensor, target: torch.Tensor,
+                         ignore_index: int = -100, stream=None):
+    """(loss, lse), both float32, one per token: lse = log sum exp of the
+    token's logits x w^T, loss = lse - logit of its target (0 for a target of
+    ignore_index, NaN for another one outside the vocabulary).  x: (tokens,
+    dim), w: (vocabulary, dim), bfloat16 or float16; target: int64.  The
+    logits are never in memory as a whole."""
+    px, pw, pt, rows, dim, vocab, dt, dev = _linear(x, w, target)
+
+    def call(s):
+        loss = torch.empty(rows, dtype=torch.float32, device=x.device)
+        lse = torch.empty_like(loss)
+        check(_L.fp8_linear_xent(px, pw, pt, rows, dim, vocab, dt, ignore_index,
+                                 loss.data_ptr(), lse.data_ptr(), s))
+        return loss, lse
+    return _run(call, dev, stream)
+
+
+def linear_cross_entropy_backward(dloss: torch.Tensor, x: torch.Tensor, w: torch.Tensor,
+                                  target: torch.Tensor, lse: torch.Tensor,
+                                  ignore_index: int = -100, stream=None):
+    """(dx, dw), in x's type, for the gradient dloss (float32, one per token)
+    of ``linear_cross_entropy``'s loss; lse is that call's."""
+    px, pw, pt, rows, dim, vocab, dt, dev = _linear(x, w, target)
+    pd = _check(dloss, "dloss", dev, torch.float32, (rows,))
+    pl = _check(lse, "lse", dev, torch.float32, (rows,))
+
+    def call(s):
+        dx, dw = torch.empty_like(x), torch.empty_like(w)
+        check(_L.fp8_linear_xent_backward(pd, px, pw, pt, pl, rows, dim, vocab, dt,
+                                          ignore_index, dx.data_ptr(), dw.data_ptr(), s))
+        return dx, dw
     return _run(call, dev, stream)

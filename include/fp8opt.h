@@ -665,6 +665,43 @@ FP8OPT_API int fp8_layer_norm_backward(
     int64_t cols, int dtype, int wdtype, void *dx, void *dweight, void *dbias,
     void *stream);
 
+/*
+ * fp8_linear_xent: softmax cross entropy of the logits z = x w^T, x rows x dim
+ * (tokens), w vocab x dim, both of type dtype (FP8OPT_BF16 or FP8OPT_F16),
+ * without keeping the logits:
+ *   lse[i] = log sum_v exp(z[i, v]),  loss[i] = lse[i] - z[i, target[i]].
+ * target (rows int64): a token whose target is ignore_index has loss 0; any
+ * other target outside [0, vocab) gives a NaN loss.  loss, lse: rows fp32.
+ *
+ * fp8_linear_xent_backward: given dloss (rows fp32, the gradient of each
+ * token's loss) and the forward pass's lse,
+ *   p[i, v] = (exp(z[i, v] - lse[i]) - [v = target[i]]) * dloss[i],
+ *   dx = p w,  dw = p^T x  (of type dtype, both overwritten).
+ * The vocabulary is taken in pieces: p exists for one piece at a time, in
+ * 16 bits scaled by a power of two against underflow.  An ignored token has dx
+ * 0 and no part in dw, whatever its row of x holds.  rows = 0 gives dw 0.
+ * Rows whose length is a multiple of 8 in 16-byte-aligned tensors are read in
+ * place, others through a copy in scratch.  Scratch: the statistics of the
+ * column tiles (forward); a copy of x, one piece of p (64 MiB, or 512 bytes a
+ * token where that is more) and, with more than one piece, dx in fp32
+ * (backward).  dim and vocab >= 1; each tensor below 2^31 rows and columns.
+ *
+ * The kernels wait for their copies and products with a limit of about two
+ * seconds; should one run out (it does not on a working device), the next
+ * call returns FP8OPT_ERR_CUDA.
+ */
+FP8OPT_API int fp8_linear_xent(const void *x, const void *w,
+                               const int64_t *target, int64_t rows,
+                               int64_t dim, int64_t vocab, int dtype,
+                               int64_t ignore_index, float *loss, float *lse,
+                               void *stream);
+FP8OPT_API int fp8_linear_xent_backward(const float *dloss, const void *x,
+                                        const void *w, const int64_t *target,
+                                        const float *lse, int64_t rows,
+                                        int64_t dim, int64_t vocab, int dtype,
+                                        int64_t ignore_index, void *dx,
+                                        void *dw, void *stream);
+
 /* Text of a status code (static storage). */
 FP8OPT_API const char *fp8opt_strerror(int status);
 
@@ -681,7 +718,8 @@ FP8OPT_API const char *fp8opt_last_error(void);
  * "cast_encode", "step_amax", "step_update", "step_w8", "cast_step_amax",
  * "reduce_amax", "reduce_encode", "grad_norm", "grad_norm_terms", "clip_coef",
  * "found", "act_save", "act_load", "gelu", "gelu_backward", "layer_norm",
- * "layer_norm_backward", "layer_norm_params"), the launches
+ * "layer_norm_backward", "layer_norm_params", "xent_logits", "xent_join",
+ * "xent_prepare", "xent_probs", "xent_grads"), the launches
  * recorded since enabling and their summed duration in milliseconds.  Returns
  * FP8OPT_ERR_ARG for an unknown name or NULL outputs. */
 FP8OPT_API int fp8opt_timing_enable(int on);

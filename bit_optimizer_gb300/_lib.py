@@ -38,7 +38,7 @@ KERNELS = ("cast_amax", "cast_encode", "step_amax", "step_update", "step_w8",
            "grad_norm_terms", "clip_coef", "found", "act_save", "act_load",
            "gelu", "gelu_backward", "layer_norm", "layer_norm_backward",
            "layer_norm_params", "xent_logits", "xent_join", "xent_prepare",
-           "xent_probs", "xent_grads")
+           "xent_grads", "xent_dx")
 MAX_SHARDS = 64
 ACT_GROUP = 128
 GELU_ERF, GELU_TANH = 0, 1

@@ -337,7 +337,7 @@ const char* const kKernelNames[kNumKernels] = {
     "cast_step_amax", "reduce_amax", "reduce_encode", "grad_norm",
     "grad_norm_terms", "clip_coef", "found", "act_save", "act_load", "gelu",
     "gelu_backward", "layer_norm", "layer_norm_backward", "layer_norm_params",
-    "xent_logits", "xent_join", "xent_prepare", "xent_probs", "xent_grads"};
+    "xent_logits", "xent_join", "xent_prepare", "xent_grads", "xent_dx"};
 
 struct Timing {
   bool on = false;

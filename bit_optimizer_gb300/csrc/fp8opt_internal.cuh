@@ -128,7 +128,7 @@ enum KernelId { kCastAmaxK = 0, kCastEncodeK, kStepAmaxK, kStepUpdateK,
                 kGradNormK, kGradNormTermsK, kClipCoefK, kFoundK,
                 kActSaveK, kActLoadK, kGeluK, kGeluBackwardK, kLayerNormK,
                 kLayerNormBackwardK, kLayerNormParamsK, kXentLogitsK,
-                kXentJoinK, kXentPrepareK, kXentProbsK, kXentGradsK,
+                kXentJoinK, kXentPrepareK, kXentGradsK, kXentDxK,
                 kNumKernels };
 
 // Called before (end = 0) and after (end = 1) each kernel launch when timing

@@ -35,9 +35,13 @@ namespace fp8opt {
 
 namespace {
 
-constexpr int kTileM = 128, kTileN = 256, kBlockK = 64, kGemmStages = 4;
-constexpr int kStageA = kTileM * kBlockK * 2, kStageB = kTileN * kBlockK * 2;
-constexpr int kGemmThreads = 192;
+// A pair of CTAs takes a tile of 256 x tile_n: 128 rows of A and half of B each.
+constexpr int kTileM = 256, kTileN = 256, kBlockK = 64, kGemmStages = 6;
+constexpr int kHalfM = kTileM / 2, kStageA = kHalfM * kBlockK * 2;
+constexpr int kStageB = kTileN / 2 * kBlockK * 2;
+// Eight epilogue warps (two for each quarter of the lanes, each with half of the
+// columns), a producer, an MMA and a scheduler warp.
+constexpr int kEpilogueWarps = 8, kGemmThreads = 32 * (kEpilogueWarps + 3);
 constexpr int kGemmSmem = 1024 + kGemmStages * (kStageA + kStageB);
 constexpr float kLog2eF = 1.4426950408889634f, kLn2F = 0.69314718055994531f;
 
@@ -49,42 +53,59 @@ __device__ __forceinline__ float exp2_approx(float x) {
 
 enum GemmMode { kStats = 0, kProbs, kDx, kDw };
 
-// One product C[m, n] = sum_k A[m, k] B[n, k] and what becomes of its tiles.
+// One product C[m, n] = sum_k A[m, k] B[n, k] in tiles of 256 x tile_n, k in
+// `splits` ranges of `kper` blocks, and what its tiles are for.
+struct GemmShape {
+  int mode;
+  int tiles_m, tiles_n, tile_n, kblocks, kper, splits;
+  int b_mn0, b_k0;         // B's coordinates of n = 0 and k = 0 (A's are 0)
+  int a_mn, b_mn;          // MN-major operands
+  int first;               // kDx: the first piece
+  int64_t v0;              // first vocabulary row of the piece
+  uint16_t* probs;         // kProbs: [token][piece]
+  __host__ __device__ int tiles() const { return tiles_m * tiles_n * splits; }
+};
 struct GemmJob {
   CUtensorMap a, b;
-  int mode;
-  int tiles_m, tiles_n, kblocks;
-  int a_mn0, a_k0, b_mn0, b_k0;   // coordinates of element (0, 0)
-  int a_mn, b_mn;                 // MN-major operands
+  GemmShape shape;
 };
 
+// What the tiles' epilogues read and write.
 struct GemmOut {
   int64_t tokens;          // rows of x in this call
   int64_t vocab, dim;
   const long long* target;
   long long ignore;
   // kStats
-  float2* partial;         // [column tile][token]: maximum, sum of exponentials
+  float2* partial;         // [half a tile's columns][token]: maximum, sum of exponentials
   float* target_logit;     // [token]
   // kProbs
   const float* lse;
   const float* dloss;
-  const float* scale;      // 2^k and 2^-k
-  uint16_t* probs;         // [token][piece]
+  const float* top_dloss;  // largest finite |dloss|
   int64_t piece;           // columns of probs
-  int64_t v0;              // first column of the piece
   // kDx, kDw
-  float* dx_sum;           // [token][dim], NULL when there is one piece
-  int first, last;         // first and last piece
-  void* dx;
+  float* dx_sum;           // [split][token][dim_pitch]
+  int64_t dim_pitch;
   void* dw;
 };
 
+// One launch: up to three products that do not depend on one another, those
+// with the longest tiles first.
+constexpr int kMaxJobs = 3;
 struct GemmArgs {
-  GemmJob job;
+  GemmJob job[kMaxJobs];
+  int jobs;
   GemmOut out;
+  int* next;               // tiles handed out beyond the first of each CTA
   int* error;              // set to 1 when a wait ran out
 };
+
+// p is held as (exp(z - lse) - [target]) * (dloss / max |dloss|) * kProbScale:
+// below 2^15, and in FP16 without underflow down to 2^-39 of the largest.  (A
+// common dloss then leaves p as it is: multiplied in before the rounding, it
+// would give every token the same rounding error.)
+constexpr float kProbScale = 32768.0f;
 
 template <bool BF16>
 __device__ __forceinline__ uint32_t pack16(float a, float b) {
@@ -108,76 +129,106 @@ __device__ __forceinline__ void store_row16(uint16_t* p, const float (&v)[32], i
   }
 }
 
-// The tile's logits of one token: running maximum and sum of exponentials.
-__device__ __forceinline__ void stats_row(const GemmOut& o, uint32_t tmem, int64_t row, int n_tile) {
-  const int64_t n0 = (int64_t)n_tile * kTileN;
-  const bool live = row < o.tokens;
-  const long long target = live ? o.target[row] : -1;
-  const int64_t rel = target >= 0 && target < o.vocab ? target - n0 : -1;
+// exp(a + shift) and exp(b + shift) of two accumulators.  The difference is
+// taken before it is scaled to base 2: its rounding error does not grow with
+// the logits.
+__device__ __forceinline__ float2 exp_pair(uint32_t a, uint32_t b, float shift) {
+  const float2 d = mul2(add2(make_float2(__uint_as_float(a), __uint_as_float(b)), splat2(shift)),
+                        splat2(kLog2eF));
+  return make_float2(exp2_approx(d.x), exp2_approx(d.y));
+}
+
+// An epilogue thread's part of a tile: one row and `cols` columns from `c0` on
+// (rows and columns of C; the columns lie in TMEM at `tmem`).
+struct Strip {
+  uint32_t tmem;
+  int64_t row, c0;
+  int cols, index;         // index: column strip of the whole product
+};
+
+// What an epilogue needs of its row, read while the tile is being computed.
+struct RowIn {
+  long long target;
+  float lse, dloss, top;
+};
+
+__device__ __forceinline__ RowIn row_in(const GemmShape& g, const GemmOut& o, int64_t row) {
+  RowIn in = {-1, 0.0f, 0.0f, 0.0f};
+  if (g.mode == kStats || g.mode == kProbs) {
+    if (row < o.tokens) {
+      in.target = o.target[row];
+      if (g.mode == kProbs) {
+        in.lse = o.lse[row];
+        in.dloss = o.dloss[row];
+      }
+    }
+  }
+  if (g.mode == kProbs || g.mode == kDw) in.top = *o.top_dloss;
+  return in;
+}
+
+// The strip's logits: maximum and sum of exponentials.
+__device__ __forceinline__ void stats_strip(const GemmOut& o, const Strip& t, const RowIn& in) {
+  const bool live = t.row < o.tokens;
+  const long long target = in.target;
+  const int rel = target >= t.c0 && target < t.c0 + t.cols && target < o.vocab
+                      ? (int)(target - t.c0) : -1;
+  const int valid = (int)min((int64_t)t.cols, o.vocab - t.c0);   // may be <= 0
   float top = -1e30f, sum = 0.0f, at_target = 0.0f;
-#pragma unroll 1
-  for (int c = 0; c < kTileN; c += 32) {
-    if (n0 + c >= o.vocab) break;
-    uint32_t r[32];
-    tmem_load32(tmem + c, r);
-    tmem_wait();
-    const int64_t left = o.vocab - n0 - c;
-    if (left < 32) {
+  tmem_columns(t.tmem, t.cols, [&](int c, uint32_t (&r)[32]) {
+    if (c + 32 > valid) {
 #pragma unroll
       for (int j = 0; j < 32; ++j)
-        if (j >= left) r[j] = 0xFF800000u;
+        if (c + j >= valid) r[j] = 0xFF800000u;
     }
     if (__any_sync(0xFFFFFFFFu, rel >= c && rel < c + 32)) {
 #pragma unroll
       for (int j = 0; j < 32; ++j)
         if (rel == c + j) at_target = __uint_as_float(r[j]);
     }
-    float m = top;
+    float m[4] = {top, top, top, top};
 #pragma unroll
-    for (int j = 0; j < 32; ++j) m = fmaxf(m, __uint_as_float(r[j]));
-    sum *= exp2_approx((top - m) * kLog2eF);
-    top = m;
-    const float shift = -m * kLog2eF;
-    float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int j = 0; j < 32; ++j) m[j & 3] = fmaxf(m[j & 3], __uint_as_float(r[j]));
+    m[0] = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+    float2 s[2] = {make_float2(sum * exp2_approx((top - m[0]) * kLog2eF), 0.0f),
+                   make_float2(0.0f, 0.0f)};
+    top = m[0];
 #pragma unroll
-    for (int j = 0; j < 32; ++j)
-      s[j & 3] += exp2_approx(__fmaf_rn(__uint_as_float(r[j]), kLog2eF, shift));
-    sum += (s[0] + s[1]) + (s[2] + s[3]);
-    __syncwarp();
-  }
+    for (int j = 0; j < 32; j += 2) s[j / 2 & 1] = add2(s[j / 2 & 1], exp_pair(r[j], r[j + 1], -top));
+    s[0] = add2(s[0], s[1]);
+    sum = s[0].x + s[0].y;
+  });
   if (live) {
-    o.partial[(int64_t)n_tile * o.tokens + row] = make_float2(top, sum);
-    if (rel >= 0 && rel < kTileN) o.target_logit[row] = at_target;
+    o.partial[(int64_t)t.index * o.tokens + t.row] = make_float2(top, sum);
+    if (rel >= 0) o.target_logit[t.row] = at_target;
   }
 }
 
-// The tile's logits of one token turned into p.
+// The strip's logits turned into p.
 template <bool BF16>
-__device__ __forceinline__ void probs_row(const GemmOut& o, uint32_t tmem, int64_t row, int n_tile) {
-  const int64_t n0 = (int64_t)n_tile * kTileN;   // within the piece
-  const bool live = row < o.tokens;
+__device__ __forceinline__ void probs_strip(const GemmShape& g, const GemmOut& o,
+                                            const Strip& t, const RowIn& in) {
+  const bool live = t.row < o.tokens;
   float shift = 0.0f, k = 0.0f;
-  int64_t rel = -1;
-  if (live) {
-    const long long target = o.target[row];
-    if (target != o.ignore) {
-      k = o.dloss[row] * o.scale[0];
-      shift = -o.lse[row] * kLog2eF;
-      rel = target - o.v0 - n0;
-      if (target < 0 || target >= o.vocab) k = __uint_as_float(0x7FC00000u);
-    }
+  int rel = -1;
+  if (live && in.target != o.ignore) {
+    k = (in.top == 0.0f ? in.dloss : __fdiv_rn(in.dloss, in.top)) * kProbScale;
+    shift = -in.lse;
+    const long long at = in.target - g.v0 - t.c0;
+    if (at >= 0 && at < t.cols) rel = (int)at;
+    if (in.target < 0 || in.target >= o.vocab) k = __uint_as_float(0x7FC00000u);
   }
   const bool zero = k == 0.0f;      // an ignored token, whatever its logits are
-#pragma unroll 1
-  for (int c = 0; c < kTileN; c += 32) {
-    uint32_t r[32];
-    tmem_load32(tmem + c, r);
-    tmem_wait();
-    const int64_t left = o.vocab - o.v0 - n0 - c;   // columns past the end are 0
+  const int valid = (int)min((int64_t)t.cols, o.vocab - g.v0 - t.c0);
+  uint16_t* const out = g.probs + t.row * o.piece + t.c0;
+  tmem_columns(t.tmem, t.cols, [&](int c, uint32_t (&r)[32]) {
     float v[32];
 #pragma unroll
-    for (int j = 0; j < 32; ++j)
-      v[j] = exp2_approx(__fmaf_rn(__uint_as_float(r[j]), kLog2eF, shift));
+    for (int j = 0; j < 32; j += 2) {
+      const float2 e = exp_pair(r[j], r[j + 1], shift);
+      v[j] = e.x;
+      v[j + 1] = e.y;
+    }
     if (__any_sync(0xFFFFFFFFu, rel >= c && rel < c + 32)) {
 #pragma unroll
       for (int j = 0; j < 32; ++j)
@@ -185,173 +236,283 @@ __device__ __forceinline__ void probs_row(const GemmOut& o, uint32_t tmem, int64
     }
 #pragma unroll
     for (int j = 0; j < 32; ++j) v[j] = zero ? 0.0f : v[j] * k;
-    if (left < 32) {
+    if (c + 32 > valid) {           // columns past the vocabulary's end are 0
 #pragma unroll
       for (int j = 0; j < 32; ++j)
-        if (j >= left) v[j] = 0.0f;
+        if (c + j >= valid) v[j] = 0.0f;
     }
-    if (live) store_row16<BF16>(o.probs + row * o.piece + n0 + c, v, 32);
-    __syncwarp();
-  }
+    if (live) store_row16<BF16>(out + c, v, 32);
+  });
 }
 
-// dx of one token: this piece's part added to the earlier ones', and on the
-// last piece scaled back and rounded.
-template <bool BF16>
-__device__ __forceinline__ void dx_row(const GemmOut& o, uint32_t tmem, int64_t row, int n_tile) {
-  const int64_t n0 = (int64_t)n_tile * kTileN;
-  const bool live = row < o.tokens;
-  const bool zero = live && o.target[row] == o.ignore;
-  const float back = o.scale[1];
-#pragma unroll 1
-  for (int c = 0; c < kTileN; c += 32) {
-    if (n0 + c >= o.dim) break;
-    uint32_t r[32];
-    tmem_load32(tmem + c, r);
-    tmem_wait();
-    const int left = (int)min((int64_t)32, o.dim - n0 - c);
-    float v[32];
+// This piece's part of dx, added to the earlier ones'.  `none`: the split has
+// no k in this piece, and nothing was accumulated.
+__device__ __forceinline__ void dx_strip(const GemmShape& g, const GemmOut& o, const Strip& t,
+                                         int split, bool none) {
+  const bool live = t.row < o.tokens;
+  float* const sum = o.dx_sum + (split * o.tokens + t.row) * o.dim_pitch + t.c0;
+  tmem_columns(t.tmem, t.cols, [&](int c, uint32_t (&r)[32]) {
+    if (!live) return;
+    float4* const p = reinterpret_cast<float4*>(sum + c);
+    float4 s[8];
 #pragma unroll
-    for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]);
-    // dx_sum has a pitch of whole tiles, so its accesses need no bound
-    float* sum = o.dx_sum + row * ((o.dim + kTileN - 1) / kTileN * kTileN) + n0 + c;
-    if (live && !o.first) {
+    for (int j = 0; j < 8; ++j)
+      s[j] = g.first ? make_float4(0.0f, 0.0f, 0.0f, 0.0f) : p[j];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float4 s = reinterpret_cast<const float4*>(sum)[j];
-        v[4 * j] += s.x;
-        v[4 * j + 1] += s.y;
-        v[4 * j + 2] += s.z;
-        v[4 * j + 3] += s.w;
+    for (int j = 0; j < 8; ++j) {
+      if (!none) {
+        s[j].x += __uint_as_float(r[4 * j]);
+        s[j].y += __uint_as_float(r[4 * j + 1]);
+        s[j].z += __uint_as_float(r[4 * j + 2]);
+        s[j].w += __uint_as_float(r[4 * j + 3]);
       }
+      p[j] = s[j];
     }
-    if (live && !o.last) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        reinterpret_cast<float4*>(sum)[j] =
-            make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
-    }
-    if (live && o.last) {
-#pragma unroll
-      for (int j = 0; j < 32; ++j) v[j] = zero ? 0.0f : v[j] * back;
-      store_row16<BF16>(static_cast<uint16_t*>(o.dx) + row * o.dim + n0 + c, v, left);
-    }
-    __syncwarp();
-  }
+  });
 }
 
 template <bool BF16>
-__device__ __forceinline__ void dw_row(const GemmOut& o, uint32_t tmem, int64_t row, int n_tile) {
-  const int64_t n0 = (int64_t)n_tile * kTileN;
-  const int64_t v0 = o.v0 + row;
-  const float back = o.scale[1];
-#pragma unroll 1
-  for (int c = 0; c < kTileN; c += 32) {
-    if (n0 + c >= o.dim) break;
-    uint32_t r[32];
-    tmem_load32(tmem + c, r);
-    tmem_wait();
+__device__ __forceinline__ void dw_strip(const GemmShape& g, const GemmOut& o, const Strip& t,
+                                         const RowIn& in) {
+  const int64_t v0 = g.v0 + t.row;
+  const float back = in.top;
+  const int valid = (int)min((int64_t)t.cols, o.dim - t.c0);
+  uint16_t* const out = static_cast<uint16_t*>(o.dw) + v0 * o.dim + t.c0;
+  tmem_columns(t.tmem, t.cols, [&](int c, uint32_t (&r)[32]) {
     float v[32];
 #pragma unroll
-    for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]) * back;
-    if (v0 < o.vocab)
-      store_row16<BF16>(static_cast<uint16_t*>(o.dw) + v0 * o.dim + n0 + c, v,
-                        (int)min((int64_t)32, o.dim - n0 - c));
-    __syncwarp();
-  }
+    for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]) * (1.0f / kProbScale) * back;
+    if (v0 < o.vocab && c < valid) store_row16<BF16>(out + c, v, valid - c);
+  });
 }
 
+// A tile as the warps of one CTA need it.  `work` is what its MMA warp reads:
+// blocks of k, tile_n / 128 and the operands' order.
+struct Tile {
+  uint32_t work;
+  int job, m, n, split;
+  int a_mn, b_mn;          // this CTA's coordinates in A and B ...
+  int a_k, b_k;            // ... and those of the first block of k
+  int pad[3];
+};
+constexpr uint32_t kNoWork = 0xFFFFFFFFu;
+static_assert(sizeof(Tile) == 48, "three 16-byte words");
+
+__device__ __forceinline__ Tile locate(const GemmArgs& args, int tile, int rank) {
+  Tile t = {};
+  GemmShape g = args.job[0].shape;
+#pragma unroll
+  for (int j = 1; j < kMaxJobs; ++j) {
+    if (t.job == j - 1 && j < args.jobs && tile >= g.tiles()) {
+      tile -= g.tiles();
+      g = args.job[j].shape;
+      t.job = j;
+    }
+  }
+  t.m = tile % g.tiles_m;
+  t.n = tile / g.tiles_m % g.tiles_n;
+  t.split = tile / g.tiles_m / g.tiles_n;
+  const int kb0 = t.split * g.kper, blocks = max(min(g.kper, g.kblocks - kb0), 0);
+  t.work = (uint32_t)blocks | (uint32_t)(g.tile_n / 128) << 24 | (uint32_t)g.a_mn << 28 |
+           (uint32_t)g.b_mn << 29;
+  t.a_mn = t.m * kTileM + rank * kHalfM;
+  t.b_mn = g.b_mn0 + t.n * g.tile_n + rank * (g.tile_n / 2);
+  t.a_k = kb0 * kBlockK;
+  t.b_k = g.b_k0 + kb0 * kBlockK;
+  return t;
+}
+
+// Tiles are handed out as pairs get free.  One warp of each CTA does nothing
+// else: the leader's takes the next tile from a counter and passes it to the
+// other CTA's, and each writes it, looked up, to a ring of four that its CTA's
+// other warps follow.  The counter's, the pair's and the look-up's latencies
+// are thereby hidden behind the tiles in the ring (in the producer warp they
+// cost 4000 clocks a tile, which the stages' depth could not cover).
+constexpr int kRing = 4;
 struct GemmBarriers {
   uint64_t full[kGemmStages], empty[kGemmStages], acc_full[2], acc_empty[2], drained;
+  uint64_t tile_full[kRing], tile_empty[kRing];
+  uint64_t pair_full, pair_empty;   // the other CTA's, the leader's
+  int pair_tile;
   uint32_t tmem;
+  Tile tile[kRing];
+};
+
+// A position in the ring; next() waits for the following tile and returns it,
+// null when the wait ran out; done() gives its slot back.  A whole warp calls
+// them, or one thread (WARP false).
+template <bool WARP>
+struct TileReader {
+  int slot = 0, phase = 0;
+  __device__ __forceinline__ const Tile* next(GemmBarriers& bar) {
+    bool ok = mbar_wait(&bar.tile_full[slot], phase);
+    if (WARP) ok = __all_sync(0xFFFFFFFFu, ok);
+    return ok ? &bar.tile[slot] : nullptr;
+  }
+  __device__ __forceinline__ void done(GemmBarriers& bar) {
+    if (WARP) __syncwarp();
+    if (!WARP || (threadIdx.x & 31) == 0) mbar_arrive(&bar.tile_empty[slot]);
+    if (++slot == kRing) slot = 0, phase ^= 1;
+  }
 };
 
 template <bool BF16>
-__global__ void __launch_bounds__(kGemmThreads, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
 gemm_kernel(const __grid_constant__ GemmArgs args) {
   extern __shared__ uint8_t dyn[];
   __shared__ GemmBarriers bar;
   uint8_t* const stages = dyn + ((1024u - (smem_addr(dyn) & 1023u)) & 1023u);
-  const GemmJob& job = args.job;
   const int warp = threadIdx.x >> 5;
-  const int tiles = job.tiles_m * job.tiles_n;
+  const uint32_t rank = cluster_rank();
+  const bool leader = rank == 0;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kGemmStages; ++i) {
-      mbar_init(&bar.full[i], 1);
+      mbar_init(&bar.full[i], 1);     // the leader's: its own, with both CTAs' bytes
       mbar_init(&bar.empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bar.acc_full[i], 1);
-      mbar_init(&bar.acc_empty[i], 4);
+      mbar_init(&bar.acc_empty[i], 2 * kEpilogueWarps);    // the leader's: of both CTAs
     }
+    for (int i = 0; i < kRing; ++i) {
+      mbar_init(&bar.tile_full[i], 1);
+      // the epilogue warps, the producer and, in the leader, the MMA warp
+      mbar_init(&bar.tile_empty[i], kEpilogueWarps + 1 + (leader ? 1 : 0));
+    }
+    mbar_init(&bar.pair_full, 1);
+    mbar_init(&bar.pair_empty, 1);
     mbar_init(&bar.drained, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 0) tmem_alloc(&bar.tmem);
   tcgen_fence_before();
   __syncthreads();
+  cluster_sync();
   tcgen_fence_after();
   const uint32_t tmem = bar.tmem;
   bool ok = true;
+  // the set-up above runs while the previous launch of the stream ends
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
 
-  if (warp == 4) {
+  if (warp == kEpilogueWarps + 2) {
     if ((threadIdx.x & 31) == 0) {
-      tma_prefetch_map(&job.a);
-      tma_prefetch_map(&job.b);
+      int total = 0;
+      for (int j = 0; j < args.jobs; ++j) total += args.job[j].shape.tiles();
+      const int pairs = (int)gridDim.x / 2;
+      int slot = 0, phase = 0, pair_phase = 0;
+      int tile = (int)blockIdx.x / 2, second = tile + pairs, asked = -1;
+      for (;;) {
+        if (leader) {
+          if (tile >= total) tile = -1;
+          if (!(ok = mbar_wait(&bar.pair_empty, pair_phase ^ 1))) break;
+          cluster_store(cluster_addr(&bar.pair_tile, 1), tile);
+          cluster_arrive(cluster_addr(&bar.pair_full, 1));
+        } else {
+          if (!(ok = mbar_wait<true>(&bar.pair_full, pair_phase))) break;
+          tile = *const_cast<volatile int*>(&bar.pair_tile);
+          if (tile >= -1) cluster_arrive_relaxed(cluster_addr(&bar.pair_empty, 0));
+        }
+        pair_phase ^= 1;
+        Tile t = {kNoWork};
+        if (tile >= 0) t = locate(args, tile, (int)rank);
+        if (!(ok = mbar_wait(&bar.tile_empty[slot], phase ^ 1))) break;
+        const uint4* from = reinterpret_cast<const uint4*>(&t);
+        uint4* to = reinterpret_cast<uint4*>(&bar.tile[slot]);
+        to[0] = from[0];
+        to[1] = from[1];
+        to[2] = from[2];
+        mbar_arrive(&bar.tile_full[slot]);
+        if (++slot == kRing) slot = 0, phase ^= 1;
+        if (tile < 0) break;
+        if (leader) {   // the first two tiles of a pair are fixed
+          tile = second >= 0 ? second : 2 * pairs + asked;
+          second = -1;
+          if (tile < total) asked = atomicAdd(args.next, 1);
+        }
+      }
+    }
+  } else if (warp == kEpilogueWarps) {
+    if ((threadIdx.x & 31) == 0) {
+      for (int j = 0; j < args.jobs; ++j) {
+        tma_prefetch_map(&args.job[j].a);
+        tma_prefetch_map(&args.job[j].b);
+      }
       int s = 0, phase = 0;
       uint32_t loads = 0;
-      for (int tile = blockIdx.x; ok && tile < tiles; tile += gridDim.x) {
-        const int m = job.a_mn0 + tile % job.tiles_m * kTileM;
-        const int n = job.b_mn0 + tile / job.tiles_m * kTileN;
-        for (int kb = 0; kb < job.kblocks; ++kb) {
+      TileReader<false> reader;
+      for (;;) {
+        const Tile* next = reader.next(bar);
+        if (!(ok = next != nullptr)) break;
+        const Tile t = *next;
+        if (t.work == kNoWork) break;
+        reader.done(bar);
+        const CUtensorMap* const map_a = &args.job[t.job].a;
+        const CUtensorMap* const map_b = &args.job[t.job].b;
+        const int blocks = (int)(t.work & 0xFFFFFFu), half_n = (int)(t.work >> 24 & 15u) * 64;
+        const bool a_mn = t.work >> 28 & 1, b_mn = t.work >> 29 & 1;
+        const uint32_t bytes = 2 * (kStageA + half_n * (kBlockK * 2));
+        for (int kb = 0; kb < blocks; ++kb) {
           if (!(ok = mbar_wait(&bar.empty[s], phase ^ 1))) break;
           uint8_t* a = stages + s * (kStageA + kStageB);
           uint8_t* b = a + kStageA;
-          mbar_expect(&bar.full[s], kStageA + kStageB);
+          const uint32_t full = cluster_addr(&bar.full[s], 0);
+          if (leader) mbar_expect(&bar.full[s], bytes);
           ++loads;
-          const int ka = job.a_k0 + kb * kBlockK, kk = job.b_k0 + kb * kBlockK;
-          if (job.a_mn) {
-            for (int i = 0; i < kTileM / 64; ++i)
-              tma_load(a + i * (kBlockK * 128), &job.a, m + 64 * i, ka, &bar.full[s]);
+          const int ka = t.a_k + kb * kBlockK, kk = t.b_k + kb * kBlockK;
+          if (a_mn) {
+            for (int i = 0; i < kHalfM / 64; ++i)
+              tma_load(a + i * (kBlockK * 128), map_a, t.a_mn + 64 * i, ka, full);
           } else {
-            tma_load(a, &job.a, ka, m, &bar.full[s]);
+            tma_load(a, map_a, ka, t.a_mn, full);
           }
-          if (job.b_mn) {
-            for (int i = 0; i < kTileN / 64; ++i)
-              tma_load(b + i * (kBlockK * 128), &job.b, n + 64 * i, kk, &bar.full[s]);
+          if (b_mn) {
+            for (int i = 0; i < half_n / 64; ++i)
+              tma_load(b + i * (kBlockK * 128), map_b, t.b_mn + 64 * i, kk, full);
           } else {
-            tma_load(b, &job.b, kk, n, &bar.full[s]);
+            tma_load(b, map_b, kk, t.b_mn, full);
           }
           if (++s == kGemmStages) s = 0, phase ^= 1;
         }
+        if (!ok) break;
       }
-      // every copy lands before the CTA's shared memory is given up
-      for (int i = 0; i < kGemmStages; ++i)
-        if (loads > i)
+      // every copy lands before the pair's shared memory is given up (the
+      // leader's barriers count the other CTA's copies too)
+      for (int i = 0; leader && i < kGemmStages; ++i)
+        if (loads > (uint32_t)i)
           ok = mbar_wait(&bar.full[i], (loads - 1 - i) / kGemmStages & 1) && ok;
     }
-  } else if (warp == 5) {
-    if ((threadIdx.x & 31) == 0) {
-      const uint32_t idesc = mma_desc(BF16, job.a_mn, job.b_mn, kTileM, kTileN);
-      const uint32_t step_a = job.a_mn ? 16 * 128 : 32, step_b = job.b_mn ? 16 * 128 : 32;
+  } else if (warp == kEpilogueWarps + 1) {
+    if (leader && (threadIdx.x & 31) == 0) {
       int s = 0, phase = 0, buf = 0, acc_phase = 0;
-      for (int tile = blockIdx.x; ok && tile < tiles; tile += gridDim.x) {
+      TileReader<false> reader;
+      for (;;) {
+        const Tile* next = reader.next(bar);
+        if (!(ok = next != nullptr)) break;
+        const uint32_t work = next->work;
+        if (work == kNoWork) break;
+        reader.done(bar);
+        const int blocks = (int)(work & 0xFFFFFFu);
+        const bool a_mn = work >> 28 & 1, b_mn = work >> 29 & 1;
+        const uint32_t idesc = mma_desc(BF16, a_mn, b_mn, kTileM, (int)(work >> 24 & 15u) * 128);
+        const uint32_t step_a = a_mn ? 16 * 128 : 32, step_b = b_mn ? 16 * 128 : 32;
         if (!(ok = mbar_wait(&bar.acc_empty[buf], acc_phase ^ 1))) break;
         tcgen_fence_after();
         const uint32_t d = tmem + buf * kTileN;
-        for (int kb = 0; kb < job.kblocks; ++kb) {
+        for (int kb = 0; kb < blocks; ++kb) {
           if (!(ok = mbar_wait(&bar.full[s], phase))) break;
           tcgen_fence_after();
           const uint32_t a = smem_addr(stages + s * (kStageA + kStageB));
-          const uint64_t da = operand_desc(a, job.a_mn, kBlockK * 128);
-          const uint64_t db = operand_desc(a + kStageA, job.b_mn, kBlockK * 128);
+          const uint64_t da = operand_desc(a, a_mn, kBlockK * 128);
+          const uint64_t db = operand_desc(a + kStageA, b_mn, kBlockK * 128);
 #pragma unroll
           for (int k = 0; k < kBlockK / 16; ++k)
             mma_f16(d, da + (k * step_a >> 4), db + (k * step_b >> 4), idesc, kb + k > 0);
           mma_commit(&bar.empty[s]);
           if (++s == kGemmStages) s = 0, phase ^= 1;
         }
+        if (!ok) break;
         mma_commit(&bar.acc_full[buf]);
         buf ^= 1;
         if (buf == 0) acc_phase ^= 1;
@@ -361,23 +522,32 @@ gemm_kernel(const __grid_constant__ GemmArgs args) {
       ok = mbar_wait(&bar.drained, 0) && ok;
     }
   } else {
+    TileReader<true> reader;
     int buf = 0, phase = 0;
-    for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
-      ok = mbar_wait(&bar.acc_full[buf], phase);
-      if (!__all_sync(0xFFFFFFFFu, ok)) {
-        ok = false;
-        break;
-      }
+    for (;;) {
+      const Tile* next = reader.next(bar);
+      if (!(ok = next != nullptr)) break;
+      const Tile t = *next;
+      if (t.work == kNoWork) break;
+      reader.done(bar);
+      const GemmShape& g = args.job[t.job].shape;
+      const int half = warp / 4, cols = (int)(t.work >> 24 & 15u) * 64;
+      const Strip strip = {tmem + buf * kTileN + half * cols + ((uint32_t)(warp % 4) << 21),
+                           (int64_t)t.m * kTileM + rank * kHalfM + (threadIdx.x & 127),
+                           ((int64_t)t.n * 2 + half) * cols, cols, 2 * t.n + half};
+      const RowIn in = row_in(g, args.out, strip.row);
+      ok = __all_sync(0xFFFFFFFFu, mbar_wait(&bar.acc_full[buf], phase));
+      if (!ok) break;
       tcgen_fence_after();
-      const int64_t row = (int64_t)(tile % job.tiles_m) * kTileM + threadIdx.x;
-      const int n = tile / job.tiles_m;
-      const uint32_t t = tmem + buf * kTileN + ((uint32_t)warp << 21);
-      if (job.mode == kStats) stats_row(args.out, t, row, n);
-      else if (job.mode == kProbs) probs_row<BF16>(args.out, t, row, n);
-      else if (job.mode == kDx) dx_row<BF16>(args.out, t, row, n);
-      else dw_row<BF16>(args.out, t, row, n);
+      if (g.mode == kStats) stats_strip(args.out, strip, in);
+      else if (g.mode == kProbs) probs_strip<BF16>(g, args.out, strip, in);
+      else if (g.mode == kDx) dx_strip(g, args.out, strip, t.split, (t.work & 0xFFFFFFu) == 0);
+      else dw_strip<BF16>(g, args.out, strip, in);
       tcgen_fence_before();
-      if ((threadIdx.x & 31) == 0) mbar_arrive(&bar.acc_empty[buf]);
+      __syncwarp();
+      // (the accumulators have been read: nothing else needs an order here)
+      if ((threadIdx.x & 31) == 0)
+        cluster_arrive_relaxed(cluster_addr(&bar.acc_empty[buf], 0));
       buf ^= 1;
       if (buf == 0) phase ^= 1;
     }
@@ -385,21 +555,22 @@ gemm_kernel(const __grid_constant__ GemmArgs args) {
   if (!ok) *args.error = 1;
   __syncwarp();
   tcgen_fence_before();
-  __syncthreads();
+  cluster_sync();
   tcgen_fence_after();
   if (warp == 0) tmem_free(tmem);
 }
 
-// Joins a token's column tiles: lane l takes tiles l, l + 32, ..., in order.
+// Joins a token's column strips: lane l takes strips l, l + 32, ..., in order.
 __global__ void __launch_bounds__(256)
-xent_join_kernel(const float2* __restrict__ partial, int tiles, int64_t tokens, int64_t vocab,
+xent_join_kernel(const float2* __restrict__ partial, int strips, int64_t tokens, int64_t vocab,
                  const long long* __restrict__ target, long long ignore,
                  const float* __restrict__ target_logit, float* __restrict__ loss,
                  float* __restrict__ lse) {
   const int64_t row = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+  asm volatile("griddepcontrol.wait;" ::: "memory");   // for the tiles' statistics
   if (row >= tokens) return;
   float m = -1e30f, s = 0.0f;
-  for (int i = threadIdx.x & 31; i < tiles; i += 32) {
+  for (int i = threadIdx.x & 31; i < strips; i += 32) {
     const float2 p = __ldg(partial + (int64_t)i * tokens + row);
     const float top = fmaxf(m, p.x);
     s = s * exp2_approx((m - top) * kLog2eF) + p.y * exp2_approx((p.x - top) * kLog2eF);
@@ -441,23 +612,49 @@ xent_copy_kernel(const uint16_t* __restrict__ src, int64_t rows, int64_t dim, in
   }
 }
 
-// scale[0] = the power of two that brings max |dloss| of the tokens that count
-// to [2^14, 2^15), scale[1] = its inverse; 1 when the maximum is 0 or not
-// finite.  (|exp(z - lse) - [target]| is at most 1, so |p| < 2^15.)
+// The largest finite |dloss| of the tokens that count (one that is not finite
+// spoils its own token's dx, not the others').
 __global__ void __launch_bounds__(1024)
-xent_scale_kernel(const float* __restrict__ dloss, const long long* __restrict__ target,
-                  long long ignore, int64_t tokens, float* __restrict__ scale) {
+xent_top_kernel(const float* __restrict__ dloss, const long long* __restrict__ target,
+                long long ignore, int64_t tokens, float* __restrict__ top) {
   __shared__ uint32_t sh[32];
   uint32_t m = 0;
   for (int64_t i = threadIdx.x; i < tokens; i += 1024)
-    if (target[i] != ignore) m = max(m, abs_bits(dloss[i]));
+    if (target[i] != ignore && !nonfinite(dloss[i])) m = max(m, abs_bits(dloss[i]));
   m = block_max_u32<1024>(m, sh);
-  if (threadIdx.x == 0) {
-    int e = (int)(m >> 23) - 127;                 // 2^e <= max < 2^(e + 1)
-    if (m == 0 || m >= 0x7F800000u) e = 14;
-    const int k = min(max(14 - e, -126), 126);
-    scale[0] = __int_as_float((127 + k) << 23);
-    scale[1] = __int_as_float((127 - k) << 23);
+  if (threadIdx.x == 0) *top = __uint_as_float(m);
+}
+
+// dx from its fp32 parts: the splits added in order, scaled back, rounded; 0
+// for an ignored token.
+template <bool BF16>
+__global__ void __launch_bounds__(256)
+xent_dx_kernel(const float* __restrict__ sum, int splits, int64_t tokens, int64_t dim,
+               int64_t pitch, const long long* __restrict__ target, long long ignore,
+               const float* __restrict__ top, uint16_t* __restrict__ dx) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const float back = *top;
+  for (int64_t r = blockIdx.x; r < tokens; r += gridDim.x) {
+    const bool zero = target[r] == ignore;
+    for (int64_t c = 2 * threadIdx.x; c < dim; c += 512) {   // pitch is even
+      float2 v = make_float2(0.0f, 0.0f);
+      for (int s = 0; s < splits; ++s) {
+        const float2 a =
+            *reinterpret_cast<const float2*>(sum + (s * tokens + r) * pitch + c);
+        v.x += a.x;
+        v.y += a.y;
+      }
+      v.x = zero ? 0.0f : v.x * (1.0f / kProbScale) * back;
+      v.y = zero ? 0.0f : v.y * (1.0f / kProbScale) * back;
+      uint16_t* out = dx + r * dim + c;
+      const uint32_t both = pack16<BF16>(v.x, v.y);
+      if ((reinterpret_cast<uintptr_t>(out) & 3u) == 0 && c + 1 < dim) {
+        *reinterpret_cast<uint32_t*>(out) = both;
+      } else {
+        out[0] = (uint16_t)both;
+        if (c + 1 < dim) out[1] = (uint16_t)(both >> 16);
+      }
+    }
   }
 }
 
@@ -497,14 +694,36 @@ cudaError_t make_map(CUtensorMap* map, bool bf16, const void* base, int64_t rows
 
 int64_t up(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
 
-cudaError_t launch_gemm(const GemmArgs& g, bool bf16, int sms, cudaStream_t stream) {
+// A launch whose set-up may overlap the end of the previous one of the stream
+// (the kernel waits for it before it reads anything).
+template <class... Params, class... Args>
+cudaError_t launch_early(void (*kernel)(Params...), unsigned grid, unsigned block, size_t smem,
+                         cudaStream_t stream, Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute early;
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &early;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+cudaError_t launch_gemm(GemmArgs& g, bool bf16, int sms, cudaStream_t stream) {
   auto kernel = bf16 ? gemm_kernel<true> : gemm_kernel<false>;
   const cudaError_t e =
       cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kGemmSmem);
   if (e != cudaSuccess) return e;
-  const int64_t tiles = (int64_t)g.job.tiles_m * g.job.tiles_n;
-  kernel<<<(unsigned)(tiles < sms ? tiles : sms), kGemmThreads, kGemmSmem, stream>>>(g);
-  return cudaGetLastError();
+  // the longest tiles first: the short ones even out the end
+  std::sort(g.job, g.job + g.jobs,
+            [](const GemmJob& a, const GemmJob& b) { return a.shape.kper > b.shape.kper; });
+  int64_t tiles = 0;
+  for (int i = 0; i < g.jobs; ++i) tiles += g.job[i].shape.tiles();
+  return launch_early(kernel, 2 * (unsigned)std::min(tiles, (int64_t)sms / 2), kGemmThreads,
+                      kGemmSmem, stream, g);
 }
 
 // Rows that TMA can read as they are.
@@ -525,67 +744,98 @@ cudaError_t copy_rows(const void* src, int64_t rows, int64_t dim, int64_t pitch,
 
 // Tokens of one forward launch: bounds the scratch of the tiles' statistics.
 constexpr int64_t kForwardTokens = 65536;
-// Bytes of p aimed at for one piece of the vocabulary.
-constexpr int64_t kPieceBytes = 64ll << 20;
+// Bytes of p aimed at for one piece of the vocabulary (two exist at a time).
+constexpr int64_t kPieceBytes = 32ll << 20;
 
 int64_t piece_columns(int64_t tokens, int64_t vocab) {
-  const int64_t fit = kPieceBytes / 2 / up(tokens, kTileM) / kTileN * kTileN;
-  return std::min(std::max(fit, (int64_t)kTileN), up(vocab, kTileN));
+  const int64_t fit = std::max(kPieceBytes / 2 / up(tokens, kTileM) / kTileN, (int64_t)1);
+  const int64_t pieces = (vocab + fit * kTileN - 1) / (fit * kTileN);
+  return up((vocab + pieces - 1) / pieces, kTileN);   // of even size
 }
 
-// Layouts of the scratch.
-struct ForwardScratch {
-  size_t x = 0, w = 0, partial = 0, logit = 0, bytes = 0;
+// Width of the tiles that cover dim columns: 128 or 256 (a CTA's half is read in
+// boxes of 64).
+int width_of(int64_t dim) {
+  const int64_t tiles = (dim + kTileN - 1) / kTileN;
+  return (int)up((dim + tiles - 1) / tiles, 128);
+}
+
+int blocks_of(int64_t k) { return (int)((k + kBlockK - 1) / kBlockK); }
+
+// Ranges of k for dx: its tiles are few and long when the tokens are few, so
+// they are cut until one is at most a third of a pair's share of a launch.
+int dx_splits(const XentArgs& a, int64_t piece, int sms) {
+  const int64_t tiles_t = up(a.rows, kTileM) / kTileM;
+  const int64_t tiles_d = (a.dim + width_of(a.dim) - 1) / width_of(a.dim);
+  const int64_t dx = tiles_t * tiles_d * blocks_of(piece);
+  const int64_t dw = up(piece, kTileM) / kTileM * tiles_d * blocks_of(a.rows);
+  const int64_t probs = tiles_t * (piece / kTileN) * blocks_of(a.dim);
+  const int64_t share = std::max((dx + dw + probs) / (sms / 2) / 3, (int64_t)4);
+  return (int)std::min((blocks_of(piece) + share - 1) / share, (int64_t)8);
+}
+
+class Layout {
+ public:
+  size_t take(int64_t bytes) {
+    const size_t at = bytes_;
+    bytes_ += (size_t)up(bytes, 256);
+    return at;
+  }
+  size_t bytes() const { return bytes_; }
+
+ private:
+  size_t bytes_ = 0;
 };
-ForwardScratch forward_scratch(const XentArgs& a) {
+
+struct ForwardScratch {
+  size_t next = 0, x = 0, w = 0, partial = 0, logit = 0, bytes = 0;
+  int tile_n = kTileN;
+};
+ForwardScratch forward_scratch(const XentArgs& a, int sms) {
   ForwardScratch s;
-  size_t at = 0;
-  const auto take = [&](int64_t n) {
-    const size_t p = at;
-    at += (size_t)up(n, 256);
-    return p;
-  };
-  const int64_t pitch = up(a.dim, 8);
-  const int64_t tokens = std::min(a.rows, kForwardTokens);
-  if (!direct(a.x, a.dim)) s.x = take(a.rows * pitch * 2);
-  if (!direct(a.w, a.dim)) s.w = take(a.vocab * pitch * 2);
-  s.partial = take(up(a.vocab, kTileN) / kTileN * tokens * 8);
-  s.logit = take(tokens * 4);
-  s.bytes = at;
+  Layout l;
+  const int64_t pitch = up(a.dim, 8), tokens = std::min(a.rows, kForwardTokens);
+  // narrow tiles where wide ones would not fill two rounds of the SMs
+  if (up(tokens, kTileM) / kTileM * (up(a.vocab, kTileN) / kTileN) < sms) s.tile_n = 128;
+  s.next = l.take(4);
+  if (!direct(a.x, a.dim)) s.x = l.take(a.rows * pitch * 2);
+  if (!direct(a.w, a.dim)) s.w = l.take(a.vocab * pitch * 2);
+  s.partial = l.take(2 * (up(a.vocab, s.tile_n) / s.tile_n) * tokens * 8);
+  s.logit = l.take(tokens * 4);
+  s.bytes = l.bytes();
   return s;
 }
 
 struct BackwardScratch {
-  size_t x = 0, w = 0, scale = 0, probs = 0, dx = 0, bytes = 0;
-  int64_t piece = 0;
+  size_t next = 0, x = 0, w = 0, top = 0, probs[2] = {0, 0}, dx = 0, bytes = 0;
+  int64_t piece = 0, pieces = 0;
+  int splits = 1;
 };
-BackwardScratch backward_scratch(const XentArgs& a) {
+BackwardScratch backward_scratch(const XentArgs& a, int sms) {
   BackwardScratch s;
-  size_t at = 0;
-  const auto take = [&](int64_t n) {
-    const size_t p = at;
-    at += (size_t)up(n, 256);
-    return p;
-  };
+  Layout l;
   const int64_t pitch = up(a.dim, 8);
   s.piece = piece_columns(a.rows, a.vocab);
-  s.x = take(a.rows * pitch * 2);
-  if (!direct(a.w, a.dim)) s.w = take(a.vocab * pitch * 2);
-  s.scale = take(8);
-  s.probs = take(a.rows * s.piece * 2);
-  if (s.piece < a.vocab) s.dx = take(a.rows * up(a.dim, kTileN) * 4);
-  s.bytes = at;
+  s.pieces = (a.vocab + s.piece - 1) / s.piece;
+  s.splits = dx_splits(a, s.piece, sms);
+  s.next = l.take((s.pieces + 1) * 4);
+  s.top = l.take(4);
+  s.x = l.take(a.rows * pitch * 2);
+  if (!direct(a.w, a.dim)) s.w = l.take(a.vocab * pitch * 2);
+  for (int i = 0; i < 2 && i < s.pieces; ++i) s.probs[i] = l.take(a.rows * s.piece * 2);
+  s.dx = l.take(s.splits * a.rows * up(a.dim, width_of(a.dim)) * 4);
+  s.bytes = l.bytes();
   return s;
 }
 
 }  // namespace
 
-size_t xent_forward_scratch(const XentArgs& a) { return forward_scratch(a).bytes; }
-size_t xent_backward_scratch(const XentArgs& a) { return backward_scratch(a).bytes; }
+size_t xent_forward_scratch(const XentArgs& a, int sms) { return forward_scratch(a, sms).bytes; }
+size_t xent_backward_scratch(const XentArgs& a, int sms) { return backward_scratch(a, sms).bytes; }
 
 cudaError_t launch_xent_forward(const XentArgs& a, char* scratch, int* error, int sms,
                                 cudaStream_t stream, LaunchMark mark) {
-  const ForwardScratch s = forward_scratch(a);
+  const ForwardScratch s = forward_scratch(a, sms);
   const bool bf16 = a.dtype == kBF16;
   const int64_t pitch = up(a.dim, 8);
   const char* x = static_cast<const char*>(a.x);
@@ -603,10 +853,15 @@ cudaError_t launch_xent_forward(const XentArgs& a, char* scratch, int* error, in
     const int64_t tokens = std::min(a.rows - t0, kForwardTokens);
     GemmArgs g = {};
     g.error = error;
-    g.job.mode = kStats;
-    g.job.tiles_m = (int)(up(tokens, kTileM) / kTileM);
-    g.job.tiles_n = (int)(up(a.vocab, kTileN) / kTileN);
-    g.job.kblocks = (int)(up(a.dim, kBlockK) / kBlockK);
+    g.next = reinterpret_cast<int*>(scratch + s.next);
+    g.jobs = 1;
+    GemmShape& j = g.job[0].shape;
+    j.mode = kStats;
+    j.tiles_m = (int)(up(tokens, kTileM) / kTileM);
+    j.tile_n = s.tile_n;
+    j.tiles_n = (int)(up(a.vocab, s.tile_n) / s.tile_n);
+    j.kblocks = j.kper = blocks_of(a.dim);
+    j.splits = 1;
     g.out.tokens = tokens;
     g.out.vocab = a.vocab;
     g.out.dim = a.dim;
@@ -614,19 +869,20 @@ cudaError_t launch_xent_forward(const XentArgs& a, char* scratch, int* error, in
     g.out.ignore = a.ignore;
     g.out.partial = reinterpret_cast<float2*>(scratch + s.partial);
     g.out.target_logit = reinterpret_cast<float*>(scratch + s.logit);
-    e = make_map(&g.job.a, bf16, x + t0 * pitch * 2, tokens, a.dim, pitch, kTileM);
-    if (e == cudaSuccess) e = make_map(&g.job.b, bf16, w, a.vocab, a.dim, pitch, kTileN);
+    e = make_map(&g.job[0].a, bf16, x + t0 * pitch * 2, tokens, a.dim, pitch, kHalfM);
+    if (e == cudaSuccess) e = make_map(&g.job[0].b, bf16, w, a.vocab, a.dim, pitch, s.tile_n / 2);
+    if (e == cudaSuccess) e = cudaMemsetAsync(g.next, 0, 4, stream);
     if (e != cudaSuccess) break;
     if (mark) mark(kXentLogitsK, 0, stream);
     e = launch_gemm(g, bf16, sms, stream);
     if (mark) mark(kXentLogitsK, 1, stream);
     if (e != cudaSuccess) break;
     if (mark) mark(kXentJoinK, 0, stream);
-    xent_join_kernel<<<(unsigned)((tokens + 7) / 8), 256, 0, stream>>>(
-        g.out.partial, g.job.tiles_n, tokens, a.vocab, g.out.target, a.ignore,
-        g.out.target_logit, a.loss + t0, a.lse_out + t0);
+    e = launch_early(xent_join_kernel, (unsigned)((tokens + 7) / 8), 256, 0, stream,
+                     (const float2*)g.out.partial, 2 * j.tiles_n, tokens, a.vocab, g.out.target,
+                     g.out.ignore, (const float*)g.out.target_logit, a.loss + t0,
+                     a.lse_out + t0);
     if (mark) mark(kXentJoinK, 1, stream);
-    e = cudaGetLastError();
   }
   return e;
 }
@@ -635,35 +891,41 @@ cudaError_t launch_xent_backward(const XentArgs& a, char* scratch, int* error, i
                                  cudaStream_t stream, LaunchMark mark) {
   const bool bf16 = a.dtype == kBF16;
   if (a.rows == 0) return cudaMemsetAsync(a.dw, 0, (size_t)(a.vocab * a.dim) * 2, stream);
-  const BackwardScratch s = backward_scratch(a);
+  const BackwardScratch s = backward_scratch(a, sms);
   const int64_t pitch = up(a.dim, 8);
+  const int width = width_of(a.dim);
+  const long long* target = reinterpret_cast<const long long*>(a.target);
   const char* x = scratch + s.x;   // rows of ignored tokens zero
   const char* w = static_cast<const char*>(a.w);
+  int* next = reinterpret_cast<int*>(scratch + s.next);
+  float* top = reinterpret_cast<float*>(scratch + s.top);
+  cudaError_t e = cudaMemsetAsync(next, 0, (size_t)(s.pieces + 1) * 4, stream);
   if (mark) mark(kXentPrepareK, 0, stream);
-  cudaError_t e = copy_rows(a.x, a.rows, a.dim, pitch, a.target, a.ignore, scratch + s.x, sms,
-                            stream);
+  if (e == cudaSuccess)
+    e = copy_rows(a.x, a.rows, a.dim, pitch, a.target, a.ignore, scratch + s.x, sms, stream);
   if (e == cudaSuccess && !direct(a.w, a.dim)) {
     e = copy_rows(a.w, a.vocab, a.dim, pitch, nullptr, 0, scratch + s.w, sms, stream);
     w = scratch + s.w;
   }
-  float* scale = reinterpret_cast<float*>(scratch + s.scale);
-  xent_scale_kernel<<<1, 1024, 0, stream>>>(a.dloss, reinterpret_cast<const long long*>(a.target),
-                                            a.ignore, a.rows, scale);
+  xent_top_kernel<<<1, 1024, 0, stream>>>(a.dloss, target, a.ignore, a.rows, top);
   if (mark) mark(kXentPrepareK, 1, stream);
   if (e == cudaSuccess) e = cudaGetLastError();
   if (e != cudaSuccess) return e;
 
   // x and w as K-major operands of the logits, and MN-major ones of dw and dx;
   // p as dx's K-major and dw's MN-major operand
-  CUtensorMap x_k, w_k, x_mn, w_mn, p_k, p_mn;
-  const char* p = scratch + s.probs;
-  if ((e = make_map(&x_k, bf16, x, a.rows, a.dim, pitch, kTileM)) != cudaSuccess ||
-      (e = make_map(&w_k, bf16, w, a.vocab, a.dim, pitch, kTileN)) != cudaSuccess ||
+  CUtensorMap x_k, w_k, x_mn, w_mn, p_k[2], p_mn[2];
+  if ((e = make_map(&x_k, bf16, x, a.rows, a.dim, pitch, kHalfM)) != cudaSuccess ||
+      (e = make_map(&w_k, bf16, w, a.vocab, a.dim, pitch, kTileN / 2)) != cudaSuccess ||
       (e = make_map(&x_mn, bf16, x, a.rows, a.dim, pitch, kBlockK)) != cudaSuccess ||
-      (e = make_map(&w_mn, bf16, w, a.vocab, a.dim, pitch, kBlockK)) != cudaSuccess ||
-      (e = make_map(&p_k, bf16, p, a.rows, s.piece, s.piece, kTileM)) != cudaSuccess ||
-      (e = make_map(&p_mn, bf16, p, a.rows, s.piece, s.piece, kBlockK)) != cudaSuccess)
+      (e = make_map(&w_mn, bf16, w, a.vocab, a.dim, pitch, kBlockK)) != cudaSuccess)
     return e;
+  for (int i = 0; i < 2 && i < s.pieces; ++i) {
+    const char* p = scratch + s.probs[i];
+    if ((e = make_map(&p_k[i], bf16, p, a.rows, s.piece, s.piece, kHalfM)) != cudaSuccess ||
+        (e = make_map(&p_mn[i], bf16, p, a.rows, s.piece, s.piece, kBlockK)) != cudaSuccess)
+      return e;
+  }
 
   GemmArgs g = {};
   g.error = error;
@@ -671,43 +933,50 @@ cudaError_t launch_xent_backward(const XentArgs& a, char* scratch, int* error, i
   o.tokens = a.rows;
   o.vocab = a.vocab;
   o.dim = a.dim;
-  o.target = reinterpret_cast<const long long*>(a.target);
+  o.target = target;
   o.ignore = a.ignore;
   o.lse = a.lse;
   o.dloss = a.dloss;
-  o.scale = scale;
-  o.probs = reinterpret_cast<uint16_t*>(scratch + s.probs);
+  o.top_dloss = top;
   o.piece = s.piece;
   o.dx_sum = reinterpret_cast<float*>(scratch + s.dx);
-  o.dx = a.dx;
+  o.dim_pitch = up(a.dim, width);
   o.dw = a.dw;
   const int tiles_t = (int)(up(a.rows, kTileM) / kTileM);
-  const int tiles_d = (int)(up(a.dim, kTileN) / kTileN);
-  for (int64_t v0 = 0; v0 < a.vocab; v0 += s.piece) {
-    const int64_t cols = std::min(s.piece, a.vocab - v0);
-    o.v0 = v0;
-    o.first = v0 == 0;
-    o.last = v0 + cols == a.vocab;
-    GemmJob& j = g.job;
-    j = GemmJob{x_k, w_k, kProbs, tiles_t, (int)(up(cols, kTileN) / kTileN),
-                (int)(up(a.dim, kBlockK) / kBlockK), 0, 0, (int)v0, 0, 0, 0};
-    if (mark) mark(kXentProbsK, 0, stream);
-    e = launch_gemm(g, bf16, sms, stream);
-    if (mark) mark(kXentProbsK, 1, stream);
-    if (e != cudaSuccess) return e;
-    if (mark) mark(kXentGradsK, 0, stream);
-    j = GemmJob{p_k, w_mn, kDx, tiles_t, tiles_d, (int)(up(cols, kBlockK) / kBlockK),
-                0, 0, 0, (int)v0, 0, 1};
-    e = launch_gemm(g, bf16, sms, stream);
-    if (e == cudaSuccess) {
-      j = GemmJob{p_mn, x_mn, kDw, (int)(up(cols, kTileM) / kTileM), tiles_d,
-                  (int)(up(a.rows, kBlockK) / kBlockK), 0, 0, 0, 0, 1, 1};
-      e = launch_gemm(g, bf16, sms, stream);
+  const int tiles_d = (int)(o.dim_pitch / width);
+  // Launch i: the gradients of piece i - 1 and the probabilities of piece i.
+  for (int64_t i = 0; i <= s.pieces; ++i) {
+    g.jobs = 0;
+    g.next = next + i;
+    if (i > 0) {
+      const int64_t v0 = (i - 1) * s.piece, cols = std::min(s.piece, a.vocab - v0);
+      const int at = (int)((i - 1) & 1), kb = blocks_of(cols);
+      g.job[g.jobs++] = {p_k[at], w_mn,
+                         {kDx, tiles_t, tiles_d, width, kb, (kb + s.splits - 1) / s.splits,
+                          s.splits, 0, (int)v0, 0, 1, i == 1, v0, nullptr}};
+      g.job[g.jobs++] = {p_mn[at], x_mn,
+                         {kDw, (int)(up(cols, kTileM) / kTileM), tiles_d, width,
+                          blocks_of(a.rows), blocks_of(a.rows), 1, 0, 0, 1, 1, 0, v0, nullptr}};
     }
+    if (i < s.pieces) {
+      const int64_t v0 = i * s.piece, cols = std::min(s.piece, a.vocab - v0);
+      g.job[g.jobs++] = {x_k, w_k,
+                         {kProbs, tiles_t, (int)(up(cols, kTileN) / kTileN), kTileN,
+                          blocks_of(a.dim), blocks_of(a.dim), 1, (int)v0, 0, 0, 0, 0, v0,
+                          reinterpret_cast<uint16_t*>(scratch + s.probs[i & 1])}};
+    }
+    if (mark) mark(kXentGradsK, 0, stream);
+    e = launch_gemm(g, bf16, sms, stream);
     if (mark) mark(kXentGradsK, 1, stream);
     if (e != cudaSuccess) return e;
   }
-  return cudaSuccess;
+  if (mark) mark(kXentDxK, 0, stream);
+  e = launch_early(bf16 ? xent_dx_kernel<true> : xent_dx_kernel<false>,
+                   (unsigned)std::min(a.rows, (int64_t)8 * sms), 256, 0, stream,
+                   (const float*)o.dx_sum, s.splits, a.rows, a.dim, o.dim_pitch, target,
+                   (long long)a.ignore, (const float*)top, static_cast<uint16_t*>(a.dx));
+  if (mark) mark(kXentDxK, 1, stream);
+  return e;
 }
 
 }  // namespace fp8opt

@@ -92,8 +92,8 @@ struct XentArgs {
   void* dw;
 };
 
-size_t xent_forward_scratch(const XentArgs& a);
-size_t xent_backward_scratch(const XentArgs& a);
+size_t xent_forward_scratch(const XentArgs& a, int sms);
+size_t xent_backward_scratch(const XentArgs& a, int sms);
 // error: a device word set to 1 when a wait in a kernel ran out.
 cudaError_t launch_xent_forward(const XentArgs& a, char* scratch, int* error, int sms,
                                 cudaStream_t stream, LaunchMark mark);
@@ -124,6 +124,16 @@ class OpCall {
 int record_error(int status, const char* what);
 
 // --------------------------------------------------------- element helpers
+
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 ra, rb, rd;\n\t"
+      "mov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\t"
+      "add.rn.f32x2 rd, ra, rb;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
 
 // Two fp32 values rounded to nearest even to a pair of DT (kBF16 or kF16),
 // the first in the low half.

@@ -40,31 +40,84 @@ __device__ __forceinline__ bool mbar_try(uint64_t* bar, uint32_t parity) {
   return done != 0;
 }
 
+// The same for barriers that threads of the other CTA of a pair arrive at.
+__device__ __forceinline__ bool mbar_try_pair(uint64_t* bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(done)
+      : "r"(smem_addr(bar)), "r"(parity)
+      : "memory");
+  return done != 0;
+}
+
 // Longest wait, in SM clocks (about two seconds): a wait that runs out means
 // a copy or a product that never completed.
 constexpr long long kWaitClocks = 4000000000ll;
 
 // Waits for the phase of the given parity; false when the wait ran out.
+template <bool PAIR = false>
 __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity) {
-  if (mbar_try(bar, parity)) return true;
+  const auto ready = [&] { return PAIR ? mbar_try_pair(bar, parity) : mbar_try(bar, parity); };
+  if (ready()) return true;
   const long long start = clock64();
   for (;;) {
 #pragma unroll 1
     for (int i = 0; i < 64; ++i)
-      if (mbar_try(bar, parity)) return true;
+      if (ready()) return true;
     if (clock64() - start > kWaitClocks) return false;
   }
 }
 
+// -------------------------------------------------------------- CTA pairs
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+
+// The address, in the cluster's shared memory, of what lies at p in CTA `rank`.
+__device__ __forceinline__ uint32_t cluster_addr(const void* p, uint32_t rank) {
+  uint32_t a;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_addr(p)), "r"(rank));
+  return a;
+}
+
+__device__ __forceinline__ void cluster_arrive(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar)
+               : "memory");
+}
+
+// Without ordering the thread's earlier memory accesses: a release would wait
+// for all its global stores.
+__device__ __forceinline__ void cluster_arrive_relaxed(uint32_t bar) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar)
+               : "memory");
+}
+
+__device__ __forceinline__ void cluster_store(uint32_t addr, int v) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+
+// Every thread of both CTAs.
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
 // -------------------------------------------------------------------- TMA
 
-// A box of a 2-D tensor to shared memory; x is the contiguous coordinate.
+// A box of a 2-D tensor to this CTA's shared memory; x is the contiguous
+// coordinate.  bar: a barrier of either CTA of the pair.
 __device__ __forceinline__ void tma_load(void* dst, const CUtensorMap* map, int x, int y,
-                                         uint64_t* bar) {
+                                         uint32_t bar) {
   asm volatile(
       "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%2, %3}], [%4];" ::"r"(smem_addr(dst)),
-      "l"(map), "r"(x), "r"(y), "r"(smem_addr(bar))
+      ".cta_group::2 [%0], [%1, {%2, %3}], [%4];" ::"r"(smem_addr(dst)),
+      "l"(map), "r"(x), "r"(y), "r"(bar)
       : "memory");
 }
 
@@ -74,16 +127,17 @@ __device__ __forceinline__ void tma_prefetch_map(const CUtensorMap* map) {
 
 // ------------------------------------------------------------------- TMEM
 
-// All of an SM's 512 columns, for a kernel that runs one CTA per SM.
+// All 512 columns of both SMs of a pair, for a kernel that runs one CTA per SM
+// (one warp of each CTA calls it).
 __device__ __forceinline__ void tmem_alloc(uint32_t* out) {
-  asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
+  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
                    smem_addr(out))
                : "memory");
-  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
 }
 
 __device__ __forceinline__ void tmem_free(uint32_t base) {
-  asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(base));
+  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(base));
 }
 
 // 32 columns of this warp's 32 lanes: register j holds column j of the
@@ -103,8 +157,34 @@ __device__ __forceinline__ void tmem_load32(uint32_t addr, uint32_t (&r)[32]) {
       : "r"(addr));
 }
 
-__device__ __forceinline__ void tmem_wait() {
-  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+// Waits for this thread's loads; r, loaded before, is written from here on.
+__device__ __forceinline__ void tmem_wait(uint32_t (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),
+                 "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]),
+                 "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]),
+                 "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
+                 "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]),
+                 "+r"(r[30]), "+r"(r[31])::"memory");
+}
+
+// f(c, r) for the columns [c, c + 32) of [0, n), n a multiple of 64.  The
+// loads and the waits for them stay in one block: a load writes its registers
+// later than the compiler knows, so none may live across a loop's end.  The
+// whole warp calls it.
+template <class F>
+__device__ __forceinline__ void tmem_columns(uint32_t addr, int n, F f) {
+#pragma unroll 1
+  for (int c = 0; c < n; c += 64) {
+    uint32_t r[32], q[32];
+    tmem_load32(addr + c, r);
+    tmem_load32(addr + c + 32, q);
+    tmem_wait(r);
+    tmem_wait(q);
+    f(c, r);
+    f(c + 32, q);
+    __syncwarp();
+  }
 }
 
 __device__ __forceinline__ void tcgen_fence_before() {
@@ -128,7 +208,9 @@ __device__ __forceinline__ uint64_t operand_desc(uint32_t addr, bool mn_major,
          (uint64_t)1 << 46 | (uint64_t)2 << 61;
 }
 
-// kind::f16 with fp32 accumulation: both operands FP16, or both BF16.
+// kind::f16 with fp32 accumulation: both operands FP16, or both BF16.  The
+// product of a pair: m rows, half of them of A in each CTA (and in its TMEM);
+// n columns, half of B's rows in each CTA.
 __host__ __device__ constexpr uint32_t mma_desc(bool bf16, bool a_mn, bool b_mn, int m, int n) {
   return 1u << 4 | (bf16 ? 1u : 0u) << 7 | (bf16 ? 1u : 0u) << 10 | (a_mn ? 1u : 0u) << 15 |
          (b_mn ? 1u : 0u) << 16 | (uint32_t)(n / 8) << 17 | (uint32_t)(m / 16) << 24;
@@ -138,16 +220,19 @@ __device__ __forceinline__ void mma_f16(uint32_t d, uint64_t a, uint64_t b, uint
                                         bool add) {
   asm volatile(
       "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
       "l"(a), "l"(b), "r"(idesc), "r"(add ? 1u : 0u)
       : "memory");
 }
 
-// The barrier gets one arrival when every product issued so far is complete.
+// The barriers at this place in both CTAs get one arrival each when every
+// product issued so far is complete.
 __device__ __forceinline__ void mma_commit(uint64_t* bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
-                   smem_addr(bar))
-               : "memory");
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
+      " [%0], %1;" ::"r"(smem_addr(bar)),
+      "h"((uint16_t)3)
+      : "memory");
 }
 
 }  // namespace fp8opt

@@ -682,9 +682,9 @@ FP8OPT_API int fp8_layer_norm_backward(
  * 0 and no part in dw, whatever its row of x holds.  rows = 0 gives dw 0.
  * Rows whose length is a multiple of 8 in 16-byte-aligned tensors are read in
  * place, others through a copy in scratch.  Scratch: the statistics of the
- * column tiles (forward); a copy of x, one piece of p (64 MiB, or 512 bytes a
- * token where that is more) and, with more than one piece, dx in fp32
- * (backward).  dim and vocab >= 1; each tensor below 2^31 rows and columns.
+ * column tiles (forward); a copy of x, two pieces of p (32 MiB each, or 512
+ * bytes a token where that is more) and dx in fp32, up to eight times when the
+ * tokens are few (backward).  dim and vocab >= 1; each tensor below 2^31 rows and columns.
  *
  * The kernels wait for their copies and products with a limit of about two
  * seconds; should one run out (it does not on a working device), the next
@@ -719,7 +719,7 @@ FP8OPT_API const char *fp8opt_last_error(void);
  * "reduce_amax", "reduce_encode", "grad_norm", "grad_norm_terms", "clip_coef",
  * "found", "act_save", "act_load", "gelu", "gelu_backward", "layer_norm",
  * "layer_norm_backward", "layer_norm_params", "xent_logits", "xent_join",
- * "xent_prepare", "xent_probs", "xent_grads"), the launches
+ * "xent_prepare", "xent_grads", "xent_dx"), the launches
  * recorded since enabling and their summed duration in milliseconds.  Returns
  * FP8OPT_ERR_ARG for an unknown name or NULL outputs. */
 FP8OPT_API int fp8opt_timing_enable(int on);

@@ -97,7 +97,9 @@ struct GemmArgs {
   GemmJob job[kMaxJobs];
   int jobs;
   GemmOut out;
-  int* next;               // tiles handed out beyond the first of each CTA
+  // Tiles handed out beyond the first two of each pair, to whichever pair gets
+  // free; NULL: a pair takes every so many-th tile (they are equally long).
+  int* next;
   int* error;              // set to 1 when a wait ran out
 };
 
@@ -426,10 +428,14 @@ gemm_kernel(const __grid_constant__ GemmArgs args) {
         mbar_arrive(&bar.tile_full[slot]);
         if (++slot == kRing) slot = 0, phase ^= 1;
         if (tile < 0) break;
-        if (leader) {   // the first two tiles of a pair are fixed
-          tile = second >= 0 ? second : 2 * pairs + asked;
-          second = -1;
-          if (tile < total) asked = atomicAdd(args.next, 1);
+        if (leader) {   // (with a counter, the first two tiles of a pair are fixed)
+          if (args.next == nullptr) {
+            tile += pairs;
+          } else {
+            tile = second >= 0 ? second : 2 * pairs + asked;
+            second = -1;
+            if (tile < total) asked = atomicAdd(args.next, 1);
+          }
         }
       }
     }
@@ -560,35 +566,49 @@ gemm_kernel(const __grid_constant__ GemmArgs args) {
   if (warp == 0) tmem_free(tmem);
 }
 
-// Joins a token's column strips: lane l takes strips l, l + 32, ..., in order.
-__global__ void __launch_bounds__(256)
+// Joins the column strips of 32 tokens, a token to each lane (neighbouring
+// tokens' statistics lie side by side): warp k takes strips k, k + 32, ... in
+// order, then the 32 warps' results are joined in order.
+__global__ void __launch_bounds__(1024)
 xent_join_kernel(const float2* __restrict__ partial, int strips, int64_t tokens, int64_t vocab,
                  const long long* __restrict__ target, long long ignore,
                  const float* __restrict__ target_logit, float* __restrict__ loss,
                  float* __restrict__ lse) {
-  const int64_t row = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+  __shared__ float2 sh[32][33];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t row = (int64_t)blockIdx.x * 32 + lane;
+  const auto join = [](float2 a, float2 b) {
+    const float top = fmaxf(a.x, b.x);
+    return make_float2(top, a.y * exp2_approx((a.x - top) * kLog2eF) +
+                                b.y * exp2_approx((b.x - top) * kLog2eF));
+  };
+  const float2 none = make_float2(-1e30f, 0.0f);
   asm volatile("griddepcontrol.wait;" ::: "memory");   // for the tiles' statistics
-  if (row >= tokens) return;
-  float m = -1e30f, s = 0.0f;
-  for (int i = threadIdx.x & 31; i < strips; i += 32) {
-    const float2 p = __ldg(partial + (int64_t)i * tokens + row);
-    const float top = fmaxf(m, p.x);
-    s = s * exp2_approx((m - top) * kLog2eF) + p.y * exp2_approx((p.x - top) * kLog2eF);
-    m = top;
-  }
+  float2 s = none;
+  for (int i = warp; i < strips; i += 8 * 32) {
+    float2 p[8];
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    const float m2 = __shfl_xor_sync(0xFFFFFFFFu, m, o), s2 = __shfl_xor_sync(0xFFFFFFFFu, s, o);
-    const float top = fmaxf(m, m2);
-    s = s * exp2_approx((m - top) * kLog2eF) + s2 * exp2_approx((m2 - top) * kLog2eF);
-    m = top;
+    for (int k = 0; k < 8; ++k)
+      p[k] = i + 32 * k < strips && row < tokens
+                 ? __ldcg(partial + (int64_t)(i + 32 * k) * tokens + row) : none;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) s = join(s, p[k]);
   }
-  if ((threadIdx.x & 31) == 0) {
-    const float l = m + logf(s);
-    lse[row] = l;
-    const long long t = target[row];
-    loss[row] = t == ignore ? 0.0f
-              : t >= 0 && t < vocab ? l - target_logit[row] : __uint_as_float(0x7FC00000u);
+  sh[warp][lane] = s;
+  __syncthreads();
+  // warp w joins token w of the block
+  s = sh[lane][warp];
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1)
+    s = join(s, make_float2(__shfl_xor_sync(0xFFFFFFFFu, s.x, o),
+                            __shfl_xor_sync(0xFFFFFFFFu, s.y, o)));
+  const int64_t mine = (int64_t)blockIdx.x * 32 + warp;
+  if (lane == 0 && mine < tokens) {
+    const float l = s.x + logf(s.y);
+    lse[mine] = l;
+    const long long t = target[mine];
+    loss[mine] = t == ignore ? 0.0f
+               : t >= 0 && t < vocab ? l - target_logit[mine] : __uint_as_float(0x7FC00000u);
   }
 }
 
@@ -744,13 +764,21 @@ cudaError_t copy_rows(const void* src, int64_t rows, int64_t dim, int64_t pitch,
 
 // Tokens of one forward launch: bounds the scratch of the tiles' statistics.
 constexpr int64_t kForwardTokens = 65536;
-// Bytes of p aimed at for one piece of the vocabulary (two exist at a time).
-constexpr int64_t kPieceBytes = 32ll << 20;
+// Columns of a piece.  A launch is one piece's gradients and the next piece's
+// p, and dw's tiles, as long as the tokens are many, have to be a small part of
+// a pair's share of it: the share over the tile's length is 3 piece dim /
+// (pairs 65536), asked to be 6 (kShare columns of a 1-wide x per pair).  8192 x
+// 1024 x 50257: 2.30 ms with 32 MiB of p a piece, 1.60 with 6 times the tile.
+// Beyond that 128 MiB, up to 256: longer launches have fewer ends (2048 x 768:
+// 0.49 ms with 32 MiB, 0.36 with 128; 8192 x 2048: 3.14 either way).
+constexpr int64_t kPieceBytes = 128ll << 20, kMostPieceBytes = 256ll << 20, kShare = 131072;
 
-int64_t piece_columns(int64_t tokens, int64_t vocab) {
-  const int64_t fit = std::max(kPieceBytes / 2 / up(tokens, kTileM) / kTileN, (int64_t)1);
-  const int64_t pieces = (vocab + fit * kTileN - 1) / (fit * kTileN);
-  return up((vocab + pieces - 1) / pieces, kTileN);   // of even size
+int64_t piece_columns(const XentArgs& a, int sms) {
+  const int64_t row = 2 * up(a.rows, kTileM);
+  const int64_t want = std::max(kPieceBytes / row, kShare * (sms / 2) / a.dim);
+  const int64_t fit = std::max(std::min(want, kMostPieceBytes / row) / kTileN, (int64_t)1);
+  const int64_t pieces = (a.vocab + fit * kTileN - 1) / (fit * kTileN);
+  return up((a.vocab + pieces - 1) / pieces, kTileN);   // of even size
 }
 
 // Width of the tiles that cover dim columns: 128 or 256 (a CTA's half is read in
@@ -788,19 +816,15 @@ class Layout {
 };
 
 struct ForwardScratch {
-  size_t next = 0, x = 0, w = 0, partial = 0, logit = 0, bytes = 0;
-  int tile_n = kTileN;
+  size_t x = 0, w = 0, partial = 0, logit = 0, bytes = 0;
 };
-ForwardScratch forward_scratch(const XentArgs& a, int sms) {
+ForwardScratch forward_scratch(const XentArgs& a) {
   ForwardScratch s;
   Layout l;
   const int64_t pitch = up(a.dim, 8), tokens = std::min(a.rows, kForwardTokens);
-  // narrow tiles where wide ones would not fill two rounds of the SMs
-  if (up(tokens, kTileM) / kTileM * (up(a.vocab, kTileN) / kTileN) < sms) s.tile_n = 128;
-  s.next = l.take(4);
   if (!direct(a.x, a.dim)) s.x = l.take(a.rows * pitch * 2);
   if (!direct(a.w, a.dim)) s.w = l.take(a.vocab * pitch * 2);
-  s.partial = l.take(2 * (up(a.vocab, s.tile_n) / s.tile_n) * tokens * 8);
+  s.partial = l.take(2 * (up(a.vocab, kTileN) / kTileN) * tokens * 8);
   s.logit = l.take(tokens * 4);
   s.bytes = l.bytes();
   return s;
@@ -815,7 +839,7 @@ BackwardScratch backward_scratch(const XentArgs& a, int sms) {
   BackwardScratch s;
   Layout l;
   const int64_t pitch = up(a.dim, 8);
-  s.piece = piece_columns(a.rows, a.vocab);
+  s.piece = piece_columns(a, sms);
   s.pieces = (a.vocab + s.piece - 1) / s.piece;
   s.splits = dx_splits(a, s.piece, sms);
   s.next = l.take((s.pieces + 1) * 4);
@@ -830,12 +854,12 @@ BackwardScratch backward_scratch(const XentArgs& a, int sms) {
 
 }  // namespace
 
-size_t xent_forward_scratch(const XentArgs& a, int sms) { return forward_scratch(a, sms).bytes; }
+size_t xent_forward_scratch(const XentArgs& a) { return forward_scratch(a).bytes; }
 size_t xent_backward_scratch(const XentArgs& a, int sms) { return backward_scratch(a, sms).bytes; }
 
 cudaError_t launch_xent_forward(const XentArgs& a, char* scratch, int* error, int sms,
                                 cudaStream_t stream, LaunchMark mark) {
-  const ForwardScratch s = forward_scratch(a, sms);
+  const ForwardScratch s = forward_scratch(a);
   const bool bf16 = a.dtype == kBF16;
   const int64_t pitch = up(a.dim, 8);
   const char* x = static_cast<const char*>(a.x);
@@ -853,13 +877,12 @@ cudaError_t launch_xent_forward(const XentArgs& a, char* scratch, int* error, in
     const int64_t tokens = std::min(a.rows - t0, kForwardTokens);
     GemmArgs g = {};
     g.error = error;
-    g.next = reinterpret_cast<int*>(scratch + s.next);
     g.jobs = 1;
     GemmShape& j = g.job[0].shape;
     j.mode = kStats;
     j.tiles_m = (int)(up(tokens, kTileM) / kTileM);
-    j.tile_n = s.tile_n;
-    j.tiles_n = (int)(up(a.vocab, s.tile_n) / s.tile_n);
+    j.tile_n = kTileN;
+    j.tiles_n = (int)(up(a.vocab, kTileN) / kTileN);
     j.kblocks = j.kper = blocks_of(a.dim);
     j.splits = 1;
     g.out.tokens = tokens;
@@ -870,15 +893,14 @@ cudaError_t launch_xent_forward(const XentArgs& a, char* scratch, int* error, in
     g.out.partial = reinterpret_cast<float2*>(scratch + s.partial);
     g.out.target_logit = reinterpret_cast<float*>(scratch + s.logit);
     e = make_map(&g.job[0].a, bf16, x + t0 * pitch * 2, tokens, a.dim, pitch, kHalfM);
-    if (e == cudaSuccess) e = make_map(&g.job[0].b, bf16, w, a.vocab, a.dim, pitch, s.tile_n / 2);
-    if (e == cudaSuccess) e = cudaMemsetAsync(g.next, 0, 4, stream);
+    if (e == cudaSuccess) e = make_map(&g.job[0].b, bf16, w, a.vocab, a.dim, pitch, kTileN / 2);
     if (e != cudaSuccess) break;
     if (mark) mark(kXentLogitsK, 0, stream);
     e = launch_gemm(g, bf16, sms, stream);
     if (mark) mark(kXentLogitsK, 1, stream);
     if (e != cudaSuccess) break;
     if (mark) mark(kXentJoinK, 0, stream);
-    e = launch_early(xent_join_kernel, (unsigned)((tokens + 7) / 8), 256, 0, stream,
+    e = launch_early(xent_join_kernel, (unsigned)((tokens + 31) / 32), 1024, 0, stream,
                      (const float2*)g.out.partial, 2 * j.tiles_n, tokens, a.vocab, g.out.target,
                      g.out.ignore, (const float*)g.out.target_logit, a.loss + t0,
                      a.lse_out + t0);

@@ -92,7 +92,7 @@ struct XentArgs {
   void* dw;
 };
 
-size_t xent_forward_scratch(const XentArgs& a, int sms);
+size_t xent_forward_scratch(const XentArgs& a);
 size_t xent_backward_scratch(const XentArgs& a, int sms);
 // error: a device word set to 1 when a wait in a kernel ran out.
 cudaError_t launch_xent_forward(const XentArgs& a, char* scratch, int* error, int sms,

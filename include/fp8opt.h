@@ -682,9 +682,9 @@ FP8OPT_API int fp8_layer_norm_backward(
  * 0 and no part in dw, whatever its row of x holds.  rows = 0 gives dw 0.
  * Rows whose length is a multiple of 8 in 16-byte-aligned tensors are read in
  * place, others through a copy in scratch.  Scratch: the statistics of the
- * column tiles (forward); a copy of x, two pieces of p (32 MiB each, or 512
- * bytes a token where that is more) and dx in fp32, up to eight times when the
- * tokens are few (backward).  dim and vocab >= 1; each tensor below 2^31 rows and columns.
+ * column tiles (forward); a copy of x, two pieces of p (128 to 256 MiB each, less
+ * for a small vocabulary, or 512 bytes a token where that is more) and dx in
+ * fp32, up to eight times when the tokens are few (backward).  dim and vocab >= 1; each tensor below 2^31 rows and columns.
  *
  * The kernels wait for their copies and products with a limit of about two
  * seconds; should one run out (it does not on a working device), the next

@@ -18,10 +18,12 @@ __device__ __forceinline__ int ln_col(int v, int e, int t) {
 }
 
 // Whether that element lies in the row (for VEC = 8 the whole vector does or
-// does not).
-template <int TPR, int VEC>
+// does not).  FULL: the row fills its threads' registers, and every element
+// does: the tests and selections were a tenth of the kernels' instructions,
+// which is what bounds them beside HBM.
+template <int TPR, int VEC, bool FULL>
 __device__ __forceinline__ bool ln_in(int v, int e, int t, int cols) {
-  return ln_col<TPR, VEC>(v, VEC == 8 ? 0 : e, t) < cols;
+  return FULL || ln_col<TPR, VEC>(v, VEC == 8 ? 0 : e, t) < cols;
 }
 
 // Eight elements of vector v as raw words (VEC 8) or widened values (VEC 1);
@@ -196,11 +198,16 @@ __device__ __forceinline__ void row_barrier(int row_slot) {
   asm volatile("bar.sync %0, %1;" ::"r"(row_slot + 1), "n"(TPR) : "memory");
 }
 
-template <int TPR>
-__device__ __forceinline__ float2 row_sum2(float a, float b, RowSums<TPR>& s, int& turn,
-                                           int row_slot) {
+// A second sum (TWO), or a maximum beside the sum (MAX: of non-negative
+// values, by their bits).
+enum RowPair { kOne, kTwo, kMax };
+
+template <RowPair KIND, int TPR>
+__device__ __forceinline__ float2 row_reduce(float a, float b, RowSums<TPR>& s, int& turn,
+                                             int row_slot) {
   a = warp_sum(a);
-  b = warp_sum(b);
+  if (KIND == kTwo) b = warp_sum(b);
+  if (KIND == kMax) b = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(b)));
   if constexpr (TPR > 32) {
     const int t = threadIdx.x % TPR;
     if ((t & 31) == 0) s.w[turn][t >> 5] = make_float2(a, b);
@@ -208,8 +215,10 @@ __device__ __forceinline__ float2 row_sum2(float a, float b, RowSums<TPR>& s, in
     a = b = 0.0f;
 #pragma unroll
     for (int i = 0; i < TPR / 32; ++i) {
-      a += s.w[turn][i].x;
-      b += s.w[turn][i].y;
+      const float2 w = s.w[turn][i];
+      a += w.x;
+      if (KIND == kTwo) b += w.y;
+      if (KIND == kMax) b = fmaxf(b, w.y);
     }
     turn ^= 1;
   }

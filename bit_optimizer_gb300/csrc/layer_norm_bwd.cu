@@ -34,13 +34,17 @@ constexpr int kRingBytes = kStages<DT> * VPT * NT * (kVecBytes<DT> + kSavedBytes
 
 // xhat of eight elements: (x - sub) * mul, with sub = mean and mul = rstd, or
 // the code's value * mul with mul = 1 / scale.
+template <bool FP8>
 __device__ __forceinline__ void ln_xhat(const float* x, float sub, float mul, float2* out) {
 #pragma unroll
-  for (int j = 0; j < 4; ++j)
-    out[j] = mul2(add2(make_float2(x[2 * j], x[2 * j + 1]), splat2(-sub)), splat2(mul));
+  for (int j = 0; j < 4; ++j) {
+    out[j] = make_float2(x[2 * j], x[2 * j + 1]);
+    if (!FP8) out[j] = add2(out[j], splat2(-sub));
+    out[j] = mul2(out[j], splat2(mul));
+  }
 }
 
-template <int DT, int VEC, int TPR, int VPT, int NT, bool FP8>
+template <int DT, int VEC, int TPR, int VPT, int NT, bool FP8, bool FULL>
 __global__ void __launch_bounds__(NT, kBwdThreads / NT)
 ln_backward_kernel(const LnBackward a, float* __restrict__ partial) {
   constexpr int RPC = NT / TPR, ST = kStages<DT>, Q = DT == kF32 ? 2 : 1;
@@ -71,7 +75,7 @@ ln_backward_kernel(const LnBackward a, float* __restrict__ partial) {
 #pragma unroll
       for (int v = 0; v < VPT; ++v) {
         const int c = ln_col<TPR, 8>(v, 0, t);
-        if (c >= cols) continue;
+        if (!FULL && c >= cols) continue;
 #pragma unroll
         for (int q = 0; q < Q; ++q) {
           copy_async<16>(at_dy(stage, v, q), static_cast<const char*>(a.dy) + (at + c) * es + 16 * q);
@@ -102,7 +106,7 @@ ln_backward_kernel(const LnBackward a, float* __restrict__ partial) {
     for (int i = 0; i < ST; ++i)   // what lies past the row's end stays zero
 #pragma unroll
       for (int v = 0; v < VPT; ++v)
-        if (ln_col<TPR, 8>(v, 0, t) >= cols) {
+        if (!ln_in<TPR, 8, FULL>(v, 0, t, cols)) {
 #pragma unroll
           for (int q = 0; q < Q; ++q) {
             *at_dy(i, v, q) = make_uint4(0, 0, 0, 0);
@@ -158,14 +162,14 @@ ln_backward_kernel(const LnBackward a, float* __restrict__ partial) {
           }
         }
       }
-      ln_xhat(e, sub, mul, x + 4 * v);
+      ln_xhat<FP8>(e, sub, mul, x + 4 * v);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const int i = 4 * v + j;
         g[i] = make_float2(d[2 * j], d[2 * j + 1]);
         // past the row's end dy is 0, and xhat must not be a NaN there
-        if (!ln_in<TPR, VEC>(v, 2 * j, t, cols)) x[i].x = 0.0f;
-        if (!ln_in<TPR, VEC>(v, 2 * j + 1, t, cols)) x[i].y = 0.0f;
+        if (!ln_in<TPR, VEC, FULL>(v, 2 * j, t, cols)) x[i].x = 0.0f;
+        if (!ln_in<TPR, VEC, FULL>(v, 2 * j + 1, t, cols)) x[i].y = 0.0f;
         aw[i] = fma2(g[i], x[i], aw[i]);
         ab[i] = add2(ab[i], g[i]);
         g[i] = mul2(g[i], w[i]);
@@ -174,7 +178,7 @@ ln_backward_kernel(const LnBackward a, float* __restrict__ partial) {
       }
     }
     if constexpr (VEC == 8) fetch(stage == 0 ? ST - 1 : stage - 1, r + (ST - 1) * step);
-    const float2 s = row_sum2<TPR>(s1.x + s1.y, s2.x + s2.y, sums[slot], turn, slot);
+    const float2 s = row_reduce<kTwo, TPR>(s1.x + s1.y, s2.x + s2.y, sums[slot], turn, slot);
     const float2 m1 = splat2(-s.x * inv_c), m2 = splat2(-s.y * inv_c), k = splat2(rstd);
 #pragma unroll
     for (int v = 0; v < VPT; ++v) {
@@ -334,10 +338,10 @@ unsigned grid_of(const LnBackward& a, int sms) {
   return (unsigned)(need < sms ? need : sms);
 }
 
-template <int DT, int VEC, int TPR, int VPT, bool FP8>
+template <int DT, int VEC, int TPR, int VPT, bool FP8, bool FULL>
 cudaError_t go_form(const LnBackward& a, float* partial, unsigned grid, cudaStream_t stream) {
   constexpr int NT = kBwdThreads, RPC = NT / TPR;
-  auto kernel = ln_backward_kernel<DT, VEC, TPR, VPT, NT, FP8>;
+  auto kernel = ln_backward_kernel<DT, VEC, TPR, VPT, NT, FP8, FULL>;
   const int ring = VEC == 8 ? kRingBytes<DT, VPT, NT, FP8> : 0;
   const int merge = RPC > 1 ? RPC * 2 * (int)sizeof(float) * (int)a.cols : 0;
   const int smem = ring > merge ? ring : merge;
@@ -352,8 +356,13 @@ cudaError_t go_form(const LnBackward& a, float* partial, unsigned grid, cudaStre
 
 template <int DT, int VEC, int TPR, int VPT>
 cudaError_t go(const LnBackward& a, float* p, unsigned grid, cudaStream_t s) {
-  return a.codes != nullptr ? go_form<DT, VEC, TPR, VPT, true>(a, p, grid, s)
-                            : go_form<DT, VEC, TPR, VPT, false>(a, p, grid, s);
+  if constexpr (VEC == 8) {
+    if (a.cols == TPR * VPT * 8)
+      return a.codes != nullptr ? go_form<DT, VEC, TPR, VPT, true, true>(a, p, grid, s)
+                                : go_form<DT, VEC, TPR, VPT, false, true>(a, p, grid, s);
+  }
+  return a.codes != nullptr ? go_form<DT, VEC, TPR, VPT, true, false>(a, p, grid, s)
+                            : go_form<DT, VEC, TPR, VPT, false, false>(a, p, grid, s);
 }
 
 template <int DT, int VEC>

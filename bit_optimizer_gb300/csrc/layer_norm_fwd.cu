@@ -12,8 +12,8 @@ namespace fp8opt {
 
 namespace {
 
-// Threads of a CTA, and CTAs of an SM (64 registers a thread).
-constexpr int kFwdThreads = 512, kFwdCtas = 2;
+// Threads of a CTA, one CTA to an SM (128 registers a thread).
+constexpr int kFwdThreads = 512, kFwdCtas = 1;
 
 // Rows in flight of a thread's ring, and the ring's bytes.
 template <int DT>
@@ -35,7 +35,7 @@ __device__ __forceinline__ float tree_sum(const float2* x) {
   return s[0].x + s[0].y;
 }
 
-template <int DT, int VEC, int TPR, int VPT, bool FP8>
+template <int DT, int VEC, int TPR, int VPT, bool FP8, bool FULL>
 __global__ void __launch_bounds__(kFwdThreads, kFwdCtas)
 ln_forward_kernel(const LnForward a) {
   constexpr int NT = kFwdThreads, RPC = NT / TPR, Q = DT == kF32 ? 2 : 1, ST = kStages<DT>;
@@ -62,7 +62,7 @@ ln_forward_kernel(const LnForward a) {
 #pragma unroll
       for (int v = 0; v < VPT; ++v) {
         const int c = ln_col<TPR, 8>(v, 0, t);
-        if (c < cols)
+        if (FULL || c < cols)
 #pragma unroll
           for (int q = 0; q < Q; ++q) copy_async<16>(at(stage, v, q), p + c * es + 16 * q);
       }
@@ -76,7 +76,7 @@ ln_forward_kernel(const LnForward a) {
     for (int i = 0; i < ST; ++i)   // what lies past the row's end stays zero
 #pragma unroll
       for (int v = 0; v < VPT; ++v)
-        if (ln_col<TPR, 8>(v, 0, t) >= cols)
+        if (!ln_in<TPR, 8, FULL>(v, 0, t, cols))
 #pragma unroll
           for (int q = 0; q < Q; ++q) *at(i, v, q) = make_uint4(0, 0, 0, 0);
   }
@@ -128,38 +128,20 @@ ln_forward_kernel(const LnForward a) {
     }
     // (what lies past the row's end is zero in both)
     const float s = tree_sum<4 * VPT>(x);
-    const float mean = row_sum2<TPR>(s, 0.0f, sums[slot], turn, slot).x / (float)cols;
-    float2 sq[4 * VPT];
-    uint32_t m = 0;
+    const float mean = row_reduce<kOne, TPR>(s, 0.0f, sums[slot], turn, slot).x / (float)cols;
+    float2 sq[4] = {splat2(0.0f), splat2(0.0f), splat2(0.0f), splat2(0.0f)};
+    float m = 0.0f;   // (a NaN passes it by, and is found in the sum of squares)
 #pragma unroll
     for (int i = 0; i < 4 * VPT; ++i) {
       x[i] = add2(x[i], splat2(-mean));
-      if (!ln_in<TPR, VEC>(i / 4, 2 * (i % 4), t, cols)) x[i].x = 0.0f;
-      if (!ln_in<TPR, VEC>(i / 4, 2 * (i % 4) + 1, t, cols)) x[i].y = 0.0f;
-      sq[i] = mul2(x[i], x[i]);
-      if (FP8) m = max(m, max(abs_bits(x[i].x), abs_bits(x[i].y)));
+      if (!ln_in<TPR, VEC, FULL>(i / 4, 2 * (i % 4), t, cols)) x[i].x = 0.0f;
+      if (!ln_in<TPR, VEC, FULL>(i / 4, 2 * (i % 4) + 1, t, cols)) x[i].y = 0.0f;
+      sq[i % 4] = fma2(x[i], x[i], sq[i % 4]);
+      if (FP8) m = fmaxf(fmaxf(m, fabsf(x[i].x)), fabsf(x[i].y));
     }
-    float q = tree_sum<4 * VPT>(sq);
-    if constexpr (FP8) {
-      // the row's max |x - mean| beside its sum of squares
-      m = __reduce_max_sync(0xFFFFFFFFu, m);
-      q = warp_sum(q);
-      if constexpr (TPR > 32) {
-        if ((t & 31) == 0) sums[slot].w[turn][t >> 5] = make_float2(q, __uint_as_float(m));
-        row_barrier<TPR>(slot);
-        q = 0.0f;
-        m = 0;
-#pragma unroll
-        for (int i = 0; i < TPR / 32; ++i) {
-          const float2 w = sums[slot].w[turn][i];
-          q += w.x;
-          m = max(m, __float_as_uint(w.y));
-        }
-        turn ^= 1;
-      }
-    } else {
-      q = row_sum2<TPR>(q, 0.0f, sums[slot], turn, slot).x;
-    }
+    const float2 qm = row_reduce<FP8 ? kMax : kOne, TPR>(tree_sum<4>(sq), m, sums[slot], turn,
+                                                         slot);
+    const float q = qm.x;
     const float rstd = __frsqrt_rn(q / (float)cols + a.eps);
     if (t == 0) {
       a.rstd[r] = rstd;
@@ -169,7 +151,7 @@ ln_forward_kernel(const LnForward a) {
     bool finite = true;
     if constexpr (FP8) {
       // |x - mean| * rstd rounds monotonically, so this is max |xhat|
-      const uint32_t amax = abs_bits(__uint_as_float(m) * rstd);
+      const uint32_t amax = abs_bits(qm.y * rstd);
       scale = scale_from_amax_bits(amax, 448.0f);
       finite = amax < 0x7F800000u;
       if (t == 0) a.scales[r] = scale;
@@ -213,7 +195,7 @@ ln_forward_kernel(const LnForward a) {
         uint8_t* codes = a.codes + (size_t)r * a.cols;
         if constexpr (VEC == 8) {
           const int c = ln_col<TPR, 8>(v, 0, t);
-          if (c < cols)
+          if (FULL || c < cols)
             __stcs(reinterpret_cast<uint2*>(codes + c),
                    finite ? enc8<kE4M3, false>(z) : enc8<kE4M3, true>(z));
         } else {
@@ -281,10 +263,10 @@ ln_forward_long_kernel(const LnForward a) {
   }
 }
 
-template <int DT, int VEC, int TPR, int VPT, bool FP8>
+template <int DT, int VEC, int TPR, int VPT, bool FP8, bool FULL>
 cudaError_t go_form(const LnForward& a, int sms, cudaStream_t stream) {
   constexpr int RPC = kFwdThreads / TPR;
-  auto kernel = ln_forward_kernel<DT, VEC, TPR, VPT, FP8>;
+  auto kernel = ln_forward_kernel<DT, VEC, TPR, VPT, FP8, FULL>;
   const int smem = (VEC == 8 ? kRingBytes<DT, VPT> : 0) + 2 * (int)sizeof(float) * TPR * 8 * VPT;
   if (smem > 48 * 1024) {
     const cudaError_t e =
@@ -298,18 +280,26 @@ cudaError_t go_form(const LnForward& a, int sms, cudaStream_t stream) {
 
 template <int DT, int VEC, int TPR, int VPT>
 cudaError_t go(const LnForward& a, int sms, cudaStream_t stream) {
-  return a.codes != nullptr ? go_form<DT, VEC, TPR, VPT, true>(a, sms, stream)
-                            : go_form<DT, VEC, TPR, VPT, false>(a, sms, stream);
+  if constexpr (VEC == 8) {
+    if (a.cols == TPR * VPT * 8)
+      return a.codes != nullptr ? go_form<DT, VEC, TPR, VPT, true, true>(a, sms, stream)
+                                : go_form<DT, VEC, TPR, VPT, false, true>(a, sms, stream);
+  }
+  return a.codes != nullptr ? go_form<DT, VEC, TPR, VPT, true, false>(a, sms, stream)
+                            : go_form<DT, VEC, TPR, VPT, false, false>(a, sms, stream);
 }
 
+// As many elements a thread as its registers take: the reductions, which cost
+// the same whatever a thread holds, then weigh least (16384 x 4096 with codes:
+// 61.7 us with 16 elements a thread, see the table of figures for 32).
 template <int DT, int VEC>
 cudaError_t by_cols(const LnForward& a, int sms, cudaStream_t stream) {
   if (a.cols <= 256) return go<DT, VEC, 32, 1>(a, sms, stream);
   if (a.cols <= 512) return go<DT, VEC, 32, 2>(a, sms, stream);
-  if (a.cols <= 1024) return go<DT, VEC, 64, 2>(a, sms, stream);
-  if (a.cols <= 2048) return go<DT, VEC, 128, 2>(a, sms, stream);
-  if (a.cols <= 4096) return go<DT, VEC, 256, 2>(a, sms, stream);
-  return go<DT, VEC, 512, 2>(a, sms, stream);
+  if (a.cols <= 1024) return go<DT, VEC, 32, 4>(a, sms, stream);
+  if (a.cols <= 2048) return go<DT, VEC, 64, 4>(a, sms, stream);
+  if (a.cols <= 4096) return go<DT, VEC, 128, 4>(a, sms, stream);
+  return go<DT, VEC, 256, 4>(a, sms, stream);
 }
 
 template <int DT>

@@ -42,7 +42,10 @@ constexpr int kStageB = kTileN / 2 * kBlockK * 2;
 // Eight epilogue warps (two for each quarter of the lanes, each with half of the
 // columns), a producer, an MMA and a scheduler warp.
 constexpr int kEpilogueWarps = 8, kGemmThreads = 32 * (kEpilogueWarps + 3);
-constexpr int kGemmSmem = 1024 + kGemmStages * (kStageA + kStageB);
+constexpr int kTurnBytes = 4096;   // of an epilogue warp
+constexpr int kGemmSmem =
+    1024 + kGemmStages * (kStageA + kStageB) + kEpilogueWarps * kTurnBytes;
+
 constexpr float kLog2eF = 1.4426950408889634f, kLn2F = 0.69314718055994531f;
 
 __device__ __forceinline__ float exp2_approx(float x) {
@@ -114,21 +117,76 @@ __device__ __forceinline__ uint32_t pack16(float a, float b) {
   return pack2<BF16 ? kBF16 : kF16>(a, b);
 }
 
-// Stores n <= 32 results of one row as 16-bit values.
+// An epilogue warp's 4 KB of shared memory: 32 rows of 128 bytes, in which its
+// lanes, a row each, turn over to eight lanes a row, so that global memory is
+// read and written in whole lines (straight from the lanes, 16 bytes of 32
+// rows at a time, the stores of p took twice the time of the product).  The
+// 16-byte words of a row are permuted so that both ways are free of conflicts.
+struct Turn {
+  uint4 w[32][8];
+  __device__ __forceinline__ uint4& at(int row, int word) { return w[row][word ^ (row & 7)]; }
+};
+static_assert(sizeof(Turn) == kTurnBytes, "");
+
+// 64 results of each lane's row as 16-bit values, at out + row * pitch; rows
+// below `rows`, columns below `cols`.
 template <bool BF16>
-__device__ __forceinline__ void store_row16(uint16_t* p, const float (&v)[32], int n) {
-  if (n >= 32 && (reinterpret_cast<uintptr_t>(p) & 15u) == 0) {
+__device__ __forceinline__ void store_rows16(Turn& turn, uint16_t* out, int64_t pitch, int rows,
+                                             int cols, const float (&v)[64]) {
+  const int lane = threadIdx.x & 31;
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-      reinterpret_cast<uint4*>(p)[j] =
-          make_uint4(pack16<BF16>(v[8 * j], v[8 * j + 1]), pack16<BF16>(v[8 * j + 2], v[8 * j + 3]),
-                     pack16<BF16>(v[8 * j + 4], v[8 * j + 5]),
-                     pack16<BF16>(v[8 * j + 6], v[8 * j + 7]));
-  } else {
+  for (int j = 0; j < 8; ++j)
+    turn.at(lane, j) =
+        make_uint4(pack16<BF16>(v[8 * j], v[8 * j + 1]), pack16<BF16>(v[8 * j + 2], v[8 * j + 3]),
+                   pack16<BF16>(v[8 * j + 4], v[8 * j + 5]),
+                   pack16<BF16>(v[8 * j + 6], v[8 * j + 7]));
+  __syncwarp();
+  const int word = lane & 7, c = 8 * word;
 #pragma unroll
-    for (int j = 0; j < 32; ++j)
-      if (j < n) p[j] = (uint16_t)pack16<BF16>(v[j], 0.0f);
+  for (int i = 0; i < 8; ++i) {
+    const int row = 4 * i + (lane >> 3);
+    const uint4 w = turn.at(row, word);
+    uint16_t* p = out + row * pitch + c;
+    if (row >= rows || c >= cols) continue;
+    if (c + 8 <= cols && (reinterpret_cast<uintptr_t>(p) & 15u) == 0) {
+      *reinterpret_cast<uint4*>(p) = w;
+    } else {
+      const uint32_t e[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (c + k < cols) p[k] = (uint16_t)(e[k / 2] >> (16 * (k & 1)));
+    }
   }
+  __syncwarp();
+}
+
+// Adds (or, `first`, stores) 32 columns of each lane's row to out + row *
+// pitch, fp32 at a 16-byte pitch; rows below `rows`.
+__device__ __forceinline__ void add_rows32(Turn& turn, float* out, int64_t pitch, int rows,
+                                           bool first, const uint32_t (&r)[32]) {
+  const int lane = threadIdx.x & 31, word = lane & 7;
+  float4 s[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int row = 4 * i + (lane >> 3);
+    s[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (!first && row < rows)
+      s[i] = *reinterpret_cast<const float4*>(out + row * pitch + 4 * word);
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    turn.at(lane, j) = make_uint4(r[4 * j], r[4 * j + 1], r[4 * j + 2], r[4 * j + 3]);
+  __syncwarp();
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int row = 4 * i + (lane >> 3);
+    const uint4 w = turn.at(row, word);
+    if (row < rows)
+      *reinterpret_cast<float4*>(out + row * pitch + 4 * word) =
+          make_float4(s[i].x + __uint_as_float(w.x), s[i].y + __uint_as_float(w.y),
+                      s[i].z + __uint_as_float(w.z), s[i].w + __uint_as_float(w.w));
+  }
+  __syncwarp();
 }
 
 // exp(a + shift) and exp(b + shift) of two accumulators.  The difference is
@@ -177,7 +235,7 @@ __device__ __forceinline__ void stats_strip(const GemmOut& o, const Strip& t, co
                       ? (int)(target - t.c0) : -1;
   const int valid = (int)min((int64_t)t.cols, o.vocab - t.c0);   // may be <= 0
   float top = -1e30f, sum = 0.0f, at_target = 0.0f;
-  tmem_columns(t.tmem, t.cols, [&](int c, uint32_t (&r)[32]) {
+  const auto add = [&](int c, uint32_t (&r)[32]) {
     if (c + 32 > valid) {
 #pragma unroll
       for (int j = 0; j < 32; ++j)
@@ -199,6 +257,10 @@ __device__ __forceinline__ void stats_strip(const GemmOut& o, const Strip& t, co
     for (int j = 0; j < 32; j += 2) s[j / 2 & 1] = add2(s[j / 2 & 1], exp_pair(r[j], r[j + 1], -top));
     s[0] = add2(s[0], s[1]);
     sum = s[0].x + s[0].y;
+  };
+  tmem_columns(t.tmem, t.cols, [&](int c, uint32_t (&r)[32], uint32_t (&q)[32]) {
+    add(c, r);
+    add(c + 32, q);
   });
   if (live) {
     o.partial[(int64_t)t.index * o.tokens + t.row] = make_float2(top, sum);
@@ -209,7 +271,7 @@ __device__ __forceinline__ void stats_strip(const GemmOut& o, const Strip& t, co
 // The strip's logits turned into p.
 template <bool BF16>
 __device__ __forceinline__ void probs_strip(const GemmShape& g, const GemmOut& o,
-                                            const Strip& t, const RowIn& in) {
+                                            const Strip& t, const RowIn& in, Turn& turn) {
   const bool live = t.row < o.tokens;
   float shift = 0.0f, k = 0.0f;
   int rel = -1;
@@ -222,69 +284,67 @@ __device__ __forceinline__ void probs_strip(const GemmShape& g, const GemmOut& o
   }
   const bool zero = k == 0.0f;      // an ignored token, whatever its logits are
   const int valid = (int)min((int64_t)t.cols, o.vocab - g.v0 - t.c0);
-  uint16_t* const out = g.probs + t.row * o.piece + t.c0;
-  tmem_columns(t.tmem, t.cols, [&](int c, uint32_t (&r)[32]) {
-    float v[32];
+  const int64_t row0 = t.row - (threadIdx.x & 31);
+  uint16_t* const out = g.probs + row0 * o.piece + t.c0;
+  const int rows = (int)min((int64_t)32, o.tokens - row0);
+  tmem_columns(t.tmem, t.cols, [&](int c, uint32_t (&r)[32], uint32_t (&q)[32]) {
+    float v[64];
 #pragma unroll
     for (int j = 0; j < 32; j += 2) {
-      const float2 e = exp_pair(r[j], r[j + 1], shift);
+      const float2 e = exp_pair(r[j], r[j + 1], shift), f = exp_pair(q[j], q[j + 1], shift);
       v[j] = e.x;
       v[j + 1] = e.y;
+      v[32 + j] = f.x;
+      v[33 + j] = f.y;
     }
-    if (__any_sync(0xFFFFFFFFu, rel >= c && rel < c + 32)) {
+    if (__any_sync(0xFFFFFFFFu, rel >= c && rel < c + 64)) {
 #pragma unroll
-      for (int j = 0; j < 32; ++j)
+      for (int j = 0; j < 64; ++j)
         if (rel == c + j) v[j] -= 1.0f;
     }
 #pragma unroll
-    for (int j = 0; j < 32; ++j) v[j] = zero ? 0.0f : v[j] * k;
-    if (c + 32 > valid) {           // columns past the vocabulary's end are 0
+    for (int j = 0; j < 64; ++j) v[j] = zero ? 0.0f : v[j] * k;
+    if (c + 64 > valid) {           // columns past the vocabulary's end are 0
 #pragma unroll
-      for (int j = 0; j < 32; ++j)
+      for (int j = 0; j < 64; ++j)
         if (c + j >= valid) v[j] = 0.0f;
     }
-    if (live) store_row16<BF16>(out + c, v, 32);
+    store_rows16<BF16>(turn, out + c, o.piece, rows, 64, v);
   });
 }
 
 // This piece's part of dx, added to the earlier ones'.  `none`: the split has
 // no k in this piece, and nothing was accumulated.
 __device__ __forceinline__ void dx_strip(const GemmShape& g, const GemmOut& o, const Strip& t,
-                                         int split, bool none) {
-  const bool live = t.row < o.tokens;
-  float* const sum = o.dx_sum + (split * o.tokens + t.row) * o.dim_pitch + t.c0;
-  tmem_columns(t.tmem, t.cols, [&](int c, uint32_t (&r)[32]) {
-    if (!live) return;
-    float4* const p = reinterpret_cast<float4*>(sum + c);
-    float4 s[8];
+                                         int split, bool none, Turn& turn) {
+  const int64_t row0 = t.row - (threadIdx.x & 31);
+  float* const sum = o.dx_sum + (split * o.tokens + row0) * o.dim_pitch + t.c0;
+  const int rows = (int)min((int64_t)32, o.tokens - row0);
+  tmem_columns(t.tmem, t.cols, [&](int c, uint32_t (&r)[32], uint32_t (&q)[32]) {
+    if (none) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-      s[j] = g.first ? make_float4(0.0f, 0.0f, 0.0f, 0.0f) : p[j];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      if (!none) {
-        s[j].x += __uint_as_float(r[4 * j]);
-        s[j].y += __uint_as_float(r[4 * j + 1]);
-        s[j].z += __uint_as_float(r[4 * j + 2]);
-        s[j].w += __uint_as_float(r[4 * j + 3]);
-      }
-      p[j] = s[j];
+      for (int j = 0; j < 32; ++j) r[j] = q[j] = 0;
     }
+    add_rows32(turn, sum + c, o.dim_pitch, rows, g.first, r);
+    add_rows32(turn, sum + c + 32, o.dim_pitch, rows, g.first, q);
   });
 }
 
 template <bool BF16>
 __device__ __forceinline__ void dw_strip(const GemmShape& g, const GemmOut& o, const Strip& t,
-                                         const RowIn& in) {
-  const int64_t v0 = g.v0 + t.row;
-  const float back = in.top;
-  const int valid = (int)min((int64_t)t.cols, o.dim - t.c0);
+                                         const RowIn& in, Turn& turn) {
+  const int64_t v0 = g.v0 + t.row - (threadIdx.x & 31);
+  const int cols = (int)min((int64_t)t.cols, o.dim - t.c0);
+  const int rows = (int)min((int64_t)32, o.vocab - v0);
   uint16_t* const out = static_cast<uint16_t*>(o.dw) + v0 * o.dim + t.c0;
-  tmem_columns(t.tmem, t.cols, [&](int c, uint32_t (&r)[32]) {
-    float v[32];
+  tmem_columns(t.tmem, t.cols, [&](int c, uint32_t (&r)[32], uint32_t (&q)[32]) {
+    float v[64];
 #pragma unroll
-    for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]) * (1.0f / kProbScale) * back;
-    if (v0 < o.vocab && c < valid) store_row16<BF16>(out + c, v, valid - c);
+    for (int j = 0; j < 32; ++j) {
+      v[j] = __uint_as_float(r[j]) * (1.0f / kProbScale) * in.top;
+      v[32 + j] = __uint_as_float(q[j]) * (1.0f / kProbScale) * in.top;
+    }
+    store_rows16<BF16>(turn, out + c, o.dim, rows, cols - c, v);
   });
 }
 
@@ -529,6 +589,7 @@ gemm_kernel(const __grid_constant__ GemmArgs args) {
     }
   } else {
     TileReader<true> reader;
+    Turn& turn = reinterpret_cast<Turn*>(stages + kGemmStages * (kStageA + kStageB))[warp];
     int buf = 0, phase = 0;
     for (;;) {
       const Tile* next = reader.next(bar);
@@ -546,9 +607,9 @@ gemm_kernel(const __grid_constant__ GemmArgs args) {
       if (!ok) break;
       tcgen_fence_after();
       if (g.mode == kStats) stats_strip(args.out, strip, in);
-      else if (g.mode == kProbs) probs_strip<BF16>(g, args.out, strip, in);
-      else if (g.mode == kDx) dx_strip(g, args.out, strip, t.split, (t.work & 0xFFFFFFu) == 0);
-      else dw_strip<BF16>(g, args.out, strip, in);
+      else if (g.mode == kProbs) probs_strip<BF16>(g, args.out, strip, in, turn);
+      else if (g.mode == kDx) dx_strip(g, args.out, strip, t.split, (t.work & 0xFFFFFFu) == 0, turn);
+      else dw_strip<BF16>(g, args.out, strip, in, turn);
       tcgen_fence_before();
       __syncwarp();
       // (the accumulators have been read: nothing else needs an order here)

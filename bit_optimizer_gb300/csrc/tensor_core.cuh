@@ -168,8 +168,8 @@ __device__ __forceinline__ void tmem_wait(uint32_t (&r)[32]) {
                  "+r"(r[30]), "+r"(r[31])::"memory");
 }
 
-// f(c, r) for the columns [c, c + 32) of [0, n), n a multiple of 64.  The
-// loads and the waits for them stay in one block: a load writes its registers
+// f(c, r, q) for the columns [c, c + 32) (r) and [c + 32, c + 64) (q) of [0, n),
+// n a multiple of 64.  The loads and the waits for them stay in one block: a load writes its registers
 // later than the compiler knows, so none may live across a loop's end.  The
 // whole warp calls it.
 template <class F>
@@ -181,8 +181,7 @@ __device__ __forceinline__ void tmem_columns(uint32_t addr, int n, F f) {
     tmem_load32(addr + c + 32, q);
     tmem_wait(r);
     tmem_wait(q);
-    f(c, r);
-    f(c + 32, q);
+    f(c, r, q);
     __syncwarp();
   }
 }

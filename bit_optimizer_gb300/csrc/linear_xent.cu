@@ -674,12 +674,28 @@ xent_join_kernel(const float2* __restrict__ partial, int strips, int64_t tokens,
 }
 
 // Rows of a matrix at a 16-byte pitch, those of ignored tokens zero (target
-// NULL: none is).
+// NULL: none is).  With `top`, one more CTA finds the largest finite |dloss| of
+// the tokens that count (one that is not finite spoils its own token's dx, not
+// the others').
 __global__ void __launch_bounds__(256)
 xent_copy_kernel(const uint16_t* __restrict__ src, int64_t rows, int64_t dim, int64_t pitch,
                  const long long* __restrict__ target, long long ignore,
-                 uint16_t* __restrict__ dst, bool vec) {
-  for (int64_t r = blockIdx.x; r < rows; r += gridDim.x) {
+                 uint16_t* __restrict__ dst, bool vec, const float* __restrict__ dloss,
+                 float* __restrict__ top) {
+  const unsigned copying = gridDim.x - (top != nullptr ? 1 : 0);
+  if (blockIdx.x == copying) {
+    __shared__ uint32_t sh[8];
+    uint32_t m = 0;
+#pragma unroll 8
+    for (int64_t i = threadIdx.x; i < rows; i += 256) {
+      const float d = dloss[i];          // (loaded whatever the target: no wait between)
+      if (target[i] != ignore && !nonfinite(d)) m = max(m, abs_bits(d));
+    }
+    m = block_max_u32<256>(m, sh);
+    if (threadIdx.x == 0) *top = __uint_as_float(m);
+    return;
+  }
+  for (int64_t r = blockIdx.x; r < rows; r += copying) {
     const bool zero = target != nullptr && target[r] == ignore;
     if (vec) {
       const uint4* s = reinterpret_cast<const uint4*>(src + r * dim);
@@ -693,21 +709,9 @@ xent_copy_kernel(const uint16_t* __restrict__ src, int64_t rows, int64_t dim, in
   }
 }
 
-// The largest finite |dloss| of the tokens that count (one that is not finite
-// spoils its own token's dx, not the others').
-__global__ void __launch_bounds__(1024)
-xent_top_kernel(const float* __restrict__ dloss, const long long* __restrict__ target,
-                long long ignore, int64_t tokens, float* __restrict__ top) {
-  __shared__ uint32_t sh[32];
-  uint32_t m = 0;
-  for (int64_t i = threadIdx.x; i < tokens; i += 1024)
-    if (target[i] != ignore && !nonfinite(dloss[i])) m = max(m, abs_bits(dloss[i]));
-  m = block_max_u32<1024>(m, sh);
-  if (threadIdx.x == 0) *top = __uint_as_float(m);
-}
-
 // dx from its fp32 parts: the splits added in order, scaled back, rounded; 0
-// for an ignored token.
+// for an ignored token.  Eight columns a thread (the parts' pitch is a multiple
+// of 128).
 template <bool BF16>
 __global__ void __launch_bounds__(256)
 xent_dx_kernel(const float* __restrict__ sum, int splits, int64_t tokens, int64_t dim,
@@ -715,26 +719,32 @@ xent_dx_kernel(const float* __restrict__ sum, int splits, int64_t tokens, int64_
                const float* __restrict__ top, uint16_t* __restrict__ dx) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const float back = *top;
-  for (int64_t r = blockIdx.x; r < tokens; r += gridDim.x) {
+  const int64_t groups = (dim + 7) / 8;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < tokens * groups;
+       i += (int64_t)gridDim.x * 256) {
+    const int64_t r = i / groups, c = (i - r * groups) * 8;
+    float4 v[2] = {make_float4(0, 0, 0, 0), make_float4(0, 0, 0, 0)};
+    for (int s = 0; s < splits; ++s) {
+      const float4* a = reinterpret_cast<const float4*>(sum + (s * tokens + r) * pitch + c);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const float4 b = __ldcs(a + h);
+        v[h] = make_float4(v[h].x + b.x, v[h].y + b.y, v[h].z + b.z, v[h].w + b.w);
+      }
+    }
+    float e[8] = {v[0].x, v[0].y, v[0].z, v[0].w, v[1].x, v[1].y, v[1].z, v[1].w};
     const bool zero = target[r] == ignore;
-    for (int64_t c = 2 * threadIdx.x; c < dim; c += 512) {   // pitch is even
-      float2 v = make_float2(0.0f, 0.0f);
-      for (int s = 0; s < splits; ++s) {
-        const float2 a =
-            *reinterpret_cast<const float2*>(sum + (s * tokens + r) * pitch + c);
-        v.x += a.x;
-        v.y += a.y;
-      }
-      v.x = zero ? 0.0f : v.x * (1.0f / kProbScale) * back;
-      v.y = zero ? 0.0f : v.y * (1.0f / kProbScale) * back;
-      uint16_t* out = dx + r * dim + c;
-      const uint32_t both = pack16<BF16>(v.x, v.y);
-      if ((reinterpret_cast<uintptr_t>(out) & 3u) == 0 && c + 1 < dim) {
-        *reinterpret_cast<uint32_t*>(out) = both;
-      } else {
-        out[0] = (uint16_t)both;
-        if (c + 1 < dim) out[1] = (uint16_t)(both >> 16);
-      }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) e[j] = zero ? 0.0f : e[j] * (1.0f / kProbScale) * back;
+    uint16_t* out = dx + r * dim + c;
+    if (c + 8 <= dim && (reinterpret_cast<uintptr_t>(out) & 15u) == 0) {
+      *reinterpret_cast<uint4*>(out) =
+          make_uint4(pack16<BF16>(e[0], e[1]), pack16<BF16>(e[2], e[3]),
+                     pack16<BF16>(e[4], e[5]), pack16<BF16>(e[6], e[7]));
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (c + j < dim) out[j] = (uint16_t)pack16<BF16>(e[j], 0.0f);
     }
   }
 }
@@ -814,12 +824,12 @@ bool direct(const void* p, int64_t dim) {
 
 cudaError_t copy_rows(const void* src, int64_t rows, int64_t dim, int64_t pitch,
                       const int64_t* target, int64_t ignore, char* dst, int sms,
-                      cudaStream_t stream) {
-  const int64_t grid = rows < 8 * sms ? rows : 8 * sms;
+                      cudaStream_t stream, const float* dloss = nullptr, float* top = nullptr) {
+  const int64_t grid = std::min(rows, (int64_t)8 * sms) + (top != nullptr ? 1 : 0);
   xent_copy_kernel<<<(unsigned)grid, 256, 0, stream>>>(
       static_cast<const uint16_t*>(src), rows, dim, pitch,
       reinterpret_cast<const long long*>(target), ignore, reinterpret_cast<uint16_t*>(dst),
-      direct(src, dim) && pitch == dim);
+      direct(src, dim) && pitch == dim, dloss, top);
   return cudaGetLastError();
 }
 
@@ -985,14 +995,13 @@ cudaError_t launch_xent_backward(const XentArgs& a, char* scratch, int* error, i
   cudaError_t e = cudaMemsetAsync(next, 0, (size_t)(s.pieces + 1) * 4, stream);
   if (mark) mark(kXentPrepareK, 0, stream);
   if (e == cudaSuccess)
-    e = copy_rows(a.x, a.rows, a.dim, pitch, a.target, a.ignore, scratch + s.x, sms, stream);
+    e = copy_rows(a.x, a.rows, a.dim, pitch, a.target, a.ignore, scratch + s.x, sms, stream,
+                  a.dloss, top);
   if (e == cudaSuccess && !direct(a.w, a.dim)) {
     e = copy_rows(a.w, a.vocab, a.dim, pitch, nullptr, 0, scratch + s.w, sms, stream);
     w = scratch + s.w;
   }
-  xent_top_kernel<<<1, 1024, 0, stream>>>(a.dloss, target, a.ignore, a.rows, top);
   if (mark) mark(kXentPrepareK, 1, stream);
-  if (e == cudaSuccess) e = cudaGetLastError();
   if (e != cudaSuccess) return e;
 
   // x and w as K-major operands of the logits, and MN-major ones of dw and dx;
@@ -1055,8 +1064,8 @@ cudaError_t launch_xent_backward(const XentArgs& a, char* scratch, int* error, i
   }
   if (mark) mark(kXentDxK, 0, stream);
   e = launch_early(bf16 ? xent_dx_kernel<true> : xent_dx_kernel<false>,
-                   (unsigned)std::min(a.rows, (int64_t)8 * sms), 256, 0, stream,
-                   (const float*)o.dx_sum, s.splits, a.rows, a.dim, o.dim_pitch, target,
+                   (unsigned)std::min((a.rows * ((a.dim + 7) / 8) + 255) / 256, (int64_t)8 * sms), 256,
+                   0, stream, (const float*)o.dx_sum, s.splits, a.rows, a.dim, o.dim_pitch, target,
                    (long long)a.ignore, (const float*)top, static_cast<uint16_t*>(a.dx));
   if (mark) mark(kXentDxK, 1, stream);
   return e;

@@ -205,6 +205,7 @@ act_forward_kernel(const void* __restrict__ x, int64_t n, void* __restrict__ y,
   const int64_t t = (int64_t)blockIdx.x * kThreads + threadIdx.x;
   const int64_t i0 = t * kPer;
   const bool live = i0 < n;         // the same for the eight threads of a group
+  begin_after_previous();
   Raw16<DT> raw = {};
   if (live) raw = load_raw16<DT>(x, i0);
   uint32_t m = amax16<DT>(raw);
@@ -231,6 +232,7 @@ act_forward_any_kernel(const void* __restrict__ x, int64_t n, int64_t g0,
                        uint8_t* __restrict__ codes, float* __restrict__ scales) {
   const int lane = threadIdx.x & 31;
   const int64_t stride = (int64_t)gridDim.x * (kThreads / 32);
+  begin_after_previous();
   for (int64_t g = g0 + (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
        g < ngroups; g += stride) {
     const int64_t base = g * kActGroup + lane;
@@ -264,6 +266,7 @@ act_backward_kernel(const void* __restrict__ dy, const uint8_t* __restrict__ cod
                     void* __restrict__ out) {
   const int64_t t = (int64_t)blockIdx.x * kThreads + threadIdx.x;
   const int64_t i0 = t * kPer;
+  begin_after_previous();
   if (i0 >= n) return;
   const uint4 c = ld_once4(codes + i0);
   const float s = __ldg(scales + i0 / kActGroup);
@@ -288,6 +291,7 @@ act_backward_any_kernel(const void* __restrict__ dy,
                         const float* __restrict__ scales, int64_t i_first,
                         int64_t n, void* __restrict__ out) {
   const int64_t stride = (int64_t)gridDim.x * kThreads;
+  begin_after_previous();
   for (int64_t i = i_first + (int64_t)blockIdx.x * kThreads + threadIdx.x; i < n;
        i += stride) {
     const float s = __ldg(scales + i / kActGroup);
@@ -301,43 +305,47 @@ act_backward_any_kernel(const void* __restrict__ dy,
 // The vector kernels take the whole groups of aligned buffers; the element
 // kernels the rest.
 template <int DT, int ACT>
-void forward(const ActArgs& a, int sms, cudaStream_t stream) {
+cudaError_t forward(const ActArgs& a, int sms, cudaStream_t stream) {
   const int64_t ngroups = (a.n + kActGroup - 1) / kActGroup;
   const int64_t whole = a.vec_ok ? a.n / kActGroup : 0;
-  if (whole > 0) {
-    const int64_t threads = whole * kLanes;
-    act_forward_kernel<DT, ACT><<<(unsigned)((threads + kThreads - 1) / kThreads),
-                                  kThreads, 0, stream>>>(
-        a.x, whole * kActGroup, a.out, a.codes_out, a.scales_out);
-  }
-  if (whole < ngroups) {
+  cudaError_t e = cudaSuccess;
+  if (whole > 0)
+    e = launch(worth_early(a.n), act_forward_kernel<DT, ACT>,
+                     (unsigned)((whole * kLanes + kThreads - 1) / kThreads), kThreads, 0, stream,
+                     a.x, whole * kActGroup, a.out, a.codes_out, a.scales_out);
+  if (e == cudaSuccess && whole < ngroups) {
     const int64_t blocks = (ngroups - whole + kThreads / 32 - 1) / (kThreads / 32);
-    act_forward_any_kernel<DT, ACT>
-        <<<(unsigned)(blocks < 16 * sms ? blocks : 16 * sms), kThreads, 0, stream>>>(
-            a.x, a.n, whole, ngroups, a.out, a.codes_out, a.scales_out);
+    e = launch(false, act_forward_any_kernel<DT, ACT>,
+                     (unsigned)(blocks < 16 * sms ? blocks : 16 * sms), kThreads, 0, stream, a.x,
+                     a.n, whole, ngroups, a.out, a.codes_out, a.scales_out);
   }
+  return e;
 }
 
 template <int DT, int ACT>
-void backward(const ActArgs& a, int sms, cudaStream_t stream) {
+cudaError_t backward(const ActArgs& a, int sms, cudaStream_t stream) {
   const int64_t whole = a.vec_ok ? a.n / kActGroup * kActGroup : 0;
+  cudaError_t e = cudaSuccess;
   if (whole > 0)
-    act_backward_kernel<DT, ACT>
-        <<<(unsigned)((whole / kPer + kThreads - 1) / kThreads), kThreads, 0, stream>>>(
-            a.x, a.codes, a.scales, whole, a.out);
-  if (whole < a.n) {
+    e = launch(worth_early(a.n), act_backward_kernel<DT, ACT>,
+                     (unsigned)((whole / kPer + kThreads - 1) / kThreads), kThreads, 0, stream,
+                     a.x, a.codes, a.scales, whole, a.out);
+  if (e == cudaSuccess && whole < a.n) {
     const int64_t blocks = (a.n - whole + kThreads - 1) / kThreads;
-    act_backward_any_kernel<DT, ACT>
-        <<<(unsigned)(blocks < 16 * sms ? blocks : 16 * sms), kThreads, 0, stream>>>(
-            a.x, a.codes, a.scales, whole, a.n, a.out);
+    e = launch(false, act_backward_any_kernel<DT, ACT>,
+                     (unsigned)(blocks < 16 * sms ? blocks : 16 * sms), kThreads, 0, stream, a.x,
+                     a.codes, a.scales, whole, a.n, a.out);
   }
+  return e;
 }
 
 template <int DT>
-void launch_dt(int act, bool fwd, const ActArgs& a, int sms, cudaStream_t s) {
-  if (act == kActSave) fwd ? forward<DT, kActSave>(a, sms, s) : backward<DT, kActSave>(a, sms, s);
-  else if (act == kActGelu) fwd ? forward<DT, kActGelu>(a, sms, s) : backward<DT, kActGelu>(a, sms, s);
-  else fwd ? forward<DT, kActGeluTanh>(a, sms, s) : backward<DT, kActGeluTanh>(a, sms, s);
+cudaError_t launch_dt(int act, bool fwd, const ActArgs& a, int sms, cudaStream_t s) {
+  if (act == kActSave)
+    return fwd ? forward<DT, kActSave>(a, sms, s) : backward<DT, kActSave>(a, sms, s);
+  if (act == kActGelu)
+    return fwd ? forward<DT, kActGelu>(a, sms, s) : backward<DT, kActGelu>(a, sms, s);
+  return fwd ? forward<DT, kActGeluTanh>(a, sms, s) : backward<DT, kActGeluTanh>(a, sms, s);
 }
 
 }  // namespace
@@ -347,11 +355,11 @@ cudaError_t launch_act(int act, bool fwd, const ActArgs& a, int sms,
   const int k = act == kActSave ? (fwd ? kActSaveK : kActLoadK)
                                 : (fwd ? kGeluK : kGeluBackwardK);
   if (mark) mark(k, 0, stream);
-  if (a.dtype == kF32) launch_dt<kF32>(act, fwd, a, sms, stream);
-  else if (a.dtype == kBF16) launch_dt<kBF16>(act, fwd, a, sms, stream);
-  else launch_dt<kF16>(act, fwd, a, sms, stream);
+  const cudaError_t e = a.dtype == kF32    ? launch_dt<kF32>(act, fwd, a, sms, stream)
+                        : a.dtype == kBF16 ? launch_dt<kBF16>(act, fwd, a, sms, stream)
+                                           : launch_dt<kF16>(act, fwd, a, sms, stream);
   if (mark) mark(k, 1, stream);
-  return cudaGetLastError();
+  return e;
 }
 
 }  // namespace fp8opt

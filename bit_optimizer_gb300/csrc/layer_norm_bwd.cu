@@ -58,6 +58,7 @@ ln_backward_kernel(const LnBackward a, float* __restrict__ partial) {
   const float inv_c = 1.0f / (float)cols;
   const int64_t step = (int64_t)gridDim.x * RPC;
   int turn = 0;
+  begin_after_previous();
 
   const auto at_dy = [&](int stage, int v, int q) -> uint4* {
     return ring + ((stage * VPT + v) * Q + q) * NT + threadIdx.x;
@@ -233,8 +234,6 @@ ln_backward_kernel(const LnBackward a, float* __restrict__ partial) {
       out[c] = v;
     }
   }
-  // the kernel that adds the CTAs' sums may be set up meanwhile
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
 // dw and db of 32 columns: the `parts` partial sums, 32 at a time, then the 32
@@ -246,7 +245,7 @@ ln_param_grad_kernel(const float* __restrict__ partial, int64_t parts, int64_t c
   const int64_t c = (int64_t)blockIdx.x * 32 + threadIdx.x;
   void* out = blockIdx.y == 0 ? dw : db;
   float s = 0.0f;
-  asm volatile("griddepcontrol.wait;" ::: "memory");   // for the partial sums
+  begin_after_previous();
   if (c < cols)
     for (int64_t p = threadIdx.y; p < parts; p += 32)
       s += __ldcg(partial + (p * 2 + blockIdx.y) * cols + c);
@@ -275,6 +274,7 @@ __global__ void __launch_bounds__(1024)
 ln_backward_long_dx_kernel(const LnBackward a) {
   __shared__ float2 sh[32];
   const float inv_c = 1.0f / (float)a.cols;
+  begin_after_previous();
   for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x) {
     const int64_t at = r * a.cols;
     const float rstd = a.rstd[r];
@@ -310,6 +310,7 @@ template <int DT, bool FP8>
 __global__ void __launch_bounds__(256)
 ln_backward_long_cols_kernel(const LnBackward a, int64_t rows_per, float* __restrict__ partial) {
   const int64_t c = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  begin_after_previous();
   if (c >= a.cols) return;
   const int64_t r1 = min(a.rows, (int64_t)(blockIdx.y + 1) * rows_per);
   float sw = 0.0f, sb = 0.0f;
@@ -350,8 +351,7 @@ cudaError_t go_form(const LnBackward& a, float* partial, unsigned grid, cudaStre
         cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
   }
-  kernel<<<grid, NT, smem, stream>>>(a, partial);
-  return cudaSuccess;
+  return launch(worth_early(a.rows * a.cols), kernel, grid, NT, smem, stream, a, partial);
 }
 
 template <int DT, int VEC, int TPR, int VPT>
@@ -384,14 +384,14 @@ cudaError_t by_type(const LnBackward& a, float* p, int sms, cudaStream_t s, int6
     *parts = a.rows < kLongParts ? a.rows : kLongParts;
     const int64_t rows_per = (a.rows + *parts - 1) / *parts;
     const dim3 cg((unsigned)((a.cols + 255) / 256), (unsigned)*parts);
-    if (a.codes != nullptr) {
-      ln_backward_long_dx_kernel<DT, true><<<grid, 1024, 0, s>>>(a);
-      ln_backward_long_cols_kernel<DT, true><<<cg, 256, 0, s>>>(a, rows_per, p);
-    } else {
-      ln_backward_long_dx_kernel<DT, false><<<grid, 1024, 0, s>>>(a);
-      ln_backward_long_cols_kernel<DT, false><<<cg, 256, 0, s>>>(a, rows_per, p);
-    }
-    return cudaSuccess;
+    const bool fp8 = a.codes != nullptr;
+    const cudaError_t e = launch(true, fp8 ? ln_backward_long_dx_kernel<DT, true>
+                                           : ln_backward_long_dx_kernel<DT, false>,
+                                       grid, 1024, 0, s, a);
+    if (e != cudaSuccess) return e;
+    return launch(true, fp8 ? ln_backward_long_cols_kernel<DT, true>
+                            : ln_backward_long_cols_kernel<DT, false>,
+                        cg, 256, 0, s, a, rows_per, p);
   }
   const unsigned grid = grid_of(a, sms);
   *parts = grid;
@@ -415,20 +415,11 @@ cudaError_t launch_ln_backward(const LnBackward& a, void* scratch, int sms, cuda
                   : a.dtype == kBF16 ? by_type<kBF16>(a, p, sms, stream, &parts)
                                      : by_type<kF16>(a, p, sms, stream, &parts);
   if (mark) mark(kLayerNormBackwardK, 1, stream);
-  if (e == cudaSuccess) e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   if (mark) mark(kLayerNormParamsK, 0, stream);
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((a.cols + 31) / 32), a.db != nullptr ? 2 : 1);
-  cfg.blockDim = dim3(32, 32);
-  cfg.stream = stream;
-  cudaLaunchAttribute early;
-  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  early.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &early;
-  cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, ln_param_grad_kernel, (const float*)p, parts, a.cols, a.wdtype,
-                         a.dw, a.db);
+  e = launch(true, ln_param_grad_kernel,
+                   dim3((unsigned)((a.cols + 31) / 32), a.db != nullptr ? 2 : 1), dim3(32, 32), 0,
+                   stream, (const float*)p, parts, a.cols, a.wdtype, a.dw, a.db);
   if (mark) mark(kLayerNormParamsK, 1, stream);
   return e;
 }

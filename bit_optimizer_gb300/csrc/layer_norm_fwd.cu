@@ -69,6 +69,7 @@ ln_forward_kernel(const LnForward a) {
     }
     copy_commit();
   };
+  begin_after_previous();
   if constexpr (VEC == 8) {
 #pragma unroll
     for (int i = 0; i < ST - 1; ++i) fetch(i, r + i * step);
@@ -233,6 +234,7 @@ template <int DT, bool FP8>
 __global__ void __launch_bounds__(1024)
 ln_forward_long_kernel(const LnForward a) {
   __shared__ float2 sh[32];
+  begin_after_previous();
   for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x) {
     const int64_t at = r * a.cols;
     float s = 0.0f;
@@ -274,8 +276,8 @@ cudaError_t go_form(const LnForward& a, int sms, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
   }
   const int64_t ctas = (a.rows + RPC - 1) / RPC, most = (int64_t)sms * kFwdCtas;
-  kernel<<<(unsigned)(ctas < most ? ctas : most), kFwdThreads, smem, stream>>>(a);
-  return cudaSuccess;
+  return launch(worth_early(a.rows * a.cols), kernel, (unsigned)(ctas < most ? ctas : most), kFwdThreads, smem, stream,
+                      a);
 }
 
 template <int DT, int VEC, int TPR, int VPT>
@@ -307,9 +309,9 @@ cudaError_t by_type(const LnForward& a, int sms, cudaStream_t stream) {
   if (a.cols > kLnMaxRegCols) {
     const int64_t most = (int64_t)sms * 2;
     const unsigned grid = (unsigned)(a.rows < most ? a.rows : most);
-    if (a.codes != nullptr) ln_forward_long_kernel<DT, true><<<grid, 1024, 0, stream>>>(a);
-    else ln_forward_long_kernel<DT, false><<<grid, 1024, 0, stream>>>(a);
-    return cudaSuccess;
+    return launch(worth_early(a.rows * a.cols), a.codes != nullptr ? ln_forward_long_kernel<DT, true>
+                                           : ln_forward_long_kernel<DT, false>,
+                        grid, 1024, 0, stream, a);
   }
   return a.vec_ok ? by_cols<DT, 8>(a, sms, stream) : by_cols<DT, 1>(a, sms, stream);
 }
@@ -323,7 +325,7 @@ cudaError_t launch_ln_forward(const LnForward& a, int sms, cudaStream_t stream,
                         : a.dtype == kBF16 ? by_type<kBF16>(a, sms, stream)
                                            : by_type<kF16>(a, sms, stream);
   if (mark) mark(kLayerNormK, 1, stream);
-  return e == cudaSuccess ? cudaGetLastError() : e;
+  return e;
 }
 
 }  // namespace fp8opt

@@ -54,7 +54,7 @@ __device__ __forceinline__ float exp2_approx(float x) {
   return y;
 }
 
-enum GemmMode { kStats = 0, kProbs, kDx, kDw };
+enum GemmMode { kStats = 0, kStatsSwapped, kProbs, kDx, kDw };
 
 // One product C[m, n] = sum_k A[m, k] B[n, k] in tiles of 256 x tile_n, k in
 // `splits` ranges of `kper` blocks, and what its tiles are for.
@@ -80,7 +80,7 @@ struct GemmOut {
   const long long* target;
   long long ignore;
   // kStats
-  float2* partial;         // [half a tile's columns][token]: maximum, sum of exponentials
+  float2* partial;         // [part of the vocabulary][token]: maximum, sum of exponentials
   float* target_logit;     // [token]
   // kProbs
   const float* lse;
@@ -227,24 +227,28 @@ __device__ __forceinline__ RowIn row_in(const GemmShape& g, const GemmOut& o, in
   return in;
 }
 
-// The strip's logits: maximum and sum of exponentials.
-__device__ __forceinline__ void stats_strip(const GemmOut& o, const Strip& t, const RowIn& in) {
-  const bool live = t.row < o.tokens;
-  const long long target = in.target;
-  const int rel = target >= t.c0 && target < t.c0 + t.cols && target < o.vocab
-                      ? (int)(target - t.c0) : -1;
-  const int valid = (int)min((int64_t)t.cols, o.vocab - t.c0);   // may be <= 0
+// Two parts of a token's logits: maximum, and sum of exponentials above it.
+__device__ __forceinline__ float2 join_stats(float2 a, float2 b) {
+  const float top = fmaxf(a.x, b.x);
+  return make_float2(top, a.y * exp2_approx((a.x - top) * kLog2eF) +
+                              b.y * exp2_approx((b.x - top) * kLog2eF));
+}
+
+// A token's running maximum and sum of exponentials, and its target's logit.
+struct Stats {
   float top = -1e30f, sum = 0.0f, at_target = 0.0f;
-  const auto add = [&](int c, uint32_t (&r)[32]) {
-    if (c + 32 > valid) {
+  // 32 more logits, of which the first `valid` count; the target's is number
+  // rel, if it is among them.
+  __device__ __forceinline__ void add(uint32_t (&r)[32], int valid, int rel) {
+    if (valid < 32) {
 #pragma unroll
       for (int j = 0; j < 32; ++j)
-        if (c + j >= valid) r[j] = 0xFF800000u;
+        if (j >= valid) r[j] = 0xFF800000u;
     }
-    if (__any_sync(0xFFFFFFFFu, rel >= c && rel < c + 32)) {
+    if (__any_sync(0xFFFFFFFFu, rel >= 0 && rel < 32)) {
 #pragma unroll
       for (int j = 0; j < 32; ++j)
-        if (rel == c + j) at_target = __uint_as_float(r[j]);
+        if (rel == j) at_target = __uint_as_float(r[j]);
     }
     float m[4] = {top, top, top, top};
 #pragma unroll
@@ -254,19 +258,81 @@ __device__ __forceinline__ void stats_strip(const GemmOut& o, const Strip& t, co
                    make_float2(0.0f, 0.0f)};
     top = m[0];
 #pragma unroll
-    for (int j = 0; j < 32; j += 2) s[j / 2 & 1] = add2(s[j / 2 & 1], exp_pair(r[j], r[j + 1], -top));
+    for (int j = 0; j < 32; j += 2)
+      s[j / 2 & 1] = add2(s[j / 2 & 1], exp_pair(r[j], r[j + 1], -top));
     s[0] = add2(s[0], s[1]);
     sum = s[0].x + s[0].y;
-  };
+  }
+};
+
+// The strip's logits: maximum and sum of exponentials.
+__device__ __forceinline__ void stats_strip(const GemmOut& o, const Strip& t, const RowIn& in) {
+  const long long target = in.target;
+  const int rel = target >= t.c0 && target < t.c0 + t.cols && target < o.vocab
+                      ? (int)(target - t.c0) : -1;
+  const int valid = (int)min((int64_t)t.cols, o.vocab - t.c0);   // may be <= 0
+  Stats s;
   tmem_columns(t.tmem, t.cols, [&](int c, uint32_t (&r)[32], uint32_t (&q)[32]) {
-    add(c, r);
-    add(c + 32, q);
+    s.add(r, valid - c, rel - c);
+    s.add(q, valid - c - 32, rel - c - 32);
   });
-  if (live) {
-    o.partial[(int64_t)t.index * o.tokens + t.row] = make_float2(top, sum);
-    if (rel >= 0) o.target_logit[t.row] = at_target;
+  if (t.row < o.tokens) {
+    o.partial[(int64_t)t.index * o.tokens + t.row] = make_float2(s.top, s.sum);
+    if (rel >= 0) o.target_logit[t.row] = s.at_target;
   }
 }
+
+// The same with the operands swapped: the tile's rows are the vocabulary's, its
+// columns the tokens (tile_n covers them, at most kSwapTokens).  Through the
+// warp's shared memory the logits of 32 rows and 32 columns are turned over, a
+// token to each lane; a warp's statistics of its two ranges of tokens run on
+// from tile to tile, and a CTA writes its own once, at the end.
+struct SwappedStats {
+  Stats s[2];
+  __device__ __forceinline__ void add(const GemmShape& g, const GemmOut& o, uint32_t tmem,
+                                      int64_t v0, int half, Turn& turn) {
+    const int lane = threadIdx.x & 31;
+    const int valid = (int)min((int64_t)32, max(o.vocab - v0, (int64_t)0));
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int c = 32 * half + 64 * k;
+      if (c >= g.tile_n) break;
+      uint32_t r[32];
+      tmem_load32(tmem + c, r);
+      tmem_wait(r);
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        turn.at(lane, j) = make_uint4(r[4 * j], r[4 * j + 1], r[4 * j + 2], r[4 * j + 3]);
+      __syncwarp();
+#pragma unroll
+      for (int j = 0; j < 32; ++j)
+        r[j] = reinterpret_cast<const uint32_t*>(&turn.at(j, lane >> 2))[lane & 3];
+      __syncwarp();
+      const int64_t token = c + lane;
+      const long long target = token < o.tokens ? o.target[token] : -1;
+      const int rel = target >= v0 && target < v0 + 32 && target < o.vocab ? (int)(target - v0)
+                                                                            : -1;
+      s[k].add(r, valid, rel);
+      if (rel >= 0) o.target_logit[token] = s[k].at_target;
+    }
+  }
+  // Every epilogue warp; turns: all warps' shared memory.
+  __device__ __forceinline__ void finish(const GemmOut& o, int warp, Turn* turns) {
+    const int lane = threadIdx.x & 31;
+    float2* const mine = reinterpret_cast<float2*>(&turns[warp]);
+    for (int k = 0; k < 2; ++k) mine[32 * k + lane] = make_float2(s[k].top, s[k].sum);
+    asm volatile("bar.sync 1, 256;" ::: "memory");
+    if (warp % 4 != 0) return;
+    for (int k = 0; k < 2; ++k) {
+      const int64_t token = 32 * (warp / 4) + 64 * k + lane;
+      if (token >= o.tokens) continue;
+      float2 a = make_float2(-1e30f, 0.0f);
+      for (int w = 0; w < 4; ++w)
+        a = join_stats(a, reinterpret_cast<const float2*>(&turns[warp + w])[32 * k + lane]);
+      o.partial[(int64_t)blockIdx.x * o.tokens + token] = a;
+    }
+  }
+};
 
 // The strip's logits turned into p.
 template <bool BF16>
@@ -349,7 +415,7 @@ __device__ __forceinline__ void dw_strip(const GemmShape& g, const GemmOut& o, c
 }
 
 // A tile as the warps of one CTA need it.  `work` is what its MMA warp reads:
-// blocks of k, tile_n / 128 and the operands' order.
+// blocks of k, tile_n / 16 and the operands' order (see its accessors).
 struct Tile {
   uint32_t work;
   int job, m, n, split;
@@ -358,6 +424,10 @@ struct Tile {
   int pad[3];
 };
 constexpr uint32_t kNoWork = 0xFFFFFFFFu;
+__device__ __forceinline__ int work_blocks(uint32_t w) { return (int)(w & 0xFFFFFFu); }
+__device__ __forceinline__ int work_tile_n(uint32_t w) { return (int)(w >> 24 & 31u) * 16; }
+__device__ __forceinline__ bool work_a_mn(uint32_t w) { return w >> 29 & 1u; }
+__device__ __forceinline__ bool work_b_mn(uint32_t w) { return w >> 30 & 1u; }
 static_assert(sizeof(Tile) == 48, "three 16-byte words");
 
 __device__ __forceinline__ Tile locate(const GemmArgs& args, int tile, int rank) {
@@ -375,8 +445,8 @@ __device__ __forceinline__ Tile locate(const GemmArgs& args, int tile, int rank)
   t.n = tile / g.tiles_m % g.tiles_n;
   t.split = tile / g.tiles_m / g.tiles_n;
   const int kb0 = t.split * g.kper, blocks = max(min(g.kper, g.kblocks - kb0), 0);
-  t.work = (uint32_t)blocks | (uint32_t)(g.tile_n / 128) << 24 | (uint32_t)g.a_mn << 28 |
-           (uint32_t)g.b_mn << 29;
+  t.work = (uint32_t)blocks | (uint32_t)(g.tile_n / 16) << 24 | (uint32_t)g.a_mn << 29 |
+           (uint32_t)g.b_mn << 30;
   t.a_mn = t.m * kTileM + rank * kHalfM;
   t.b_mn = g.b_mn0 + t.n * g.tile_n + rank * (g.tile_n / 2);
   t.a_k = kb0 * kBlockK;
@@ -455,8 +525,7 @@ gemm_kernel(const __grid_constant__ GemmArgs args) {
   const uint32_t tmem = bar.tmem;
   bool ok = true;
   // the set-up above runs while the previous launch of the stream ends
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  begin_after_previous();
 
   if (warp == kEpilogueWarps + 2) {
     if ((threadIdx.x & 31) == 0) {
@@ -516,8 +585,8 @@ gemm_kernel(const __grid_constant__ GemmArgs args) {
         reader.done(bar);
         const CUtensorMap* const map_a = &args.job[t.job].a;
         const CUtensorMap* const map_b = &args.job[t.job].b;
-        const int blocks = (int)(t.work & 0xFFFFFFu), half_n = (int)(t.work >> 24 & 15u) * 64;
-        const bool a_mn = t.work >> 28 & 1, b_mn = t.work >> 29 & 1;
+        const int blocks = work_blocks(t.work), half_n = work_tile_n(t.work) / 2;
+        const bool a_mn = work_a_mn(t.work), b_mn = work_b_mn(t.work);
         const uint32_t bytes = 2 * (kStageA + half_n * (kBlockK * 2));
         for (int kb = 0; kb < blocks; ++kb) {
           if (!(ok = mbar_wait(&bar.empty[s], phase ^ 1))) break;
@@ -559,9 +628,9 @@ gemm_kernel(const __grid_constant__ GemmArgs args) {
         const uint32_t work = next->work;
         if (work == kNoWork) break;
         reader.done(bar);
-        const int blocks = (int)(work & 0xFFFFFFu);
-        const bool a_mn = work >> 28 & 1, b_mn = work >> 29 & 1;
-        const uint32_t idesc = mma_desc(BF16, a_mn, b_mn, kTileM, (int)(work >> 24 & 15u) * 128);
+        const int blocks = work_blocks(work);
+        const bool a_mn = work_a_mn(work), b_mn = work_b_mn(work);
+        const uint32_t idesc = mma_desc(BF16, a_mn, b_mn, kTileM, work_tile_n(work));
         const uint32_t step_a = a_mn ? 16 * 128 : 32, step_b = b_mn ? 16 * 128 : 32;
         if (!(ok = mbar_wait(&bar.acc_empty[buf], acc_phase ^ 1))) break;
         tcgen_fence_after();
@@ -589,7 +658,9 @@ gemm_kernel(const __grid_constant__ GemmArgs args) {
     }
   } else {
     TileReader<true> reader;
-    Turn& turn = reinterpret_cast<Turn*>(stages + kGemmStages * (kStageA + kStageB))[warp];
+    Turn* const turns = reinterpret_cast<Turn*>(stages + kGemmStages * (kStageA + kStageB));
+    Turn& turn = turns[warp];
+    SwappedStats swapped;
     int buf = 0, phase = 0;
     for (;;) {
       const Tile* next = reader.next(bar);
@@ -598,7 +669,7 @@ gemm_kernel(const __grid_constant__ GemmArgs args) {
       if (t.work == kNoWork) break;
       reader.done(bar);
       const GemmShape& g = args.job[t.job].shape;
-      const int half = warp / 4, cols = (int)(t.work >> 24 & 15u) * 64;
+      const int half = warp / 4, cols = work_tile_n(t.work) / 2;
       const Strip strip = {tmem + buf * kTileN + half * cols + ((uint32_t)(warp % 4) << 21),
                            (int64_t)t.m * kTileM + rank * kHalfM + (threadIdx.x & 127),
                            ((int64_t)t.n * 2 + half) * cols, cols, 2 * t.n + half};
@@ -607,8 +678,11 @@ gemm_kernel(const __grid_constant__ GemmArgs args) {
       if (!ok) break;
       tcgen_fence_after();
       if (g.mode == kStats) stats_strip(args.out, strip, in);
+      else if (g.mode == kStatsSwapped)
+        swapped.add(g, args.out, tmem + buf * kTileN + ((uint32_t)(warp % 4) << 21),
+                    strip.row - (threadIdx.x & 31), half, turn);
       else if (g.mode == kProbs) probs_strip<BF16>(g, args.out, strip, in, turn);
-      else if (g.mode == kDx) dx_strip(g, args.out, strip, t.split, (t.work & 0xFFFFFFu) == 0, turn);
+      else if (g.mode == kDx) dx_strip(g, args.out, strip, t.split, work_blocks(t.work) == 0, turn);
       else dw_strip<BF16>(g, args.out, strip, in, turn);
       tcgen_fence_before();
       __syncwarp();
@@ -618,6 +692,7 @@ gemm_kernel(const __grid_constant__ GemmArgs args) {
       buf ^= 1;
       if (buf == 0) phase ^= 1;
     }
+    if (args.job[0].shape.mode == kStatsSwapped) swapped.finish(args.out, warp, turns);
   }
   if (!ok) *args.error = 1;
   __syncwarp();
@@ -638,13 +713,8 @@ xent_join_kernel(const float2* __restrict__ partial, int strips, int64_t tokens,
   __shared__ float2 sh[32][33];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t row = (int64_t)blockIdx.x * 32 + lane;
-  const auto join = [](float2 a, float2 b) {
-    const float top = fmaxf(a.x, b.x);
-    return make_float2(top, a.y * exp2_approx((a.x - top) * kLog2eF) +
-                                b.y * exp2_approx((b.x - top) * kLog2eF));
-  };
   const float2 none = make_float2(-1e30f, 0.0f);
-  asm volatile("griddepcontrol.wait;" ::: "memory");   // for the tiles' statistics
+  begin_after_previous();
   float2 s = none;
   for (int i = warp; i < strips; i += 8 * 32) {
     float2 p[8];
@@ -653,7 +723,7 @@ xent_join_kernel(const float2* __restrict__ partial, int strips, int64_t tokens,
       p[k] = i + 32 * k < strips && row < tokens
                  ? __ldcg(partial + (int64_t)(i + 32 * k) * tokens + row) : none;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) s = join(s, p[k]);
+    for (int k = 0; k < 8; ++k) s = join_stats(s, p[k]);
   }
   sh[warp][lane] = s;
   __syncthreads();
@@ -661,8 +731,8 @@ xent_join_kernel(const float2* __restrict__ partial, int strips, int64_t tokens,
   s = sh[lane][warp];
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1)
-    s = join(s, make_float2(__shfl_xor_sync(0xFFFFFFFFu, s.x, o),
-                            __shfl_xor_sync(0xFFFFFFFFu, s.y, o)));
+    s = join_stats(s, make_float2(__shfl_xor_sync(0xFFFFFFFFu, s.x, o),
+                                  __shfl_xor_sync(0xFFFFFFFFu, s.y, o)));
   const int64_t mine = (int64_t)blockIdx.x * 32 + warp;
   if (lane == 0 && mine < tokens) {
     const float l = s.x + logf(s.y);
@@ -683,6 +753,7 @@ xent_copy_kernel(const uint16_t* __restrict__ src, int64_t rows, int64_t dim, in
                  uint16_t* __restrict__ dst, bool vec, const float* __restrict__ dloss,
                  float* __restrict__ top) {
   const unsigned copying = gridDim.x - (top != nullptr ? 1 : 0);
+  begin_after_previous();
   if (blockIdx.x == copying) {
     __shared__ uint32_t sh[8];
     uint32_t m = 0;
@@ -717,7 +788,7 @@ __global__ void __launch_bounds__(256)
 xent_dx_kernel(const float* __restrict__ sum, int splits, int64_t tokens, int64_t dim,
                int64_t pitch, const long long* __restrict__ target, long long ignore,
                const float* __restrict__ top, uint16_t* __restrict__ dx) {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  begin_after_previous();
   const float back = *top;
   const int64_t groups = (dim + 7) / 8;
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < tokens * groups;
@@ -785,22 +856,8 @@ cudaError_t make_map(CUtensorMap* map, bool bf16, const void* base, int64_t rows
 
 int64_t up(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
 
-// A launch whose set-up may overlap the end of the previous one of the stream
-// (the kernel waits for it before it reads anything).
-template <class... Params, class... Args>
-cudaError_t launch_early(void (*kernel)(Params...), unsigned grid, unsigned block, size_t smem,
-                         cudaStream_t stream, Args... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(block);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cudaLaunchAttribute early;
-  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  early.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &early;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, args...);
+unsigned gemm_ctas(int64_t tiles, int sms) {
+  return 2 * (unsigned)std::min(tiles, (int64_t)sms / 2);
 }
 
 cudaError_t launch_gemm(GemmArgs& g, bool bf16, int sms, cudaStream_t stream) {
@@ -813,8 +870,7 @@ cudaError_t launch_gemm(GemmArgs& g, bool bf16, int sms, cudaStream_t stream) {
             [](const GemmJob& a, const GemmJob& b) { return a.shape.kper > b.shape.kper; });
   int64_t tiles = 0;
   for (int i = 0; i < g.jobs; ++i) tiles += g.job[i].shape.tiles();
-  return launch_early(kernel, 2 * (unsigned)std::min(tiles, (int64_t)sms / 2), kGemmThreads,
-                      kGemmSmem, stream, g);
+  return launch(true, kernel, gemm_ctas(tiles, sms), kGemmThreads, kGemmSmem, stream, g);
 }
 
 // Rows that TMA can read as they are.
@@ -826,11 +882,11 @@ cudaError_t copy_rows(const void* src, int64_t rows, int64_t dim, int64_t pitch,
                       const int64_t* target, int64_t ignore, char* dst, int sms,
                       cudaStream_t stream, const float* dloss = nullptr, float* top = nullptr) {
   const int64_t grid = std::min(rows, (int64_t)8 * sms) + (top != nullptr ? 1 : 0);
-  xent_copy_kernel<<<(unsigned)grid, 256, 0, stream>>>(
-      static_cast<const uint16_t*>(src), rows, dim, pitch,
-      reinterpret_cast<const long long*>(target), ignore, reinterpret_cast<uint16_t*>(dst),
-      direct(src, dim) && pitch == dim, dloss, top);
-  return cudaGetLastError();
+  return launch(true, xent_copy_kernel, (unsigned)grid, 256, 0, stream,
+                      static_cast<const uint16_t*>(src), rows, dim, pitch,
+                      reinterpret_cast<const long long*>(target), (long long)ignore,
+                      reinterpret_cast<uint16_t*>(dst), direct(src, dim) && pitch == dim, dloss,
+                      top);
 }
 
 // Tokens of one forward launch: bounds the scratch of the tiles' statistics.
@@ -886,16 +942,27 @@ class Layout {
   size_t bytes_ = 0;
 };
 
+// Few tokens: the vocabulary's rows take the tiles' 256 rows and the tokens
+// their columns, as many as there are; a stage then holds little besides w,
+// which is all that has to be read.  (See the table of figures for both ways.)
+constexpr int64_t kSwapTokens = 128;
+
 struct ForwardScratch {
   size_t x = 0, w = 0, partial = 0, logit = 0, bytes = 0;
+  bool swapped = false;
+  int64_t strips = 0;
 };
-ForwardScratch forward_scratch(const XentArgs& a) {
+ForwardScratch forward_scratch(const XentArgs& a, int sms) {
   ForwardScratch s;
   Layout l;
   const int64_t pitch = up(a.dim, 8), tokens = std::min(a.rows, kForwardTokens);
   if (!direct(a.x, a.dim)) s.x = l.take(a.rows * pitch * 2);
   if (!direct(a.w, a.dim)) s.w = l.take(a.vocab * pitch * 2);
-  s.partial = l.take(2 * (up(a.vocab, kTileN) / kTileN) * tokens * 8);
+  s.swapped = a.rows <= kSwapTokens;
+  // a CTA's share of the vocabulary, or half a tile's columns
+  s.strips = s.swapped ? gemm_ctas(up(a.vocab, kTileM) / kTileM, sms)
+                       : 2 * (up(a.vocab, kTileN) / kTileN);
+  s.partial = l.take(s.strips * tokens * 8);
   s.logit = l.take(tokens * 4);
   s.bytes = l.bytes();
   return s;
@@ -925,12 +992,12 @@ BackwardScratch backward_scratch(const XentArgs& a, int sms) {
 
 }  // namespace
 
-size_t xent_forward_scratch(const XentArgs& a) { return forward_scratch(a).bytes; }
+size_t xent_forward_scratch(const XentArgs& a, int sms) { return forward_scratch(a, sms).bytes; }
 size_t xent_backward_scratch(const XentArgs& a, int sms) { return backward_scratch(a, sms).bytes; }
 
 cudaError_t launch_xent_forward(const XentArgs& a, char* scratch, int* error, int sms,
                                 cudaStream_t stream, LaunchMark mark) {
-  const ForwardScratch s = forward_scratch(a);
+  const ForwardScratch s = forward_scratch(a, sms);
   const bool bf16 = a.dtype == kBF16;
   const int64_t pitch = up(a.dim, 8);
   const char* x = static_cast<const char*>(a.x);
@@ -949,13 +1016,12 @@ cudaError_t launch_xent_forward(const XentArgs& a, char* scratch, int* error, in
     GemmArgs g = {};
     g.error = error;
     g.jobs = 1;
-    GemmShape& j = g.job[0].shape;
-    j.mode = kStats;
-    j.tiles_m = (int)(up(tokens, kTileM) / kTileM);
-    j.tile_n = kTileN;
-    j.tiles_n = (int)(up(a.vocab, kTileN) / kTileN);
-    j.kblocks = j.kper = blocks_of(a.dim);
-    j.splits = 1;
+    const int tiles_t = (int)(up(tokens, kTileM) / kTileM), kb = blocks_of(a.dim);
+    const int tiles_v = (int)(up(a.vocab, kTileN) / kTileN);
+    if (s.swapped)
+      g.job[0].shape = {kStatsSwapped, tiles_v, 1, (int)up(tokens, 32), kb, kb, 1};
+    else
+      g.job[0].shape = {kStats, tiles_t, tiles_v, kTileN, kb, kb, 1};
     g.out.tokens = tokens;
     g.out.vocab = a.vocab;
     g.out.dim = a.dim;
@@ -963,16 +1029,20 @@ cudaError_t launch_xent_forward(const XentArgs& a, char* scratch, int* error, in
     g.out.ignore = a.ignore;
     g.out.partial = reinterpret_cast<float2*>(scratch + s.partial);
     g.out.target_logit = reinterpret_cast<float*>(scratch + s.logit);
-    e = make_map(&g.job[0].a, bf16, x + t0 * pitch * 2, tokens, a.dim, pitch, kHalfM);
-    if (e == cudaSuccess) e = make_map(&g.job[0].b, bf16, w, a.vocab, a.dim, pitch, kTileN / 2);
+    CUtensorMap& of_x = s.swapped ? g.job[0].b : g.job[0].a;
+    CUtensorMap& of_w = s.swapped ? g.job[0].a : g.job[0].b;
+    e = make_map(&of_x, bf16, x + t0 * pitch * 2, tokens, a.dim, pitch,
+                 s.swapped ? g.job[0].shape.tile_n / 2 : kHalfM);
+    if (e == cudaSuccess)
+      e = make_map(&of_w, bf16, w, a.vocab, a.dim, pitch, s.swapped ? kHalfM : kTileN / 2);
     if (e != cudaSuccess) break;
     if (mark) mark(kXentLogitsK, 0, stream);
     e = launch_gemm(g, bf16, sms, stream);
     if (mark) mark(kXentLogitsK, 1, stream);
     if (e != cudaSuccess) break;
     if (mark) mark(kXentJoinK, 0, stream);
-    e = launch_early(xent_join_kernel, (unsigned)((tokens + 31) / 32), 1024, 0, stream,
-                     (const float2*)g.out.partial, 2 * j.tiles_n, tokens, a.vocab, g.out.target,
+    e = launch(true, xent_join_kernel, (unsigned)((tokens + 31) / 32), 1024, 0, stream,
+                     (const float2*)g.out.partial, (int)s.strips, tokens, a.vocab, g.out.target,
                      g.out.ignore, (const float*)g.out.target_logit, a.loss + t0,
                      a.lse_out + t0);
     if (mark) mark(kXentJoinK, 1, stream);
@@ -1063,7 +1133,7 @@ cudaError_t launch_xent_backward(const XentArgs& a, char* scratch, int* error, i
     if (e != cudaSuccess) return e;
   }
   if (mark) mark(kXentDxK, 0, stream);
-  e = launch_early(bf16 ? xent_dx_kernel<true> : xent_dx_kernel<false>,
+  e = launch(true, bf16 ? xent_dx_kernel<true> : xent_dx_kernel<false>,
                    (unsigned)std::min((a.rows * ((a.dim + 7) / 8) + 255) / 256, (int64_t)8 * sms), 256,
                    0, stream, (const float*)o.dx_sum, s.splits, a.rows, a.dim, o.dim_pitch, target,
                    (long long)a.ignore, (const float*)top, static_cast<uint16_t*>(a.dx));

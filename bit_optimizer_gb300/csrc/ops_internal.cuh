@@ -92,7 +92,7 @@ struct XentArgs {
   void* dw;
 };
 
-size_t xent_forward_scratch(const XentArgs& a);
+size_t xent_forward_scratch(const XentArgs& a, int sms);
 size_t xent_backward_scratch(const XentArgs& a, int sms);
 // error: a device word set to 1 when a wait in a kernel ran out.
 cudaError_t launch_xent_forward(const XentArgs& a, char* scratch, int* error, int sms,
@@ -122,6 +122,42 @@ class OpCall {
 };
 
 int record_error(int status, const char* what);
+
+// Launches an operator's kernel; `early`: so that it may be set up, and its
+// CTAs start, while the previous kernel of the stream ends (programmatic
+// dependent launch).  Each kernel begins with begin_after_previous(), before
+// which it reads and writes nothing in global memory.  Such a launch costs 1.5
+// us more of the host's time, and saves about 2.5 us of the GPU's.
+template <class... Params, class... Args>
+cudaError_t launch(bool early, void (*kernel)(Params...), dim3 grid, dim3 block, size_t smem,
+                   cudaStream_t stream, Args... args) {
+  if (!early) {
+    kernel<<<grid, block, smem, stream>>>(args...);
+    return cudaGetLastError();
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+// Whether a memory-bound kernel over this many elements is long enough (some 8
+// us, at four bytes and more an element) for its launch to be an early one: a
+// shorter one is over before the host has launched the next (128 x 768 norm:
+// 6.8 us a call, 8.4 early; 16384 x 4096: 59.1 us, 56.6 early).
+inline bool worth_early(int64_t elements) { return elements >= (int64_t)12 << 20; }
+
+__device__ __forceinline__ void begin_after_previous() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
 
 // --------------------------------------------------------- element helpers
 

@@ -235,7 +235,8 @@ extern "C" int fp8_linear_xent(const void* x, const void* w, const int64_t* targ
     cudaStream_t stream = static_cast<cudaStream_t>(stream_ptr);
     OpCall call;
     int* error = nullptr;
-    if ((st = call.open(fn, stream, xent_forward_scratch(a))) != FP8OPT_OK ||
+    if ((st = call.open(fn, stream, 0)) != FP8OPT_OK ||
+        (st = call.open(fn, stream, xent_forward_scratch(a, call.sms))) != FP8OPT_OK ||
         (st = call.error_word(fn, &error)) != FP8OPT_OK)
       return st;
     return call.done(fn, launch_xent_forward(a, call.scratch, error, call.sms, stream,

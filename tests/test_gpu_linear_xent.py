@@ -98,6 +98,18 @@ def test_forward_and_backward(bo, rows, dim, vocab, dtype):
     check_backward(bo, x, w, t, dloss)
 
 
+@pytest.mark.parametrize("rows", [1, 31, 33, 70, 128, 129, 256, 257])
+def test_few_tokens_over_a_large_vocabulary(bo, rows):
+    """More tiles of the vocabulary than pairs of SMs, for both ways of laying
+    the tokens out, with targets at both ends and at tile borders."""
+    x, w, t, dloss = inputs(rows, 64, 50257, torch.bfloat16, seed=rows, ignored=0.0)
+    ends = torch.tensor([50256, 0, 255, 256, 50175, 50176, 31, 32], device="cuda")[:rows]
+    t[:len(ends)] = ends
+    check_forward(bo, x, w, t)
+    if rows in (1, 129):
+        check_backward(bo, x, w, t, dloss)
+
+
 @pytest.mark.parametrize("dim", [1, 7, 65, 130])
 def test_row_lengths_that_are_no_multiple_of_eight(bo, dim):
     x, w, t, dloss = inputs(70, dim, 301, torch.float16, seed=dim)

@@ -9,8 +9,13 @@
 // global memory, and a second small kernel adds the CTAs' sums in CTA order.
 // No atomics, so the result does not depend on the schedule.
 //
-// Bound by HBM: 3 e bytes per element, or 2 e + 1 from the codes.  The next
-// row's loads are issued before the current row's reductions.
+// Bound by HBM, 3 e bytes per element, or 2 e + 1 from the codes, and close
+// behind by instructions (63% of the issue slots).  The coming rows' copies run
+// through a ring in shared memory: held in registers, two rows ahead was all
+// there was room for, and a 16381 x 2048 gradient from codes took 57 us; now
+// 34.6 us, 4.85 TB/s, 0.71 of the measured copy bandwidth; 65536 x 1024 from x:
+// 0.82.  With the row slots' sums added one slot after the other the end of a
+// CTA alone took 30 us; side by side it is one pass.
 #include "layer_norm.cuh"
 
 namespace fp8opt {

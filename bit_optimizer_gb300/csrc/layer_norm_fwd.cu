@@ -5,7 +5,11 @@
 //
 // Bound by HBM: e bytes in, e out, 1 more for the codes.  A row stays in
 // registers between its three uses (sum, centred squares, result), so the
-// variance is the two-pass one, without cancellation, at the price of one read.
+// variance is the two-pass one, without cancellation, at the price of one read;
+// the next rows are on their way through the ring meanwhile, and weight and
+// bias wait in shared memory (read from L1 they were evicted by the rows: 77.8
+// us).  16384 x 4096 BF16 with codes: 56.6 us, 5.93 TB/s, 0.87 of the measured
+// copy bandwidth; 65536 x 1024 without: 47 us, 0.83.
 #include "layer_norm.cuh"
 
 namespace fp8opt {
@@ -293,7 +297,7 @@ cudaError_t go(const LnForward& a, int sms, cudaStream_t stream) {
 
 // As many elements a thread as its registers take: the reductions, which cost
 // the same whatever a thread holds, then weigh least (16384 x 4096 with codes:
-// 61.7 us with 16 elements a thread, see the table of figures for 32).
+// 61.7 us with 16 elements a thread, 59.1 with 32).
 template <int DT, int VEC>
 cudaError_t by_cols(const LnForward& a, int sms, cudaStream_t stream) {
   if (a.cols <= 256) return go<DT, VEC, 32, 1>(a, sms, stream);

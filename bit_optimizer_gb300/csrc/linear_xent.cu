@@ -4,25 +4,37 @@
 //
 // forward   One product on the tensor cores.  A tile's epilogue reduces its
 //           logits, still in TMEM, to each token's maximum and sum of
-//           exponentials over the tile's columns (base-2, fp32) and takes the
-//           target's logit where it lies in the tile; a small kernel joins the
-//           tiles of a token in column order.
+//           exponentials (base 2, fp32, the difference taken before it is
+//           scaled) and takes the target's logit where it meets it; a small
+//           kernel joins the parts of a token in order.
 // backward  The vocabulary goes in pieces.  For each piece the logits are
 //           computed again and turned into p = (exp(z - lse) - [target]) *
 //           dloss in the operands' 16-bit type, tokens x piece, in scratch;
-//           then dx += p w_piece (fp32 in scratch between pieces) and dw_piece
-//           = p^T x.  p is scaled by a power of two taken from max |dloss|, so
-//           that FP16 holds it without underflow, and the results are scaled
-//           back in fp32: the one rounding to 16 bits besides the results'.
-//           Where p rounds, the error is random per element and of the size
-//           of the operands' own rounding.
+//           then dx += p w_piece (fp32 in scratch) and dw_piece = p^T x.  p is
+//           scaled by a power of two and max |dloss| against underflow in
+//           FP16: the one rounding to 16 bits besides the results', random per
+//           element and of the size of the operands' own.  A launch holds one
+//           piece's dx and dw and the next piece's p, so that its end, where
+//           pairs run out of tiles, comes once a piece and is filled with the
+//           short tiles of p.
 //
-// Every product is the same kernel: persistent CTAs of six warps, one tile of
-// 128 x 256 at a time.  Warp 4 feeds four stages of 64-deep operand blocks by
-// TMA, warp 5 issues tcgen05.mma into one of two TMEM accumulators, warps 0 to
-// 3 empty the other one, a row of the tile to each thread.  x and w are K-major
-// in the logits product; w in dx, and both operands of dw, are read MN-major,
-// so nothing is ever transposed in memory.
+// Every product is the same persistent kernel on pairs of CTAs (cta_group::2),
+// one tile of 256 x 256 at a time: a producer warp in each CTA copies its half
+// of A and B by TMA into six stages of 64-deep blocks, the leader's MMA warp
+// issues tcgen05.mma into one of two TMEM accumulators, eight epilogue warps
+// in each CTA empty the other, and a scheduler warp looks tiles up ahead of
+// everybody.  x and w are K-major in the logits product; w in dx, and both
+// operands of dw, are read MN-major, so nothing is transposed in memory.
+//
+// Bound by the tensor cores: 8192 x 2048 x 50257 forward 0.83 ms, 2.03 PFLOP/s
+// in a short run (cuBLAS' measured burst: 1.91); in a long one the power limit
+// lowers the clock for both (8192 x 1024: 1.72 PFLOP/s; cuBLAS 1.70).  The
+// gradients of 8192 x 2048: 3.0 ms, 1.69 PFLOP/s, the tensor pipe active 86% of
+// the cycles.  Few tokens are bound by reading w: 24 x 768 x 200000, 55 us, 5.6
+// TB/s.  What a step brought: single CTAs with tiles of 128 x 256 and four
+// stages reached 86% of the pipe forward; pairs need two thirds of the L2
+// traffic and, with the tile look-up in a warp of its own (in the producer it
+// left the pipe idle 4000 clocks a tile), 95%.
 //
 // Tokens whose target is `ignore` have no loss and give no gradient whatever
 // is in their row of x: their p is 0 and dw reads a copy of x in which such
@@ -66,6 +78,12 @@ struct GemmShape {
   int first;               // kDx: the first piece
   int64_t v0;              // first vocabulary row of the piece
   uint16_t* probs;         // kProbs: [token][piece]
+  // A's rows where they all lie in the leader's half of one row of tiles (a
+  // multiple of 8, K-major): only these are copied, the leader alone, and the
+  // rest of its stage, like the other CTA's, keeps what was there, which makes
+  // rows of C that nobody reads.  (Copies that end past a tensor are slow to
+  // fill up with zeros.)  0: any other A.
+  int a_rows;
   __host__ __device__ int tiles() const { return tiles_m * tiles_n * splits; }
 };
 struct GemmJob {
@@ -421,7 +439,8 @@ struct Tile {
   int job, m, n, split;
   int a_mn, b_mn;          // this CTA's coordinates in A and B ...
   int a_k, b_k;            // ... and those of the first block of k
-  int pad[3];
+  int a_rows;              // GemmShape's
+  int pad[2];
 };
 constexpr uint32_t kNoWork = 0xFFFFFFFFu;
 __device__ __forceinline__ int work_blocks(uint32_t w) { return (int)(w & 0xFFFFFFu); }
@@ -448,6 +467,7 @@ __device__ __forceinline__ Tile locate(const GemmArgs& args, int tile, int rank)
   t.work = (uint32_t)blocks | (uint32_t)(g.tile_n / 16) << 24 | (uint32_t)g.a_mn << 29 |
            (uint32_t)g.b_mn << 30;
   t.a_mn = t.m * kTileM + rank * kHalfM;
+  t.a_rows = g.a_rows;
   t.b_mn = g.b_mn0 + t.n * g.tile_n + rank * (g.tile_n / 2);
   t.a_k = kb0 * kBlockK;
   t.b_k = g.b_k0 + kb0 * kBlockK;
@@ -587,7 +607,9 @@ gemm_kernel(const __grid_constant__ GemmArgs args) {
         const CUtensorMap* const map_b = &args.job[t.job].b;
         const int blocks = work_blocks(t.work), half_n = work_tile_n(t.work) / 2;
         const bool a_mn = work_a_mn(t.work), b_mn = work_b_mn(t.work);
-        const uint32_t bytes = 2 * (kStageA + half_n * (kBlockK * 2));
+        const uint32_t bytes_a = t.a_rows > 0 ? t.a_rows * (kBlockK * 2) : 2 * kStageA;
+        const uint32_t bytes = bytes_a + 2 * half_n * (kBlockK * 2);
+        const bool copies_a = leader || t.a_rows == 0;
         for (int kb = 0; kb < blocks; ++kb) {
           if (!(ok = mbar_wait(&bar.empty[s], phase ^ 1))) break;
           uint8_t* a = stages + s * (kStageA + kStageB);
@@ -599,7 +621,7 @@ gemm_kernel(const __grid_constant__ GemmArgs args) {
           if (a_mn) {
             for (int i = 0; i < kHalfM / 64; ++i)
               tma_load(a + i * (kBlockK * 128), map_a, t.a_mn + 64 * i, ka, full);
-          } else {
+          } else if (copies_a) {
             tma_load(a, map_a, ka, t.a_mn, full);
           }
           if (b_mn) {
@@ -794,14 +816,23 @@ xent_dx_kernel(const float* __restrict__ sum, int splits, int64_t tokens, int64_
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < tokens * groups;
        i += (int64_t)gridDim.x * 256) {
     const int64_t r = i / groups, c = (i - r * groups) * 8;
-    float4 v[2] = {make_float4(0, 0, 0, 0), make_float4(0, 0, 0, 0)};
-    for (int s = 0; s < splits; ++s) {
-      const float4* a = reinterpret_cast<const float4*>(sum + (s * tokens + r) * pitch + c);
+    const float4* a = reinterpret_cast<const float4*>(sum + r * pitch + c);
+    const int64_t next = tokens * pitch / 4;
+    float4 v[2] = {a[0], a[1]};
+    for (int s = 1; s < splits; s += 5) {     // five splits' loads at a time
+      float4 b[5][2];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const float4 b = __ldcs(a + h);
-        v[h] = make_float4(v[h].x + b.x, v[h].y + b.y, v[h].z + b.z, v[h].w + b.w);
+      for (int k = 0; k < 5; ++k) {
+        const bool in = s + k < splits;
+        b[k][0] = in ? a[(s + k) * next] : make_float4(0, 0, 0, 0);
+        b[k][1] = in ? a[(s + k) * next + 1] : make_float4(0, 0, 0, 0);
       }
+#pragma unroll
+      for (int k = 0; k < 5; ++k)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          v[h] = make_float4(v[h].x + b[k][h].x, v[h].y + b[k][h].y, v[h].z + b[k][h].z,
+                             v[h].w + b[k][h].w);
     }
     float e[8] = {v[0].x, v[0].y, v[0].z, v[0].w, v[1].x, v[1].y, v[1].z, v[1].w};
     const bool zero = target[r] == ignore;
@@ -918,7 +949,8 @@ int width_of(int64_t dim) {
 int blocks_of(int64_t k) { return (int)((k + kBlockK - 1) / kBlockK); }
 
 // Ranges of k for dx: its tiles are few and long when the tokens are few, so
-// they are cut until one is at most a third of a pair's share of a launch.
+// they are cut until one is at most a third of a pair's share of a launch, into
+// 8 or, while the parts fit 64 MiB, up to 16 (more cost more to add up).
 int dx_splits(const XentArgs& a, int64_t piece, int sms) {
   const int64_t tiles_t = up(a.rows, kTileM) / kTileM;
   const int64_t tiles_d = (a.dim + width_of(a.dim) - 1) / width_of(a.dim);
@@ -926,7 +958,9 @@ int dx_splits(const XentArgs& a, int64_t piece, int sms) {
   const int64_t dw = up(piece, kTileM) / kTileM * tiles_d * blocks_of(a.rows);
   const int64_t probs = tiles_t * (piece / kTileN) * blocks_of(a.dim);
   const int64_t share = std::max((dx + dw + probs) / (sms / 2) / 3, (int64_t)4);
-  return (int)std::min((blocks_of(piece) + share - 1) / share, (int64_t)8);
+  const int64_t fit = (64ll << 20) / (a.rows * tiles_d * width_of(a.dim) * 4);
+  return (int)std::min((blocks_of(piece) + share - 1) / share,
+                       std::min(std::max(fit, (int64_t)8), (int64_t)16));
 }
 
 class Layout {
@@ -944,7 +978,8 @@ class Layout {
 
 // Few tokens: the vocabulary's rows take the tiles' 256 rows and the tokens
 // their columns, as many as there are; a stage then holds little besides w,
-// which is all that has to be read.  (See the table of figures for both ways.)
+// which is all that has to be read.  24 x 768 x 50257: 19.9 us, 27.3 with the
+// tokens as rows (mostly past x's end); 128 x 768 x 200000: 56 us against 75.
 constexpr int64_t kSwapTokens = 128;
 
 struct ForwardScratch {
@@ -1077,14 +1112,15 @@ cudaError_t launch_xent_backward(const XentArgs& a, char* scratch, int* error, i
   // x and w as K-major operands of the logits, and MN-major ones of dw and dx;
   // p as dx's K-major and dw's MN-major operand
   CUtensorMap x_k, w_k, x_mn, w_mn, p_k[2], p_mn[2];
-  if ((e = make_map(&x_k, bf16, x, a.rows, a.dim, pitch, kHalfM)) != cudaSuccess ||
+  const int a_rows = a.rows <= kHalfM ? (int)up(a.rows, 8) : 0, box = a_rows > 0 ? a_rows : kHalfM;
+  if ((e = make_map(&x_k, bf16, x, a.rows, a.dim, pitch, box)) != cudaSuccess ||
       (e = make_map(&w_k, bf16, w, a.vocab, a.dim, pitch, kTileN / 2)) != cudaSuccess ||
       (e = make_map(&x_mn, bf16, x, a.rows, a.dim, pitch, kBlockK)) != cudaSuccess ||
       (e = make_map(&w_mn, bf16, w, a.vocab, a.dim, pitch, kBlockK)) != cudaSuccess)
     return e;
   for (int i = 0; i < 2 && i < s.pieces; ++i) {
     const char* p = scratch + s.probs[i];
-    if ((e = make_map(&p_k[i], bf16, p, a.rows, s.piece, s.piece, kHalfM)) != cudaSuccess ||
+    if ((e = make_map(&p_k[i], bf16, p, a.rows, s.piece, s.piece, box)) != cudaSuccess ||
         (e = make_map(&p_mn[i], bf16, p, a.rows, s.piece, s.piece, kBlockK)) != cudaSuccess)
       return e;
   }
@@ -1115,17 +1151,17 @@ cudaError_t launch_xent_backward(const XentArgs& a, char* scratch, int* error, i
       const int at = (int)((i - 1) & 1), kb = blocks_of(cols);
       g.job[g.jobs++] = {p_k[at], w_mn,
                          {kDx, tiles_t, tiles_d, width, kb, (kb + s.splits - 1) / s.splits,
-                          s.splits, 0, (int)v0, 0, 1, i == 1, v0, nullptr}};
+                          s.splits, 0, (int)v0, 0, 1, i == 1, v0, nullptr, a_rows}};
       g.job[g.jobs++] = {p_mn[at], x_mn,
                          {kDw, (int)(up(cols, kTileM) / kTileM), tiles_d, width,
-                          blocks_of(a.rows), blocks_of(a.rows), 1, 0, 0, 1, 1, 0, v0, nullptr}};
+                          blocks_of(a.rows), blocks_of(a.rows), 1, 0, 0, 1, 1, 0, v0, nullptr, 0}};
     }
     if (i < s.pieces) {
       const int64_t v0 = i * s.piece, cols = std::min(s.piece, a.vocab - v0);
       g.job[g.jobs++] = {x_k, w_k,
                          {kProbs, tiles_t, (int)(up(cols, kTileN) / kTileN), kTileN,
                           blocks_of(a.dim), blocks_of(a.dim), 1, (int)v0, 0, 0, 0, 0, v0,
-                          reinterpret_cast<uint16_t*>(scratch + s.probs[i & 1])}};
+                          reinterpret_cast<uint16_t*>(scratch + s.probs[i & 1]), a_rows}};
     }
     if (mark) mark(kXentGradsK, 0, stream);
     e = launch_gemm(g, bf16, sms, stream);

@@ -152,7 +152,7 @@ ln_forward_kernel(const LnForward a) {
       a.rstd[r] = rstd;
       if (!FP8) a.mean[r] = mean;
     }
-    float scale = 1.0f;
+    float scale = 1.0f, to_code = 1.0f;
     bool finite = true;
     if constexpr (FP8) {
       // |x - mean| * rstd rounds monotonically, so this is max |xhat|
@@ -160,6 +160,10 @@ ln_forward_kernel(const LnForward a) {
       scale = scale_from_amax_bits(amax, 448.0f);
       finite = amax < 0x7F800000u;
       if (t == 0) a.scales[r] = scale;
+      // xhat * scale = (x - mean) * 448 / max |x - mean|: taken so, the codes
+      // carry the rounding of one quotient instead of rstd's and the scale's
+      to_code = __fdiv_rn(448.0f, qm.y);
+      if (scale == 1.0f || nonfinite(to_code)) to_code = rstd * scale;
     }
 #pragma unroll
     for (int v = 0; v < VPT; ++v) {
@@ -190,7 +194,7 @@ ln_forward_kernel(const LnForward a) {
         y[2 * j] = p.x;
         y[2 * j + 1] = p.y;
         if constexpr (FP8) {
-          const float2 c = mul2(h, splat2(scale));
+          const float2 c = mul2(x[4 * v + j], splat2(to_code));
           z[2 * j] = c.x;
           z[2 * j + 1] = c.y;
         }

@@ -159,20 +159,20 @@ __device__ __forceinline__ void store_rows16(Turn& turn, uint16_t* out, int64_t 
                    pack16<BF16>(v[8 * j + 4], v[8 * j + 5]),
                    pack16<BF16>(v[8 * j + 6], v[8 * j + 7]));
   __syncwarp();
-  const int word = lane & 7, c = 8 * word;
+  const int word = lane & 7, c = 8 * word, row0 = lane >> 3;
+  uint16_t* p = out + row0 * pitch + c;
+  const int64_t step = 4 * pitch;
+  if (c + 8 <= cols && (((uint64_t)reinterpret_cast<uintptr_t>(p) | (uint64_t)pitch * 2) & 15u) == 0) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int row = 4 * i + (lane >> 3);
-    const uint4 w = turn.at(row, word);
-    uint16_t* p = out + row * pitch + c;
-    if (row >= rows || c >= cols) continue;
-    if (c + 8 <= cols && (reinterpret_cast<uintptr_t>(p) & 15u) == 0) {
-      *reinterpret_cast<uint4*>(p) = w;
-    } else {
+    for (int i = 0; i < 8; ++i, p += step)
+      if (4 * i + row0 < rows) *reinterpret_cast<uint4*>(p) = turn.at(4 * i + row0, word);
+  } else if (c < cols) {
+    for (int i = 0; i < 8; ++i, p += step) {
+      const uint4 w = turn.at(4 * i + row0, word);
       const uint32_t e[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
       for (int k = 0; k < 8; ++k)
-        if (c + k < cols) p[k] = (uint16_t)(e[k / 2] >> (16 * (k & 1)));
+        if (4 * i + row0 < rows && c + k < cols) p[k] = (uint16_t)(e[k / 2] >> (16 * (k & 1)));
     }
   }
   __syncwarp();
@@ -182,14 +182,14 @@ __device__ __forceinline__ void store_rows16(Turn& turn, uint16_t* out, int64_t 
 // pitch, fp32 at a 16-byte pitch; rows below `rows`.
 __device__ __forceinline__ void add_rows32(Turn& turn, float* out, int64_t pitch, int rows,
                                            bool first, const uint32_t (&r)[32]) {
-  const int lane = threadIdx.x & 31, word = lane & 7;
+  const int lane = threadIdx.x & 31, word = lane & 7, row0 = lane >> 3;
+  float* const p = out + row0 * pitch + 4 * word;
+  const int64_t step = 4 * pitch;
   float4 s[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const int row = 4 * i + (lane >> 3);
     s[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    if (!first && row < rows)
-      s[i] = *reinterpret_cast<const float4*>(out + row * pitch + 4 * word);
+    if (!first && 4 * i + row0 < rows) s[i] = *reinterpret_cast<const float4*>(p + i * step);
   }
 #pragma unroll
   for (int j = 0; j < 8; ++j)
@@ -197,10 +197,9 @@ __device__ __forceinline__ void add_rows32(Turn& turn, float* out, int64_t pitch
   __syncwarp();
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const int row = 4 * i + (lane >> 3);
-    const uint4 w = turn.at(row, word);
-    if (row < rows)
-      *reinterpret_cast<float4*>(out + row * pitch + 4 * word) =
+    const uint4 w = turn.at(4 * i + row0, word);
+    if (4 * i + row0 < rows)
+      *reinterpret_cast<float4*>(p + i * step) =
           make_float4(s[i].x + __uint_as_float(w.x), s[i].y + __uint_as_float(w.y),
                       s[i].z + __uint_as_float(w.z), s[i].w + __uint_as_float(w.w));
   }
@@ -684,21 +683,33 @@ gemm_kernel(const __grid_constant__ GemmArgs args) {
     Turn& turn = turns[warp];
     SwappedStats swapped;
     int buf = 0, phase = 0;
-    for (;;) {
+    // A tile's row inputs are asked for one tile ahead, so that their latency
+    // lies under the tile before.
+    const auto read = [&](Tile* t, RowIn* in) {
       const Tile* next = reader.next(bar);
-      if (!(ok = next != nullptr)) break;
-      const Tile t = *next;
-      if (t.work == kNoWork) break;
+      if (next == nullptr) return false;
+      *t = *next;
+      if (t->work == kNoWork) return true;
       reader.done(bar);
+      *in = row_in(args.job[t->job].shape, args.out,
+                   (int64_t)t->m * kTileM + rank * kHalfM + (threadIdx.x & 127));
+      return true;
+    };
+    Tile t;
+    RowIn in;
+    ok = read(&t, &in);
+    while (ok && t.work != kNoWork) {
       const GemmShape& g = args.job[t.job].shape;
       const int half = warp / 4, cols = work_tile_n(t.work) / 2;
       const Strip strip = {tmem + buf * kTileN + half * cols + ((uint32_t)(warp % 4) << 21),
                            (int64_t)t.m * kTileM + rank * kHalfM + (threadIdx.x & 127),
                            ((int64_t)t.n * 2 + half) * cols, cols, 2 * t.n + half};
-      const RowIn in = row_in(g, args.out, strip.row);
       ok = __all_sync(0xFFFFFFFFu, mbar_wait(&bar.acc_full[buf], phase));
       if (!ok) break;
       tcgen_fence_after();
+      Tile after;
+      RowIn in_after;
+      if (!(ok = read(&after, &in_after))) break;
       if (g.mode == kStats) stats_strip(args.out, strip, in);
       else if (g.mode == kStatsSwapped)
         swapped.add(g, args.out, tmem + buf * kTileN + ((uint32_t)(warp % 4) << 21),
@@ -713,6 +724,8 @@ gemm_kernel(const __grid_constant__ GemmArgs args) {
         cluster_arrive_relaxed(cluster_addr(&bar.acc_empty[buf], 0));
       buf ^= 1;
       if (buf == 0) phase ^= 1;
+      t = after;
+      in = in_after;
     }
     if (args.job[0].shape.mode == kStatsSwapped) swapped.finish(args.out, warp, turns);
   }
@@ -766,29 +779,17 @@ xent_join_kernel(const float2* __restrict__ partial, int strips, int64_t tokens,
 }
 
 // Rows of a matrix at a 16-byte pitch, those of ignored tokens zero (target
-// NULL: none is).  With `top`, one more CTA finds the largest finite |dloss| of
-// the tokens that count (one that is not finite spoils its own token's dx, not
-// the others').
+// NULL: none is).  With `top` (zeroed before), also the largest finite |dloss|
+// of the tokens that count (one that is not finite spoils its own token's dx,
+// not the others'); a maximum, so the order of the CTAs does not matter.
 __global__ void __launch_bounds__(256)
 xent_copy_kernel(const uint16_t* __restrict__ src, int64_t rows, int64_t dim, int64_t pitch,
                  const long long* __restrict__ target, long long ignore,
                  uint16_t* __restrict__ dst, bool vec, const float* __restrict__ dloss,
-                 float* __restrict__ top) {
-  const unsigned copying = gridDim.x - (top != nullptr ? 1 : 0);
+                 uint32_t* __restrict__ top) {
   begin_after_previous();
-  if (blockIdx.x == copying) {
-    __shared__ uint32_t sh[8];
-    uint32_t m = 0;
-#pragma unroll 8
-    for (int64_t i = threadIdx.x; i < rows; i += 256) {
-      const float d = dloss[i];          // (loaded whatever the target: no wait between)
-      if (target[i] != ignore && !nonfinite(d)) m = max(m, abs_bits(d));
-    }
-    m = block_max_u32<256>(m, sh);
-    if (threadIdx.x == 0) *top = __uint_as_float(m);
-    return;
-  }
-  for (int64_t r = blockIdx.x; r < rows; r += copying) {
+  uint32_t most = 0;
+  for (int64_t r = blockIdx.x; r < rows; r += gridDim.x) {
     const bool zero = target != nullptr && target[r] == ignore;
     if (vec) {
       const uint4* s = reinterpret_cast<const uint4*>(src + r * dim);
@@ -799,7 +800,10 @@ xent_copy_kernel(const uint16_t* __restrict__ src, int64_t rows, int64_t dim, in
       for (int64_t c = threadIdx.x; c < pitch; c += 256)
         dst[r * pitch + c] = zero || c >= dim ? (uint16_t)0 : src[r * dim + c];
     }
+    if (top != nullptr && threadIdx.x == 0 && !zero && !nonfinite(dloss[r]))
+      most = max(most, abs_bits(dloss[r]));
   }
+  if (most > 0) atomicMax(top, most);
 }
 
 // dx from its fp32 parts: the splits added in order, scaled back, rounded; 0
@@ -912,12 +916,12 @@ bool direct(const void* p, int64_t dim) {
 cudaError_t copy_rows(const void* src, int64_t rows, int64_t dim, int64_t pitch,
                       const int64_t* target, int64_t ignore, char* dst, int sms,
                       cudaStream_t stream, const float* dloss = nullptr, float* top = nullptr) {
-  const int64_t grid = std::min(rows, (int64_t)8 * sms) + (top != nullptr ? 1 : 0);
+  const int64_t grid = std::min(rows, (int64_t)8 * sms);
   return launch(true, xent_copy_kernel, (unsigned)grid, 256, 0, stream,
                       static_cast<const uint16_t*>(src), rows, dim, pitch,
                       reinterpret_cast<const long long*>(target), (long long)ignore,
                       reinterpret_cast<uint16_t*>(dst), direct(src, dim) && pitch == dim, dloss,
-                      top);
+                      reinterpret_cast<uint32_t*>(top));
 }
 
 // Tokens of one forward launch: bounds the scratch of the tiles' statistics.
@@ -1015,8 +1019,8 @@ BackwardScratch backward_scratch(const XentArgs& a, int sms) {
   s.piece = piece_columns(a, sms);
   s.pieces = (a.vocab + s.piece - 1) / s.piece;
   s.splits = dx_splits(a, s.piece, sms);
-  s.next = l.take((s.pieces + 1) * 4);
-  s.top = l.take(4);
+  s.next = l.take((s.pieces + 2) * 4);     // the launches' counters, and max |dloss|
+  s.top = s.next + (size_t)(s.pieces + 1) * 4;
   s.x = l.take(a.rows * pitch * 2);
   if (!direct(a.w, a.dim)) s.w = l.take(a.vocab * pitch * 2);
   for (int i = 0; i < 2 && i < s.pieces; ++i) s.probs[i] = l.take(a.rows * s.piece * 2);
@@ -1097,7 +1101,7 @@ cudaError_t launch_xent_backward(const XentArgs& a, char* scratch, int* error, i
   const char* w = static_cast<const char*>(a.w);
   int* next = reinterpret_cast<int*>(scratch + s.next);
   float* top = reinterpret_cast<float*>(scratch + s.top);
-  cudaError_t e = cudaMemsetAsync(next, 0, (size_t)(s.pieces + 1) * 4, stream);
+  cudaError_t e = cudaMemsetAsync(next, 0, (size_t)(s.pieces + 2) * 4, stream);
   if (mark) mark(kXentPrepareK, 0, stream);
   if (e == cudaSuccess)
     e = copy_rows(a.x, a.rows, a.dim, pitch, a.target, a.ignore, scratch + s.x, sms, stream,

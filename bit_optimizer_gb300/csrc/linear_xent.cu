@@ -162,17 +162,26 @@ __device__ __forceinline__ void store_rows16(Turn& turn, uint16_t* out, int64_t 
   const int word = lane & 7, c = 8 * word, row0 = lane >> 3;
   uint16_t* p = out + row0 * pitch + c;
   const int64_t step = 4 * pitch;
-  if (c + 8 <= cols && (((uint64_t)reinterpret_cast<uintptr_t>(p) | (uint64_t)pitch * 2) & 15u) == 0) {
+  // (with rows of whole 16-byte words, cols is a multiple of 8 as well)
+  if ((((uint64_t)reinterpret_cast<uintptr_t>(out) | (uint64_t)pitch * 2) & 15u) == 0) {
 #pragma unroll
     for (int i = 0; i < 8; ++i, p += step)
-      if (4 * i + row0 < rows) *reinterpret_cast<uint4*>(p) = turn.at(4 * i + row0, word);
-  } else if (c < cols) {
-    for (int i = 0; i < 8; ++i, p += step) {
-      const uint4 w = turn.at(4 * i + row0, word);
-      const uint32_t e[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-      for (int k = 0; k < 8; ++k)
-        if (4 * i + row0 < rows && c + k < cols) p[k] = (uint16_t)(e[k / 2] >> (16 * (k & 1)));
+      if (c < cols && 4 * i + row0 < rows)
+        *reinterpret_cast<uint4*>(p) = turn.at(4 * i + row0, word);
+  } else {
+    // rows that start anywhere: a row at a time, a pair of columns to a lane, in
+    // aligned pairs of the row's memory
+    const int n = min(64, cols);
+    for (int i = 0; i < rows && i < 32; ++i) {
+      const uint32_t w = reinterpret_cast<const uint32_t*>(&turn.at(i, lane >> 2))[lane & 3];
+      const uint32_t next = __shfl_down_sync(0xFFFFFFFFu, w, 1);
+      uint16_t* q = out + i * pitch;
+      const bool odd = (reinterpret_cast<uintptr_t>(q) & 2u) != 0;
+      const uint32_t both = odd ? w >> 16 | next << 16 : w;
+      const int first = 2 * lane + (odd ? 1 : 0);
+      if (odd && lane == 0 && n > 0) q[0] = (uint16_t)w;
+      if (first + 1 < n) *reinterpret_cast<uint32_t*>(q + first) = both;
+      else if (first < n) q[first] = (uint16_t)both;
     }
   }
   __syncwarp();
@@ -789,18 +798,44 @@ xent_copy_kernel(const uint16_t* __restrict__ src, int64_t rows, int64_t dim, in
                  uint32_t* __restrict__ top) {
   begin_after_previous();
   uint32_t most = 0;
-  for (int64_t r = blockIdx.x; r < rows; r += gridDim.x) {
+  const int lane = threadIdx.x & 31;   // a warp to a row
+  for (int64_t r = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); r < rows;
+       r += (int64_t)gridDim.x * 8) {
     const bool zero = target != nullptr && target[r] == ignore;
     if (vec) {
       const uint4* s = reinterpret_cast<const uint4*>(src + r * dim);
       uint4* d = reinterpret_cast<uint4*>(dst + r * pitch);
-      for (int64_t c = threadIdx.x; c < dim / 8; c += 256)
+#pragma unroll 4
+      for (int64_t c = lane; c < dim / 8; c += 32)
         d[c] = zero ? make_uint4(0, 0, 0, 0) : s[c];
     } else {
-      for (int64_t c = threadIdx.x; c < pitch; c += 256)
-        dst[r * pitch + c] = zero || c >= dim ? (uint16_t)0 : src[r * dim + c];
+      // (the pitch is a multiple of 8 and dst aligned; src may be neither)
+      const uint16_t* from = src + r * dim;
+      const bool even = (reinterpret_cast<uintptr_t>(from) & 2u) == 0;
+#pragma unroll 2
+      for (int64_t c = 8 * lane; c < pitch; c += 8 * 32) {
+        uint32_t w[4] = {0, 0, 0, 0};
+        const uint16_t* p = from + c;
+        if (zero) {
+        } else if (c + 8 > dim) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            if (c + k < dim) w[k / 2] |= (uint32_t)p[k] << (16 * (k & 1));
+        } else if (even) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) w[k] = reinterpret_cast<const uint32_t*>(p)[k];
+        } else {   // the first element, three words that start at the second, the last
+          const uint32_t* q = reinterpret_cast<const uint32_t*>(p + 1);
+          const uint32_t first = p[0], a = q[0], b = q[1], d = q[2], last = p[7];
+          w[0] = first | a << 16;
+          w[1] = a >> 16 | b << 16;
+          w[2] = b >> 16 | d << 16;
+          w[3] = d >> 16 | last << 16;
+        }
+        *reinterpret_cast<uint4*>(dst + r * pitch + c) = make_uint4(w[0], w[1], w[2], w[3]);
+      }
     }
-    if (top != nullptr && threadIdx.x == 0 && !zero && !nonfinite(dloss[r]))
+    if (top != nullptr && lane == 0 && !zero && !nonfinite(dloss[r]))
       most = max(most, abs_bits(dloss[r]));
   }
   if (most > 0) atomicMax(top, most);
@@ -916,7 +951,7 @@ bool direct(const void* p, int64_t dim) {
 cudaError_t copy_rows(const void* src, int64_t rows, int64_t dim, int64_t pitch,
                       const int64_t* target, int64_t ignore, char* dst, int sms,
                       cudaStream_t stream, const float* dloss = nullptr, float* top = nullptr) {
-  const int64_t grid = std::min(rows, (int64_t)8 * sms);
+  const int64_t grid = std::min((rows + 7) / 8, (int64_t)8 * sms);
   return launch(true, xent_copy_kernel, (unsigned)grid, 256, 0, stream,
                       static_cast<const uint16_t*>(src), rows, dim, pitch,
                       reinterpret_cast<const long long*>(target), (long long)ignore,

@@ -112,7 +112,10 @@ struct GemmOut {
 };
 
 // One launch: up to three products that do not depend on one another, those
-// with the longest tiles first.
+// with the longest tiles first.  (Two of them tile by tile in turn, which would
+// put p's long epilogues between longer products, was slower, 1.92 against 1.51
+// ms at 8192 x 1024: pairs that work on one product at a time read the same
+// operands at about the same time.)
 constexpr int kMaxJobs = 3;
 struct GemmArgs {
   GemmJob job[kMaxJobs];
@@ -749,7 +752,7 @@ gemm_kernel(const __grid_constant__ GemmArgs args) {
 // Joins the column strips of 32 tokens, a token to each lane (neighbouring
 // tokens' statistics lie side by side): warp k takes strips k, k + 32, ... in
 // order, then the 32 warps' results are joined in order.
-__global__ void __launch_bounds__(1024)
+__global__ void __launch_bounds__(1024, 2)
 xent_join_kernel(const float2* __restrict__ partial, int strips, int64_t tokens, int64_t vocab,
                  const long long* __restrict__ target, long long ignore,
                  const float* __restrict__ target_logit, float* __restrict__ loss,

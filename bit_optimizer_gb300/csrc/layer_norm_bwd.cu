@@ -351,7 +351,7 @@ cudaError_t go_form(const LnBackward& a, float* partial, unsigned grid, cudaStre
   const int ring = VEC == 8 ? kRingBytes<DT, VPT, NT, FP8> : 0;
   const int merge = RPC > 1 ? RPC * 2 * (int)sizeof(float) * (int)a.cols : 0;
   const int smem = ring > merge ? ring : merge;
-  if (smem > 48 * 1024) {
+  if (smem > 47 * 1024) {   // with the static arrays beside it, above 48 KB
     const cudaError_t e =
         cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;

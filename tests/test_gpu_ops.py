@@ -266,6 +266,17 @@ def test_layer_norm_unaligned_and_without_bias(bo, cols):
     check_norm_grad(bo, dy, w, r, codes=shifted(codes), scales=scales)
 
 
+@pytest.mark.parametrize("cols", [383, 384, 764, 767, 768, 1535, 1536, 3070])
+def test_layer_norm_gradient_of_unaligned_rows_near_a_shared_memory_limit(bo, cols):
+    """Widths whose row sums take almost 48 KB of a CTA's shared memory."""
+    x = shifted(randn(40, cols, dtype=torch.bfloat16, seed=1))
+    w = 1 + 0.1 * randn(cols, seed=2)
+    dy = shifted(randn(40, cols, dtype=torch.bfloat16, seed=3))
+    m, r, codes, scales = check_norm(bo, x, w, None, 1e-6)
+    check_norm_grad(bo, dy, w, r, x=x, mean=m)
+    check_norm_grad(bo, dy, w, r, codes=shifted(codes), scales=scales)
+
+
 def test_layer_norm_many_rows(bo):
     """More rows than one visit of every CTA, and a row count that is no
     multiple of the rows a CTA takes at a time."""

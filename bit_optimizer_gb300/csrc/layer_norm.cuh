@@ -5,7 +5,11 @@
 // are used.  VEC = 8: vector v of thread t holds elements [8 (v TPR + t), + 8)
 // (C and the buffers allow 16-byte accesses); VEC = 1: its element e is number
 // (8 v + e) TPR + t, so that neighbouring threads read neighbouring elements
-// of rows that start anywhere.
+// of rows that start anywhere.  VEC = kLnFlat: the vectors are those of the flat
+// tensor; the first one of a row begins `shift` = (row C) mod 8 elements before
+// the row, and the vectors at its ends are masked.  A CTA's row slots step by a
+// multiple of 8 rows, so that shift, and with it what a thread holds of the
+// parameters and their gradients, is the same for all rows of a slot.
 #pragma once
 
 #include "ops_internal.cuh"
@@ -14,7 +18,7 @@ namespace fp8opt {
 
 template <int TPR, int VEC>
 __device__ __forceinline__ int ln_col(int v, int e, int t) {
-  return VEC == 8 ? (v * TPR + t) * 8 + e : (v * 8 + e) * TPR + t;
+  return VEC != 1 ? (v * TPR + t) * 8 + e : (v * 8 + e) * TPR + t;
 }
 
 // Whether that element lies in the row (for VEC = 8 the whole vector does or
@@ -25,6 +29,36 @@ template <int TPR, int VEC, bool FULL>
 __device__ __forceinline__ bool ln_in(int v, int e, int t, int cols) {
   return FULL || ln_col<TPR, VEC>(v, VEC == 8 ? 0 : e, t) < cols;
 }
+
+// kLnFlat: of the vector at c, counted from the first vector's start, the
+// elements from shift to end = shift + C belong to the row.
+__device__ __forceinline__ void ln_mask(float* x, int c, int shift, int end) {
+  if (c < shift || c + 8 > end) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (c + e < shift || c + e >= end) x[e] = 0.0f;
+  }
+}
+
+__device__ __forceinline__ void ln_mask(float2* x, int c, int shift, int end) {
+  if (c < shift || c + 8 > end) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      if (c + 2 * e < shift || c + 2 * e >= end) x[e].x = 0.0f;
+      if (c + 2 * e + 1 < shift || c + 2 * e + 1 >= end) x[e].y = 0.0f;
+    }
+  }
+}
+
+// Rows of one slot that are to have the same shift: CTAs of a launch of at most
+// `most`, when some visit more than one row a slot.
+inline int64_t ln_grid(int64_t ctas, int64_t most, int form) {
+  if (form == kLnFlat && most >= 8) most &= ~(int64_t)7;
+  return ctas < most ? ctas : most;
+}
+
+// Columns that the threads of a row have to hold.
+inline int64_t ln_span(int64_t cols, int form) { return form == kLnFlat ? cols + 7 : cols; }
 
 // Eight elements of vector v as raw words (VEC 8) or widened values (VEC 1);
 // the elements past the row's end are zero.
@@ -109,6 +143,21 @@ __device__ __forceinline__ void ln_store(void* row, int v, int t, int cols, cons
   }
 }
 
+// kLnFlat: the same to the row at `row` (elements of a row of another CTA lie
+// in its end vectors).
+template <int DT, int TPR>
+__device__ __forceinline__ void ln_store_flat(char* row, int v, int t, int shift, int end,
+                                              const float* x) {
+  const int c = ln_col<TPR, 8>(v, 0, t);
+  if (c >= shift && c + 8 <= end) {
+    ln_store<DT, 8, TPR>(row - shift * (DT == kF32 ? 4 : 2), v, t, end, x);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (c + e >= shift && c + e < end) store1<DT>(row, c + e - shift, x[e]);
+  }
+}
+
 // One element of a parameter vector of any element type.
 __device__ __forceinline__ float ln_param1(const void* p, int dtype, int64_t c) {
   return dtype == kF32 ? load1<kF32>(p, c)
@@ -152,9 +201,20 @@ __device__ __forceinline__ void ln_param(const void* p, int dtype, float missing
   }
 }
 
+// kLnFlat: the same of a thread's share of a row that begins at shift.
+template <int TPR>
+__device__ __forceinline__ void ln_param_flat(const void* p, int dtype, int v, int t, int shift,
+                                              int end, float* x) {
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const int c = ln_col<TPR, 8>(v, e, t);
+    x[e] = c >= shift && c < end ? ln_param1(p, dtype, c - shift) : 0.0f;
+  }
+}
+
 // ------------------------------------------------------------ the row ring
 //
-// With VEC = 8 a thread copies its own share of the coming rows into shared
+// With vectors a thread copies its own share of the coming rows into shared
 // memory with cp.async, STAGES - 1 rows ahead, and reads back only what it
 // copied itself, so the ring needs no barrier: HBM latency is covered by
 // copies in flight instead of by registers or more threads.
@@ -166,6 +226,28 @@ __device__ __forceinline__ void copy_async(void* smem, const void* global) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(d), "l"(global) : "memory");
   else
     asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(d), "l"(global) : "memory");
+}
+
+// The first `bytes` of them, and zeros.
+template <int BYTES>
+__device__ __forceinline__ void copy_async(void* smem, const void* global, int bytes) {
+  const uint32_t d = (uint32_t)__cvta_generic_to_shared(smem);
+  if constexpr (BYTES == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;"
+                 ::"r"(d), "l"(global), "r"(bytes) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;"
+                 ::"r"(d), "l"(global), "r"(bytes) : "memory");
+}
+
+// Elements from the start of the row's first vector to the tensor's end, where
+// that matters (kLnFlat: the last vector ends where the tensor does).
+__device__ __forceinline__ int ln_left(int64_t rows, int64_t cols, int shift) {
+  return (int)min(rows * cols, (int64_t)1 << 20) + shift;
+}
+
+__device__ __forceinline__ int ln_bytes(int elements, int size, int skip, int most) {
+  return min(max(elements * size - skip, 0), most);
 }
 
 __device__ __forceinline__ void copy_commit() {

@@ -16,6 +16,8 @@
 // 34.6 us, 4.85 TB/s, 0.71 of the measured copy bandwidth; 65536 x 1024 from x:
 // 0.82.  With the row slots' sums added one slot after the other the end of a
 // CTA alone took 30 us; side by side it is one pass.
+// Rows that start anywhere, from x (by elements): 32768 x 1501 83 us, 0.52 (183),
+// 32768 x 2041 84 us (237), 32768 x 2049 161 us (301).
 #include "layer_norm.cuh"
 
 namespace fp8opt {
@@ -75,20 +77,35 @@ ln_backward_kernel(const LnBackward a, float* __restrict__ partial) {
   const auto at_code = [&](int stage, int v) -> uint2* {
     return reinterpret_cast<uint2*>(ring2) + (stage * VPT + v) * NT + threadIdx.x;
   };
+  int64_t r = (int64_t)blockIdx.x * RPC + slot;
+  const int shift = VEC == kLnFlat ? (int)(r * a.cols & 7) : 0, end = cols + shift;
   const auto fetch = [&](int stage, int64_t row) {
     if (row < a.rows) {
-      const size_t at = (size_t)row * a.cols;
+      const size_t at = (size_t)row * a.cols - shift;
+      const int left = VEC == kLnFlat ? ln_left(a.rows - row, a.cols, shift) : 0;
 #pragma unroll
       for (int v = 0; v < VPT; ++v) {
         const int c = ln_col<TPR, 8>(v, 0, t);
-        if (!FULL && c >= cols) continue;
+        if (!FULL && c >= end) continue;
+        if constexpr (VEC == kLnFlat) {
 #pragma unroll
-        for (int q = 0; q < Q; ++q) {
-          copy_async<16>(at_dy(stage, v, q), static_cast<const char*>(a.dy) + (at + c) * es + 16 * q);
-          if (!FP8)
-            copy_async<16>(at_x(stage, v, q), static_cast<const char*>(a.x) + (at + c) * es + 16 * q);
+          for (int q = 0; q < Q; ++q) {
+            const int n = ln_bytes(left - c, (int)es, 16 * q, 16);
+            const size_t off = (at + c) * es + 16 * q;
+            if (n <= 0) continue;
+            copy_async<16>(at_dy(stage, v, q), static_cast<const char*>(a.dy) + off, n);
+            if (!FP8) copy_async<16>(at_x(stage, v, q), static_cast<const char*>(a.x) + off, n);
+          }
+          if (FP8) copy_async<8>(at_code(stage, v), a.codes + at + c, ln_bytes(left - c, 1, 0, 8));
+        } else {
+#pragma unroll
+          for (int q = 0; q < Q; ++q) {
+            const size_t off = (at + c) * es + 16 * q;
+            copy_async<16>(at_dy(stage, v, q), static_cast<const char*>(a.dy) + off);
+            if (!FP8) copy_async<16>(at_x(stage, v, q), static_cast<const char*>(a.x) + off);
+          }
+          if (FP8) copy_async<8>(at_code(stage, v), a.codes + at + c);
         }
-        if (FP8) copy_async<8>(at_code(stage, v), a.codes + at + c);
       }
     }
     copy_commit();
@@ -98,7 +115,10 @@ ln_backward_kernel(const LnBackward a, float* __restrict__ partial) {
 #pragma unroll
   for (int v = 0; v < VPT; ++v) {
     float p[8];
-    ln_param<VEC, TPR>(a.weight, a.wdtype, 0.0f, v, t, cols, p);
+    if constexpr (VEC == kLnFlat)
+      ln_param_flat<TPR>(a.weight, a.wdtype, v, t, shift, end, p);
+    else
+      ln_param<VEC, TPR>(a.weight, a.wdtype, 0.0f, v, t, cols, p);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       w[4 * v + j] = make_float2(p[2 * j], p[2 * j + 1]);
@@ -106,7 +126,6 @@ ln_backward_kernel(const LnBackward a, float* __restrict__ partial) {
     }
   }
 
-  int64_t r = (int64_t)blockIdx.x * RPC + slot;
   if constexpr (VEC == 8) {
 #pragma unroll
     for (int i = 0; i < ST; ++i)   // what lies past the row's end stays zero
@@ -120,6 +139,8 @@ ln_backward_kernel(const LnBackward a, float* __restrict__ partial) {
           }
           if (FP8) *at_code(i, v) = make_uint2(0, 0);
         }
+  }
+  if constexpr (VEC != 1) {
 #pragma unroll
     for (int i = 0; i < ST - 1; ++i) fetch(i, r + i * step);
   }
@@ -138,13 +159,18 @@ ln_backward_kernel(const LnBackward a, float* __restrict__ partial) {
       rstd_next = __ldg(a.rstd + r + step);
       other_next = __ldg(other + r + step);
     }
-    if constexpr (VEC == 8) copy_wait<ST - 2>();
+    if constexpr (VEC != 1) copy_wait<ST - 2>();
     float2 g[4 * VPT], x[4 * VPT];
     float2 s1 = make_float2(0.0f, 0.0f), s2 = s1;
 #pragma unroll
     for (int v = 0; v < VPT; ++v) {
       float d[8], e[8];
-      if constexpr (VEC == 8) {
+      if (VEC == kLnFlat && ln_col<TPR, 8>(v, 0, t) >= end) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) g[4 * v + j] = x[4 * v + j] = splat2(0.0f);
+        continue;
+      }
+      if constexpr (VEC != 1) {
         LnRaw<DT, 8> raw;
 #pragma unroll
         for (int q = 0; q < Q; ++q) raw.v[q] = *at_dy(stage, v, q);
@@ -169,13 +195,20 @@ ln_backward_kernel(const LnBackward a, float* __restrict__ partial) {
         }
       }
       ln_xhat<FP8>(e, sub, mul, x + 4 * v);
+      if constexpr (VEC == kLnFlat) {
+        const int c = ln_col<TPR, 8>(v, 0, t);
+        ln_mask(d, c, shift, end);
+        ln_mask(x + 4 * v, c, shift, end);
+      }
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const int i = 4 * v + j;
         g[i] = make_float2(d[2 * j], d[2 * j + 1]);
         // past the row's end dy is 0, and xhat must not be a NaN there
-        if (!ln_in<TPR, VEC, FULL>(v, 2 * j, t, cols)) x[i].x = 0.0f;
-        if (!ln_in<TPR, VEC, FULL>(v, 2 * j + 1, t, cols)) x[i].y = 0.0f;
+        if constexpr (VEC != kLnFlat) {
+          if (!ln_in<TPR, VEC, FULL>(v, 2 * j, t, cols)) x[i].x = 0.0f;
+          if (!ln_in<TPR, VEC, FULL>(v, 2 * j + 1, t, cols)) x[i].y = 0.0f;
+        }
         aw[i] = fma2(g[i], x[i], aw[i]);
         ab[i] = add2(ab[i], g[i]);
         g[i] = mul2(g[i], w[i]);
@@ -183,19 +216,22 @@ ln_backward_kernel(const LnBackward a, float* __restrict__ partial) {
         s2 = fma2(g[i], x[i], s2);
       }
     }
-    if constexpr (VEC == 8) fetch(stage == 0 ? ST - 1 : stage - 1, r + (ST - 1) * step);
+    if constexpr (VEC != 1) fetch(stage == 0 ? ST - 1 : stage - 1, r + (ST - 1) * step);
     const float2 s = row_reduce<kTwo, TPR>(s1.x + s1.y, s2.x + s2.y, sums[slot], turn, slot);
     const float2 m1 = splat2(-s.x * inv_c), m2 = splat2(-s.y * inv_c), k = splat2(rstd);
 #pragma unroll
     for (int v = 0; v < VPT; ++v) {
       float d[8];
+      if (VEC == kLnFlat && ln_col<TPR, 8>(v, 0, t) >= end) continue;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const float2 y = mul2(k, fma2(x[4 * v + j], m2, add2(g[4 * v + j], m1)));
         d[2 * j] = y.x;
         d[2 * j + 1] = y.y;
       }
-      ln_store<DT, VEC, TPR>(static_cast<char*>(a.dx) + (size_t)r * a.cols * es, v, t, cols, d);
+      char* const out = static_cast<char*>(a.dx) + (size_t)r * a.cols * es;
+      if constexpr (VEC == kLnFlat) ln_store_flat<DT, TPR>(out, v, t, shift, end, d);
+      else ln_store<DT, VEC, TPR>(out, v, t, cols, d);
     }
   }
 
@@ -224,8 +260,8 @@ ln_backward_kernel(const LnBackward a, float* __restrict__ partial) {
       } else {
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          const int c = ln_col<TPR, 1>(v, j, t);
-          if (c < cols) p[c] = (j & 1) ? s[h][j / 2].y : s[h][j / 2].x;
+          const int c = ln_col<TPR, VEC>(v, j, t) - shift;
+          if (c >= 0 && c < cols) p[c] = (j & 1) ? s[h][j / 2].y : s[h][j / 2].x;
         }
       }
     }
@@ -334,21 +370,20 @@ ln_backward_long_cols_kernel(const LnBackward a, int64_t rows_per, float* __rest
 constexpr int kLongParts = 16;   // row ranges of the long rows' dw and db
 
 // Rows that a CTA of the kernel that by_cols() picks visits at a time.
-int rows_per_cta(int64_t cols) {
+int rows_per_cta(int64_t cols) {   // (cols: with the shift)
   return cols <= 512 ? 16 : cols <= 1024 ? 8 : cols <= 2048 ? 4 : cols <= 4096 ? 2 : 1;
 }
 
 unsigned grid_of(const LnBackward& a, int sms) {
-  const int64_t rpc = rows_per_cta(a.cols);
-  const int64_t need = (a.rows + rpc - 1) / rpc;
-  return (unsigned)(need < sms ? need : sms);
+  const int64_t rpc = rows_per_cta(ln_span(a.cols, a.form));
+  return (unsigned)ln_grid((a.rows + rpc - 1) / rpc, sms, a.form);
 }
 
 template <int DT, int VEC, int TPR, int VPT, bool FP8, bool FULL>
 cudaError_t go_form(const LnBackward& a, float* partial, unsigned grid, cudaStream_t stream) {
   constexpr int NT = kBwdThreads, RPC = NT / TPR;
   auto kernel = ln_backward_kernel<DT, VEC, TPR, VPT, NT, FP8, FULL>;
-  const int ring = VEC == 8 ? kRingBytes<DT, VPT, NT, FP8> : 0;
+  const int ring = VEC != 1 ? kRingBytes<DT, VPT, NT, FP8> : 0;
   const int merge = RPC > 1 ? RPC * 2 * (int)sizeof(float) * (int)a.cols : 0;
   const int smem = ring > merge ? ring : merge;
   if (smem > 47 * 1024) {   // with the static arrays beside it, above 48 KB
@@ -372,11 +407,12 @@ cudaError_t go(const LnBackward& a, float* p, unsigned grid, cudaStream_t s) {
 
 template <int DT, int VEC>
 cudaError_t by_cols(const LnBackward& a, float* p, unsigned grid, cudaStream_t s) {
-  if (a.cols <= 256) return go<DT, VEC, 32, 1>(a, p, grid, s);
-  if (a.cols <= 512) return go<DT, VEC, 32, 2>(a, p, grid, s);
-  if (a.cols <= 1024) return go<DT, VEC, 64, 2>(a, p, grid, s);
-  if (a.cols <= 2048) return go<DT, VEC, 128, 2>(a, p, grid, s);
-  if (a.cols <= 4096) return go<DT, VEC, 256, 2>(a, p, grid, s);
+  const int64_t span = ln_span(a.cols, VEC);
+  if (span <= 256) return go<DT, VEC, 32, 1>(a, p, grid, s);
+  if (span <= 512) return go<DT, VEC, 32, 2>(a, p, grid, s);
+  if (span <= 1024) return go<DT, VEC, 64, 2>(a, p, grid, s);
+  if (span <= 2048) return go<DT, VEC, 128, 2>(a, p, grid, s);
+  if (span <= 4096) return go<DT, VEC, 256, 2>(a, p, grid, s);
   return go<DT, VEC, 512, 2>(a, p, grid, s);
 }
 
@@ -400,7 +436,9 @@ cudaError_t by_type(const LnBackward& a, float* p, int sms, cudaStream_t s, int6
   }
   const unsigned grid = grid_of(a, sms);
   *parts = grid;
-  return a.vec_ok ? by_cols<DT, 8>(a, p, grid, s) : by_cols<DT, 1>(a, p, grid, s);
+  if (a.form == kLnVectors) return by_cols<DT, 8>(a, p, grid, s);
+  if (a.form == kLnFlat) return by_cols<DT, kLnFlat>(a, p, grid, s);
+  return by_cols<DT, 1>(a, p, grid, s);
 }
 
 }  // namespace

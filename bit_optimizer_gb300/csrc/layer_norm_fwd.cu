@@ -9,7 +9,10 @@
 // the next rows are on their way through the ring meanwhile, and weight and
 // bias wait in shared memory (read from L1 they were evicted by the rows: 77.8
 // us).  16384 x 4096 BF16 with codes: 56.6 us, 5.93 TB/s, 0.87 of the measured
-// copy bandwidth; 65536 x 1024 without: 47 us, 0.83.
+// copy bandwidth; 65536 x 1024 without: 47 us, 0.83.  Rows that start anywhere
+// take scalar reads of weight and bias and masked ends: 65536 x 767 59 us, 0.50
+// (768: 34 us), 32768 x 1501 53 us (by elements 99), 32768 x 2041 58 (111); just
+// above a power of two half of a row's threads idle: 32768 x 2049 107 (159).
 #include "layer_norm.cuh"
 
 namespace fp8opt {
@@ -46,7 +49,9 @@ ln_forward_kernel(const LnForward a) {
   __shared__ RowSums<TPR> sums[RPC];
   // Weight and bias as fp32, then the ring [ST][VPT][Q][NT].  VEC 8: [2]
   // [VPT][2][TPR] quads, so that a warp's quads lie side by side; VEC 1:
-  // [2][TPR * 8 * VPT] elements.
+  // [2][TPR * 8 * VPT] elements; kLnFlat: pairs of both, element c at [c mod 8]
+  // [c / 8], where the elements e of a warp's vectors lie side by side for
+  // every shift.
   extern __shared__ uint4 shared[];
   const int slot = threadIdx.x / TPR, t = threadIdx.x % TPR;
   const int cols = (int)a.cols;
@@ -56,27 +61,39 @@ ln_forward_kernel(const LnForward a) {
   int64_t r = (int64_t)blockIdx.x * RPC + slot;
   float* const sw = reinterpret_cast<float*>(shared);
   float* const sb = sw + TPR * 8 * VPT;
+  float2* const pairs = reinterpret_cast<float2*>(shared);
   uint4* const ring = shared + TPR * 4 * VPT;
   const auto at = [&](int stage, int v, int q) -> uint4* {
     return ring + ((stage * VPT + v) * Q + q) * NT + threadIdx.x;
   };
+  const int shift = VEC == kLnFlat ? (int)(r * a.cols & 7) : 0, end = cols + shift;
   const auto fetch = [&](int stage, int64_t row) {
     if (row < a.rows) {
-      const char* p = static_cast<const char*>(a.x) + (size_t)row * a.cols * es;
+      const char* p = static_cast<const char*>(a.x) + ((size_t)row * a.cols - shift) * es;
+      const int left = VEC == kLnFlat ? ln_left(a.rows - row, a.cols, shift) : 0;
 #pragma unroll
       for (int v = 0; v < VPT; ++v) {
         const int c = ln_col<TPR, 8>(v, 0, t);
-        if (FULL || c < cols)
+        if (FULL || c < end)
 #pragma unroll
-          for (int q = 0; q < Q; ++q) copy_async<16>(at(stage, v, q), p + c * es + 16 * q);
+          for (int q = 0; q < Q; ++q) {
+            if constexpr (VEC == kLnFlat) {
+              const int n = ln_bytes(left - c, (int)es, 16 * q, 16);
+              if (n > 0) copy_async<16>(at(stage, v, q), p + c * es + 16 * q, n);
+            } else {
+              copy_async<16>(at(stage, v, q), p + c * es + 16 * q);
+            }
+          }
       }
     }
     copy_commit();
   };
   begin_after_previous();
-  if constexpr (VEC == 8) {
+  if constexpr (VEC != 1) {
 #pragma unroll
     for (int i = 0; i < ST - 1; ++i) fetch(i, r + i * step);
+  }
+  if constexpr (VEC == 8) {
 #pragma unroll
     for (int i = 0; i < ST; ++i)   // what lies past the row's end stays zero
 #pragma unroll
@@ -87,8 +104,9 @@ ln_forward_kernel(const LnForward a) {
   }
   for (int i = threadIdx.x; i < TPR * VPT; i += NT) {
     float w[8], b[8];
-    ln_param<VEC, TPR>(a.weight, a.wdtype, 0.0f, i / TPR, i % TPR, cols, w);
-    ln_param<VEC, TPR>(a.bias, a.wdtype, 0.0f, i / TPR, i % TPR, cols, b);
+    constexpr int PV = VEC == 8 ? 8 : 1;
+    ln_param<PV, TPR>(a.weight, a.wdtype, 0.0f, i / TPR, i % TPR, cols, w);
+    ln_param<PV, TPR>(a.bias, a.wdtype, 0.0f, i / TPR, i % TPR, cols, b);
     if constexpr (VEC == 8) {
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
@@ -101,23 +119,42 @@ ln_forward_kernel(const LnForward a) {
     } else {
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        sw[ln_col<TPR, 1>(i / TPR, e, i % TPR)] = w[e];
-        sb[ln_col<TPR, 1>(i / TPR, e, i % TPR)] = b[e];
+        const int c = ln_col<TPR, 1>(i / TPR, e, i % TPR);
+        if constexpr (VEC == kLnFlat) {
+          pairs[(c & 7) * (TPR * VPT) + (c >> 3)] = make_float2(w[e], b[e]);
+        } else {
+          sw[c] = w[e];
+          sb[c] = b[e];
+        }
       }
     }
+  }
+  // where the elements e of vector 0 of thread 0 lie (masked ones before the
+  // row: at the end of the line before, never before the first)
+  int at_e[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const unsigned u = (unsigned)(8 + e - shift);   // its column + 8
+    at_e[e] = (int)((u & 7u) * (TPR * VPT) + (u >> 3)) + t - 1;
   }
   __syncthreads();
   for (int stage = 0; r < a.rows; r += step, stage = stage + 1 == ST ? 0 : stage + 1) {
     float2 x[4 * VPT];
-    if constexpr (VEC == 8) {
+    if constexpr (VEC != 1) {
       copy_wait<ST - 2>();
 #pragma unroll
       for (int v = 0; v < VPT; ++v) {
         LnRaw<DT, 8> raw;
         float f[8];
+        if (VEC == kLnFlat && ln_col<TPR, 8>(v, 0, t) >= end) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) x[4 * v + j] = splat2(0.0f);
+          continue;
+        }
 #pragma unroll
         for (int q = 0; q < Q; ++q) raw.v[q] = *at(stage, v, q);
         ln_widen<DT, 8>(raw, f);
+        if (VEC == kLnFlat) ln_mask(f, ln_col<TPR, 8>(v, 0, t), shift, end);
 #pragma unroll
         for (int j = 0; j < 4; ++j) x[4 * v + j] = make_float2(f[2 * j], f[2 * j + 1]);
       }
@@ -138,9 +175,18 @@ ln_forward_kernel(const LnForward a) {
     float m = 0.0f;   // (a NaN passes it by, and is found in the sum of squares)
 #pragma unroll
     for (int i = 0; i < 4 * VPT; ++i) {
-      x[i] = add2(x[i], splat2(-mean));
-      if (!ln_in<TPR, VEC, FULL>(i / 4, 2 * (i % 4), t, cols)) x[i].x = 0.0f;
-      if (!ln_in<TPR, VEC, FULL>(i / 4, 2 * (i % 4) + 1, t, cols)) x[i].y = 0.0f;
+      if constexpr (VEC == kLnFlat) {
+        if (ln_col<TPR, 8>(i / 4, 0, t) >= end) continue;
+        if (i % 4 == 0) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) x[i + j] = add2(x[i + j], splat2(-mean));
+          ln_mask(x + i, ln_col<TPR, 8>(i / 4, 0, t), shift, end);
+        }
+      } else {
+        x[i] = add2(x[i], splat2(-mean));
+        if (!ln_in<TPR, VEC, FULL>(i / 4, 2 * (i % 4), t, cols)) x[i].x = 0.0f;
+        if (!ln_in<TPR, VEC, FULL>(i / 4, 2 * (i % 4) + 1, t, cols)) x[i].y = 0.0f;
+      }
       sq[i % 4] = fma2(x[i], x[i], sq[i % 4]);
       if (FP8) m = fmaxf(fmaxf(m, fabsf(x[i].x)), fabsf(x[i].y));
     }
@@ -167,6 +213,7 @@ ln_forward_kernel(const LnForward a) {
     }
 #pragma unroll
     for (int v = 0; v < VPT; ++v) {
+      if (VEC == kLnFlat && ln_col<TPR, 8>(v, 0, t) >= end) continue;
       float y[8], z[8];
       float4 w4[2], b4[2];
       if constexpr (VEC == 8) {
@@ -185,6 +232,10 @@ ln_forward_kernel(const LnForward a) {
                       : make_float2(w4[j / 2].x, w4[j / 2].y);
           b = (j & 1) ? make_float2(b4[j / 2].z, b4[j / 2].w)
                       : make_float2(b4[j / 2].x, b4[j / 2].y);
+        } else if constexpr (VEC == kLnFlat) {
+          const float2 p0 = pairs[at_e[2 * j] + v * TPR], p1 = pairs[at_e[2 * j + 1] + v * TPR];
+          w = make_float2(p0.x, p1.x);
+          b = make_float2(p0.y, p1.y);
         } else {
           const int c0 = ln_col<TPR, 1>(v, 2 * j, t), c1 = ln_col<TPR, 1>(v, 2 * j + 1, t);
           w = make_float2(sw[c0], sw[c1]);
@@ -199,7 +250,9 @@ ln_forward_kernel(const LnForward a) {
           z[2 * j + 1] = c.y;
         }
       }
-      ln_store<DT, VEC, TPR>(static_cast<char*>(a.y) + (size_t)r * a.cols * es, v, t, cols, y);
+      char* const out = static_cast<char*>(a.y) + (size_t)r * a.cols * es;
+      if constexpr (VEC == kLnFlat) ln_store_flat<DT, TPR>(out, v, t, shift, end, y);
+      else ln_store<DT, VEC, TPR>(out, v, t, cols, y);
       if constexpr (FP8) {
         uint8_t* codes = a.codes + (size_t)r * a.cols;
         if constexpr (VEC == 8) {
@@ -207,6 +260,17 @@ ln_forward_kernel(const LnForward a) {
           if (FULL || c < cols)
             __stcs(reinterpret_cast<uint2*>(codes + c),
                    finite ? enc8<kE4M3, false>(z) : enc8<kE4M3, true>(z));
+        } else if constexpr (VEC == kLnFlat) {
+          const int c = ln_col<TPR, 8>(v, 0, t);
+          const uint2 p = finite ? enc8<kE4M3, false>(z) : enc8<kE4M3, true>(z);
+          if (c >= shift && c + 8 <= end) {
+            __stcs(reinterpret_cast<uint2*>(codes - shift + c), p);
+          } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              if (c + e >= shift && c + e < end)
+                codes[c + e - shift] = (uint8_t)((e < 4 ? p.x : p.y) >> (8 * (e & 3)));
+          }
         } else {
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
@@ -277,15 +341,14 @@ template <int DT, int VEC, int TPR, int VPT, bool FP8, bool FULL>
 cudaError_t go_form(const LnForward& a, int sms, cudaStream_t stream) {
   constexpr int RPC = kFwdThreads / TPR;
   auto kernel = ln_forward_kernel<DT, VEC, TPR, VPT, FP8, FULL>;
-  const int smem = (VEC == 8 ? kRingBytes<DT, VPT> : 0) + 2 * (int)sizeof(float) * TPR * 8 * VPT;
+  const int smem = (VEC != 1 ? kRingBytes<DT, VPT> : 0) + 2 * (int)sizeof(float) * TPR * 8 * VPT;
   if (smem > 48 * 1024) {
     const cudaError_t e =
         cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
   }
-  const int64_t ctas = (a.rows + RPC - 1) / RPC, most = (int64_t)sms * kFwdCtas;
-  return launch(worth_early(a.rows * a.cols), kernel, (unsigned)(ctas < most ? ctas : most), kFwdThreads, smem, stream,
-                      a);
+  const int64_t grid = ln_grid((a.rows + RPC - 1) / RPC, (int64_t)sms * kFwdCtas, a.form);
+  return launch(worth_early(a.rows * a.cols), kernel, (unsigned)grid, kFwdThreads, smem, stream, a);
 }
 
 template <int DT, int VEC, int TPR, int VPT>
@@ -304,11 +367,13 @@ cudaError_t go(const LnForward& a, int sms, cudaStream_t stream) {
 // 61.7 us with 16 elements a thread, 59.1 with 32).
 template <int DT, int VEC>
 cudaError_t by_cols(const LnForward& a, int sms, cudaStream_t stream) {
-  if (a.cols <= 256) return go<DT, VEC, 32, 1>(a, sms, stream);
-  if (a.cols <= 512) return go<DT, VEC, 32, 2>(a, sms, stream);
-  if (a.cols <= 1024) return go<DT, VEC, 32, 4>(a, sms, stream);
-  if (a.cols <= 2048) return go<DT, VEC, 64, 4>(a, sms, stream);
-  if (a.cols <= 4096) return go<DT, VEC, 128, 4>(a, sms, stream);
+  const int64_t span = ln_span(a.cols, VEC);
+  if constexpr (VEC != kLnFlat)
+    if (span <= 256) return go<DT, VEC, 32, 1>(a, sms, stream);
+  if (span <= 512) return go<DT, VEC, 32, 2>(a, sms, stream);
+  if (span <= 1024) return go<DT, VEC, 32, 4>(a, sms, stream);
+  if (span <= 2048) return go<DT, VEC, 64, 4>(a, sms, stream);
+  if (span <= 4096) return go<DT, VEC, 128, 4>(a, sms, stream);
   return go<DT, VEC, 256, 4>(a, sms, stream);
 }
 
@@ -321,7 +386,9 @@ cudaError_t by_type(const LnForward& a, int sms, cudaStream_t stream) {
                                            : ln_forward_long_kernel<DT, false>,
                         grid, 1024, 0, stream, a);
   }
-  return a.vec_ok ? by_cols<DT, 8>(a, sms, stream) : by_cols<DT, 1>(a, sms, stream);
+  if (a.form == kLnVectors) return by_cols<DT, 8>(a, sms, stream);
+  if (a.form == kLnFlat) return by_cols<DT, kLnFlat>(a, sms, stream);
+  return by_cols<DT, 1>(a, sms, stream);
 }
 
 }  // namespace

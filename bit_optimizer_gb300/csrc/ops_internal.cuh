@@ -36,6 +36,23 @@ cudaError_t launch_act(int act, bool fwd, const ActArgs& a, int sms,
 // Longest row that a CTA keeps in registers.
 constexpr int64_t kLnMaxRegCols = 8192;
 
+// How layer norm reaches its rows: by elements; in vectors of eight, every row
+// and the parameters starting at a 16-byte boundary; or in vectors of eight of
+// the flat tensor, which does, though its rows may start anywhere (a row's
+// threads then hold up to seven elements before it as well).
+enum LnForm { kLnElements = 1, kLnFlat = 2, kLnVectors = 8 };
+
+// kLnFlat from `least` columns: masking the ends costs a short row more than
+// its element accesses.  65536 rows BF16, x kept, elements and flat: forward
+// 321 columns 37.6 and 43.6 us, 385 49.4 and 43.8, 755 92.4 and 56.5; backward
+// 129 27.3 and 29.2 us, 249 42.4 and 26.8, 755 176 and 92.5.
+constexpr int64_t kLnFlatForward = 352, kLnFlatBackward = 192;
+
+inline int ln_form(bool rows_aligned, bool params_aligned, int64_t cols, int64_t least) {
+  if (rows_aligned && params_aligned && cols % 8 == 0) return kLnVectors;
+  return rows_aligned && cols >= least && cols + 7 <= kLnMaxRegCols ? kLnFlat : kLnElements;
+}
+
 // Layer norm over rows of `cols` elements; x, y, dy and dx of type dtype, the
 // parameters and their gradients of type wdtype.  codes and scales (one per
 // row) hold xhat in 8 bits; without them mean and x are kept instead.
@@ -50,7 +67,7 @@ struct LnForward {
   float* scales;
   int64_t rows, cols;
   int dtype, wdtype;
-  bool vec_ok;               // cols and every buffer allow 16-byte accesses
+  int form;                  // of the row accesses: an LnForm
   float eps;
 };
 
@@ -67,7 +84,7 @@ struct LnBackward {
   void* db;                  // may be NULL
   int64_t rows, cols;
   int dtype, wdtype;
-  bool vec_ok;
+  int form;
 };
 
 cudaError_t launch_ln_forward(const LnForward& a, int sms, cudaStream_t stream,

@@ -157,9 +157,9 @@ extern "C" int fp8_layer_norm(const void* x, const void* weight, const void* bia
     if (fp8 != (scales != nullptr) || fp8 == (mean != nullptr))
       return bad(fn, "give mean, or codes and scales");
     LnForward a = {x, weight, bias, y, mean, rstd, codes, scales, rows, cols, dtype,
-                   wdtype, false, eps};
-    a.vec_ok = cols % 8 == 0 && aligned_all(x, weight, bias, y) &&
-               (reinterpret_cast<uintptr_t>(codes) & 7u) == 0;
+                   wdtype, kLnElements, eps};
+    a.form = ln_form(aligned_all(x, y) && (reinterpret_cast<uintptr_t>(codes) & 7u) == 0,
+                     aligned_all(weight, bias), cols, kLnFlatForward);
     cudaStream_t stream = static_cast<cudaStream_t>(stream_ptr);
     OpCall call;
     if ((st = call.open(fn, stream, 0)) != FP8OPT_OK) return st;
@@ -183,9 +183,9 @@ extern "C" int fp8_layer_norm_backward(const void* dy, const void* x, const floa
                      fp8 == (x != nullptr)))
       return bad(fn, "give x and mean, or codes and scales");
     LnBackward a = {dy, x, weight, mean, rstd, codes, scales, dx, dweight, dbias,
-                    rows, cols, dtype, wdtype, false};
-    a.vec_ok = cols % 8 == 0 && aligned_all(dy, x, weight, dx) &&
-               (reinterpret_cast<uintptr_t>(codes) & 7u) == 0;
+                    rows, cols, dtype, wdtype, kLnElements};
+    a.form = ln_form(aligned_all(dy, x, dx) && (reinterpret_cast<uintptr_t>(codes) & 7u) == 0,
+                     aligned_all(weight), cols, kLnFlatBackward);
     cudaStream_t stream = static_cast<cudaStream_t>(stream_ptr);
     OpCall call;
     // the SM count sizes the grid, and the grid the scratch

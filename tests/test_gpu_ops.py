@@ -288,6 +288,58 @@ def test_layer_norm_many_rows(bo):
     check_norm_grad(bo, dy, w, r, codes=codes, scales=scales)
 
 
+@pytest.mark.parametrize("rows,cols", [(5001, 129), (2600, 1023), (1300, 1530), (800, 2049),
+                                       (400, 4090), (160, 8185), (150, 8191), (7, 3), (3000, 201),
+                                       (2500, 353)])
+def test_layer_norm_rows_that_start_anywhere(bo, rows, cols):
+    """Several rows a thread, at every offset from a 16-byte boundary that the
+    width gives, with a NaN row whose neighbours share its end vectors."""
+    x = randn(rows, cols, dtype=torch.bfloat16, seed=cols) + 0.3
+    w = (1 + 0.3 * randn(cols, seed=1)).half()
+    dy = randn(rows, cols, dtype=torch.bfloat16, seed=2)
+    m, r, codes, scales = check_norm(bo, x, w, w, 1e-5)
+    check_norm_grad(bo, dy, w, r, x=x, mean=m)
+    dx, _, _ = check_norm_grad(bo, dy, w, r, codes=codes, scales=scales)
+    y = bo.layer_norm(x, w, w, 1e-5)[0]
+    for bad in (0, rows // 2, rows - 1):
+        x2, dy2 = x.clone(), dy.clone()
+        x2[bad], dy2[bad] = float("nan"), float("inf")
+        others = torch.arange(rows, device="cuda") != bad
+        y2, codes2, scales2, r2 = bo.layer_norm(x2, w, w, 1e-5, save="fp8")
+        assert torch.equal(y2[others], y[others]) and torch.isnan(y2[bad]).all()
+        assert torch.equal(codes2[others], codes[others])
+        dx2 = bo.layer_norm_backward(dy2, w, r2, codes=codes2, scales=scales2)[0]
+        assert torch.equal(dx2[others], dx[others])
+
+
+def test_layer_norm_writes_its_own_rows_only(bo):
+    """Outputs inside larger buffers: what lies beside them keeps its bytes."""
+    for rows, cols in ((3, 13), (1, 7), (3, 357), (200, 1021)):
+        n = rows * cols
+        x = randn(rows, cols, dtype=torch.bfloat16, seed=cols)
+        w = torch.ones(cols, device="cuda")
+        want = bo.layer_norm(x, w, w, save="fp8")
+        room = [torch.full((n + 64,), 7, dtype=t, device="cuda")
+                for t in (torch.bfloat16, torch.uint8, torch.bfloat16)]
+        y, codes, dx = (t[32:32 + n] for t in room)
+        scales, r = torch.empty_like(want[2]), torch.empty_like(want[3])
+        dw = torch.empty_like(w)
+        stream = torch.cuda.current_stream().cuda_stream
+        assert bo._lib.load().fp8_layer_norm(
+            x.data_ptr(), w.data_ptr(), w.data_ptr(), rows, cols, bo._lib.BF16, bo._lib.F32, 1e-5,
+            y.data_ptr(), None, r.data_ptr(), codes.data_ptr(), scales.data_ptr(), stream) == 0
+        assert bo._lib.load().fp8_layer_norm_backward(
+            x.data_ptr(), None, None, codes.data_ptr(), scales.data_ptr(), r.data_ptr(),
+            w.data_ptr(), rows, cols, bo._lib.BF16, bo._lib.F32, dx.data_ptr(), dw.data_ptr(),
+            None, stream) == 0
+        assert torch.equal(y.view(rows, cols), want[0])
+        assert torch.equal(codes.view(rows, cols), want[1])
+        back = bo.layer_norm_backward(x, w, r, codes=want[1], scales=want[2], need_bias=False)
+        assert torch.equal(dx.view(rows, cols), back[0]) and torch.equal(dw, back[1])
+        for t in room:
+            assert (t[:32] == 7).all() and (t[32 + n:] == 7).all()
+
+
 def test_layer_norm_of_special_rows(bo):
     x = randn(7, 640, seed=7)
     x[1] = 2.5                 # constant: variance 0

@@ -652,6 +652,13 @@ gemm_kernel(const __grid_constant__ GemmArgs args) {
       for (int i = 0; leader && i < kGemmStages; ++i)
         if (loads > (uint32_t)i)
           ok = mbar_wait(&bar.full[i], (loads - 1 - i) / kGemmStages & 1) && ok;
+      // and so does every arrival from the MMA warp, which commits to both CTAs:
+      // the last ones of the stages, and the very last one, which in the leader
+      // its own MMA warp waits for
+      for (int i = 0; ok && i < kGemmStages; ++i)
+        if (loads > (uint32_t)i)
+          ok = mbar_wait<true>(&bar.empty[i], (loads - 1 - i) / kGemmStages & 1);
+      if (!leader) ok = mbar_wait<true>(&bar.drained, 0) && ok;
     }
   } else if (warp == kEpilogueWarps + 1) {
     if (leader && (threadIdx.x & 31) == 0) {

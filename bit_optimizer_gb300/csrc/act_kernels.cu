@@ -227,7 +227,7 @@ template <int DT, int ACT>
 __device__ __forceinline__ void backward_group(const void* dy, const uint8_t* codes,
                                                const float* scales, int64_t n, int64_t g,
                                                void* out) {
-  const float r = __fdiv_rn(1.0f, __ldg(scales + g));
+  const float r = __fdiv_rn(1.0f, __ldcg(scales + g));
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     const int64_t i = g * kActGroup + 32 * j + (threadIdx.x & 31);
@@ -243,7 +243,7 @@ __device__ __forceinline__ void backward_group(const void* dy, const uint8_t* co
 // instead, the end of the tensor cost the GELU gradient 7%).
 template <int DT, int ACT>
 __global__ void __launch_bounds__(kThreads)
-act_forward_kernel(const void* __restrict__ x, int64_t n, void* __restrict__ y,
+act_forward_kernel(const void* x, int64_t n, void* __restrict__ y,
                    uint8_t* __restrict__ codes, float* __restrict__ scales) {
   begin_after_previous();
   const int64_t whole = n / kActGroup * kActGroup;
@@ -274,8 +274,7 @@ act_forward_kernel(const void* __restrict__ x, int64_t n, void* __restrict__ y,
 // ACT kActSave: x = decode(code) / scale; else dx = dy * gelu'(x).
 template <int DT, int ACT>
 __global__ void __launch_bounds__(kThreads)
-act_backward_kernel(const void* __restrict__ dy, const uint8_t* __restrict__ codes,
-                    const float* __restrict__ scales, int64_t n,
+act_backward_kernel(const void* dy, const uint8_t* codes, const float* scales, int64_t n,
                     void* __restrict__ out) {
   begin_after_previous();
   const int64_t whole = n / kActGroup * kActGroup;
@@ -286,7 +285,7 @@ act_backward_kernel(const void* __restrict__ dy, const uint8_t* __restrict__ cod
   }
   if (i0 >= whole) return;
   const uint4 c = ld_once4(codes + i0);
-  const float s = __ldg(scales + i0 / kActGroup);
+  const float s = __ldcg(scales + i0 / kActGroup);
   Raw16<DT> raw;
   if (ACT != kActSave) raw = load_raw16<DT>(dy, i0);
   float v[kPer];

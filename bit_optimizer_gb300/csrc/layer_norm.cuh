@@ -176,12 +176,12 @@ __device__ __forceinline__ void ln_param(const void* p, int dtype, float missing
     const int c = ln_col<TPR, 8>(v, 0, t);
     if (c >= cols) return;
     if (dtype == kF32) {
-      const float4 a = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(p) + c));
-      const float4 b = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(p) + c) + 1);
+      const float4 a = __ldcg(reinterpret_cast<const float4*>(static_cast<const float*>(p) + c));
+      const float4 b = __ldcg(reinterpret_cast<const float4*>(static_cast<const float*>(p) + c) + 1);
       x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
       x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
     } else {
-      const uint4 a = ld_keep4(static_cast<const uint16_t*>(p) + c);
+      const uint4 a = __ldcg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + c));
       LnRaw<kF16, 8> r;
       r.v[0] = a;
       if (dtype == kF16) {

@@ -148,16 +148,16 @@ ln_backward_kernel(const LnBackward a, float* __restrict__ partial) {
   const float* const other = FP8 ? a.scales : a.mean;
   float rstd_next = 0.0f, other_next = 1.0f;
   if (r < a.rows) {
-    rstd_next = __ldg(a.rstd + r);
-    other_next = __ldg(other + r);
+    rstd_next = __ldcg(a.rstd + r);
+    other_next = __ldcg(other + r);
   }
   for (int stage = 0; r < a.rows; r += step, stage = stage + 1 == ST ? 0 : stage + 1) {
     const float rstd = rstd_next;
     const float sub = FP8 ? 0.0f : other_next;
     const float mul = FP8 ? __fdiv_rn(1.0f, other_next) : rstd;
     if (r + step < a.rows) {
-      rstd_next = __ldg(a.rstd + r + step);
-      other_next = __ldg(other + r + step);
+      rstd_next = __ldcg(a.rstd + r + step);
+      other_next = __ldcg(other + r + step);
     }
     if constexpr (VEC != 1) copy_wait<ST - 2>();
     float2 g[4 * VPT], x[4 * VPT];
@@ -280,7 +280,7 @@ ln_backward_kernel(const LnBackward a, float* __restrict__ partial) {
 // dw and db of 32 columns: the `parts` partial sums, 32 at a time, then the 32
 // sums of this block, each in order.
 __global__ void __launch_bounds__(1024)
-ln_param_grad_kernel(const float* __restrict__ partial, int64_t parts, int64_t cols,
+ln_param_grad_kernel(const float* partial, int64_t parts, int64_t cols,
                      int wdtype, void* dw, void* db) {
   __shared__ float sh[32][33];
   const int64_t c = (int64_t)blockIdx.x * 32 + threadIdx.x;
@@ -356,8 +356,8 @@ ln_backward_long_cols_kernel(const LnBackward a, int64_t rows_per, float* __rest
   const int64_t r1 = min(a.rows, (int64_t)(blockIdx.y + 1) * rows_per);
   float sw = 0.0f, sb = 0.0f;
   for (int64_t r = (int64_t)blockIdx.y * rows_per; r < r1; ++r) {
-    const float k = FP8 ? __fdiv_rn(1.0f, __ldg(a.scales + r)) : __ldg(a.rstd + r);
-    const float sub = FP8 ? 0.0f : __ldg(a.mean + r);
+    const float k = FP8 ? __fdiv_rn(1.0f, __ldcg(a.scales + r)) : __ldcg(a.rstd + r);
+    const float sub = FP8 ? 0.0f : __ldcg(a.mean + r);
     const float g = load1<DT>(a.dy, r * a.cols + c);
     sw = __fmaf_rn(g, long_xhat<DT, FP8>(a, r * a.cols + c, sub, k), sw);
     sb += g;

@@ -762,10 +762,9 @@ gemm_kernel(const __grid_constant__ GemmArgs args) {
 // tokens' statistics lie side by side): warp k takes strips k, k + 32, ... in
 // order, then the 32 warps' results are joined in order.
 __global__ void __launch_bounds__(1024, 2)
-xent_join_kernel(const float2* __restrict__ partial, int strips, int64_t tokens, int64_t vocab,
-                 const long long* __restrict__ target, long long ignore,
-                 const float* __restrict__ target_logit, float* __restrict__ loss,
-                 float* __restrict__ lse) {
+xent_join_kernel(const float2* partial, int strips, int64_t tokens, int64_t vocab,
+                 const long long* target, long long ignore, const float* target_logit,
+                 float* __restrict__ loss, float* __restrict__ lse) {
   __shared__ float2 sh[32][33];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t row = (int64_t)blockIdx.x * 32 + lane;
@@ -804,10 +803,9 @@ xent_join_kernel(const float2* __restrict__ partial, int strips, int64_t tokens,
 // of the tokens that count (one that is not finite spoils its own token's dx,
 // not the others'); a maximum, so the order of the CTAs does not matter.
 __global__ void __launch_bounds__(256)
-xent_copy_kernel(const uint16_t* __restrict__ src, int64_t rows, int64_t dim, int64_t pitch,
-                 const long long* __restrict__ target, long long ignore,
-                 uint16_t* __restrict__ dst, bool vec, const float* __restrict__ dloss,
-                 uint32_t* __restrict__ top) {
+xent_copy_kernel(const uint16_t* src, int64_t rows, int64_t dim, int64_t pitch,
+                 const long long* target, long long ignore, uint16_t* __restrict__ dst, bool vec,
+                 const float* dloss, uint32_t* top) {
   begin_after_previous();
   uint32_t most = 0;
   const int lane = threadIdx.x & 31;   // a warp to a row
@@ -817,9 +815,15 @@ xent_copy_kernel(const uint16_t* __restrict__ src, int64_t rows, int64_t dim, in
     if (vec) {
       const uint4* s = reinterpret_cast<const uint4*>(src + r * dim);
       uint4* d = reinterpret_cast<uint4*>(dst + r * pitch);
-#pragma unroll 4
-      for (int64_t c = lane; c < dim / 8; c += 32)
-        d[c] = zero ? make_uint4(0, 0, 0, 0) : s[c];
+      for (int64_t c = lane; c < dim / 8; c += 4 * 32) {
+        uint4 v[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          v[k] = !zero && c + 32 * k < dim / 8 ? __ldcg(s + c + 32 * k) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if (c + 32 * k < dim / 8) d[c + 32 * k] = v[k];
+      }
     } else {
       // (the pitch is a multiple of 8 and dst aligned; src may be neither)
       const uint16_t* from = src + r * dim;
@@ -858,9 +862,9 @@ xent_copy_kernel(const uint16_t* __restrict__ src, int64_t rows, int64_t dim, in
 // of 128).
 template <bool BF16>
 __global__ void __launch_bounds__(256)
-xent_dx_kernel(const float* __restrict__ sum, int splits, int64_t tokens, int64_t dim,
-               int64_t pitch, const long long* __restrict__ target, long long ignore,
-               const float* __restrict__ top, uint16_t* __restrict__ dx) {
+xent_dx_kernel(const float* sum, int splits, int64_t tokens, int64_t dim, int64_t pitch,
+               const long long* target, long long ignore, const float* top,
+               uint16_t* __restrict__ dx) {
   begin_after_previous();
   const float back = *top;
   const int64_t groups = (dim + 7) / 8;

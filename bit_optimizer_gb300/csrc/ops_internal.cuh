@@ -145,6 +145,11 @@ int record_error(int status, const char* what);
 // dependent launch).  Each kernel begins with begin_after_previous(), before
 // which it reads and writes nothing in global memory.  Such a launch costs 1.5
 // us more of the host's time, and saves about 2.5 us of the GPU's.
+//
+// A kernel launched early lives while its predecessor still writes what it will
+// read, so none of its inputs is read-only in the sense of the non-coherent
+// path: inputs are neither const __restrict__ parameters nor read with __ldg,
+// but with plain, __ldcg or __ldcs loads behind begin_after_previous().
 template <class... Params, class... Args>
 cudaError_t launch(bool early, void (*kernel)(Params...), dim3 grid, dim3 block, size_t smem,
                    cudaStream_t stream, Args... args) {

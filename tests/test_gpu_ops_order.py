@@ -42,3 +42,46 @@ def test_tensor_core_launches_back_to_back(bo):
         rows = [both(*c) for c in calls]
         for got, want in zip(rows, alone):
             assert all(torch.equal(a, b) for a, b in zip(got, want)), repeat
+
+
+def test_large_calls_that_read_what_the_one_before_wrote(bo):
+    """Tensors above 12 Mi elements, whose kernels are set up while the one
+    before still runs.  Every kind of input comes from the call before: rows,
+    codes, scales, statistics and parameters; and every round finds other
+    values than the last at the same addresses.  All of each result is
+    compared."""
+    rows, cols = 6200, 2048
+    assert rows * cols >= 12 << 20
+
+    def chain(x, w, wait):
+        out = []
+
+        def keep(*tensors):
+            out.extend(tensors)
+            if wait:
+                torch.cuda.synchronize()
+            return tensors
+        y, codes, scales = keep(*bo.gelu(x, "tanh"))
+        codes, scales = keep(*bo.act_save(y))
+        z, = keep(bo.act_load(codes, scales, torch.bfloat16))
+        g, = keep(bo.gelu_backward(z, codes, scales, "none"))
+        y, mean, rstd = keep(*bo.layer_norm(g, w, w))
+        dx, dw, db = keep(*bo.layer_norm_backward(y, w, rstd, x=g, mean=mean))
+        y, codes, scales, rstd = keep(*bo.layer_norm(dx, dw, db, save="fp8"))
+        dx, dw, db = keep(*bo.layer_norm_backward(y, dw, rstd, codes=codes, scales=scales))
+        keep(*bo.layer_norm(dx[:, :2041].contiguous(), dw[:2041], db[:2041]))
+        return out
+    x = torch.empty(rows, cols, dtype=torch.bfloat16, device="cuda")
+    w = torch.empty(cols, device="cuda")
+    want = []
+    for k in range(4):
+        x.copy_(randn(rows, cols, dtype=torch.bfloat16, seed=k))
+        w.copy_(1 + 0.1 * randn(cols, dtype=torch.float32, seed=k + 50))
+        want.append([t.clone() for t in chain(x, w, True)])
+    for repeat in range(3):
+        for k in range(4):
+            x.copy_(randn(rows, cols, dtype=torch.bfloat16, seed=k))
+            w.copy_(1 + 0.1 * randn(cols, dtype=torch.float32, seed=k + 50))
+            got = chain(x, w, False)
+            for i, (a, b) in enumerate(zip(got, want[k])):
+                assert torch.equal(a, b), (repeat, k, i)

@@ -461,6 +461,7 @@ __device__ __forceinline__ int work_tile_n(uint32_t w) { return (int)(w >> 24 & 
 __device__ __forceinline__ bool work_a_mn(uint32_t w) { return w >> 29 & 1u; }
 __device__ __forceinline__ bool work_b_mn(uint32_t w) { return w >> 30 & 1u; }
 static_assert(sizeof(Tile) == 48, "three 16-byte words");
+static_assert(kXentMostSummed <= kBlockK * 0xFFFFFFll, "a tile's blocks fit work_blocks");
 
 __device__ __forceinline__ Tile locate(const GemmArgs& args, int tile, int rank) {
   Tile t = {};

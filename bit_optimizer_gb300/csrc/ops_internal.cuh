@@ -93,6 +93,12 @@ size_t ln_backward_scratch(const LnBackward& a, int sms);
 cudaError_t launch_ln_backward(const LnBackward& a, void* scratch, int sms,
                                cudaStream_t stream, LaunchMark mark);
 
+// Most rows of a tensor of the cross entropy (coordinates are ints), and the
+// longest sum of its products (dim, and backward the tokens): a tile's count of
+// 64-deep blocks has 24 bits.
+constexpr int64_t kXentMost = ((int64_t)1 << 31) - 1;
+constexpr int64_t kXentMostSummed = 64 * (((int64_t)1 << 24) - 1);
+
 // Cross entropy of the linear layer z = x w^T: x rows x dim, w vocab x dim, of
 // type dtype (kBF16 or kF16).
 struct XentArgs {

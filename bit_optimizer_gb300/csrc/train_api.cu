@@ -199,10 +199,10 @@ extern "C" int fp8_layer_norm_backward(const void* dy, const void* x, const floa
 namespace fp8opt {
 namespace {
 
-int check_xent(const char* fn, const XentArgs& a) {
-  constexpr int64_t kMost = (int64_t)1 << 31;
-  if (a.rows < 0 || a.rows >= kMost || a.dim < 1 || a.dim >= kMost || a.vocab < 1 ||
-      a.vocab >= kMost || a.rows > kMaxElems / a.dim || a.vocab > kMaxElems / a.dim)
+// most_rows: the rows of x that the call takes.
+int check_xent(const char* fn, const XentArgs& a, int64_t most_rows) {
+  if (a.rows < 0 || a.rows > most_rows || a.dim < 1 || a.dim > kXentMostSummed || a.vocab < 1 ||
+      a.vocab > kXentMost || a.rows > kMaxElems / a.dim || a.vocab > kMaxElems / a.dim)
     return bad(fn, "rows < 0, dim < 1, vocab < 1, or a size above its maximum");
   if (a.dtype != FP8OPT_BF16 && a.dtype != FP8OPT_F16)
     return unsupported(fn, "dtype is neither BF16 nor FP16");
@@ -229,7 +229,7 @@ extern "C" int fp8_linear_xent(const void* x, const void* w, const int64_t* targ
     a.dtype = dtype;
     a.loss = loss;
     a.lse_out = lse;
-    int st = check_xent(fn, a);
+    int st = check_xent(fn, a, kXentMost);
     if (st != FP8OPT_OK || rows == 0) return st;
     if (!x || !w || !target || !loss || !lse) return bad(fn, "NULL pointer");
     cudaStream_t stream = static_cast<cudaStream_t>(stream_ptr);
@@ -264,7 +264,7 @@ extern "C" int fp8_linear_xent_backward(const float* dloss, const void* x, const
     a.lse = lse;
     a.dx = dx;
     a.dw = dw;
-    int st = check_xent(fn, a);
+    int st = check_xent(fn, a, kXentMostSummed);
     if (st != FP8OPT_OK) return st;
     if (!dw || (rows > 0 && (!dloss || !x || !w || !target || !lse || !dx)))
       return bad(fn, "NULL pointer");

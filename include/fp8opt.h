@@ -685,7 +685,8 @@ FP8OPT_API int fp8_layer_norm_backward(
  * column tiles (forward); a copy of x, two pieces of p (128 to 256 MiB each, less
  * for a small vocabulary, or 512 bytes a token where that is more) and dx in
  * fp32, up to eight times, or 16 within 64 MiB (backward).  dim and vocab >= 1;
- * each tensor below 2^31 rows and columns.
+ * vocab, and forward rows, below 2^31; dim, and backward rows, at most 2^30 -
+ * 64.
  *
  * The kernels wait for their copies and products with a limit of about two
  * seconds; should one run out (it does not on a working device), the next

@@ -90,6 +90,24 @@ def test_linear_cross_entropy(lib):
     assert grad(dl=None) == grad(lse=None) == grad(dx=None) == grad(dw=None) == lib.ERR_ARG
 
 
+def test_linear_cross_entropy_refuses_sums_longer_than_its_tiles_count(lib):
+    """dim, and backward the tokens, are summed in blocks of 64 whose number has
+    24 bits; the first size past that is refused, the vocabulary is not bound."""
+    L = lib.load()
+    most = 2 ** 30 - 64
+    for dim in (most + 1, 2 ** 30, 2 ** 31 - 1):
+        assert L.fp8_linear_xent(P, P, P, 1, dim, 1, 1, -100, P, P, None) == lib.ERR_ARG
+        assert L.fp8_linear_xent_backward(P, P, P, P, P, 1, dim, 1, 1, -100, P, P,
+                                          None) == lib.ERR_ARG
+    assert L.fp8_linear_xent_backward(P, P, P, P, P, most + 1, 1, 1, 1, -100, P, P,
+                                      None) == lib.ERR_ARG
+    # accepted sizes get as far as the NULL pointer
+    assert L.fp8_linear_xent(None, P, P, 2 ** 31 - 1, 1, 2 ** 31 - 1, 1, -100, P, P,
+                             None) == lib.ERR_ARG and "NULL" in text(lib)
+    assert L.fp8_linear_xent_backward(P, None, P, P, P, most, 1, 1, 1, -100, P, P,
+                                      None) == lib.ERR_ARG and "NULL" in text(lib)
+
+
 def test_binding_refuses_cpu_tensors():
     torch = pytest.importorskip("torch")
     import bit_optimizer_gb300 as bo

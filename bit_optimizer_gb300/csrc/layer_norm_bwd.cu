@@ -13,7 +13,7 @@
 // behind by instructions (63% of the issue slots).  The coming rows' copies run
 // through a ring in shared memory: held in registers, two rows ahead was all
 // there was room for, and a 16381 x 2048 gradient from codes took 57 us; now
-// 34.6 us, 4.85 TB/s, 0.71 of the measured copy bandwidth; 65536 x 1024 from x:
+// 35.0 us, 4.79 TB/s, 0.71 of the measured copy bandwidth; 65536 x 1024 from x:
 // 0.82.  With the row slots' sums added one slot after the other the end of a
 // CTA alone took 30 us; side by side it is one pass.
 // Rows that start anywhere, from x (by elements): 32768 x 1501 83 us, 0.52 (183),
@@ -148,16 +148,16 @@ ln_backward_kernel(const LnBackward a, float* __restrict__ partial) {
   const float* const other = FP8 ? a.scales : a.mean;
   float rstd_next = 0.0f, other_next = 1.0f;
   if (r < a.rows) {
-    rstd_next = __ldcg(a.rstd + r);
-    other_next = __ldcg(other + r);
+    rstd_next = __ldca(a.rstd + r);
+    other_next = __ldca(other + r);
   }
   for (int stage = 0; r < a.rows; r += step, stage = stage + 1 == ST ? 0 : stage + 1) {
     const float rstd = rstd_next;
     const float sub = FP8 ? 0.0f : other_next;
     const float mul = FP8 ? __fdiv_rn(1.0f, other_next) : rstd;
     if (r + step < a.rows) {
-      rstd_next = __ldcg(a.rstd + r + step);
-      other_next = __ldcg(other + r + step);
+      rstd_next = __ldca(a.rstd + r + step);
+      other_next = __ldca(other + r + step);
     }
     if constexpr (VEC != 1) copy_wait<ST - 2>();
     float2 g[4 * VPT], x[4 * VPT];
@@ -356,8 +356,8 @@ ln_backward_long_cols_kernel(const LnBackward a, int64_t rows_per, float* __rest
   const int64_t r1 = min(a.rows, (int64_t)(blockIdx.y + 1) * rows_per);
   float sw = 0.0f, sb = 0.0f;
   for (int64_t r = (int64_t)blockIdx.y * rows_per; r < r1; ++r) {
-    const float k = FP8 ? __fdiv_rn(1.0f, __ldcg(a.scales + r)) : __ldcg(a.rstd + r);
-    const float sub = FP8 ? 0.0f : __ldcg(a.mean + r);
+    const float k = FP8 ? __fdiv_rn(1.0f, __ldca(a.scales + r)) : __ldca(a.rstd + r);
+    const float sub = FP8 ? 0.0f : __ldca(a.mean + r);
     const float g = load1<DT>(a.dy, r * a.cols + c);
     sw = __fmaf_rn(g, long_xhat<DT, FP8>(a, r * a.cols + c, sub, k), sw);
     sb += g;

@@ -155,7 +155,7 @@ int record_error(int status, const char* what);
 // A kernel launched early lives while its predecessor still writes what it will
 // read, so none of its inputs is read-only in the sense of the non-coherent
 // path: inputs are neither const __restrict__ parameters nor read with __ldg,
-// but with plain, __ldcg or __ldcs loads behind begin_after_previous().
+// but with plain, __ldca, __ldcg or __ldcs loads behind begin_after_previous().
 template <class... Params, class... Args>
 cudaError_t launch(bool early, void (*kernel)(Params...), dim3 grid, dim3 block, size_t smem,
                    cudaStream_t stream, Args... args) {

@@ -13,7 +13,9 @@
 //           then dx += p w_piece (fp32 in scratch) and dw_piece = p^T x.  p is
 //           scaled by a power of two and max |dloss| against underflow in
 //           FP16: the one rounding to 16 bits besides the results', random per
-//           element and of the size of the operands' own.  A launch holds one
+//           element and of the size of the operands' own (a token whose dloss
+//           is far below the largest has a scale of its own: see dloss_shift()).
+//           A launch holds one
 //           piece's dx and dw and the next piece's p, so that its end, where
 //           pairs run out of tiles, comes once a piece and is filled with the
 //           short tiles of p.
@@ -40,8 +42,8 @@
 //
 // Tokens whose target is `ignore` have no loss and give no gradient whatever
 // is in their row of x: their p is 0 and dw reads a copy of x in which such
-// rows are zero.  The copy also brings rows that TMA cannot read (a row
-// length that is not a multiple of 8, unaligned tensors) to a 16-byte pitch.
+// rows are zero.  Rows that TMA cannot read (a row length that is not a
+// multiple of 8, unaligned tensors) are copied to a 16-byte pitch.
 #include "ops_internal.cuh"
 #include "tensor_core.cuh"
 
@@ -105,7 +107,7 @@ struct GemmOut {
   // kProbs
   const float* lse;
   const float* dloss;
-  const float* top_dloss;  // largest finite |dloss|
+  const float* top;        // largest finite |dloss|
   int64_t piece;           // columns of probs
   // kDx, kDw
   float* dx_sum;           // [split][token][dim_pitch]
@@ -129,11 +131,23 @@ struct GemmArgs {
   int* error;              // set to 1 when a wait ran out
 };
 
-// p is held as (exp(z - lse) - [target]) * (dloss / max |dloss|) * kProbScale:
-// below 2^15, and in FP16 without underflow down to 2^-39 of the largest.  (A
-// common dloss then leaves p as it is: multiplied in before the rounding, it
-// would give every token the same rounding error.)
+// p is held as (exp(z - lse) - [target]) * (2^b dloss / max |dloss|) *
+// kProbScale: below 2^15, and in FP16 without underflow down to 2^-39.  (A common
+// dloss then leaves p as it is: multiplied in before the rounding, it would give
+// every token the same rounding error.)
 constexpr float kProbScale = 32768.0f;
+
+// b of a token: 0 for a dloss within 2^12 of the largest.  A smaller one would
+// push the token's small probabilities below FP16's range, and its dx with them
+// (1 / 50257 of 2^-20 keeps three bits).  So 2^-b is left out of p and put where
+// it is exact: on the token's row of dx, in fp32, and on its row of dw's copy of
+// x (in FP16 exact until x 2^-b is below 2^-14; beyond that its part of dw is
+// off by at most 2^-37 of a like token's of the largest dloss).
+constexpr int kFullRange = 12;
+__device__ __forceinline__ int dloss_shift(float dloss, float top) {
+  if (dloss == 0.0f || top == 0.0f || nonfinite(dloss)) return 0;
+  return max(ilogbf(top) - ilogbf(dloss) - kFullRange, 0);
+}
 
 template <bool BF16>
 __device__ __forceinline__ uint32_t pack16(float a, float b) {
@@ -254,7 +268,7 @@ __device__ __forceinline__ RowIn row_in(const GemmShape& g, const GemmOut& o, in
       }
     }
   }
-  if (g.mode == kProbs || g.mode == kDw) in.top = *o.top_dloss;
+  if (g.mode == kProbs || g.mode == kDw) in.top = *o.top;
   return in;
 }
 
@@ -373,7 +387,8 @@ __device__ __forceinline__ void probs_strip(const GemmShape& g, const GemmOut& o
   float shift = 0.0f, k = 0.0f;
   int rel = -1;
   if (live && in.target != o.ignore) {
-    k = (in.top == 0.0f ? in.dloss : __fdiv_rn(in.dloss, in.top)) * kProbScale;
+    const float own = ldexpf(in.dloss, dloss_shift(in.dloss, in.top));
+    k = (in.top == 0.0f ? own : __fdiv_rn(own, in.top)) * kProbScale;
     shift = -in.lse;
     const long long at = in.target - g.v0 - t.c0;
     if (at >= 0 && at < t.cols) rel = (int)at;
@@ -799,31 +814,70 @@ xent_join_kernel(const float2* partial, int strips, int64_t tokens, int64_t voca
   }
 }
 
-// Rows of a matrix at a 16-byte pitch, those of ignored tokens zero (target
-// NULL: none is).  With `top` (zeroed before), also the largest finite |dloss|
-// of the tokens that count (one that is not finite spoils its own token's dx,
-// not the others'); a maximum, so the order of the CTAs does not matter.
-__global__ void __launch_bounds__(256)
-xent_copy_kernel(const uint16_t* src, int64_t rows, int64_t dim, int64_t pitch,
-                 const long long* target, long long ignore, uint16_t* __restrict__ dst, bool vec,
-                 const float* dloss, uint32_t* top) {
-  begin_after_previous();
+// The largest finite |dloss| of the tokens that count (one that is not finite
+// spoils its own token's dx, not the others'), for every thread of the CTA.
+__device__ float top_dloss(const float* dloss, const long long* target, long long ignore,
+                           int64_t rows) {
+  __shared__ uint32_t sh[8];
   uint32_t most = 0;
+  for (int64_t r = threadIdx.x; r < rows; r += 256) {
+    const float d = dloss[r];
+    if (target[r] != ignore && !nonfinite(d)) most = max(most, abs_bits(d));
+  }
+  most = __reduce_max_sync(0xFFFFFFFFu, most);
+  if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = most;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < 8; ++i) most = max(most, sh[i]);
+  return __uint_as_float(most);
+}
+
+// x 2^-b of two elements, in their type.
+__device__ __forceinline__ uint32_t scaled_pair(uint32_t w, int b, bool bf16) {
+  const float2 f = bf16 ? make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u))
+                        : h2_to_f2(w);
+  const float lo = ldexpf(f.x, -b), hi = ldexpf(f.y, -b);
+  return bf16 ? pack2<kBF16>(lo, hi) : pack2<kF16>(lo, hi);
+}
+
+// Rows of a matrix at a 16-byte pitch.  With dloss, those of x for dw: zero for
+// an ignored token, with the token's 2^-b; then top gets the largest |dloss|
+// (every CTA finds it for itself: 12 bytes a token, from L2), and `plain`, unless
+// NULL, the rows as they are.
+__global__ void __launch_bounds__(256)
+xent_copy_kernel(const uint16_t* src, int64_t rows, int64_t dim, int64_t pitch, bool vec,
+                 bool bf16, const long long* target, long long ignore, const float* dloss,
+                 float* top, uint16_t* __restrict__ dst, uint16_t* __restrict__ plain) {
+  begin_after_previous();
   const int lane = threadIdx.x & 31;   // a warp to a row
+  float most = 0.0f;
+  if (dloss != nullptr) {
+    most = top_dloss(dloss, target, ignore, rows);
+    if (blockIdx.x == 0 && threadIdx.x == 0) *top = most;
+  }
   for (int64_t r = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); r < rows;
        r += (int64_t)gridDim.x * 8) {
-    const bool zero = target != nullptr && target[r] == ignore;
+    const bool zero = dloss != nullptr && target[r] == ignore;
+    const int b = dloss != nullptr && !zero ? dloss_shift(dloss[r], most) : 0;
+    // one 16-byte word of the row
+    const auto put = [&](int64_t c, uint4 v) {
+      if (plain != nullptr) *reinterpret_cast<uint4*>(plain + r * pitch + c) = v;
+      if (zero) v = make_uint4(0, 0, 0, 0);
+      if (b > 0)
+        v = make_uint4(scaled_pair(v.x, b, bf16), scaled_pair(v.y, b, bf16),
+                       scaled_pair(v.z, b, bf16), scaled_pair(v.w, b, bf16));
+      *reinterpret_cast<uint4*>(dst + r * pitch + c) = v;
+    };
     if (vec) {
       const uint4* s = reinterpret_cast<const uint4*>(src + r * dim);
-      uint4* d = reinterpret_cast<uint4*>(dst + r * pitch);
       for (int64_t c = lane; c < dim / 8; c += 4 * 32) {
         uint4 v[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k)
-          v[k] = !zero && c + 32 * k < dim / 8 ? __ldcg(s + c + 32 * k) : make_uint4(0, 0, 0, 0);
+          v[k] = c + 32 * k < dim / 8 ? __ldcg(s + c + 32 * k) : make_uint4(0, 0, 0, 0);
 #pragma unroll
         for (int k = 0; k < 4; ++k)
-          if (c + 32 * k < dim / 8) d[c + 32 * k] = v[k];
+          if (c + 32 * k < dim / 8) put(8 * (c + 32 * k), v[k]);
       }
     } else {
       // (the pitch is a multiple of 8 and dst aligned; src may be neither)
@@ -833,8 +887,7 @@ xent_copy_kernel(const uint16_t* src, int64_t rows, int64_t dim, int64_t pitch,
       for (int64_t c = 8 * lane; c < pitch; c += 8 * 32) {
         uint32_t w[4] = {0, 0, 0, 0};
         const uint16_t* p = from + c;
-        if (zero) {
-        } else if (c + 8 > dim) {
+        if (c + 8 > dim) {
 #pragma unroll
           for (int k = 0; k < 8; ++k)
             if (c + k < dim) w[k / 2] |= (uint32_t)p[k] << (16 * (k & 1));
@@ -843,31 +896,28 @@ xent_copy_kernel(const uint16_t* src, int64_t rows, int64_t dim, int64_t pitch,
           for (int k = 0; k < 4; ++k) w[k] = reinterpret_cast<const uint32_t*>(p)[k];
         } else {   // the first element, three words that start at the second, the last
           const uint32_t* q = reinterpret_cast<const uint32_t*>(p + 1);
-          const uint32_t first = p[0], a = q[0], b = q[1], d = q[2], last = p[7];
+          const uint32_t first = p[0], a = q[0], b2 = q[1], d = q[2], last = p[7];
           w[0] = first | a << 16;
-          w[1] = a >> 16 | b << 16;
-          w[2] = b >> 16 | d << 16;
+          w[1] = a >> 16 | b2 << 16;
+          w[2] = b2 >> 16 | d << 16;
           w[3] = d >> 16 | last << 16;
         }
-        *reinterpret_cast<uint4*>(dst + r * pitch + c) = make_uint4(w[0], w[1], w[2], w[3]);
+        put(c, make_uint4(w[0], w[1], w[2], w[3]));
       }
     }
-    if (top != nullptr && lane == 0 && !zero && !nonfinite(dloss[r]))
-      most = max(most, abs_bits(dloss[r]));
   }
-  if (most > 0) atomicMax(top, most);
 }
 
-// dx from its fp32 parts: the splits added in order, scaled back, rounded; 0
-// for an ignored token.  Eight columns a thread (the parts' pitch is a multiple
+// dx from its fp32 parts: the splits added in order, scaled back (with the
+// token's own 2^-b), rounded; 0 for an ignored token.  Eight columns a thread (the parts' pitch is a multiple
 // of 128).
 template <bool BF16>
 __global__ void __launch_bounds__(256)
 xent_dx_kernel(const float* sum, int splits, int64_t tokens, int64_t dim, int64_t pitch,
-               const long long* target, long long ignore, const float* top,
+               const long long* target, long long ignore, const float* dloss, const float* top,
                uint16_t* __restrict__ dx) {
   begin_after_previous();
-  const float back = *top;
+  const float most = *top;
   const int64_t groups = (dim + 7) / 8;
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < tokens * groups;
        i += (int64_t)gridDim.x * 256) {
@@ -892,6 +942,7 @@ xent_dx_kernel(const float* sum, int splits, int64_t tokens, int64_t dim, int64_
     }
     float e[8] = {v[0].x, v[0].y, v[0].z, v[0].w, v[1].x, v[1].y, v[1].z, v[1].w};
     const bool zero = target[r] == ignore;
+    const float back = ldexpf(most, -dloss_shift(dloss[r], most));
 #pragma unroll
     for (int j = 0; j < 8; ++j) e[j] = zero ? 0.0f : e[j] * (1.0f / kProbScale) * back;
     uint16_t* out = dx + r * dim + c;
@@ -965,15 +1016,23 @@ bool direct(const void* p, int64_t dim) {
   return dim % 8 == 0 && (reinterpret_cast<uintptr_t>(p) & 15u) == 0;
 }
 
-cudaError_t copy_rows(const void* src, int64_t rows, int64_t dim, int64_t pitch,
-                      const int64_t* target, int64_t ignore, char* dst, int sms,
-                      cudaStream_t stream, const float* dloss = nullptr, float* top = nullptr) {
+// For dw's copy of x: what its rows depend on, and where else they go.
+struct CopyFor {
+  const int64_t* target = nullptr;
+  int64_t ignore = 0;
+  const float* dloss = nullptr;
+  float* top = nullptr;
+  char* plain = nullptr;
+};
+
+cudaError_t copy_rows(const void* src, int64_t rows, int64_t dim, int64_t pitch, bool bf16,
+                      char* dst, int sms, cudaStream_t stream, const CopyFor& f = CopyFor()) {
   const int64_t grid = std::min((rows + 7) / 8, (int64_t)8 * sms);
   return launch(true, xent_copy_kernel, (unsigned)grid, 256, 0, stream,
-                      static_cast<const uint16_t*>(src), rows, dim, pitch,
-                      reinterpret_cast<const long long*>(target), (long long)ignore,
-                      reinterpret_cast<uint16_t*>(dst), direct(src, dim) && pitch == dim, dloss,
-                      reinterpret_cast<uint32_t*>(top));
+                static_cast<const uint16_t*>(src), rows, dim, pitch,
+                direct(src, dim) && pitch == dim, bf16,
+                reinterpret_cast<const long long*>(f.target), (long long)f.ignore, f.dloss, f.top,
+                reinterpret_cast<uint16_t*>(dst), reinterpret_cast<uint16_t*>(f.plain));
 }
 
 // Tokens of one forward launch: bounds the scratch of the tiles' statistics.
@@ -1061,7 +1120,7 @@ ForwardScratch forward_scratch(const XentArgs& a, int sms) {
 }
 
 struct BackwardScratch {
-  size_t next = 0, x = 0, w = 0, top = 0, probs[2] = {0, 0}, dx = 0, bytes = 0;
+  size_t next = 0, x = 0, x_plain = 0, w = 0, top = 0, probs[2] = {0, 0}, dx = 0, bytes = 0;
   int64_t piece = 0, pieces = 0;
   int splits = 1;
 };
@@ -1072,9 +1131,10 @@ BackwardScratch backward_scratch(const XentArgs& a, int sms) {
   s.piece = piece_columns(a, sms);
   s.pieces = (a.vocab + s.piece - 1) / s.piece;
   s.splits = dx_splits(a, s.piece, sms);
-  s.next = l.take((s.pieces + 2) * 4);     // the launches' counters, and max |dloss|
-  s.top = s.next + (size_t)(s.pieces + 1) * 4;
+  s.next = l.take((s.pieces + 1) * 4);     // the launches' counters
+  s.top = l.take(4);                       // max |dloss|
   s.x = l.take(a.rows * pitch * 2);
+  if (!direct(a.x, a.dim)) s.x_plain = l.take(a.rows * pitch * 2);
   if (!direct(a.w, a.dim)) s.w = l.take(a.vocab * pitch * 2);
   for (int i = 0; i < 2 && i < s.pieces; ++i) s.probs[i] = l.take(a.rows * s.piece * 2);
   s.dx = l.take(s.splits * a.rows * up(a.dim, width_of(a.dim)) * 4);
@@ -1096,11 +1156,11 @@ cudaError_t launch_xent_forward(const XentArgs& a, char* scratch, int* error, in
   const char* w = static_cast<const char*>(a.w);
   cudaError_t e = cudaSuccess;
   if (!direct(a.x, a.dim)) {
-    e = copy_rows(a.x, a.rows, a.dim, pitch, nullptr, 0, scratch + s.x, sms, stream);
+    e = copy_rows(a.x, a.rows, a.dim, pitch, bf16, scratch + s.x, sms, stream);
     x = scratch + s.x;
   }
   if (e == cudaSuccess && !direct(a.w, a.dim)) {
-    e = copy_rows(a.w, a.vocab, a.dim, pitch, nullptr, 0, scratch + s.w, sms, stream);
+    e = copy_rows(a.w, a.vocab, a.dim, pitch, bf16, scratch + s.w, sms, stream);
     w = scratch + s.w;
   }
   for (int64_t t0 = 0; e == cudaSuccess && t0 < a.rows; t0 += kForwardTokens) {
@@ -1150,17 +1210,20 @@ cudaError_t launch_xent_backward(const XentArgs& a, char* scratch, int* error, i
   const int64_t pitch = up(a.dim, 8);
   const int width = width_of(a.dim);
   const long long* target = reinterpret_cast<const long long*>(a.target);
-  const char* x = scratch + s.x;   // rows of ignored tokens zero
+  // the logits' x, and dw's: zero for ignored tokens, scaled for a small dloss
+  const bool x_direct = direct(a.x, a.dim);
+  const char* x = x_direct ? static_cast<const char*>(a.x) : scratch + s.x_plain;
+  const char* x_dw = scratch + s.x;
   const char* w = static_cast<const char*>(a.w);
   int* next = reinterpret_cast<int*>(scratch + s.next);
   float* top = reinterpret_cast<float*>(scratch + s.top);
-  cudaError_t e = cudaMemsetAsync(next, 0, (size_t)(s.pieces + 2) * 4, stream);
+  cudaError_t e = cudaMemsetAsync(next, 0, (size_t)(s.pieces + 1) * 4, stream);
   if (mark) mark(kXentPrepareK, 0, stream);
   if (e == cudaSuccess)
-    e = copy_rows(a.x, a.rows, a.dim, pitch, a.target, a.ignore, scratch + s.x, sms, stream,
-                  a.dloss, top);
+    e = copy_rows(a.x, a.rows, a.dim, pitch, bf16, scratch + s.x, sms, stream,
+                  {a.target, a.ignore, a.dloss, top, x_direct ? nullptr : scratch + s.x_plain});
   if (e == cudaSuccess && !direct(a.w, a.dim)) {
-    e = copy_rows(a.w, a.vocab, a.dim, pitch, nullptr, 0, scratch + s.w, sms, stream);
+    e = copy_rows(a.w, a.vocab, a.dim, pitch, bf16, scratch + s.w, sms, stream);
     w = scratch + s.w;
   }
   if (mark) mark(kXentPrepareK, 1, stream);
@@ -1172,7 +1235,7 @@ cudaError_t launch_xent_backward(const XentArgs& a, char* scratch, int* error, i
   const int a_rows = a.rows <= kHalfM ? (int)up(a.rows, 8) : 0, box = a_rows > 0 ? a_rows : kHalfM;
   if ((e = make_map(&x_k, bf16, x, a.rows, a.dim, pitch, box)) != cudaSuccess ||
       (e = make_map(&w_k, bf16, w, a.vocab, a.dim, pitch, kTileN / 2)) != cudaSuccess ||
-      (e = make_map(&x_mn, bf16, x, a.rows, a.dim, pitch, kBlockK)) != cudaSuccess ||
+      (e = make_map(&x_mn, bf16, x_dw, a.rows, a.dim, pitch, kBlockK)) != cudaSuccess ||
       (e = make_map(&w_mn, bf16, w, a.vocab, a.dim, pitch, kBlockK)) != cudaSuccess)
     return e;
   for (int i = 0; i < 2 && i < s.pieces; ++i) {
@@ -1192,7 +1255,7 @@ cudaError_t launch_xent_backward(const XentArgs& a, char* scratch, int* error, i
   o.ignore = a.ignore;
   o.lse = a.lse;
   o.dloss = a.dloss;
-  o.top_dloss = top;
+  o.top = top;
   o.piece = s.piece;
   o.dx_sum = reinterpret_cast<float*>(scratch + s.dx);
   o.dim_pitch = up(a.dim, width);
@@ -1229,7 +1292,8 @@ cudaError_t launch_xent_backward(const XentArgs& a, char* scratch, int* error, i
   e = launch(true, bf16 ? xent_dx_kernel<true> : xent_dx_kernel<false>,
                    (unsigned)std::min((a.rows * ((a.dim + 7) / 8) + 255) / 256, (int64_t)8 * sms), 256,
                    0, stream, (const float*)o.dx_sum, s.splits, a.rows, a.dim, o.dim_pitch, target,
-                   (long long)a.ignore, (const float*)top, static_cast<uint16_t*>(a.dx));
+                   (long long)a.ignore, a.dloss, (const float*)top,
+                   static_cast<uint16_t*>(a.dx));
   if (mark) mark(kXentDxK, 1, stream);
   return e;
 }

@@ -678,11 +678,13 @@ FP8OPT_API int fp8_layer_norm_backward(
  *   p[i, v] = (exp(z[i, v] - lse[i]) - [v = target[i]]) * dloss[i],
  *   dx = p w,  dw = p^T x  (of type dtype, both overwritten).
  * The vocabulary is taken in pieces: p exists for one piece at a time, in
- * 16 bits scaled by a power of two against underflow.  An ignored token has dx
- * 0 and no part in dw, whatever its row of x holds.  rows = 0 gives dw 0.
+ * 16 bits, each token's scaled against underflow, so that a token's dx does not
+ * suffer from a dloss far below the others'.  An ignored token has dx 0 and no
+ * part in dw, whatever its row of x holds.  rows = 0 gives dw 0.
  * Rows whose length is a multiple of 8 in 16-byte-aligned tensors are read in
  * place, others through a copy in scratch.  Scratch: the statistics of the
- * column tiles (forward); a copy of x, two pieces of p (128 to 256 MiB each, less
+ * column tiles (forward); a copy of x (two of rows that are not read in place),
+ * two pieces of p (128 to 256 MiB each, less
  * for a small vocabulary, or 512 bytes a token where that is more) and dx in
  * fp32, up to eight times, or 16 within 64 MiB (backward).  dim and vocab >= 1;
  * vocab, and forward rows, below 2^31; dim, and backward rows, at most 2^30 -

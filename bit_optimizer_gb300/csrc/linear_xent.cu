@@ -62,7 +62,7 @@ constexpr int kTurnBytes = 4096;   // of an epilogue warp
 constexpr int kGemmSmem =
     1024 + kGemmStages * (kStageA + kStageB) + kEpilogueWarps * kTurnBytes;
 
-constexpr float kLog2eF = 1.4426950408889634f, kLn2F = 0.69314718055994531f;
+constexpr float kLog2eF = 1.4426950408889634f;
 
 __device__ __forceinline__ float exp2_approx(float x) {
   float y;
@@ -279,9 +279,12 @@ __device__ __forceinline__ float2 join_stats(float2 a, float2 b) {
                               b.y * exp2_approx((b.x - top) * kLog2eF));
 }
 
-// A token's running maximum and sum of exponentials, and its target's logit.
+// A token's running maximum and sum of exponentials, and its target's logit.  The
+// maximum starts at fp32's lowest number, which is above no logit but -inf and
+// makes its exponential 0 (from -inf the difference of two would be NaN).
+constexpr float kLowest = -3.402823466e38f;
 struct Stats {
-  float top = -1e30f, sum = 0.0f, at_target = 0.0f;
+  float top = kLowest, sum = 0.0f, at_target = 0.0f;
   // 32 more logits, of which the first `valid` count; the target's is number
   // rel, if it is among them.
   __device__ __forceinline__ void add(uint32_t (&r)[32], int valid, int rel) {
@@ -371,7 +374,7 @@ struct SwappedStats {
     for (int k = 0; k < 2; ++k) {
       const int64_t token = 32 * (warp / 4) + 64 * k + lane;
       if (token >= o.tokens) continue;
-      float2 a = make_float2(-1e30f, 0.0f);
+      float2 a = make_float2(kLowest, 0.0f);
       for (int w = 0; w < 4; ++w)
         a = join_stats(a, reinterpret_cast<const float2*>(&turns[warp + w])[32 * k + lane]);
       o.partial[(int64_t)blockIdx.x * o.tokens + token] = a;
@@ -784,7 +787,7 @@ xent_join_kernel(const float2* partial, int strips, int64_t tokens, int64_t voca
   __shared__ float2 sh[32][33];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t row = (int64_t)blockIdx.x * 32 + lane;
-  const float2 none = make_float2(-1e30f, 0.0f);
+  const float2 none = make_float2(kLowest, 0.0f);
   begin_after_previous();
   float2 s = none;
   for (int i = warp; i < strips; i += 8 * 32) {

@@ -63,3 +63,36 @@ def test_loss_gradients_far_apart(bo, rows, dim, vocab, dtype, span):
         tol += h * (ref.abs() + tol) + TINY[dtype]
         off = (got.double() - ref).abs() - tol
         assert off.le(0).all(), off.max()
+
+
+@pytest.mark.parametrize("rows", [5, 128, 300])
+def test_logits_near_the_ends_of_fp32(bo, rows):
+    """Tokens whose logits are all far below zero, above it, or minus infinity.
+    A logit is 8 products of powers of two, exact in fp32, so lse is off by its
+    logarithm's and sums' 2^-22 relative and 2^-20 absolute."""
+    dim, vocab = 8, 700
+    scale = torch.exp2(torch.arange(rows) % 5 * 30.0 - 60)          # 2^-60 .. 2^60
+    x = scale[:, None].expand(rows, dim).to(torch.bfloat16).cuda()
+    w = -torch.exp2(torch.arange(vocab) % 9 + 52.0)                 # -2^52 .. -2^60
+    w = w[:, None].expand(vocab, dim).to(torch.bfloat16).cuda()
+    t = torch.arange(rows, device="cuda") * 9 % vocab               # the largest logits
+    for sign in (1, -1):
+        z = (x.double() @ (sign * w.double()).T)
+        assert z.abs().max() > 1e36 and z.abs().max() < 3e38
+        lse64 = torch.logsumexp(z, 1)
+        loss64 = lse64 - z.gather(1, t[:, None])[:, 0]
+        loss, lse = bo.linear_cross_entropy(x, sign * w, t)
+        assert ((lse.double() - lse64).abs() <= 2.0 ** -20 + 2.0 ** -22 * lse64.abs()).all()
+        assert ((loss.double() - loss64).abs()
+                <= 2.0 ** -19 + 2.0 ** -21 * (lse64.abs() + loss64)).all()
+    # logits of minus infinity beside finite ones, and nothing else
+    one = torch.ones(rows, dim, dtype=torch.bfloat16, device="cuda")
+    w[::3] = float("-inf")
+    w[1::3], w[2::3] = 0.5, -0.25
+    t = torch.full((rows,), 1, device="cuda")
+    loss, lse = bo.linear_cross_entropy(one, w, t)
+    z = torch.where(torch.isinf(w[:, 0]), w[:, 0].double(), 8 * w[:, 0].double())
+    assert ((lse.double() - torch.logsumexp(z, 0)).abs() <= 2.0 ** -19).all()
+    assert ((loss.double() - (torch.logsumexp(z, 0) - 4)).abs() <= 2.0 ** -18).all()
+    w[:] = float("-inf")
+    assert (bo.linear_cross_entropy(one, w, t)[1] == float("-inf")).all()

@@ -186,7 +186,7 @@ struct Workspace {
   DevBuf saved_scales;       // n floats: m_scale before the step
   DevBuf norm_buf;           // gradient norm: 2n sum words, norm, clip
   DevBuf dev_scalars;        // the *_dev calls' DevScalars
-  DevBuf op_scratch;         // the training operators' scratch
+  DevBuf op_scratch;         // the training operators' scratch (frozen on its own)
   // cast tables
   std::vector<fp8opt_cast_item> cast_key;
   DevBuf cast_descs, cast_chunks;
@@ -205,14 +205,15 @@ struct Workspace {
   uint32_t reduce_nchunks = 0;
   bool have_cast = false, have_step = false, have_reduce = false;
   // A CUDA graph captured on this stream refers to these buffers and tables:
-  // from then on they neither move nor change to another list.
+  // from then on they neither move nor change to another list.  (The operators'
+  // scratch is no part of it: those calls share nothing else with the lists'.)
   bool frozen = false;
 
   void freeze() {
     frozen = true;
-    for (DevBuf* b : {&slots, &saved_scales, &norm_buf, &dev_scalars, &op_scratch,
-                      &cast_descs, &cast_chunks, &step_descs, &step_chunks,
-                      &reduce_descs, &reduce_chunks})
+    for (DevBuf* b : {&slots, &saved_scales, &norm_buf, &dev_scalars, &cast_descs,
+                      &cast_chunks, &step_descs, &step_chunks, &reduce_descs,
+                      &reduce_chunks})
       b->frozen = true;
   }
 
@@ -497,7 +498,7 @@ int record_error(int status, const char* what) { return fail(status, what); }
 
 // The call scope of the training operators.  The scratch follows the other
 // workspace buffers' rules: it only grows, not while the stream captures a
-// CUDA graph, and not after one was captured with it.
+// CUDA graph, and not after an operator was captured with it.
 OpCall::OpCall() : lock_(g_mu) {}
 
 int OpCall::open(const char* fn, cudaStream_t stream, size_t scratch_bytes) {
@@ -514,7 +515,7 @@ int OpCall::open(const char* fn, cudaStream_t stream, size_t scratch_bytes) {
   if (graph && scratch_bytes > ws->op_scratch.cap) e = cudaErrorStreamCaptureUnsupported;
   if (e == cudaSuccess) e = ws->op_scratch.reserve(scratch_bytes);
   if (e != cudaSuccess) return cuda_fail(e, (std::string(fn) + ": workspace").c_str());
-  if (graph) ws->freeze();
+  if (graph) ws->op_scratch.frozen = true;
   scratch = static_cast<char*>(ws->op_scratch.ptr);
   return FP8OPT_OK;
 }

@@ -601,8 +601,10 @@ FP8OPT_API int fp8_norm_terms_from_limbs(const int64_t *limbs_dev,
  * path.  Outputs may not overlap inputs.  An empty tensor may have a NULL
  * address.  No call waits for the stream.  Results do not depend on the
  * schedule: repeated calls give the same bits.  Scratch (the backward passes
- * and the cross entropy) comes from the stream's workspace, with its rules on
- * growth and capture.
+ * and the cross entropy) belongs to the stream: it grows when a call needs more,
+ * not while the stream captures a CUDA graph, and not after an operator that
+ * uses it was captured (until fp8opt_release_stream).  Captured operators and
+ * captured lists do not freeze each other's memory.
  */
 
 /* Elements that share one scale of an activation checkpoint. */

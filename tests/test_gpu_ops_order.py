@@ -85,3 +85,70 @@ def test_large_calls_that_read_what_the_one_before_wrote(bo):
             got = chain(x, w, False)
             for i, (a, b) in enumerate(zip(got, want[k])):
                 assert torch.equal(a, b), (repeat, k, i)
+
+
+@pytest.fixture
+def stream(bo):
+    """A stream for capturing, its workspace freed afterwards."""
+    import gc
+    s = torch.cuda.Stream()
+    yield s
+    gc.collect()
+    torch.cuda.synchronize()
+    bo.release_stream(s)
+
+
+def cast_plan(bo, n):
+    x = torch.randn(n, device="cuda").bfloat16()
+    return bo.CastPlan([x], [torch.empty(n, dtype=torch.uint8, device="cuda")],
+                       torch.empty(1, device="cuda"), torch.empty(1, device="cuda"), "e4m3")
+
+
+def norm_gradient(bo, rows, cols):
+    x = torch.randn(rows, cols, device="cuda").bfloat16()
+    w = torch.ones(cols, device="cuda")
+    mean, rstd = torch.zeros(rows, device="cuda"), torch.ones(rows, device="cuda")
+    return lambda: bo.layer_norm_backward(x, w, rstd, x=x, mean=mean)
+
+
+def test_a_captured_list_leaves_the_operators_scratch_free(bo, stream):
+    """A graph that holds a cast uses none of the operators' scratch: it may
+    still be allocated, and grow, on the stream; and the graph still replays."""
+    plan = cast_plan(bo, 5000)
+    grads = [norm_gradient(bo, 64, 256), norm_gradient(bo, 3000, 4096)]
+    torch.cuda.synchronize()
+    want = [g() for g in grads]
+    with torch.cuda.stream(stream):
+        plan(stream)
+    stream.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=stream):
+        plan(stream)
+    with torch.cuda.stream(stream):
+        got = [g() for g in grads]
+        graph.replay()
+    torch.cuda.synchronize()
+    for a, b in zip(got, want):
+        assert all(torch.equal(s, t) for s, t in zip(a, b))
+
+
+def test_a_captured_operator_leaves_the_lists_free(bo, stream):
+    """A graph that holds a norm's gradient refers to none of the lists'
+    tables: the stream still takes other lists; its scratch does not grow."""
+    grad, larger = norm_gradient(bo, 64, 256), norm_gradient(bo, 3000, 4096)
+    plans = [cast_plan(bo, 5000), cast_plan(bo, 70001)]
+    torch.cuda.synchronize()
+    with torch.cuda.stream(stream):
+        want = grad()
+    stream.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=stream):
+        got = grad()
+    with torch.cuda.stream(stream):
+        for p in plans:
+            p(stream)
+        with pytest.raises(bo.Fp8OptError):
+            larger()
+        graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(s, t) for s, t in zip(got, want))

@@ -127,6 +127,9 @@ int fail(int status, const std::string& what) {
 }
 
 int cuda_fail(cudaError_t e, const char* where) {
+  // The runtime keeps the error for cudaGetLastError(), which the next launch
+  // asks: an allocation that failed is not that launch's.
+  cudaGetLastError();
   return fail(FP8OPT_ERR_CUDA,
               std::string(where) + ": " + cudaGetErrorName(e) + ": " +
                   cudaGetErrorString(e));

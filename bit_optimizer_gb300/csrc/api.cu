@@ -152,7 +152,14 @@ struct DevBuf {
     }
     size_t want = bytes < 4096 ? 4096 : bytes + bytes / 4;
     cudaError_t e = cudaMalloc(&ptr, want);
-    if (e != cudaSuccess) return e;
+    if (e == cudaErrorMemoryAllocation) {   // without room to grow, then
+      cudaGetLastError();
+      e = cudaMalloc(&ptr, want = bytes);
+    }
+    if (e != cudaSuccess) {
+      ptr = nullptr;
+      return e;
+    }
     cap = want;
     return cudaSuccess;
   }

@@ -9,11 +9,13 @@
 #include <Python.h>
 
 #include <ATen/ops/empty.h>
+#include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <cstring>
 #include <string>
 
 namespace {
@@ -21,9 +23,10 @@ namespace {
 using at::Tensor;
 using at::ScalarType;
 
-// The C entry points, in the order of ops.py's list.
+// The C entry points, in the order of ops.py's list (the last one gives the text
+// of a call's error).
 enum { kActSave, kActLoad, kGelu, kGeluBackward, kNorm, kNormBackward, kXent, kXentBackward,
-       kEntries };
+       kLastError, kEntries };
 void* g_fn[kEntries];
 PyObject* g_fail = nullptr;   // ops.py's function that raises for a status
 
@@ -139,12 +142,24 @@ Tensor fresh(at::IntArrayRef shape, ScalarType type, int device) {
   return at::empty(shape, at::TensorOptions().dtype(type).device(at::kCUDA, (c10::DeviceIndex)device));
 }
 
+bool out_of_memory() {
+  const char* text = reinterpret_cast<const char* (*)()>(g_fn[kLastError])();
+  return std::strstr(text, "cudaErrorMemoryAllocation") != nullptr;
+}
+
 // Calls C entry point i without the interpreter's lock; raises for a status.
+// The library's scratch is not torch's memory: where there is no room for it,
+// torch gives back what it caches, as for an allocation of its own.
 template <class... T>
 void call(int i, T... a) {
   int status = 0;
   Py_BEGIN_ALLOW_THREADS
-  status = reinterpret_cast<int (*)(T...)>(g_fn[i])(a...);
+  const auto fn = reinterpret_cast<int (*)(T...)>(g_fn[i]);
+  status = fn(a...);
+  if (status != 0 && out_of_memory()) {
+    c10::cuda::CUDACachingAllocator::emptyCache();
+    status = fn(a...);
+  }
   Py_END_ALLOW_THREADS
   if (status == 0) return;
   PyObject* r = PyObject_CallFunction(g_fail, "i", status);   // raises

@@ -13,7 +13,10 @@ dtype raises TypeError, a wrong shape, layout or option ValueError, and what the
 library itself refuses Fp8OptError.  Outputs are allocated on ``stream`` (the
 current stream unless given), where the work runs too, and the caller orders
 other streams' use of the inputs and outputs against it, as for any CUDA work.
-No function waits for the GPU.
+No function waits for the GPU, but when the scratch of the backward passes and
+the cross entropy has to grow: the stream keeps its scratch (a quarter more than
+the largest call's, where there is room), outside torch's memory, until
+``release_stream`` or ``release``.
 
 ``bit_optimizer_gb300.nn`` wraps these functions for autograd.
 """
@@ -39,7 +42,7 @@ BINDING_PATH = os.path.join(_lib.HERE, "_build", "fp8opt_binding.so")
 # The C entry points the binding calls, in its order.
 _ENTRIES = ("fp8_act_save", "fp8_act_load", "fp8_gelu", "fp8_gelu_backward",
             "fp8_layer_norm", "fp8_layer_norm_backward", "fp8_linear_xent",
-            "fp8_linear_xent_backward")
+            "fp8_linear_xent_backward", "fp8opt_last_error")
 
 
 def _load_binding():

@@ -599,10 +599,12 @@ FP8OPT_API int fp8_norm_terms_from_limbs(const int64_t *limbs_dev,
  * rounded to its type once.  16-byte-aligned buffers (and, for layer norm, a
  * row length that is a multiple of 8) take the vector path, others an element
  * path.  Outputs may not overlap inputs.  An empty tensor may have a NULL
- * address.  No call waits for the stream.  Results do not depend on the
+ * address.  No call waits for the stream, but when its scratch grows.  Results do not depend on the
  * schedule: repeated calls give the same bits.  Scratch (the backward passes
- * and the cross entropy) belongs to the stream: it grows when a call needs more,
- * not while the stream captures a CUDA graph, and not after an operator that
+ * and the cross entropy) belongs to the stream and is kept: it grows when a call
+ * needs more (the old block is freed, which waits for the device, and a quarter
+ * more than needed allocated, or what is needed where that does not fit), not
+ * while the stream captures a CUDA graph, and not after an operator that
  * uses it was captured (until fp8opt_release_stream).  Captured operators and
  * captured lists do not freeze each other's memory.
  */

@@ -31,3 +31,41 @@ def test_a_call_whose_scratch_does_not_fit_leaves_no_error_behind(bo):
         loss_gradient(bo, total // 512 + 1, 1, 1)()
     assert torch.equal(bo.layer_norm(x, w, w)[0], y)
     torch.cuda.synchronize()
+
+
+def room(bytes_left):
+    """A tensor that leaves this much of the device's free memory."""
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    return torch.empty(torch.cuda.mem_get_info()[0] - bytes_left, dtype=torch.uint8,
+                       device="cuda")
+
+
+# 2^21 tokens x 8 x 256 words, one piece: p 1 GiB, dx in fp32 (128 columns) 1 GiB, a
+# copy of x 32 MiB: 2.03 GiB, and a quarter more 2.54.
+ROWS, NEED = 1 << 21, (2 << 30) + (32 << 20)
+
+
+def test_scratch_without_room_to_grow_takes_what_it_needs(bo):
+    call = loss_gradient(bo, ROWS, 8, 256)
+    bo.release()
+    hog = room(NEED + (300 << 20))       # (the outputs' 34 MB come first)
+    dx, dw = call()
+    torch.cuda.synchronize()
+    assert (dx == 0).all() and (dw == 0).all()
+    del hog
+    torch.cuda.empty_cache()
+    bo.release()
+
+
+def test_scratch_takes_the_memory_that_torch_caches(bo):
+    """As an allocation of torch's own would."""
+    call = loss_gradient(bo, ROWS, 8, 256)
+    bo.release()
+    hog = room(1 << 30)
+    del hog                              # torch keeps it, free
+    assert torch.cuda.mem_get_info()[0] < NEED
+    dx, dw = call()
+    torch.cuda.synchronize()
+    assert (dx == 0).all() and (dw == 0).all()
+    bo.release()

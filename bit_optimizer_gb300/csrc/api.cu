@@ -530,24 +530,30 @@ int OpCall::open(const char* fn, cudaStream_t stream, size_t scratch_bytes) {
   return FP8OPT_OK;
 }
 
-int OpCall::error_word(const char* fn, int** device) {
-  static int* host = nullptr;   // guarded by the lock
-  if (host == nullptr) {
-    const cudaError_t e = cudaHostAlloc(reinterpret_cast<void**>(&host), sizeof(int),
-                                        cudaHostAllocPortable | cudaHostAllocMapped);
-    if (e != cudaSuccess) {
-      host = nullptr;
-      return cuda_fail(e, (std::string(fn) + ": workspace").c_str());
+int OpCall::error_word(const char* fn, cudaStream_t stream, int** device) {
+  static std::map<int, int*> words;   // of each device; guarded by the lock
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  int* host = nullptr;
+  if (e == cudaSuccess) host = words[dev];
+  if (e == cudaSuccess && host == nullptr) {
+    // (an allocation would end a capture of the stream)
+    e = capturing(stream) ? cudaErrorStreamCaptureUnsupported
+                          : cudaHostAlloc(reinterpret_cast<void**>(&host), sizeof(int),
+                                          cudaHostAllocPortable | cudaHostAllocMapped);
+    if (e == cudaSuccess) {
+      *host = 0;
+      words[dev] = host;
     }
-    *host = 0;
   }
-  if (*static_cast<volatile int*>(host) != 0) {
+  if (e == cudaSuccess && *static_cast<volatile int*>(host) != 0) {
     *static_cast<volatile int*>(host) = 0;
     return fail(FP8OPT_ERR_CUDA, std::string(fn) + ": a wait inside a kernel of an earlier call "
-                                 "ran out; that call's results are not complete");
+                                 "on this device ran out; that call's results are not complete, "
+                                 "and this one was not made");
   }
   void* p = nullptr;
-  const cudaError_t e = cudaHostGetDevicePointer(&p, host, 0);
+  if (e == cudaSuccess) e = cudaHostGetDevicePointer(&p, host, 0);
   if (e != cudaSuccess) return cuda_fail(e, (std::string(fn) + ": workspace").c_str());
   *device = static_cast<int*>(p);
   return FP8OPT_OK;

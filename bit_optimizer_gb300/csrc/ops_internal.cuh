@@ -132,10 +132,10 @@ class OpCall {
   OpCall();
   int open(const char* fn, cudaStream_t stream, size_t scratch_bytes);
   int done(const char* fn, cudaError_t e);   // the call's status
-  // The word in which kernels record that a wait of theirs ran out: pinned
-  // host memory, so that a later call sees it without waiting for the GPU and
-  // fails.
-  int error_word(const char* fn, int** device);
+  // The device's word in which kernels record that a wait of theirs ran out:
+  // pinned host memory, so that a call made after such a kernel's end sees it
+  // without waiting for the GPU, and fails.
+  int error_word(const char* fn, cudaStream_t stream, int** device);
   char* scratch = nullptr;
   int sms = 0;
   LaunchMark mark = nullptr;

@@ -237,7 +237,7 @@ extern "C" int fp8_linear_xent(const void* x, const void* w, const int64_t* targ
     int* error = nullptr;
     if ((st = call.open(fn, stream, 0)) != FP8OPT_OK ||
         (st = call.open(fn, stream, xent_forward_scratch(a, call.sms))) != FP8OPT_OK ||
-        (st = call.error_word(fn, &error)) != FP8OPT_OK)
+        (st = call.error_word(fn, stream, &error)) != FP8OPT_OK)
       return st;
     return call.done(fn, launch_xent_forward(a, call.scratch, error, call.sms, stream,
                                              call.mark));
@@ -274,7 +274,7 @@ extern "C" int fp8_linear_xent_backward(const float* dloss, const void* x, const
     if ((st = call.open(fn, stream, 0)) != FP8OPT_OK) return st;
     const size_t bytes = rows > 0 ? xent_backward_scratch(a, call.sms) : 0;
     if ((st = call.open(fn, stream, bytes)) != FP8OPT_OK ||
-        (st = call.error_word(fn, &error)) != FP8OPT_OK)
+        (st = call.error_word(fn, stream, &error)) != FP8OPT_OK)
       return st;
     return call.done(fn, launch_xent_backward(a, call.scratch, error, call.sms, stream,
                                               call.mark));

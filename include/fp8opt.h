@@ -695,8 +695,11 @@ FP8OPT_API int fp8_layer_norm_backward(
  * 64.
  *
  * The kernels wait for their copies and products with a limit of about two
- * seconds; should one run out (it does not on a working device), the next
- * call returns FP8OPT_ERR_CUDA.
+ * seconds.  Should one run out (it does not on a working device), the call's
+ * results are not complete, and the first fp8_linear_xent or
+ * fp8_linear_xent_backward issued on the device after that kernel has ended
+ * returns FP8OPT_ERR_CUDA and launches nothing.  Calls issued earlier, other
+ * calls and replays of a captured graph do not look.
  */
 FP8OPT_API int fp8_linear_xent(const void *x, const void *w,
                                const int64_t *target, int64_t rows,

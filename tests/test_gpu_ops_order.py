@@ -152,3 +152,44 @@ def test_a_captured_operator_leaves_the_lists_free(bo, stream):
         graph.replay()
     torch.cuda.synchronize()
     assert all(torch.equal(s, t) for s, t in zip(got, want))
+
+
+def test_the_first_loss_under_capture_is_refused_and_the_capture_goes_on(bo, tmp_path):
+    """In a fresh process, whose device has no error word yet: the stream has
+    scratch enough from a norm's gradient, so the word is all that is missing.
+    Allocating it would end the capture."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    script = tmp_path / "capture.py"
+    script.write_text(f"""
+import sys
+sys.path.insert(0, {root!r})
+import torch, bit_optimizer_gb300 as bo
+s = torch.cuda.Stream()
+x, w = torch.randn(3000, 4096, device="cuda"), torch.ones(4096, device="cuda")
+r = torch.ones(3000, device="cuda")
+a = torch.randn(8, 64, device="cuda").half()
+t = torch.arange(8, device="cuda")
+with torch.cuda.stream(s):
+    want = bo.layer_norm_backward(x, w, r, x=x, mean=r)
+torch.cuda.synchronize()
+graph, refused = torch.cuda.CUDAGraph(), False
+with torch.cuda.graph(graph, stream=s):
+    got = bo.layer_norm_backward(x, w, r, x=x, mean=r)
+    try:
+        bo.linear_cross_entropy(a, a, t)
+    except bo.Fp8OptError as e:
+        refused = "StreamCaptureUnsupported" in str(e)
+graph.replay()
+torch.cuda.synchronize()
+assert refused and all(torch.equal(p, q) for p, q in zip(got, want))
+with torch.cuda.stream(s):
+    loss, _ = bo.linear_cross_entropy(a, a, t)
+torch.cuda.synchronize()
+assert torch.isfinite(loss).all()
+print("went on")
+""")
+    r = subprocess.run([sys.executable, str(script)], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "went on" in r.stdout, r.stderr[-2000:]

@@ -12,6 +12,7 @@ and square root keep nvcc's IEEE defaults (``-prec-div=true
 from __future__ import annotations
 
 import concurrent.futures as cf
+import importlib.metadata
 import importlib.util
 import os
 import shutil
@@ -24,6 +25,7 @@ CSRC = os.path.join(HERE, "csrc")
 OUT_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(OUT_DIR, "libfp8opt.so")
 BINDING = os.path.join(OUT_DIR, "fp8opt_binding.so")
+BINDING_STAMP = BINDING + ".torch"
 BINDING_SOURCE = os.path.join(CSRC, "binding.cpp")
 SOURCES = ["api.cu", "cast_kernels.cu", "step_kernels.cu", "fused_kernels.cu",
            "noalloc.cu", "reduce_kernels.cu", "norm_kernels.cu", "train_api.cu",
@@ -45,6 +47,18 @@ def _stale(out, sources) -> bool:
         return True
     t = os.path.getmtime(out)
     return any(os.path.getmtime(p) > t for p in [*sources, __file__])
+
+
+def _torch() -> str:
+    """The torch and Python that a binding is built against."""
+    return f"{importlib.metadata.version('torch')} {sys.version}"
+
+
+def _binding_stale() -> bool:
+    if _stale(BINDING, [BINDING_SOURCE]) or not os.path.exists(BINDING_STAMP):
+        return True
+    with open(BINDING_STAMP) as f:
+        return f.read() != _torch()
 
 
 def _compile(src: str, verbose: bool) -> str:
@@ -75,13 +89,16 @@ def _compile_binding() -> None:
     if r.returncode != 0:
         raise RuntimeError(f"compiling binding.cpp failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, BINDING)
+    with open(BINDING_STAMP, "w") as f:
+        f.write(_torch())
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile and link libfp8opt.so and the binding where a source is newer;
-    return the library's path."""
+    """Compile and link libfp8opt.so and the binding where a source is newer,
+    the binding also where it was built against another torch; return the
+    library's path."""
     lib = force or _stale(LIB, [os.path.join(CSRC, s) for s in SOURCES + DEPS])
-    binding = force or _stale(BINDING, [BINDING_SOURCE])
+    binding = force or _binding_stale()
     os.makedirs(OUT_DIR, exist_ok=True)
     with cf.ThreadPoolExecutor(len(SOURCES) + 1) as ex:
         other = ex.submit(_compile_binding) if binding else None

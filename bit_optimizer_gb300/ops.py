@@ -26,6 +26,7 @@ import ctypes as C
 import importlib.machinery
 import importlib.util
 import os
+import threading
 
 import torch
 
@@ -60,7 +61,20 @@ def _load_binding():
     return module
 
 
-_b = _load_binding()
+class _Unloaded:
+    """Stands for the binding until a function below is first called: the
+    optimizer needs the C library alone, and is there without it."""
+    _lock = threading.Lock()
+
+    def __getattr__(self, name):
+        global _b
+        with self._lock:
+            if _b is self:
+                _b = _load_binding()
+        return getattr(_b, name)
+
+
+_b = _Unloaded()
 
 
 # ------------------------------------------------- activation checkpoints

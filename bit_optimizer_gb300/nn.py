@@ -14,6 +14,10 @@ stream in FP16 or BF16:
     h = nn.layer_norm(x, ln_w, ln_b)
     x = x + nn.linear(nn.gelu(nn.linear(h, fc_w, fc_b)), proj_w, proj_b)
     loss = nn.linear_cross_entropy(nn.layer_norm(x, lnf_w, lnf_b), wte, target)
+
+Under torch.autocast the two linear layers cast their input and parameters to
+its dtype, as torch's do, so FP32 weights get FP32 gradients; ``layer_norm`` and
+``gelu`` take what they are given, and their result has its type.
 """
 from __future__ import annotations
 
@@ -112,8 +116,18 @@ def gelu(x, approximate: str = "tanh"):
     return _Gelu.apply(x.contiguous(), approximate)
 
 
+def _autocast(*tensors):
+    """The tensors in autocast's dtype where it is on (float64 stays, as there)."""
+    if not torch.is_autocast_enabled("cuda"):
+        return tensors
+    dtype = torch.get_autocast_dtype("cuda")
+    return tuple(t if t is None or not t.is_floating_point() or t.dtype == torch.float64
+                 else t.to(dtype) for t in tensors)
+
+
 def linear(x, weight, bias=None):
     """x weight^T + bias."""
+    x, weight, bias = _autocast(x, weight, bias)
     return _Linear.apply(x.contiguous(), weight, bias)
 
 
@@ -125,6 +139,7 @@ def linear_cross_entropy(x, weight, target, ignore_index: int = -100,
     when all are)."""
     if reduction not in ("none", "sum", "mean"):
         raise ValueError(f"reduction must be 'none', 'sum' or 'mean', not {reduction!r}")
+    x, weight = _autocast(x, weight)
     loss = _LinearCrossEntropy.apply(x.contiguous().view(-1, x.shape[-1]), weight,
                                      target.contiguous().view(-1), ignore_index)
     if reduction == "none":

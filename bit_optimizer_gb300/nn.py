@@ -5,8 +5,9 @@ pass what the operator's 8-bit form keeps, and nothing else.
 * ``gelu``: the input in E4M3.
 * ``linear``: the product is torch's; its input, which the weight's gradient
   needs, is kept in E4M3.
-* ``linear_cross_entropy``: the input, the weight and one float per token; the
-  logits are never in memory as a whole.
+* ``linear_cross_entropy``: the input, the weight and one float per token; no
+  logits (the backward pass makes the probabilities again, two pieces of the
+  vocabulary at a time).
 
 A GPT block's feed-forward half and its loss are then, with x the residual
 stream in FP16 or BF16:
@@ -17,7 +18,8 @@ stream in FP16 or BF16:
 
 Under torch.autocast the two linear layers cast their input and parameters to
 its dtype, as torch's do, so FP32 weights get FP32 gradients; ``layer_norm`` and
-``gelu`` take what they are given, and their result has its type.
+``gelu`` take what they are given, and their result has its type.  Under no_grad
+the checkpoints are written all the same, and freed.
 """
 from __future__ import annotations
 

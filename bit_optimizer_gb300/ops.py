@@ -18,7 +18,8 @@ the cross entropy has to grow: the stream keeps its scratch (a quarter more than
 the largest call's, where there is room), outside torch's memory, until
 ``release_stream`` or ``release``.
 
-``bit_optimizer_gb300.nn`` wraps these functions for autograd.
+These functions are not seen by autograd: their results require no gradient,
+whatever the arguments do.  ``bit_optimizer_gb300.nn`` wraps them for it.
 """
 from __future__ import annotations
 
@@ -138,7 +139,7 @@ def linear_cross_entropy(x: torch.Tensor, w: torch.Tensor, target: torch.Tensor,
     token's logits x w^T, loss = lse - logit of its target (0 for a target of
     ignore_index, NaN for another one outside the vocabulary).  x: (tokens,
     dim), w: (vocabulary, dim), bfloat16 or float16; target: int64.  The
-    logits are never in memory as a whole."""
+    logits are never in memory."""
     return _b.linear_cross_entropy(x, w, target, ignore_index, stream)
 
 
@@ -146,5 +147,7 @@ def linear_cross_entropy_backward(dloss: torch.Tensor, x: torch.Tensor, w: torch
                                   target: torch.Tensor, lse: torch.Tensor,
                                   ignore_index: int = -100, stream=None):
     """(dx, dw), in x's type, for the gradient dloss (float32, one per token)
-    of ``linear_cross_entropy``'s loss; lse is that call's."""
+    of ``linear_cross_entropy``'s loss; lse is that call's.  In scratch: the
+    probabilities of two pieces of the vocabulary, in 16 bits (128 to 256 MiB each;
+    for few tokens that is all of them)."""
     return _b.linear_cross_entropy_backward(dloss, x, w, target, lse, ignore_index, stream)

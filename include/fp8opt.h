@@ -596,17 +596,22 @@ FP8OPT_API int fp8_norm_terms_from_limbs(const int64_t *limbs_dev,
  *
  * Common rules: tensors are contiguous; `dtype` is FP8OPT_F32, FP8OPT_BF16 or
  * FP8OPT_F16; sums, statistics and exponentials are fp32, and a result is
- * rounded to its type once.  16-byte-aligned buffers (and, for layer norm, a
- * row length that is a multiple of 8) take the vector path, others an element
- * path.  Outputs may not overlap inputs.  An empty tensor may have a NULL
- * address.  No call waits for the stream, but when its scratch grows.  Results do not depend on the
- * schedule: repeated calls give the same bits.  Scratch (the backward passes
- * and the cross entropy) belongs to the stream and is kept: it grows when a call
- * needs more (the old block is freed, which waits for the device, and a quarter
- * more than needed allocated, or what is needed where that does not fit), not
- * while the stream captures a CUDA graph, and not after an operator that
- * uses it was captured (until fp8opt_release_stream).  Captured operators and
- * captured lists do not freeze each other's memory.
+ * rounded to its type once.  Buffers at 16-byte boundaries are read and
+ * written in vectors, others by elements.  Layer norm's rows of up to 8192
+ * elements go in vectors of the row where its length is a multiple of 8 (and
+ * weight and bias are aligned too), else, from 352 elements forward and 192
+ * backward, in vectors of the whole tensor with the row's ends masked, and
+ * shorter ones by elements; longer rows are read element by element, more than
+ * once.  Outputs may not overlap inputs.  An empty tensor may have a NULL
+ * address.  No call waits for the stream, but when its scratch grows.  Results
+ * do not depend on the schedule: repeated calls give the same bits.  Scratch
+ * (the backward passes and the cross entropy) belongs to the stream and is
+ * kept: it grows when a call needs more (the old block is freed, which waits
+ * for the device, and a quarter more than needed allocated, or what is needed
+ * where that does not fit), not while the stream captures a CUDA graph, and
+ * not after an operator that uses it was captured (until
+ * fp8opt_release_stream).  Captured operators and captured lists do not freeze
+ * each other's memory.
  */
 
 /* Elements that share one scale of an activation checkpoint. */
@@ -681,18 +686,18 @@ FP8OPT_API int fp8_layer_norm_backward(
  * token's loss) and the forward pass's lse,
  *   p[i, v] = (exp(z[i, v] - lse[i]) - [v = target[i]]) * dloss[i],
  *   dx = p w,  dw = p^T x  (of type dtype, both overwritten).
- * The vocabulary is taken in pieces: p exists for one piece at a time, in
- * 16 bits, each token's scaled against underflow, so that a token's dx does not
- * suffer from a dloss far below the others'.  An ignored token has dx 0 and no
- * part in dw, whatever its row of x holds.  rows = 0 gives dw 0.
+ * The vocabulary is taken in pieces: p exists for two pieces at a time (of
+ * some 128 to 256 MiB each: for up to 2600 tokens over 50257 words that is all
+ * of it), in 16 bits, each token's scaled against underflow, so that a token's
+ * dx does not suffer from a dloss far below the others'.  An ignored token has
+ * dx 0 and no part in dw, whatever its row of x holds.  rows = 0 gives dw 0.
  * Rows whose length is a multiple of 8 in 16-byte-aligned tensors are read in
  * place, others through a copy in scratch.  Scratch: the statistics of the
- * column tiles (forward); a copy of x (two of rows that are not read in place),
- * two pieces of p (128 to 256 MiB each, less
- * for a small vocabulary, or 512 bytes a token where that is more) and dx in
- * fp32, up to eight times, or 16 within 64 MiB (backward).  dim and vocab >= 1;
- * vocab, and forward rows, below 2^31; dim, and backward rows, at most 2^30 -
- * 64.
+ * column tiles (forward); a copy of x (two of rows that are not read in
+ * place), two pieces of p (128 to 256 MiB each, less for a small vocabulary,
+ * or 512 bytes a token where that is more) and dx in fp32, up to eight times,
+ * or 16 within 64 MiB (backward).  dim and vocab >= 1; vocab, and forward
+ * rows, below 2^31; dim, and backward rows, at most 2^30 - 64.
  *
  * The kernels wait for their copies and products with a limit of about two
  * seconds.  Should one run out (it does not on a working device), the call's

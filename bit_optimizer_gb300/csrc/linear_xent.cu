@@ -28,11 +28,11 @@
 // everybody.  x and w are K-major in the logits product; w in dx, and both
 // operands of dw, are read MN-major, so nothing is transposed in memory.
 //
-// Bound by the tensor cores: 8192 x 2048 x 50257 forward 0.83 ms, 2.03 PFLOP/s
-// in a short run (cuBLAS' measured burst: 1.91); in a long one the power limit
-// lowers the clock for both (8192 x 1024: 1.72 PFLOP/s; cuBLAS 1.70).  The
-// gradients of 8192 x 2048: 3.0 ms, 1.69 PFLOP/s, the tensor pipe active 86% of
-// the cycles.  Few tokens are bound by reading w: 24 x 768 x 200000, 55 us, 5.6
+// Bound by the tensor cores: 8192 x 2048 x 50257 forward 0.92 ms, 1.83 PFLOP/s in
+// calls in a row (cuBLAS' measured burst: 1.91); in loops of seconds the power
+// limit lowers the clock for both (8192 x 1024: 1.73 PFLOP/s; cuBLAS 1.70).  The
+// gradients of 8191 x 2048: 3.2 ms, 1.58 PFLOP/s, the tensor pipe active 87% of the
+// cycles.  Few tokens are bound by reading w: 24 x 768 x 200000, 55 us, 5.6
 // TB/s.  What a step brought: single CTAs with tiles of 128 x 256 and four
 // stages, a launch for each product: 353 us forward and 1540 us backward at 8192
 // x 2048 x 20224; pairs, which need two thirds of the L2 traffic, six stages and

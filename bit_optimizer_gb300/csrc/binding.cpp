@@ -142,6 +142,15 @@ Tensor fresh(at::IntArrayRef shape, ScalarType type, int device) {
   return at::empty(shape, at::TensorOptions().dtype(type).device(at::kCUDA, (c10::DeviceIndex)device));
 }
 
+// The interpreter's lock, given up for a scope: taken back also where something
+// in it throws.
+struct Unlocked {
+  Unlocked() : state(PyEval_SaveThread()) {}
+  ~Unlocked() { PyEval_RestoreThread(state); }
+  Unlocked(const Unlocked&) = delete;
+  PyThreadState* state;
+};
+
 bool out_of_memory() {
   const char* text = reinterpret_cast<const char* (*)()>(g_fn[kLastError])();
   return std::strstr(text, "cudaErrorMemoryAllocation") != nullptr;
@@ -153,14 +162,15 @@ bool out_of_memory() {
 template <class... T>
 void call(int i, T... a) {
   int status = 0;
-  Py_BEGIN_ALLOW_THREADS
-  const auto fn = reinterpret_cast<int (*)(T...)>(g_fn[i]);
-  status = fn(a...);
-  if (status != 0 && out_of_memory()) {
-    c10::cuda::CUDACachingAllocator::emptyCache();
+  {
+    Unlocked scope;
+    const auto fn = reinterpret_cast<int (*)(T...)>(g_fn[i]);
     status = fn(a...);
+    if (status != 0 && out_of_memory()) {
+      c10::cuda::CUDACachingAllocator::emptyCache();
+      status = fn(a...);
+    }
   }
-  Py_END_ALLOW_THREADS
   if (status == 0) return;
   PyObject* r = PyObject_CallFunction(g_fail, "i", status);   // raises
   Py_XDECREF(r);

@@ -10,9 +10,10 @@ from ._lib import (BF16, E4M3, E5M2, EXPORTS, F16, F32, KERNELS, Fp8OptError,
 from .api import (AdamWPlan, CastPlan, CastStepPlan, Fp8AdamW, ReducePlan,
                   StepState, arena_views, fp8_adamw_step, fp8_cast_scaled,
                   fp8_reduce_scaled)
-from .ops import (act_load, act_save, gelu, gelu_backward, layer_norm,
-                  layer_norm_backward, linear_cross_entropy,
-                  linear_cross_entropy_backward)
+from .ops import (act_load, act_save, embedding, embedding_backward, gelu,
+                  gelu_backward, layer_norm, layer_norm_backward,
+                  linear_cross_entropy, linear_cross_entropy_backward, policy_loss,
+                  policy_loss_backward)
 
 load()
 
@@ -23,4 +24,5 @@ __all__ = ["fp8_cast_scaled", "fp8_adamw_step", "fp8_reduce_scaled",
            "LIB_PATH", "EXPORTS",
            "KERNELS", "timing_enable", "timing_read", "act_save", "act_load",
            "gelu", "gelu_backward", "layer_norm", "layer_norm_backward",
-           "linear_cross_entropy", "linear_cross_entropy_backward"]
+           "linear_cross_entropy", "linear_cross_entropy_backward", "embedding",
+           "embedding_backward", "policy_loss", "policy_loss_backward"]

@@ -29,7 +29,8 @@ EXPORTS = ("fp8_cast_scaled", "fp8_adamw_step", "fp8_adam_step",
            "fp8_reduce_scaled_finish", "fp8_norm_terms_from_limbs",
            "fp8_act_save", "fp8_act_load", "fp8_gelu", "fp8_gelu_backward",
            "fp8_layer_norm", "fp8_layer_norm_backward", "fp8_linear_xent",
-           "fp8_linear_xent_backward",
+           "fp8_linear_xent_backward", "fp8_embedding", "fp8_embedding_backward",
+           "fp8_policy_loss", "fp8_policy_loss_backward",
            "fp8opt_strerror",
            "fp8opt_last_error", "fp8opt_timing_enable", "fp8opt_timing_read",
            "fp8opt_release", "fp8opt_release_stream")
@@ -38,10 +39,13 @@ KERNELS = ("cast_amax", "cast_encode", "step_amax", "step_update", "step_w8",
            "grad_norm_terms", "clip_coef", "found", "act_save", "act_load",
            "gelu", "gelu_backward", "layer_norm", "layer_norm_backward",
            "layer_norm_params", "xent_logits", "xent_join", "xent_prepare",
-           "xent_grads", "xent_dx")
+           "xent_grads", "xent_dx", "embedding", "embedding_order",
+           "embedding_sums", "embedding_join", "policy_loss", "policy_join",
+           "policy_backward")
 MAX_SHARDS = 64
 ACT_GROUP = 128
 GELU_ERF, GELU_TANH = 0, 1
+MEAN_TOKEN, MEAN_SEQUENCE = 0, 1
 
 
 class CastItem(C.Structure):
@@ -179,7 +183,7 @@ def load(path: str = LIB_PATH) -> C.CDLL:
         C.POINTER(CastItem), C.POINTER(Param), C.c_int, C.c_int, C.c_float,
         C.c_float, C.c_float, C.c_float, C.c_int, C.c_float, C.c_void_p,
         C.c_void_p, C.c_void_p, C.c_void_p]
-    p, i64, i32 = C.c_void_p, C.c_int64, C.c_int
+    p, i64, i32, f64 = C.c_void_p, C.c_int64, C.c_int, C.c_double
     for name, args in (
             ("fp8_act_save", [p, i64, i32, p, p, p]),
             ("fp8_act_load", [p, p, i64, i32, p, p]),
@@ -191,7 +195,14 @@ def load(path: str = LIB_PATH) -> C.CDLL:
                                          i32, p, p, p, p]),
             ("fp8_linear_xent", [p, p, p, i64, i64, i64, i32, i64, p, p, p]),
             ("fp8_linear_xent_backward", [p, p, p, p, p, i64, i64, i64, i32,
-                                          i64, p, p, p])):
+                                          i64, p, p, p]),
+            ("fp8_embedding", [p, p, i64, i64, i64, i32, C.c_float, p, p]),
+            ("fp8_embedding_backward", [p, p, i64, i64, i64, i32, C.c_float, i64,
+                                        p, p]),
+            ("fp8_policy_loss", [p, p, p, p, p, i64, i64, i32, f64, f64, f64,
+                                 i32, p, p, p]),
+            ("fp8_policy_loss_backward", [p, p, p, p, p, p, p, i64, i64, i32,
+                                          f64, f64, f64, p, p])):
         fn = getattr(L, name)
         fn.restype, fn.argtypes = C.c_int, args
     L.fp8opt_strerror.restype = C.c_char_p

@@ -30,7 +30,7 @@ BINDING_SOURCE = os.path.join(CSRC, "binding.cpp")
 SOURCES = ["api.cu", "cast_kernels.cu", "step_kernels.cu", "fused_kernels.cu",
            "noalloc.cu", "reduce_kernels.cu", "norm_kernels.cu", "train_api.cu",
            "act_kernels.cu", "layer_norm_fwd.cu", "layer_norm_bwd.cu",
-           "linear_xent.cu"]
+           "linear_xent.cu", "embedding.cu", "policy_loss.cu"]
 DEPS = ["fp8opt_internal.cuh", "ops_internal.cuh", "layer_norm.cuh",
         "tensor_core.cuh", os.path.join("..", "..", "include", "fp8opt.h")]
 

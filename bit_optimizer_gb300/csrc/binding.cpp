@@ -17,6 +17,7 @@
 
 #include <cstring>
 #include <string>
+#include <vector>
 
 namespace {
 
@@ -26,7 +27,7 @@ using at::ScalarType;
 // The C entry points, in the order of ops.py's list (the last one gives the text
 // of a call's error).
 enum { kActSave, kActLoad, kGelu, kGeluBackward, kNorm, kNormBackward, kXent, kXentBackward,
-       kLastError, kEntries };
+       kEmbedding, kEmbeddingBackward, kPolicy, kPolicyBackward, kLastError, kEntries };
 void* g_fn[kEntries];
 PyObject* g_fail = nullptr;   // ops.py's function that raises for a status
 
@@ -440,6 +441,134 @@ PyObject* xent_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// embedding(ids, w, scale, stream) -> (y,)
+PyObject* embedding(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return entry(n, 4, [&] {
+    Args args;
+    const Tensor& ids = args.tensor(a[0], "ids");
+    if (ids.scalar_type() != ScalarType::Long)
+      refuse(PyExc_TypeError, std::string("ids must be Long, not ") + c10::toString(ids.scalar_type()));
+    const Tensor& w = args.tensor(a[1], "w");
+    const int dt = dtype_of(w, "w");
+    if (w.dim() != 2 || w.size(0) < 1 || w.size(1) < 1)
+      refuse(PyExc_ValueError, "w must have shape (vocabulary, dim), not " + shape_text(w.sizes()));
+    const float scale = number(a[2], "scale");
+    std::vector<int64_t> shape(ids.sizes().begin(), ids.sizes().end());
+    shape.push_back(w.size(1));
+    OnStream on(a[3], args.device);
+    const Tensor y = fresh(shape, w.scalar_type(), args.device);
+    call(kEmbedding, ids.data_ptr(), w.data_ptr(), ids.numel(), w.size(1), w.size(0), dt, scale,
+         y.data_ptr(), on.handle);
+    return give(y);
+  });
+}
+
+// embedding_backward(dy, ids, vocab, scale, padding_idx or None, stream) -> (dw,)
+PyObject* embedding_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return entry(n, 6, [&] {
+    Args args;
+    const Tensor& dy = args.tensor(a[0], "dy");
+    const int dt = dtype_of(dy, "dy");
+    const int64_t dim = columns(dy, "dy");
+    const Tensor& ids = args.tensor(a[1], "ids", ScalarType::Long,
+                                    dy.sizes().slice(0, dy.dim() - 1));
+    const int64_t vocab = whole(a[2], "vocab");
+    if (vocab < 1) refuse(PyExc_ValueError, "vocab must be at least 1");
+    const float scale = number(a[3], "scale");
+    const int64_t padding = a[4] == Py_None ? -1 : whole(a[4], "padding_idx");
+    if (a[4] != Py_None && (padding < 0 || padding >= vocab))
+      refuse(PyExc_ValueError, "padding_idx must be in [0, vocab)");
+    OnStream on(a[5], args.device);
+    const Tensor dw = fresh({vocab, dim}, dy.scalar_type(), args.device);
+    call(kEmbeddingBackward, dy.data_ptr(), ids.data_ptr(), ids.numel(), dim, vocab, dt, scale,
+         padding, dw.data_ptr(), on.handle);
+    return give(dw);
+  });
+}
+
+// What both directions of the policy loss take.
+struct Policy {
+  const Tensor* logp;
+  const void *old_logp, *advantage, *mask = nullptr, *ref = nullptr;
+  int64_t batch, length;
+  int per_token;
+  double low, high, kl;
+};
+
+double real(PyObject* o, const char* name) {
+  const double v = PyFloat_AsDouble(o);
+  if (v == -1.0 && PyErr_Occurred()) {
+    PyErr_Clear();
+    refuse(PyExc_TypeError, std::string(name) + " must be a number");
+  }
+  return v;
+}
+
+// a: logp, old_logp, advantage, mask or None, ref_logp or None, clip_low,
+// clip_high, kl_coef
+Policy policy(Args& args, PyObject* const* a) {
+  Policy p;
+  p.logp = &args.tensor(a[0], "logp");
+  if (p.logp->scalar_type() != ScalarType::Float)
+    refuse(PyExc_TypeError, std::string("logp must be Float, not ") +
+                                c10::toString(p.logp->scalar_type()));
+  if (p.logp->dim() != 2)
+    refuse(PyExc_ValueError, "logp must have shape (batch, length), not " +
+                                 shape_text(p.logp->sizes()));
+  const at::IntArrayRef shape = p.logp->sizes();
+  p.batch = shape[0];
+  p.length = shape[1];
+  p.old_logp = args.tensor(a[1], "old_logp", ScalarType::Float, shape).data_ptr();
+  const Tensor& adv = args.tensor(a[2], "advantage");
+  p.per_token = adv.dim() == 2;
+  p.advantage = args.tensor(a[2], "advantage", ScalarType::Float,
+                            p.per_token ? shape : shape.slice(0, 1)).data_ptr();
+  if (a[3] != Py_None) p.mask = args.tensor(a[3], "mask", ScalarType::Bool, shape).data_ptr();
+  if (a[4] != Py_None) p.ref = args.tensor(a[4], "ref_logp", ScalarType::Float, shape).data_ptr();
+  p.low = real(a[5], "clip_low");
+  p.high = real(a[6], "clip_high");
+  p.kl = real(a[7], "kl_coef");
+  return p;
+}
+
+// policy_loss(logp, old_logp, advantage, mask, ref_logp, clip_low, clip_high,
+// kl_coef, reduction code, stream) -> stats, weight
+PyObject* policy_loss(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return entry(n, 10, [&] {
+    Args args;
+    const Policy p = policy(args, a);
+    const int reduction = (int)whole(a[8], "reduction");
+    OnStream on(a[9], args.device);
+    const Tensor stats = fresh({4}, ScalarType::Float, args.device);
+    const Tensor weight = fresh({p.batch}, ScalarType::Float, args.device);
+    call(kPolicy, p.logp->data_ptr(), p.old_logp, p.advantage, p.mask, p.ref, p.batch, p.length,
+         p.per_token, p.low, p.high, p.kl, reduction, stats.data_ptr(), weight.data_ptr(),
+         on.handle);
+    return give(stats, weight);
+  });
+}
+
+// policy_loss_backward(dloss, weight, logp, old_logp, advantage, mask, ref_logp,
+// clip_low, clip_high, kl_coef, stream) -> (dlogp,)
+PyObject* policy_loss_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return entry(n, 11, [&] {
+    Args args;
+    const Policy p = policy(args, a + 2);
+    const Tensor& dloss = args.tensor(a[0], "dloss");
+    if (dloss.scalar_type() != ScalarType::Float)
+      refuse(PyExc_TypeError, std::string("dloss must be Float, not ") +
+                                  c10::toString(dloss.scalar_type()));
+    if (dloss.numel() != 1) refuse(PyExc_ValueError, "dloss must have one element");
+    const Tensor& weight = args.tensor(a[1], "weight", ScalarType::Float, {p.batch});
+    OnStream on(a[10], args.device);
+    const Tensor dlogp = fresh(p.logp->sizes(), ScalarType::Float, args.device);
+    call(kPolicyBackward, dloss.data_ptr(), p.logp->data_ptr(), p.old_logp, p.advantage,
+         weight.data_ptr(), p.mask, p.ref, p.batch, p.length, p.per_token, p.low, p.high, p.kl,
+         dlogp.data_ptr(), on.handle);
+    return give(dlogp);
+  });
+}
+
 // bind(addresses of the C entry points, function that raises for a status)
 PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return entry(n, kEntries + 1, [&]() -> PyObject* {
@@ -460,7 +589,9 @@ PyMethodDef g_methods[] = {
     METHOD("gelu", gelu), METHOD("gelu_backward", gelu_backward),
     METHOD("layer_norm", layer_norm), METHOD("layer_norm_backward", layer_norm_backward),
     METHOD("linear_cross_entropy", xent),
-    METHOD("linear_cross_entropy_backward", xent_backward), {nullptr, nullptr, 0, nullptr}};
+    METHOD("linear_cross_entropy_backward", xent_backward), METHOD("embedding", embedding),
+    METHOD("embedding_backward", embedding_backward), METHOD("policy_loss", policy_loss),
+    METHOD("policy_loss_backward", policy_loss_backward), {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "fp8opt_binding", nullptr, -1, g_methods,
                         nullptr, nullptr, nullptr, nullptr};

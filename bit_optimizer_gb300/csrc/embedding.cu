@@ -1,0 +1,641 @@
+// The embedding lookup, y[i] = scale w[ids[i]], and the dense gradient of its
+// table, dw[v] = scale * sum of dy[i] over the tokens i with ids[i] = v.
+//
+// forward   Bound by memory: every thread has four 16-byte vectors of the
+//           result under way, each an id, its row's vector and a store.
+// backward  Three steps, each sum in the tokens' order, without float atomics:
+//           order   The tokens sorted by word, stably, while other CTAs fill dw
+//                   with zeros (which takes as long).  Few tokens: each finds its
+//                   place by comparing its key with all others, in one launch.
+//                   More: a radix sort of eight bits a pass.
+//           sums    A warp takes 32 consecutive tokens of the order and the
+//                   columns that its lanes' 16-byte vectors cover, and adds rows
+//                   of one word in fp32.  A word whose tokens lie within the
+//                   chunk is written at once, a part of a word that goes on
+//                   beyond it to scratch.
+//           join    The parts of such words, in order.
+// A frequent word's tokens are thereby spread over as many warps as any others.
+#include "ops_internal.cuh"
+
+namespace fp8opt {
+
+namespace {
+
+constexpr int kCtaThreads = 256, kCtaWarps = kCtaThreads / 32;
+
+// --------------------------------------------------------------- elements
+
+template <int DT>
+__device__ __forceinline__ float load1(const void* p, int64_t i) {
+  if (DT == kF32) return static_cast<const float*>(p)[i];
+  const uint32_t h = static_cast<const uint16_t*>(p)[i];
+  return DT == kBF16 ? __uint_as_float(h << 16) : h2_to_f2(h).x;
+}
+
+// Elements of a lane's 16-byte vector.
+template <int DT>
+constexpr int kPer = DT == kF32 ? 4 : 8;
+
+template <int DT>
+__device__ __forceinline__ void unpack(const uint4& v, float (&e)[kPer<DT>]) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    if constexpr (DT == kF32) {
+      e[k] = __uint_as_float(w[k]);
+    } else {
+      const float2 f = DT == kBF16 ? make_float2(__uint_as_float(w[k] << 16),
+                                                 __uint_as_float(w[k] & 0xFFFF0000u))
+                                   : h2_to_f2(w[k]);
+      e[2 * k] = f.x;
+      e[2 * k + 1] = f.y;
+    }
+  }
+}
+
+template <int DT>
+__device__ __forceinline__ uint4 pack(const float (&e)[kPer<DT>]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    if constexpr (DT == kF32) w[k] = __float_as_uint(e[k]);
+    else w[k] = pack2<DT>(e[2 * k], e[2 * k + 1]);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// ---------------------------------------------------------------- forward
+
+constexpr int kForwardVectors = 4;   // of a thread
+
+// Rows of `vectors` 16-byte vectors.
+template <int DT>
+__global__ void __launch_bounds__(kCtaThreads)
+embedding_kernel(const long long* ids, const uint4* w, int64_t rows, int64_t vectors,
+                 int64_t vocab, float scale, uint4* __restrict__ y) {
+  begin_after_previous();
+  const int64_t total = rows * vectors;
+  const int64_t i0 = (int64_t)blockIdx.x * (kForwardVectors * kCtaThreads) + threadIdx.x;
+  uint4 v[kForwardVectors];
+  bool known[kForwardVectors];
+#pragma unroll
+  for (int k = 0; k < kForwardVectors; ++k) {
+    const int64_t i = i0 + k * kCtaThreads;
+    known[k] = false;
+    v[k] = make_uint4(0, 0, 0, 0);
+    if (i < total) {
+      const int64_t row = total <= 0xFFFFFFFFll ? (int64_t)((uint32_t)i / (uint32_t)vectors)
+                                                 : i / vectors;
+      const long long id = ids[row];
+      known[k] = id >= 0 && id < vocab;
+      if (known[k]) v[k] = w[id * vectors + (i - row * vectors)];
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < kForwardVectors; ++k) {
+    float e[kPer<DT>];
+    unpack<DT>(v[k], e);
+#pragma unroll
+    for (int j = 0; j < kPer<DT>; ++j)
+      e[j] = known[k] ? e[j] * scale : __uint_as_float(0x7FC00000u);
+    const int64_t i = i0 + k * kCtaThreads;
+    if (i < total) __stcs(y + i, pack<DT>(e));
+  }
+}
+
+// Rows that start anywhere: a warp takes kRowPart elements of a row.
+constexpr int kRowPart = 512;
+template <int DT>
+__global__ void __launch_bounds__(kCtaThreads)
+embedding_any_kernel(const long long* ids, const void* w, int64_t rows, int64_t dim,
+                     int64_t vocab, float scale, void* y) {
+  begin_after_previous();
+  const int64_t parts = (dim + kRowPart - 1) / kRowPart;
+  const int64_t unit = (int64_t)blockIdx.x * kCtaWarps + (threadIdx.x >> 5);
+  const int64_t row = unit / parts, c0 = (unit - row * parts) * kRowPart + (threadIdx.x & 31);
+  if (row >= rows) return;
+  const long long id = ids[row];
+  const bool known = id >= 0 && id < vocab;
+  float e[kRowPart / 32];
+#pragma unroll
+  for (int k = 0; k < kRowPart / 32; ++k)
+    e[k] = known && c0 + 32 * k < dim ? load1<DT>(w, id * dim + c0 + 32 * k) * scale
+                                      : __uint_as_float(0x7FC00000u);
+#pragma unroll
+  for (int k = 0; k < kRowPart / 32; ++k)
+    if (c0 + 32 * k < dim) store1<DT>(y, row * dim + c0 + 32 * k, e[k]);
+}
+
+// ------------------------------------------------------------------ order
+
+// A token's key: its word, or `vocab` where it takes no part (padding, or no
+// word of the table), which sorts last.
+__device__ __forceinline__ uint32_t key_of(long long id, uint32_t vocab, long long padding) {
+  return id >= 0 && id < (long long)vocab && id != padding ? (uint32_t)id : vocab;
+}
+
+// Part `part` of `parts` of the zeros in `bytes` at p, which are elements of
+// `size` bytes at any of their boundaries.
+struct Fill {
+  char* p;
+  int64_t bytes;
+  int size, part, parts;
+};
+
+// CTA `cta` of `ctas`.
+__device__ __forceinline__ void fill_zeros(const Fill& f, int64_t cta, int64_t ctas) {
+  const int64_t head = min((int64_t)(-reinterpret_cast<intptr_t>(f.p) & 15), f.bytes);
+  const int64_t words = (f.bytes - head) / 16, tail = head + 16 * words;
+  uint4* const q = reinterpret_cast<uint4*>(f.p + head);
+  const int64_t lo = words / f.parts * f.part;
+  const int64_t hi = f.part + 1 == f.parts ? words : words / f.parts * (f.part + 1);
+  for (int64_t i = lo + cta * blockDim.x + threadIdx.x; i < hi; i += ctas * blockDim.x)
+    q[i] = make_uint4(0, 0, 0, 0);
+  // at most 15 bytes at either end
+  if (f.part == 0 && cta == 0 && threadIdx.x < 16) {
+    const int64_t a = (int64_t)threadIdx.x * f.size, b = tail + a;
+    if (f.size == 2) {
+      if (a < head) *reinterpret_cast<uint16_t*>(f.p + a) = 0;
+      if (b < f.bytes) *reinterpret_cast<uint16_t*>(f.p + b) = 0;
+    } else {
+      if (a < head) *reinterpret_cast<uint32_t*>(f.p + a) = 0;
+      if (b < f.bytes) *reinterpret_cast<uint32_t*>(f.p + b) = 0;
+    }
+  }
+}
+
+// Few tokens: the place of each is the number of smaller keys, and of equal ones
+// before it.  A CTA places 32 tokens, its warps comparing them with a share of all
+// keys each; the CTAs from `sorters` on fill.
+constexpr int64_t kRankTokens = 8192;
+
+__global__ void __launch_bounds__(kCtaThreads)
+embedding_rank_kernel(const long long* ids, int n, uint32_t vocab, long long padding, int sorters,
+                      uint32_t* __restrict__ keys, uint32_t* __restrict__ tokens, Fill fill) {
+  extern __shared__ uint4 all4[];
+  __shared__ int smaller[kCtaWarps][32];
+  begin_after_previous();
+  if ((int)blockIdx.x >= sorters) {
+    fill_zeros(fill, blockIdx.x - sorters, gridDim.x - sorters);
+    return;
+  }
+  uint32_t* const all = reinterpret_cast<uint32_t*>(all4);
+  const int share = ((n + kCtaWarps - 1) / kCtaWarps + 31) / 32 * 32;     // of a warp
+  for (int i = threadIdx.x; i < share * kCtaWarps; i += kCtaThreads)
+    all[i] = i < n ? key_of(ids[i], vocab, padding) : 0xFFFFFFFFu;
+  __syncthreads();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int first = blockIdx.x * 32, i = first + lane;
+  const uint32_t key = all[min(i, n - 1)];
+  const int lo = warp * share, hi = lo + share;
+  int count = 0;
+  const auto below = [&](int a, int b, uint32_t limit) {
+#pragma unroll 4
+    for (int j = a / 4; j < b / 4; ++j) {
+      const uint4 k = all4[j];
+      count += (k.x < limit) + (k.y < limit) + (k.z < limit) + (k.w < limit);
+    }
+  };
+  // equal keys count where they come before (limits: key + 1 and key)
+  below(lo, min(hi, first), key + 1);
+  for (int j = max(lo, first); j < min(hi, first + 32); ++j) count += all[j] < key + (j < i);
+  below(max(lo, first + 32), hi, key);
+  smaller[warp][lane] = count;
+  __syncthreads();
+  if (warp == 0 && i < n) {
+    int at = 0;
+#pragma unroll
+    for (int w = 0; w < kCtaWarps; ++w) at += smaller[w][lane];
+    keys[at] = key;
+    tokens[at] = (uint32_t)i;
+  }
+}
+
+// More tokens: a stable sort by eight bits of the key, in tiles of a CTA each (a
+// multiple of kSortStep tokens).  First the tiles' counts of each digit ...
+constexpr int kSortThreads = 1024, kSortWarps = kSortThreads / 32, kDigits = 256;
+constexpr int kRounds = 2, kSortStep = kRounds * kSortThreads;
+
+struct SortPass {
+  const long long* ids;      // the first pass's input; else NULL
+  const uint32_t* keys;      // the later ones'
+  const uint32_t* tokens;
+  int64_t n, tile;
+  int tiles, shift;
+  uint32_t vocab;
+  long long padding;
+  uint32_t* counts;          // [tile][digit]
+  uint32_t* keys_out;
+  uint32_t* tokens_out;
+  __device__ __forceinline__ uint32_t key(int64_t i) const {
+    return ids != nullptr ? key_of(ids[i], vocab, padding) : keys[i];
+  }
+};
+
+__global__ void __launch_bounds__(kSortThreads)
+embedding_count_kernel(SortPass s, Fill fill) {
+  __shared__ uint32_t count[kDigits];
+  begin_after_previous();
+  if ((int)blockIdx.x >= s.tiles) {
+    fill_zeros(fill, blockIdx.x - s.tiles, gridDim.x - s.tiles);
+    return;
+  }
+  if (threadIdx.x < kDigits) count[threadIdx.x] = 0;
+  __syncthreads();
+  const int64_t lo = blockIdx.x * s.tile, hi = min(lo + s.tile, s.n);
+  for (int64_t i = lo + threadIdx.x; i < hi; i += kSortThreads)
+    atomicAdd(&count[s.key(i) >> s.shift & (kDigits - 1)], 1u);
+  __syncthreads();
+  if (threadIdx.x < kDigits)
+    s.counts[(int64_t)blockIdx.x * kDigits + threadIdx.x] = count[threadIdx.x];
+}
+
+// ... then every token to its place: those of smaller digits, of its digit in
+// earlier tiles, in its tile's earlier warps and in its own warp come before it.
+__global__ void __launch_bounds__(kSortThreads)
+embedding_place_kernel(SortPass s, Fill fill) {
+  __shared__ uint32_t base[kDigits], sums[kDigits / 32];
+  __shared__ uint32_t before[kSortWarps][kDigits];   // a warp's tokens, then where they start
+  begin_after_previous();
+  if ((int)blockIdx.x >= s.tiles) {
+    fill_zeros(fill, blockIdx.x - s.tiles, gridDim.x - s.tiles);
+    return;
+  }
+  const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
+  if (t < kDigits) {
+    uint32_t all = 0, mine = 0;
+#pragma unroll 8
+    for (int k = 0; k < s.tiles; ++k) {
+      const uint32_t c = s.counts[(int64_t)k * kDigits + t];
+      all += c;
+      mine += k < (int)blockIdx.x ? c : 0;
+    }
+    uint32_t up = all;     // of the digits up to this one, first within the warp
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t v = __shfl_up_sync(0xFFFFFFFFu, up, o);
+      if (lane >= o) up += v;
+    }
+    if (lane == 31) sums[warp] = up;
+    base[t] = up - all + mine;
+  }
+  __syncthreads();
+  if (t < kDigits)
+    for (int w = 0; w < warp; ++w) base[t] += sums[w];
+  const int64_t lo = blockIdx.x * s.tile, hi = min(lo + s.tile, s.n);
+  for (int64_t step = lo; step < hi; step += kSortStep) {
+    for (int i = t; i < kSortWarps * kDigits; i += kSortThreads) (&before[0][0])[i] = 0;
+    __syncthreads();
+    // a warp's kRounds x 32 consecutive tokens, in order
+    uint32_t key[kRounds], rank[kRounds];
+    const int64_t i0 = step + warp * (kRounds * 32) + lane;
+#pragma unroll
+    for (int r = 0; r < kRounds; ++r) {
+      const bool in = i0 + 32 * r < hi;
+      key[r] = in ? s.key(i0 + 32 * r) : 0;
+      const int digit = in ? (int)(key[r] >> s.shift & (kDigits - 1)) : kDigits;
+      const unsigned same = __match_any_sync(0xFFFFFFFFu, digit);
+      const unsigned earlier = same & ((1u << lane) - 1);
+      rank[r] = __popc(earlier) + (in ? before[warp][digit] : 0);
+      __syncwarp();
+      if (in && earlier == 0) before[warp][digit] += __popc(same);
+      __syncwarp();
+    }
+    __syncthreads();
+    if (t < kDigits) {
+      uint32_t at = base[t];
+#pragma unroll 8
+      for (int w = 0; w < kSortWarps; ++w) {
+        const uint32_t c = before[w][t];
+        before[w][t] = at;
+        at += c;
+      }
+      base[t] = at;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int r = 0; r < kRounds; ++r) {
+      const int64_t i = i0 + 32 * r;
+      if (i < hi) {
+        const uint32_t at = before[warp][key[r] >> s.shift & (kDigits - 1)] + rank[r];
+        s.keys_out[at] = key[r];
+        s.tokens_out[at] = s.ids != nullptr ? (uint32_t)i : s.tokens[i];
+      }
+    }
+    __syncthreads();
+  }
+}
+
+// ------------------------------------------------------------------- sums
+
+constexpr int kChunk = 32;     // tokens of a warp: one to a lane while it reads them
+
+struct Sums {
+  const uint32_t* keys;
+  const uint32_t* tokens;
+  int64_t n, dim;
+  uint32_t vocab;
+  int64_t slices;              // of 32 lanes' columns
+  const void* dy;
+  float scale;
+  float* parts;                // [chunk][2][dim]: the first word's, the last word's
+  void* dw;
+};
+
+// A lane's columns: VEC, kPer in a row; else every 32nd.
+template <int DT, bool VEC>
+__global__ void __launch_bounds__(kCtaThreads)
+embedding_sums_kernel(const Sums s) {
+  begin_after_previous();
+  constexpr int E = kPer<DT>, kAhead = 8;
+  const int lane = threadIdx.x & 31;
+  const int64_t unit = (int64_t)blockIdx.x * kCtaWarps + (threadIdx.x >> 5);
+  const int64_t chunk = unit / s.slices, slice = unit - chunk * s.slices;
+  const int64_t first = chunk * kChunk, at = first + lane;
+  if (first >= s.n) return;
+  const uint32_t none = s.vocab;
+  const uint32_t key = at < s.n ? s.keys[at] : none;
+  const uint32_t token = at < s.n ? s.tokens[at] : 0;
+  uint32_t before = none, after = none;
+  if (first > 0) before = s.keys[first - 1];
+  if (first + kChunk < s.n) after = s.keys[first + kChunk];
+  uint32_t next = __shfl_down_sync(0xFFFFFFFFu, key, 1);
+  if (lane == 31) next = after;
+  const unsigned live = __ballot_sync(0xFFFFFFFFu, key != none);
+  const unsigned ends = __ballot_sync(0xFFFFFFFFu, key != none && (next != key));
+  if (live == 0) return;
+  bool goes_on = before == __shfl_sync(0xFFFFFFFFu, key, 0);   // from the chunk before
+  const int count = __popc(live);                              // (those without a part come last)
+
+  const int64_t c0 = slice * (32 * E) + (VEC ? lane * E : lane);
+  constexpr int kStep = VEC ? 1 : 32;
+  float sum[E];
+#pragma unroll
+  for (int j = 0; j < E; ++j) sum[j] = 0.0f;
+  const auto put = [&](uint32_t word, float* part) {
+    if (part != nullptr) {
+#pragma unroll
+      for (int j = 0; j < E; ++j)
+        if (c0 + j * kStep < s.dim) part[c0 + j * kStep] = sum[j];
+    } else {
+      float e[E];
+#pragma unroll
+      for (int j = 0; j < E; ++j) e[j] = sum[j] * s.scale;
+      if constexpr (VEC) {
+        if (c0 < s.dim)
+          *reinterpret_cast<uint4*>(static_cast<char*>(s.dw) +
+                                    ((int64_t)word * s.dim + c0) * (16 / E)) = pack<DT>(e);
+      } else {
+#pragma unroll
+        for (int j = 0; j < E; ++j)
+          if (c0 + j * kStep < s.dim)
+            store1<DT>(s.dw, (int64_t)word * s.dim + c0 + j * kStep, e[j]);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < E; ++j) sum[j] = 0.0f;
+  };
+  float* const parts = s.parts + chunk * 2 * s.dim;
+  for (int r = 0; r < count; r += kAhead) {
+    uint4 raw[VEC ? kAhead : 1];
+    float val[VEC ? 1 : kAhead][E];
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      const int64_t row = __shfl_sync(0xFFFFFFFFu, token, r + k);
+      if constexpr (VEC) {
+        raw[k] = make_uint4(0, 0, 0, 0);
+        if (r + k < count && c0 < s.dim)
+          raw[k] = __ldcs(reinterpret_cast<const uint4*>(static_cast<const char*>(s.dy) +
+                                                         (row * s.dim + c0) * (16 / E)));
+      } else {
+#pragma unroll
+        for (int j = 0; j < E; ++j)
+          val[k][j] = r + k < count && c0 + j * kStep < s.dim
+                          ? load1<DT>(s.dy, row * s.dim + c0 + j * kStep) : 0.0f;
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      float e[E];
+      if constexpr (VEC) {
+        unpack<DT>(raw[k], e);
+      } else {
+#pragma unroll
+        for (int j = 0; j < E; ++j) e[j] = val[k][j];
+      }
+#pragma unroll
+      for (int j = 0; j < E; ++j) sum[j] += e[j];
+      const uint32_t word = __shfl_sync(0xFFFFFFFFu, key, r + k);
+      if (ends >> (r + k) & 1u) {
+        put(word, goes_on ? parts : nullptr);
+        goes_on = false;
+      }
+    }
+  }
+  if (!(ends >> (count - 1) & 1u)) put(0, goes_on ? parts : parts + s.dim);
+}
+
+// A word that goes on from chunk c, in which it starts, to later ones: c's last
+// part, then the first parts of the chunks that it reaches.  kJoinGroups groups of
+// threads add a range of them each, 512 columns of float4s wide.
+constexpr int kJoinColumns = 128, kJoinGroups = 4;
+
+template <int DT>
+__global__ void __launch_bounds__(kJoinColumns * kJoinGroups)
+embedding_join_kernel(const Sums s, bool vec) {
+  __shared__ float4 sh[kJoinGroups][kJoinColumns];
+  begin_after_previous();
+  const int64_t slices = (s.dim + 4 * kJoinColumns - 1) / (4 * kJoinColumns);
+  const int64_t chunk = blockIdx.x / slices, last = chunk * kChunk + kChunk - 1;
+  if (last + 1 >= s.n) return;
+  const uint32_t key = s.keys[last];
+  if (key == s.vocab || s.keys[last + 1] != key) return;
+  if (chunk > 0 && s.keys[last - kChunk] == key) return;    // it starts before
+  // the chunks it reaches: those whose first token is the word's
+  int64_t lo = chunk + 1, hi = (s.n + kChunk - 1) / kChunk;  // first past them, in (lo, hi]
+  while (hi - lo > 1) {
+    const int64_t mid = (lo + hi) / 2;
+    if (s.keys[mid * kChunk] == key) lo = mid;
+    else hi = mid;
+  }
+  const int64_t count = hi - chunk;       // parts
+  const int group = threadIdx.x / kJoinColumns;
+  const int64_t c = ((blockIdx.x - chunk * slices) * kJoinColumns + threadIdx.x % kJoinColumns) * 4;
+  const int64_t a = count * group / kJoinGroups, b = count * (group + 1) / kJoinGroups;
+  float4 sum = make_float4(0, 0, 0, 0);
+  if (c < s.dim) {
+    const auto part = [&](int64_t i) {
+      const float* p = s.parts + ((chunk + i) * 2 + (i == 0 ? 1 : 0)) * s.dim + c;
+      if (vec) return *reinterpret_cast<const float4*>(p);
+      return make_float4(p[0], c + 1 < s.dim ? p[1] : 0.0f, c + 2 < s.dim ? p[2] : 0.0f,
+                         c + 3 < s.dim ? p[3] : 0.0f);
+    };
+    int64_t i = a;
+    for (; i + 4 <= b; i += 4) {
+      float4 v[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) v[k] = part(i + k);
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        sum = make_float4(sum.x + v[k].x, sum.y + v[k].y, sum.z + v[k].z, sum.w + v[k].w);
+    }
+    for (; i < b; ++i) {
+      const float4 v = part(i);
+      sum = make_float4(sum.x + v.x, sum.y + v.y, sum.z + v.z, sum.w + v.w);
+    }
+  }
+  sh[group][threadIdx.x % kJoinColumns] = sum;
+  __syncthreads();
+  if (group > 0 || c >= s.dim) return;
+#pragma unroll
+  for (int g = 1; g < kJoinGroups; ++g) {
+    const float4 v = sh[g][threadIdx.x];
+    sum = make_float4(sum.x + v.x, sum.y + v.y, sum.z + v.z, sum.w + v.w);
+  }
+  const float e[4] = {sum.x, sum.y, sum.z, sum.w};
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    if (c + j < s.dim) store1<DT>(s.dw, (int64_t)key * s.dim + c + j, e[j] * s.scale);
+}
+
+int64_t element_size(int dtype) { return dtype == kF32 ? 4 : 2; }
+
+bool vectors_ok(const void* a, const void* b, int64_t dim, int dtype) {
+  return ((reinterpret_cast<uintptr_t>(a) | reinterpret_cast<uintptr_t>(b) |
+           (uintptr_t)(dim * element_size(dtype))) & 15u) == 0;
+}
+
+int64_t blocks(int64_t n, int64_t per) { return (n + per - 1) / per; }
+
+struct Scratch {
+  size_t keys[2] = {0, 0}, tokens[2] = {0, 0}, counts = 0, parts = 0, bytes = 0;
+  int64_t tile = 0;
+  int tiles = 0, passes = 0;
+};
+
+Scratch backward_scratch(const EmbeddingArgs& a, int sms) {
+  Scratch s;
+  const auto take = [&](int64_t bytes) {
+    const size_t at = s.bytes;
+    s.bytes += (size_t)((bytes + 255) / 256 * 256);
+    return at;
+  };
+  for (int i = 0; i < (a.rows <= kRankTokens ? 1 : 2); ++i) {
+    s.keys[i] = take(a.rows * 4);
+    s.tokens[i] = take(a.rows * 4);
+  }
+  if (a.rows > kRankTokens) {
+    s.tile = blocks(blocks(a.rows, 2 * sms), kSortStep) * kSortStep;
+    s.tiles = (int)blocks(a.rows, s.tile);
+    for (int64_t v = a.vocab; v > 0; v >>= 8) ++s.passes;    // (keys go up to vocab)
+    s.counts = take((int64_t)s.tiles * kDigits * 4);
+  }
+  s.parts = take(blocks(a.rows, kChunk) * 2 * a.dim * 4);
+  return s;
+}
+
+template <int DT>
+cudaError_t forward(const EmbeddingArgs& a, cudaStream_t stream) {
+  const long long* ids = reinterpret_cast<const long long*>(a.ids);
+  const bool early = worth_early(a.rows * a.dim);
+  if (vectors_ok(a.in, a.out, a.dim, DT)) {
+    const int64_t vectors = a.dim / kPer<DT>;
+    return launch(early, embedding_kernel<DT>,
+                  (unsigned)blocks(a.rows * vectors, kForwardVectors * kCtaThreads), kCtaThreads, 0,
+                  stream, ids, static_cast<const uint4*>(a.in), a.rows, vectors, a.vocab, a.scale,
+                  static_cast<uint4*>(a.out));
+  }
+  return launch(early, embedding_any_kernel<DT>,
+                (unsigned)blocks(a.rows * blocks(a.dim, kRowPart), kCtaWarps), kCtaThreads, 0,
+                stream, ids, a.in, a.rows, a.dim, a.vocab, a.scale, a.out);
+}
+
+template <int DT>
+cudaError_t backward(const EmbeddingArgs& a, char* scratch, int sms, cudaStream_t stream,
+                     LaunchMark mark) {
+  const Scratch l = backward_scratch(a, sms);
+  const auto at = [&](size_t offset) { return reinterpret_cast<uint32_t*>(scratch + offset); };
+  const int64_t size = element_size(DT);
+  Fill fill = {static_cast<char*>(a.out), a.vocab * a.dim * size, (int)size, 0, 1};
+  const int fillers = 4 * sms;
+  const long long* ids = reinterpret_cast<const long long*>(a.ids);
+  cudaError_t e = cudaSuccess;
+  int last = 0;
+  if (mark) mark(kEmbeddingOrderK, 0, stream);
+  if (a.rows <= kRankTokens) {
+    const int n = (int)a.rows, sorters = (int)blocks(n, 32);
+    const size_t smem = (size_t)blocks(blocks(n, kCtaWarps), 32) * 32 * kCtaWarps * 4;
+    e = launch(true, embedding_rank_kernel, sorters + fillers, kCtaThreads, smem, stream, ids, n,
+               (uint32_t)a.vocab, (long long)a.padding, sorters, at(l.keys[0]), at(l.tokens[0]),
+               fill);
+  } else {
+    SortPass s = {};
+    s.n = a.rows;
+    s.tile = l.tile;
+    s.tiles = l.tiles;
+    s.vocab = (uint32_t)a.vocab;
+    s.padding = a.padding;
+    s.counts = at(l.counts);
+    fill.parts = 2 * l.passes;
+    for (int p = 0; e == cudaSuccess && p < l.passes; ++p) {
+      s.ids = p == 0 ? ids : nullptr;
+      s.keys = at(l.keys[last]);
+      s.tokens = at(l.tokens[last]);
+      if (p > 0) last ^= 1;
+      s.keys_out = at(l.keys[last]);
+      s.tokens_out = at(l.tokens[last]);
+      s.shift = 8 * p;
+      fill.part = 2 * p;
+      e = launch(true, embedding_count_kernel, l.tiles + fillers / 2, kSortThreads, 0, stream, s,
+                 fill);
+      fill.part = 2 * p + 1;
+      if (e == cudaSuccess)
+        e = launch(true, embedding_place_kernel, l.tiles + fillers / 2, kSortThreads, 0, stream,
+                   s, fill);
+    }
+  }
+  if (mark) mark(kEmbeddingOrderK, 1, stream);
+  if (e != cudaSuccess) return e;
+  const bool vec = vectors_ok(a.in, a.out, a.dim, DT);
+  Sums s = {at(l.keys[last]), at(l.tokens[last]), a.rows, a.dim, (uint32_t)a.vocab,
+            blocks(a.dim, 32 * kPer<DT>), a.in, a.scale,
+            reinterpret_cast<float*>(scratch + l.parts), a.out};
+  const int64_t chunks = blocks(a.rows, kChunk);
+  if (mark) mark(kEmbeddingSumsK, 0, stream);
+  e = launch(true, vec ? embedding_sums_kernel<DT, true> : embedding_sums_kernel<DT, false>,
+             (unsigned)blocks(chunks * s.slices, kCtaWarps), kCtaThreads, 0, stream, s);
+  if (mark) mark(kEmbeddingSumsK, 1, stream);
+  if (e != cudaSuccess || chunks == 1) return e;
+  if (mark) mark(kEmbeddingJoinK, 0, stream);
+  e = launch(true, embedding_join_kernel<DT>,
+             (unsigned)(chunks * blocks(a.dim, 4 * kJoinColumns)), kJoinColumns * kJoinGroups, 0,
+             stream, s, a.dim % 4 == 0);
+  if (mark) mark(kEmbeddingJoinK, 1, stream);
+  return e;
+}
+
+}  // namespace
+
+size_t embedding_backward_scratch(const EmbeddingArgs& a, int sms) {
+  return backward_scratch(a, sms).bytes;
+}
+
+cudaError_t launch_embedding(const EmbeddingArgs& a, cudaStream_t stream, LaunchMark mark) {
+  if (mark) mark(kEmbeddingK, 0, stream);
+  const cudaError_t e = a.dtype == kF32    ? forward<kF32>(a, stream)
+                        : a.dtype == kBF16 ? forward<kBF16>(a, stream)
+                                           : forward<kF16>(a, stream);
+  if (mark) mark(kEmbeddingK, 1, stream);
+  return e;
+}
+
+cudaError_t launch_embedding_backward(const EmbeddingArgs& a, char* scratch, int sms,
+                                      cudaStream_t stream, LaunchMark mark) {
+  if (a.rows == 0)
+    return cudaMemsetAsync(a.out, 0, (size_t)(a.vocab * a.dim * element_size(a.dtype)), stream);
+  if (a.dtype == kF32) return backward<kF32>(a, scratch, sms, stream, mark);
+  return a.dtype == kBF16 ? backward<kBF16>(a, scratch, sms, stream, mark)
+                          : backward<kF16>(a, scratch, sms, stream, mark);
+}
+
+}  // namespace fp8opt

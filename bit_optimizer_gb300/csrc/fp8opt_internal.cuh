@@ -129,6 +129,8 @@ enum KernelId { kCastAmaxK = 0, kCastEncodeK, kStepAmaxK, kStepUpdateK,
                 kActSaveK, kActLoadK, kGeluK, kGeluBackwardK, kLayerNormK,
                 kLayerNormBackwardK, kLayerNormParamsK, kXentLogitsK,
                 kXentJoinK, kXentPrepareK, kXentGradsK, kXentDxK,
+                kEmbeddingK, kEmbeddingOrderK, kEmbeddingSumsK, kEmbeddingJoinK,
+                kPolicyLossK, kPolicyJoinK, kPolicyBackwardK,
                 kNumKernels };
 
 // Called before (end = 0) and after (end = 1) each kernel launch when timing

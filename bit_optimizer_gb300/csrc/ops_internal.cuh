@@ -123,6 +123,45 @@ cudaError_t launch_xent_forward(const XentArgs& a, char* scratch, int* error, in
 cudaError_t launch_xent_backward(const XentArgs& a, char* scratch, int* error, int sms,
                                  cudaStream_t stream, LaunchMark mark);
 
+// The embedding: in is the table w (vocab x dim), out the rows y (rows x dim);
+// backward in is dy and out dw.
+struct EmbeddingArgs {
+  const int64_t* ids;
+  const void* in;
+  void* out;
+  int64_t rows, dim, vocab;
+  int64_t padding;           // backward: a word that gets no gradient
+  int dtype;
+  float scale;
+};
+
+cudaError_t launch_embedding(const EmbeddingArgs& a, cudaStream_t stream, LaunchMark mark);
+size_t embedding_backward_scratch(const EmbeddingArgs& a, int sms);
+cudaError_t launch_embedding_backward(const EmbeddingArgs& a, char* scratch, int sms,
+                                      cudaStream_t stream, LaunchMark mark);
+
+// The clipped policy loss over `batch` sequences of `length` tokens.
+struct PolicyArgs {
+  const float* logp;
+  const float* old_logp;
+  const float* advantage;    // of every token (per_token), or of every sequence
+  const uint8_t* mask;       // NULL: every token counts
+  const float* ref_logp;     // NULL: no KL term
+  int64_t batch, length;
+  bool per_token, by_sequence;
+  double clip_low, clip_high, kl_coef;
+  float* stats;              // forward: loss, policy term, KL, clipped part
+  float* weight_out;         // of each sequence's tokens
+  const float* dloss;        // backward
+  const float* weight;
+  float* dlogp;
+};
+
+size_t policy_scratch(const PolicyArgs& a);
+cudaError_t launch_policy(const PolicyArgs& a, char* scratch, cudaStream_t stream,
+                          LaunchMark mark);
+cudaError_t launch_policy_backward(const PolicyArgs& a, cudaStream_t stream, LaunchMark mark);
+
 // Holds the library lock for one operator call, with the current device's SM
 // count, the launch marks, and `scratch_bytes` of the stream's workspace
 // (contents undefined; the call's own until its work on the stream ends).

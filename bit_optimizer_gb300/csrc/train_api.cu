@@ -280,3 +280,117 @@ extern "C" int fp8_linear_xent_backward(const float* dloss, const void* x, const
                                               call.mark));
   });
 }
+
+namespace fp8opt {
+namespace {
+
+int check_embedding(const char* fn, const EmbeddingArgs& a) {
+  if (a.rows < 0 || a.rows > kXentMost || a.dim < 1 || a.dim > kMaxElems || a.vocab < 1 ||
+      a.vocab > kXentMost || a.rows > kMaxElems / a.dim || a.vocab > kMaxElems / a.dim)
+    return bad(fn, "rows < 0, dim < 1, vocab < 1, or a size above its maximum");
+  if (!known(a.dtype)) return unsupported(fn, "unknown dtype");
+  if (!std::isfinite(a.scale)) return bad(fn, "scale is not finite");
+  return FP8OPT_OK;
+}
+
+}  // namespace
+}  // namespace fp8opt
+
+extern "C" int fp8_embedding(const int64_t* ids, const void* w, int64_t rows, int64_t dim,
+                             int64_t vocab, int dtype, float scale, void* y, void* stream_ptr) {
+  return entry([&] {
+    const char* fn = "fp8_embedding";
+    const EmbeddingArgs a = {ids, w, y, rows, dim, vocab, -1, dtype, scale};
+    int st = check_embedding(fn, a);
+    if (st != FP8OPT_OK || rows == 0) return st;
+    if (!ids || !w || !y) return bad(fn, "NULL pointer");
+    cudaStream_t stream = static_cast<cudaStream_t>(stream_ptr);
+    OpCall call;
+    if ((st = call.open(fn, stream, 0)) != FP8OPT_OK) return st;
+    return call.done(fn, launch_embedding(a, stream, call.mark));
+  });
+}
+
+extern "C" int fp8_embedding_backward(const void* dy, const int64_t* ids, int64_t rows,
+                                      int64_t dim, int64_t vocab, int dtype, float scale,
+                                      int64_t padding_idx, void* dw, void* stream_ptr) {
+  return entry([&] {
+    const char* fn = "fp8_embedding_backward";
+    const EmbeddingArgs a = {ids, dy, dw, rows, dim, vocab, padding_idx, dtype, scale};
+    int st = check_embedding(fn, a);
+    if (st != FP8OPT_OK) return st;
+    if (!dw || (rows > 0 && (!dy || !ids))) return bad(fn, "NULL pointer");
+    cudaStream_t stream = static_cast<cudaStream_t>(stream_ptr);
+    OpCall call;
+    if ((st = call.open(fn, stream, 0)) != FP8OPT_OK) return st;
+    const size_t bytes = rows > 0 ? embedding_backward_scratch(a, call.sms) : 0;
+    if ((st = call.open(fn, stream, bytes)) != FP8OPT_OK) return st;
+    return call.done(fn, launch_embedding_backward(a, call.scratch, call.sms, stream,
+                                                   call.mark));
+  });
+}
+
+namespace fp8opt {
+namespace {
+
+int check_policy(const char* fn, const PolicyArgs& a) {
+  if (a.batch < 0 || a.batch > kXentMost || a.length < 0 || a.length > kXentMost ||
+      (a.length > 0 && a.batch > kMaxElems / a.length))
+    return bad(fn, "batch < 0, length < 0, or a size above its maximum");
+  if (!(a.clip_low >= 0.0 && a.clip_low <= 1.0)) return bad(fn, "clip_low outside [0, 1]");
+  if (!(a.clip_high >= 0.0)) return bad(fn, "clip_high is negative or NaN");
+  if (!std::isfinite(a.kl_coef)) return bad(fn, "kl_coef is not finite");
+  return FP8OPT_OK;
+}
+
+}  // namespace
+}  // namespace fp8opt
+
+extern "C" int fp8_policy_loss(const float* logp, const float* old_logp, const float* advantage,
+                               const uint8_t* mask, const float* ref_logp, int64_t batch,
+                               int64_t length, int per_token, double clip_low, double clip_high,
+                               double kl_coef, int reduction, float* stats, float* weight,
+                               void* stream_ptr) {
+  return entry([&] {
+    const char* fn = "fp8_policy_loss";
+    PolicyArgs a = {logp, old_logp, advantage, mask, ref_logp, batch, length, per_token != 0,
+                    reduction == FP8OPT_MEAN_SEQUENCE, clip_low, clip_high, kl_coef};
+    a.stats = stats;
+    a.weight_out = weight;
+    int st = check_policy(fn, a);
+    if (st != FP8OPT_OK) return st;
+    if (reduction != FP8OPT_MEAN_TOKEN && reduction != FP8OPT_MEAN_SEQUENCE)
+      return unsupported(fn, "unknown reduction");
+    const bool any = batch > 0 && length > 0;
+    if (!stats || (batch > 0 && !weight) || (any && (!logp || !old_logp || !advantage)))
+      return bad(fn, "NULL pointer");
+    cudaStream_t stream = static_cast<cudaStream_t>(stream_ptr);
+    OpCall call;
+    if ((st = call.open(fn, stream, policy_scratch(a))) != FP8OPT_OK) return st;
+    return call.done(fn, launch_policy(a, call.scratch, stream, call.mark));
+  });
+}
+
+extern "C" int fp8_policy_loss_backward(const float* dloss, const float* logp,
+                                        const float* old_logp, const float* advantage,
+                                        const float* weight, const uint8_t* mask,
+                                        const float* ref_logp, int64_t batch, int64_t length,
+                                        int per_token, double clip_low, double clip_high,
+                                        double kl_coef, float* dlogp, void* stream_ptr) {
+  return entry([&] {
+    const char* fn = "fp8_policy_loss_backward";
+    PolicyArgs a = {logp, old_logp, advantage, mask, ref_logp, batch, length, per_token != 0,
+                    false, clip_low, clip_high, kl_coef};
+    a.dloss = dloss;
+    a.weight = weight;
+    a.dlogp = dlogp;
+    int st = check_policy(fn, a);
+    if (st != FP8OPT_OK || batch == 0 || length == 0) return st;
+    if (!dloss || !logp || !old_logp || !advantage || !weight || !dlogp)
+      return bad(fn, "NULL pointer");
+    cudaStream_t stream = static_cast<cudaStream_t>(stream_ptr);
+    OpCall call;
+    if ((st = call.open(fn, stream, 0)) != FP8OPT_OK) return st;
+    return call.done(fn, launch_policy_backward(a, stream, call.mark));
+  });
+}

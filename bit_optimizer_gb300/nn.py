@@ -8,6 +8,8 @@ pass what the operator's 8-bit form keeps, and nothing else.
 * ``linear_cross_entropy``: the input, the weight and one float per token; no
   logits (the backward pass makes the probabilities again, two pieces of the
   vocabulary at a time).
+* ``embedding``: the ids.
+* ``policy_loss``: its inputs, and one float per sequence.
 
 A GPT block's feed-forward half and its loss are then, with x the residual
 stream in FP16 or BF16:
@@ -15,6 +17,12 @@ stream in FP16 or BF16:
     h = nn.layer_norm(x, ln_w, ln_b)
     x = x + nn.linear(nn.gelu(nn.linear(h, fc_w, fc_b)), proj_w, proj_b)
     loss = nn.linear_cross_entropy(nn.layer_norm(x, lnf_w, lnf_b), wte, target)
+
+and x starts as nn.embedding(tokens, wte).  The policy loss takes the log
+probabilities that the cross entropy gives:
+
+    logp = -nn.linear_cross_entropy(x, wte, answer, reduction="none")
+    loss, stats = nn.policy_loss(logp, old_logp, advantage, mask, ref_logp, kl_coef=0.04)
 
 Under torch.autocast the two linear layers cast their input and parameters to
 its dtype, as torch's do, so FP32 weights get FP32 gradients; ``layer_norm`` and
@@ -29,7 +37,8 @@ from torch.autograd.function import once_differentiable
 
 from . import ops
 
-__all__ = ["layer_norm", "gelu", "linear", "linear_cross_entropy"]
+__all__ = ["layer_norm", "gelu", "linear", "linear_cross_entropy", "embedding",
+           "policy_loss"]
 
 
 class _LayerNorm(Function):
@@ -108,6 +117,35 @@ class _LinearCrossEntropy(Function):
         return dx, dw, None, None
 
 
+class _Embedding(Function):
+    @staticmethod
+    def forward(ctx, ids, weight, scale, padding_idx):
+        ctx.save_for_backward(ids)
+        ctx.args = weight.shape[0], scale, padding_idx
+        return ops.embedding(ids, weight, scale)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy):
+        return None, ops.embedding_backward(dy.contiguous(), *ctx.saved_tensors, *ctx.args), None, None
+
+
+class _PolicyLoss(Function):
+    @staticmethod
+    def forward(ctx, logp, old_logp, advantage, mask, ref_logp, low, high, kl_coef, reduction):
+        stats, weight = ops.policy_loss(logp, old_logp, advantage, mask, ref_logp, low, high,
+                                        kl_coef, reduction)
+        ctx.save_for_backward(logp, old_logp, advantage, weight, mask, ref_logp)
+        ctx.args = low, high, kl_coef
+        ctx.mark_non_differentiable(stats)
+        return stats[0].clone(), stats
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dloss, _):
+        return (ops.policy_loss_backward(dloss, *ctx.saved_tensors, *ctx.args), *[None] * 8)
+
+
 def layer_norm(x, weight, bias=None, eps: float = 1e-5, save: str = "fp8"):
     """Layer norm over the last dimension (``ops.layer_norm``)."""
     return _LayerNorm.apply(x.contiguous(), weight, bias, eps, save)
@@ -149,3 +187,19 @@ def linear_cross_entropy(x, weight, target, ignore_index: int = -100,
     if reduction == "sum":
         return loss.sum()
     return loss.sum() / (target != ignore_index).sum().clamp(min=1)
+
+
+def embedding(ids, weight, scale: float = 1.0, padding_idx=None):
+    """scale * weight[ids] (``ops.embedding``); the word padding_idx gets no gradient."""
+    if padding_idx is not None and not 0 <= padding_idx < weight.shape[0]:
+        raise ValueError(f"padding_idx must be in [0, {weight.shape[0]}), not {padding_idx}")
+    return _Embedding.apply(ids.contiguous(), weight, scale, padding_idx)
+
+
+def policy_loss(logp, old_logp, advantage, mask=None, ref_logp=None, clip_low: float = 0.2,
+                clip_high: float = 0.2, kl_coef: float = 0.0, reduction: str = "token"):
+    """(loss, stats) of ``ops.policy_loss``: the mean loss, for whose gradient logp is
+    the only input, and what it consists of, without a gradient."""
+    mask, ref_logp = (t if t is None else t.contiguous() for t in (mask, ref_logp))
+    return _PolicyLoss.apply(logp.contiguous(), old_logp.contiguous(), advantage.contiguous(),
+                             mask, ref_logp, clip_low, clip_high, kl_coef, reduction)

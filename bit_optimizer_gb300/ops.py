@@ -1,6 +1,7 @@
 """The training operators around the optimizer: 8-bit activation checkpoints,
-GELU, layer norm and the cross entropy of a linear layer over a large
-vocabulary, forward and backward, as functions of CUDA tensors.
+GELU, layer norm, the cross entropy of a linear layer over a large vocabulary,
+the embedding and the clipped policy loss, forward and backward, as functions of
+CUDA tensors.
 
 Like the rest of the package this is argument checking and marshalling: every
 step runs in the library's kernels (include/fp8opt.h describes the arithmetic).
@@ -36,15 +37,18 @@ from ._lib import BF16, F16, F32
 
 __all__ = ["act_save", "act_load", "gelu", "gelu_backward", "layer_norm",
            "layer_norm_backward", "linear_cross_entropy",
-           "linear_cross_entropy_backward", "ACT_GROUP"]
+           "linear_cross_entropy_backward", "embedding", "embedding_backward",
+           "policy_loss", "policy_loss_backward", "ACT_GROUP"]
 
 ACT_GROUP = _lib.ACT_GROUP
+_REDUCTIONS = {"token": _lib.MEAN_TOKEN, "sequence": _lib.MEAN_SEQUENCE}
 _DT = {torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16}
 BINDING_PATH = os.path.join(_lib.HERE, "_build", "fp8opt_binding.so")
 # The C entry points the binding calls, in its order.
 _ENTRIES = ("fp8_act_save", "fp8_act_load", "fp8_gelu", "fp8_gelu_backward",
             "fp8_layer_norm", "fp8_layer_norm_backward", "fp8_linear_xent",
-            "fp8_linear_xent_backward", "fp8opt_last_error")
+            "fp8_linear_xent_backward", "fp8_embedding", "fp8_embedding_backward",
+            "fp8_policy_loss", "fp8_policy_loss_backward", "fp8opt_last_error")
 
 
 def _load_binding():
@@ -151,3 +155,53 @@ def linear_cross_entropy_backward(dloss: torch.Tensor, x: torch.Tensor, w: torch
     probabilities of two pieces of the vocabulary, in 16 bits (128 to 256 MiB each;
     for few tokens that is all of them)."""
     return _b.linear_cross_entropy_backward(dloss, x, w, target, lse, ignore_index, stream)
+
+
+# --------------------------------------------------------------- embedding
+
+def embedding(ids: torch.Tensor, w: torch.Tensor, scale: float = 1.0,
+              stream=None) -> torch.Tensor:
+    """scale * w[ids], ids' shape and a last dimension of w's rows.  ids: int64, w:
+    (vocabulary, dim).  An id outside the vocabulary gives a row of NaN."""
+    return _b.embedding(ids, w, scale, stream)[0]
+
+
+def embedding_backward(dy: torch.Tensor, ids: torch.Tensor, vocab: int, scale: float = 1.0,
+                       padding_idx=None, stream=None) -> torch.Tensor:
+    """dw (vocab, dim) of ``embedding`` in dy's type: scale times the sum of the
+    rows of dy that belong to each word, in their order; 0 for the word padding_idx
+    and words without tokens.  Ids outside the vocabulary take no part."""
+    return _b.embedding_backward(dy, ids, vocab, scale, padding_idx, stream)[0]
+
+
+# ------------------------------------------------------------- policy loss
+
+def policy_loss(logp: torch.Tensor, old_logp: torch.Tensor, advantage: torch.Tensor,
+                mask=None, ref_logp=None, clip_low: float = 0.2, clip_high: float = 0.2,
+                kl_coef: float = 0.0, reduction: str = "token", stream=None):
+    """(stats, weight) of the clipped policy loss with a KL term on the tokens' log
+    probabilities (float32, (batch, length)): with r = exp(logp - old_logp) and e =
+    ref_logp - logp a token's loss is
+
+        -min(r A, clip(r, 1 - clip_low, 1 + clip_high) A) + kl_coef (exp(e) - 1 - e).
+
+    advantage A: (batch,) or (batch, length).  mask (bool): False where a token takes
+    no part, whatever its values are.  stats (float32): the mean loss, the means of
+    its first term and of exp(e) - 1 - e, and the part of the tokens that are
+    clipped.  The mean is over all tokens (reduction="token"), or of each sequence's
+    own mean, over the sequences that have tokens ("sequence"); weight (batch,) is
+    what a token of each sequence weighs in it, which the backward pass takes."""
+    if reduction not in _REDUCTIONS:
+        raise ValueError(f"reduction must be 'token' or 'sequence', not {reduction!r}")
+    return _b.policy_loss(logp, old_logp, advantage, mask, ref_logp, clip_low, clip_high,
+                          kl_coef, _REDUCTIONS[reduction], stream)
+
+
+def policy_loss_backward(dloss: torch.Tensor, logp: torch.Tensor, old_logp: torch.Tensor,
+                         advantage: torch.Tensor, weight: torch.Tensor, mask=None,
+                         ref_logp=None, clip_low: float = 0.2, clip_high: float = 0.2,
+                         kl_coef: float = 0.0, stream=None) -> torch.Tensor:
+    """dlogp (float32) for the gradient dloss (one float32, on the device) of the mean
+    loss of ``policy_loss``; weight is that call's."""
+    return _b.policy_loss_backward(dloss, weight, logp, old_logp, advantage, mask, ref_logp,
+                                   clip_low, clip_high, kl_coef, stream)[0]

@@ -718,6 +718,67 @@ FP8OPT_API int fp8_linear_xent_backward(const float *dloss, const void *x,
                                         int64_t ignore_index, void *dx,
                                         void *dw, void *stream);
 
+/*
+ * fp8_embedding: y[i] = scale * w[ids[i]], one rounding, w vocab x dim and y rows x
+ * dim of type dtype, ids rows int64.  An id outside [0, vocab) gives a row of
+ * NaN.
+ * fp8_embedding_backward: dw[v] = scale * sum over the tokens i with ids[i] = v
+ * of dy[i], vocab x dim, overwritten (0 for a word without tokens).  The word
+ * padding_idx gets no gradient (any number outside [0, vocab): none is left
+ * out), and an id outside [0, vocab) takes no part.  rows = 0 gives dw 0.  The
+ * tokens are sorted by word and a word's rows added in their order, in fp32.
+ * Scratch: 16 bytes a token and dim / 4 a token.  rows and vocab below 2^31,
+ * dim >= 1, scale finite.
+ */
+FP8OPT_API int fp8_embedding(const int64_t *ids, const void *w, int64_t rows,
+                             int64_t dim, int64_t vocab, int dtype,
+                             float scale, void *y, void *stream);
+FP8OPT_API int fp8_embedding_backward(const void *dy, const int64_t *ids,
+                                      int64_t rows, int64_t dim, int64_t vocab,
+                                      int dtype, float scale,
+                                      int64_t padding_idx, void *dw,
+                                      void *stream);
+
+/* Means of the policy loss: over all tokens that count, or of each sequence's
+ * mean over its own, over the sequences that have any. */
+#define FP8OPT_MEAN_TOKEN    0
+#define FP8OPT_MEAN_SEQUENCE 1
+
+/*
+ * fp8_policy_loss: the clipped policy loss with a KL term, of `batch` sequences
+ * of `length` tokens: with r = exp(logp - old_logp), e = ref_logp - logp and A
+ * the advantage of the token (per_token != 0: batch x length) or of its sequence
+ * (batch),
+ *   l = -min(r A, clip(r, 1 - clip_low, 1 + clip_high) A)
+ *       + kl_coef (exp(e) - 1 - e),
+ * all fp32.  mask (batch x length bytes; NULL: all 1): a token of mask 0 takes
+ * no part, whatever its values are.  ref_logp NULL: no KL term.  stats (4 fp32):
+ * the mean of l, of its first term, of exp(e) - 1 - e, and the part of the
+ * tokens that are clipped (r A is above the clipped term); all 0 where no token
+ * counts.  weight (batch fp32): what a token of each sequence weighs in the mean
+ * (0 for a sequence without any).  Whether a token is clipped follows from the
+ * exact difference logp - old_logp; sums over more than 1024 tokens are fp64.
+ *
+ * fp8_policy_loss_backward: dlogp (batch x length fp32) = *dloss * weight *
+ * dl / dlogp, dl / dlogp = -r A (0 where clipped) + kl_coef (1 - exp(e)); 0 where
+ * the mask is.  dloss: one fp32 on the device; weight: the forward call's.
+ *
+ * clip_low in [0, 1], clip_high >= 0 (infinity: no upper bound), kl_coef finite;
+ * batch and length below 2^31.
+ */
+FP8OPT_API int fp8_policy_loss(const float *logp, const float *old_logp,
+                               const float *advantage, const uint8_t *mask,
+                               const float *ref_logp, int64_t batch,
+                               int64_t length, int per_token, double clip_low,
+                               double clip_high, double kl_coef, int reduction,
+                               float *stats, float *weight, void *stream);
+FP8OPT_API int fp8_policy_loss_backward(
+    const float *dloss, const float *logp, const float *old_logp,
+    const float *advantage, const float *weight, const uint8_t *mask,
+    const float *ref_logp, int64_t batch, int64_t length, int per_token,
+    double clip_low, double clip_high, double kl_coef, float *dlogp,
+    void *stream);
+
 /* Text of a status code (static storage). */
 FP8OPT_API const char *fp8opt_strerror(int status);
 
@@ -735,8 +796,9 @@ FP8OPT_API const char *fp8opt_last_error(void);
  * "reduce_amax", "reduce_encode", "grad_norm", "grad_norm_terms", "clip_coef",
  * "found", "act_save", "act_load", "gelu", "gelu_backward", "layer_norm",
  * "layer_norm_backward", "layer_norm_params", "xent_logits", "xent_join",
- * "xent_prepare", "xent_grads", "xent_dx"), the launches
- * recorded since enabling and their summed duration in milliseconds.  Returns
+ * "xent_prepare", "xent_grads", "xent_dx", "embedding", "embedding_order",
+ * "embedding_sums", "embedding_join", "policy_loss", "policy_join",
+ * "policy_backward"), the launches recorded since enabling and their summed duration in milliseconds.  Returns
  * FP8OPT_ERR_ARG for an unknown name or NULL outputs. */
 FP8OPT_API int fp8opt_timing_enable(int on);
 FP8OPT_API int fp8opt_timing_read(const char *kernel, int *launches,

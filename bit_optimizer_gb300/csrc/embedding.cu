@@ -328,7 +328,10 @@ embedding_place_kernel(SortPass s, Fill fill) {
 
 // ------------------------------------------------------------------- sums
 
-constexpr int kChunk = 32;     // tokens of a warp: one to a lane while it reads them
+// Tokens of a warp, at most one to a lane: 32, or where that makes few warps, 16
+// or 8 (whose rows are all under way at once).
+constexpr int kMostChunk = 32, kLeastChunk = 8;
+constexpr int kSumWarps = 4;
 
 struct Sums {
   const uint32_t* keys;
@@ -336,6 +339,7 @@ struct Sums {
   int64_t n, dim;
   uint32_t vocab;
   int64_t slices;              // of 32 lanes' columns
+  int chunk;                   // tokens of a warp
   const void* dy;
   float scale;
   float* parts;                // [chunk][2][dim]: the first word's, the last word's
@@ -344,23 +348,24 @@ struct Sums {
 
 // A lane's columns: VEC, kPer in a row; else every 32nd.
 template <int DT, bool VEC>
-__global__ void __launch_bounds__(kCtaThreads)
+__global__ void __launch_bounds__(32 * kSumWarps)
 embedding_sums_kernel(const Sums s) {
   begin_after_previous();
   constexpr int E = kPer<DT>, kAhead = 8;
   const int lane = threadIdx.x & 31;
-  const int64_t unit = (int64_t)blockIdx.x * kCtaWarps + (threadIdx.x >> 5);
+  const int64_t unit = (int64_t)blockIdx.x * kSumWarps + (threadIdx.x >> 5);
   const int64_t chunk = unit / s.slices, slice = unit - chunk * s.slices;
-  const int64_t first = chunk * kChunk, at = first + lane;
+  const int64_t first = chunk * s.chunk, at = first + lane;
   if (first >= s.n) return;
   const uint32_t none = s.vocab;
-  const uint32_t key = at < s.n ? s.keys[at] : none;
-  const uint32_t token = at < s.n ? s.tokens[at] : 0;
+  const bool mine = lane < s.chunk && at < s.n;
+  const uint32_t key = mine ? s.keys[at] : none;
+  const uint32_t token = mine ? s.tokens[at] : 0;
   uint32_t before = none, after = none;
   if (first > 0) before = s.keys[first - 1];
-  if (first + kChunk < s.n) after = s.keys[first + kChunk];
+  if (first + s.chunk < s.n) after = s.keys[first + s.chunk];
   uint32_t next = __shfl_down_sync(0xFFFFFFFFu, key, 1);
-  if (lane == 31) next = after;
+  if (lane == s.chunk - 1) next = after;
   const unsigned live = __ballot_sync(0xFFFFFFFFu, key != none);
   const unsigned ends = __ballot_sync(0xFFFFFFFFu, key != none && (next != key));
   if (live == 0) return;
@@ -435,67 +440,96 @@ embedding_sums_kernel(const Sums s) {
   if (!(ends >> (count - 1) & 1u)) put(0, goes_on ? parts : parts + s.dim);
 }
 
-// A word that goes on from chunk c, in which it starts, to later ones: c's last
-// part, then the first parts of the chunks that it reaches.  kJoinGroups groups of
-// threads add a range of them each, 512 columns of float4s wide.
-constexpr int kJoinColumns = 128, kJoinGroups = 4;
+// The words that go on from one chunk to the next: a word's last part in the
+// chunk where it starts, then the first parts of the chunks that it reaches, in
+// order.  A CTA for every chunk, with the word that goes on behind it.  Up to
+// kFewParts parts: the CTA where the word starts adds them, a thread to four
+// columns.  More: all CTAs that the word goes on behind take 32 columns each in
+// turn, 32 ranges of parts side by side.
+constexpr int kJoinThreads = 256, kFewParts = 16, kJoinColumns = 32;
+constexpr int kJoinLanes = kJoinColumns / 4, kJoinRanges = kJoinThreads / kJoinLanes;
+
+// The last number in [lo, hi) for which f holds, which holds for lo and, if for
+// any number, for all smaller ones.  A whole warp; 32 probes a round, neighbours
+// first.
+template <class F>
+__device__ __forceinline__ int64_t last_of(int64_t lo, int64_t hi, F f) {
+  int64_t step = 1;
+  while (hi - lo > 1) {
+    const int64_t at = lo + (threadIdx.x % 32 + 1) * step;
+    const int holds = __popc(__ballot_sync(0xFFFFFFFFu, at < hi && f(at)));
+    if (holds < 32) hi = min(hi, lo + (holds + 1) * step);
+    lo += holds * step;
+    step = (hi - lo + 32) / 33;
+  }
+  return lo;
+}
 
 template <int DT>
-__global__ void __launch_bounds__(kJoinColumns * kJoinGroups)
+__global__ void __launch_bounds__(kJoinThreads)
 embedding_join_kernel(const Sums s, bool vec) {
-  __shared__ float4 sh[kJoinGroups][kJoinColumns];
+  __shared__ float4 sh[kJoinRanges][kJoinLanes];
   begin_after_previous();
-  const int64_t slices = (s.dim + 4 * kJoinColumns - 1) / (4 * kJoinColumns);
-  const int64_t chunk = blockIdx.x / slices, last = chunk * kChunk + kChunk - 1;
+  const int64_t chunk = blockIdx.x, last = (chunk + 1) * s.chunk - 1;
   if (last + 1 >= s.n) return;
-  const uint32_t key = s.keys[last];
-  if (key == s.vocab || s.keys[last + 1] != key) return;
-  if (chunk > 0 && s.keys[last - kChunk] == key) return;    // it starts before
-  // the chunks it reaches: those whose first token is the word's
-  int64_t lo = chunk + 1, hi = (s.n + kChunk - 1) / kChunk;  // first past them, in (lo, hi]
-  while (hi - lo > 1) {
-    const int64_t mid = (lo + hi) / 2;
-    if (s.keys[mid * kChunk] == key) lo = mid;
-    else hi = mid;
-  }
-  const int64_t count = hi - chunk;       // parts
-  const int group = threadIdx.x / kJoinColumns;
-  const int64_t c = ((blockIdx.x - chunk * slices) * kJoinColumns + threadIdx.x % kJoinColumns) * 4;
-  const int64_t a = count * group / kJoinGroups, b = count * (group + 1) / kJoinGroups;
-  float4 sum = make_float4(0, 0, 0, 0);
-  if (c < s.dim) {
-    const auto part = [&](int64_t i) {
-      const float* p = s.parts + ((chunk + i) * 2 + (i == 0 ? 1 : 0)) * s.dim + c;
-      if (vec) return *reinterpret_cast<const float4*>(p);
-      return make_float4(p[0], c + 1 < s.dim ? p[1] : 0.0f, c + 2 < s.dim ? p[2] : 0.0f,
-                         c + 3 < s.dim ? p[3] : 0.0f);
-    };
-    int64_t i = a;
-    for (; i + 4 <= b; i += 4) {
-      float4 v[4];
+  const uint32_t key = s.keys[last], next = s.keys[last + 1];
+  if (key == s.vocab || next != key) return;
+  // the first and the last chunk of the word
+  const auto ends_before = [&](int64_t c) { return s.keys[(c + 1) * s.chunk - 1] == key; };
+  const auto starts_in = [&](int64_t c) { return s.keys[c * s.chunk] == key; };
+  const int64_t chunks = (s.n + s.chunk - 1) / s.chunk;
+  const int64_t from = -last_of(-chunk, 1, [&](int64_t c) { return ends_before(-c); });
+  const int64_t to = last_of(chunk + 1, chunks, starts_in);
+  const int64_t count = to - from + 1;
+  const auto part = [&](int64_t i, int64_t c) {
+    const float* p = s.parts + ((from + i) * 2 + (i == 0 ? 1 : 0)) * s.dim + c;
+    if (vec) return *reinterpret_cast<const float4*>(p);
+    return make_float4(p[0], c + 1 < s.dim ? p[1] : 0.0f, c + 2 < s.dim ? p[2] : 0.0f,
+                       c + 3 < s.dim ? p[3] : 0.0f);
+  };
+  // parts [a, b) of four columns
+  const auto sum_of = [&](int64_t a, int64_t b, int64_t c) {
+    float4 sum = make_float4(0, 0, 0, 0);
+    for (int64_t i = a; i < b; i += 8) {
+      float4 v[8];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) v[k] = part(i + k);
+      for (int k = 0; k < 8; ++k)
+        v[k] = i + k < b ? part(i + k, c) : make_float4(0, 0, 0, 0);
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
+      for (int k = 0; k < 8; ++k)
         sum = make_float4(sum.x + v[k].x, sum.y + v[k].y, sum.z + v[k].z, sum.w + v[k].w);
     }
-    for (; i < b; ++i) {
-      const float4 v = part(i);
-      sum = make_float4(sum.x + v.x, sum.y + v.y, sum.z + v.z, sum.w + v.w);
+    return sum;
+  };
+  const auto put = [&](const float4& sum, int64_t c) {
+    const float e[4] = {sum.x, sum.y, sum.z, sum.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (c + j < s.dim) store1<DT>(s.dw, (int64_t)key * s.dim + c + j, e[j] * s.scale);
+  };
+  if (count <= kFewParts) {
+    if (chunk != from) return;
+    for (int64_t c = 4 * threadIdx.x; c < s.dim; c += 4 * kJoinThreads)
+      put(sum_of(0, count, c), c);
+    return;
+  }
+  const int lane = threadIdx.x % kJoinLanes, range = threadIdx.x / kJoinLanes;
+  const int64_t a = count * range / kJoinRanges, b = count * (range + 1) / kJoinRanges;
+  for (int64_t c0 = (chunk - from) * kJoinColumns; c0 < s.dim; c0 += (count - 1) * kJoinColumns) {
+    const int64_t c = c0 + 4 * lane;
+    sh[range][lane] = c < s.dim ? sum_of(a, b, c) : make_float4(0, 0, 0, 0);
+    __syncthreads();
+    if (range == 0 && c < s.dim) {
+      float4 sum = sh[0][lane];
+#pragma unroll 8
+      for (int r = 1; r < kJoinRanges; ++r) {
+        const float4 v = sh[r][lane];
+        sum = make_float4(sum.x + v.x, sum.y + v.y, sum.z + v.z, sum.w + v.w);
+      }
+      put(sum, c);
     }
+    __syncthreads();
   }
-  sh[group][threadIdx.x % kJoinColumns] = sum;
-  __syncthreads();
-  if (group > 0 || c >= s.dim) return;
-#pragma unroll
-  for (int g = 1; g < kJoinGroups; ++g) {
-    const float4 v = sh[g][threadIdx.x];
-    sum = make_float4(sum.x + v.x, sum.y + v.y, sum.z + v.z, sum.w + v.w);
-  }
-  const float e[4] = {sum.x, sum.y, sum.z, sum.w};
-#pragma unroll
-  for (int j = 0; j < 4; ++j)
-    if (c + j < s.dim) store1<DT>(s.dw, (int64_t)key * s.dim + c + j, e[j] * s.scale);
 }
 
 int64_t element_size(int dtype) { return dtype == kF32 ? 4 : 2; }
@@ -512,6 +546,15 @@ struct Scratch {
   int64_t tile = 0;
   int tiles = 0, passes = 0;
 };
+
+// The largest chunk with which every SM still has kSumUnits warps.
+constexpr int64_t kSumUnits = 16;
+int chunk_of(const EmbeddingArgs& a, int sms) {
+  const int64_t slices = blocks(a.dim, 32 * (a.dtype == kF32 ? kPer<kF32> : kPer<kF16>));
+  int chunk = kMostChunk;
+  while (chunk > kLeastChunk && blocks(a.rows, chunk) * slices < kSumUnits * sms) chunk /= 2;
+  return chunk;
+}
 
 Scratch backward_scratch(const EmbeddingArgs& a, int sms) {
   Scratch s;
@@ -530,7 +573,7 @@ Scratch backward_scratch(const EmbeddingArgs& a, int sms) {
     for (int64_t v = a.vocab; v > 0; v >>= 8) ++s.passes;    // (keys go up to vocab)
     s.counts = take((int64_t)s.tiles * kDigits * 4);
   }
-  s.parts = take(blocks(a.rows, kChunk) * 2 * a.dim * 4);
+  s.parts = take(blocks(a.rows, chunk_of(a, sms)) * 2 * a.dim * 4);
   return s;
 }
 
@@ -598,18 +641,17 @@ cudaError_t backward(const EmbeddingArgs& a, char* scratch, int sms, cudaStream_
   if (e != cudaSuccess) return e;
   const bool vec = vectors_ok(a.in, a.out, a.dim, DT);
   Sums s = {at(l.keys[last]), at(l.tokens[last]), a.rows, a.dim, (uint32_t)a.vocab,
-            blocks(a.dim, 32 * kPer<DT>), a.in, a.scale,
+            blocks(a.dim, 32 * kPer<DT>), chunk_of(a, sms), a.in, a.scale,
             reinterpret_cast<float*>(scratch + l.parts), a.out};
-  const int64_t chunks = blocks(a.rows, kChunk);
+  const int64_t chunks = blocks(a.rows, s.chunk);
   if (mark) mark(kEmbeddingSumsK, 0, stream);
   e = launch(true, vec ? embedding_sums_kernel<DT, true> : embedding_sums_kernel<DT, false>,
-             (unsigned)blocks(chunks * s.slices, kCtaWarps), kCtaThreads, 0, stream, s);
+             (unsigned)blocks(chunks * s.slices, kSumWarps), 32 * kSumWarps, 0, stream, s);
   if (mark) mark(kEmbeddingSumsK, 1, stream);
   if (e != cudaSuccess || chunks == 1) return e;
   if (mark) mark(kEmbeddingJoinK, 0, stream);
-  e = launch(true, embedding_join_kernel<DT>,
-             (unsigned)(chunks * blocks(a.dim, 4 * kJoinColumns)), kJoinColumns * kJoinGroups, 0,
-             stream, s, a.dim % 4 == 0);
+  e = launch(true, embedding_join_kernel<DT>, (unsigned)chunks, kJoinThreads, 0, stream, s,
+             a.dim % 4 == 0);
   if (mark) mark(kEmbeddingJoinK, 1, stream);
   return e;
 }

@@ -4,9 +4,12 @@
 // its mean over the tokens that count, and dl / dlogp = -[not clipped] r A +
 // kl_coef (1 - exp(e)).
 //
-// Bound by memory for large batches, by launches for small ones.  A warp takes
-// up to kPiece tokens of one sequence and writes its sums; one CTA joins them in
-// order, in fp64 (a batch's terms cancel down to their mean).
+// Bound by memory for large batches, by launches for small ones.  A warp takes a
+// piece of one sequence and makes its sums; one CTA joins them in order.  Small
+// batches: a cluster of eight CTAs, whose warps leave their sums in the first
+// one's shared memory, in a single launch.  (A batch's terms cancel down to their
+// mean: sums over lanes and pieces are held in two floats, 48 bits.  The same in
+// fp64, which the GB300 has little of, took 37 us for 8 sequences and 73 for 512.)
 //
 // Whether a token is clipped decides between its whole gradient and none, so it
 // is decided exactly: logp - old, as the fp32 difference and its rounding error,
@@ -14,14 +17,17 @@
 #include <cmath>
 
 #include "ops_internal.cuh"
+#include "tensor_core.cuh"
 
 namespace fp8opt {
 
 namespace {
 
 constexpr int kCtaThreads = 256, kCtaWarps = kCtaThreads / 32;
-constexpr int kPiece = 1024;      // tokens of a warp
+// Tokens of a warp: a power of two, at most 32 of a lane.
+constexpr int kLeastPiece = 128, kMostPiece = 1024;
 constexpr int kJoinThreads = 1024;
+constexpr int kClusterCtas = 8, kClusterUnits = kClusterCtas * kJoinThreads / 32;
 
 struct Border {
   float hi, lo;                   // log of the border
@@ -35,6 +41,7 @@ struct Policy {
   const uint8_t* mask;
   const float* ref_logp;
   int64_t length, pieces, units;  // a unit: a piece of a sequence
+  int piece;
   bool per_token;
   Border low, high;
   float kl_coef;
@@ -70,63 +77,104 @@ __device__ __forceinline__ Token token_of(const Policy& p, float logp, float old
   return {expf(d), (a > 0.0f && above) || (a < 0.0f && below)};
 }
 
-// Calls f(token of the sequence, values) for the lane's tokens of a piece; VEC:
-// four at a time, in 16-byte words.
+__device__ __forceinline__ bool counts(uint32_t m, int k) { return (m >> (8 * k) & 0xFFu) != 0; }
+
+// Calls f(first token, values, mask) for the lane's tokens of a unit; VEC: four at
+// a time, in 16-byte words.  Values of tokens that do not count are not read
+// where all of a call's do not.
 template <bool VEC, class F>
 __device__ __forceinline__ void each_token(const Policy& p, int64_t unit, F f) {
   const int lane = threadIdx.x & 31;
-  const int64_t b = unit / p.pieces, t0 = (unit - b * p.pieces) * kPiece;
-  const int64_t base = b * p.length;
-  const int n = (int)min((int64_t)kPiece, p.length - t0);
+  const int64_t b = unit / p.pieces, t0 = (unit - b * p.pieces) * p.piece;
+  const int64_t base = b * p.length + t0;
+  const int n = (int)min((int64_t)p.piece, p.length - t0);
   const float a_all = p.per_token ? 0.0f : p.advantage[b];
-  if constexpr (VEC) {
-#pragma unroll 2
-    for (int i = 4 * lane; i < n; i += 128) {
-      const int64_t at = base + t0 + i;
-      const float4 lp = *reinterpret_cast<const float4*>(p.logp + at);
-      const float4 old = *reinterpret_cast<const float4*>(p.old_logp + at);
-      float4 ref = make_float4(0, 0, 0, 0), a = make_float4(a_all, a_all, a_all, a_all);
+  constexpr int N = VEC ? 4 : 1;
+#pragma unroll(VEC ? 2 : 4)
+  for (int i = N * lane; i < n; i += 32 * N) {
+    const int64_t at = base + i;
+    float lp[N] = {}, old[N] = {}, ref[N] = {}, a[N];
+#pragma unroll
+    for (int k = 0; k < N; ++k) a[k] = a_all;
+    if constexpr (VEC) {
       uint32_t m = 0x01010101u;
-      if (p.ref_logp != nullptr) ref = *reinterpret_cast<const float4*>(p.ref_logp + at);
-      if (p.per_token) a = *reinterpret_cast<const float4*>(p.advantage + at);
       if (p.mask != nullptr) m = *reinterpret_cast<const uint32_t*>(p.mask + at);
-      const float l4[4] = {lp.x, lp.y, lp.z, lp.w}, o4[4] = {old.x, old.y, old.z, old.w};
-      const float r4[4] = {ref.x, ref.y, ref.z, ref.w}, a4[4] = {a.x, a.y, a.z, a.w};
-      f(at, l4, o4, r4, a4, m);
-    }
-  } else {
-#pragma unroll 4
-    for (int i = lane; i < n; i += 32) {
-      const int64_t at = base + t0 + i;
-      const float l1[1] = {p.logp[at]}, o1[1] = {p.old_logp[at]};
-      const float r1[1] = {p.ref_logp != nullptr ? p.ref_logp[at] : 0.0f};
-      const float a1[1] = {p.per_token ? p.advantage[at] : a_all};
-      f(at, l1, o1, r1, a1, p.mask != nullptr ? (uint32_t)p.mask[at] : 1u);
+      const auto read = [&](float (&to)[N], const float* from) {
+        const float4 v = *reinterpret_cast<const float4*>(from + at);
+        to[0] = v.x;
+        to[1] = v.y;
+        to[2] = v.z;
+        to[3] = v.w;
+      };
+      if (m != 0) {
+        read(lp, p.logp);
+        read(old, p.old_logp);
+        if (p.ref_logp != nullptr) read(ref, p.ref_logp);
+        if (p.per_token) read(a, p.advantage);
+      }
+      f(at, lp, old, ref, a, m);
+    } else {
+      const uint32_t m = p.mask != nullptr ? (uint32_t)p.mask[at] : 1u;
+      if (m != 0) {
+        lp[0] = p.logp[at];
+        old[0] = p.old_logp[at];
+        if (p.ref_logp != nullptr) ref[0] = p.ref_logp[at];
+        if (p.per_token) a[0] = p.advantage[at];
+      }
+      f(at, lp, old, ref, a, m);
     }
   }
 }
 
-__device__ __forceinline__ bool counts(uint32_t m, int k) { return (m >> (8 * k) & 0xFFu) != 0; }
+// A sum in two floats: hi, and what it was off by so far.
+struct Two {
+  float hi, lo;
+};
+
+__device__ __forceinline__ Two add(Two a, Two b) {
+  const float s = a.hi + b.hi, back = s - a.hi;
+  const float e = (a.hi - (s - back)) + (b.hi - back) + (a.lo + b.lo);
+  if (nonfinite(s)) return {s, 0.0f};
+  const float hi = s + e;
+  return {hi, e - (hi - s)};
+}
+
+__device__ __forceinline__ Two scaled(Two a, float k) {
+  if (nonfinite(a.hi)) return {a.hi * k, 0.0f};
+  const float hi = a.hi * k;
+  return {hi, fmaf(a.hi, k, -hi) + a.lo * k};
+}
+
+__device__ __forceinline__ Two shuffled(Two a, int o) {
+  return {__shfl_xor_sync(0xFFFFFFFFu, a.hi, o), __shfl_xor_sync(0xFFFFFFFFu, a.lo, o)};
+}
+
+// 1 / x.
+__device__ __forceinline__ float reciprocal(unsigned long long x) {
+  const float hi = __ull2float_rn(x);
+  const float lo = (float)(long long)(x - (unsigned long long)hi);
+  const float q = 1.0f / hi;
+  return q + q * (fmaf(-q, hi, 1.0f) - q * lo);
+}
 
 // A unit's sums.
 struct Part {
-  double policy, kl;
+  Two policy, kl;
   int clipped, count;
 };
+constexpr int kPartWords = 6;
+static_assert(sizeof(Part) == 4 * kPartWords, "");
 
 __device__ __forceinline__ Part add(const Part& a, const Part& b) {
-  return {a.policy + b.policy, a.kl + b.kl, a.clipped + b.clipped, a.count + b.count};
+  return {add(a.policy, b.policy), add(a.kl, b.kl), a.clipped + b.clipped, a.count + b.count};
 }
 
 // Over groups of `width` lanes.
 __device__ __forceinline__ Part reduce(Part p, int width) {
-  for (int o = width / 2; o > 0; o >>= 1) {
-    const Part q = {__shfl_xor_sync(0xFFFFFFFFu, p.policy, o),
-                    __shfl_xor_sync(0xFFFFFFFFu, p.kl, o),
-                    __shfl_xor_sync(0xFFFFFFFFu, p.clipped, o),
-                    __shfl_xor_sync(0xFFFFFFFFu, p.count, o)};
-    p = add(p, q);
-  }
+  for (int o = width / 2; o > 0; o >>= 1)
+    p = add(p, {shuffled(p.policy, o), shuffled(p.kl, o),
+                __shfl_xor_sync(0xFFFFFFFFu, p.clipped, o),
+                __shfl_xor_sync(0xFFFFFFFFu, p.count, o)});
   return p;
 }
 
@@ -137,18 +185,93 @@ __device__ __forceinline__ Part part_of(const Policy& p, int64_t unit) {
   int clipped = 0, count = 0;
   each_token<VEC>(p, unit, [&](int64_t, const float (&lp)[N], const float (&old)[N],
                                const float (&ref)[N], const float (&a)[N], uint32_t m) {
+    if (m == 0) return;
 #pragma unroll
     for (int k = 0; k < N; ++k) {
-      if (!counts(m, k)) continue;
       const Token t = token_of(p, lp[k], old[k], a[k]);
-      policy -= (t.clipped ? (a[k] > 0.0f ? p.high.ratio : p.low.ratio) : t.ratio) * a[k];
-      if (p.ref_logp != nullptr) kl += kl_of(ref[k] - lp[k]);
-      clipped += t.clipped;
-      ++count;
+      const float r = t.clipped ? (a[k] > 0.0f ? p.high.ratio : p.low.ratio) : t.ratio;
+      const float d = p.ref_logp != nullptr ? kl_of(ref[k] - lp[k]) : 0.0f;
+      if (counts(m, k)) {
+        policy -= r * a[k];
+        kl += d;
+        clipped += t.clipped;
+        ++count;
+      }
     }
   });
-  return reduce({(double)policy, (double)kl, clipped, count}, 32);
+  return reduce({{policy, 0.0f}, {kl, 0.0f}, clipped, count}, 32);
 }
+
+// What the batch's sums come to: by_sequence, of the sequences' means, else of
+// all tokens.
+struct Total {
+  Two policy, kl, clipped;
+  unsigned long long count;        // tokens, or sequences that have any
+  __device__ __forceinline__ void take(const Part& p, bool by_sequence) {
+    if (p.count == 0) return;
+    const float w = by_sequence ? reciprocal(p.count) : 1.0f;
+    policy = add(policy, scaled(p.policy, w));
+    kl = add(kl, scaled(p.kl, w));
+    clipped = add(clipped, scaled({(float)(p.clipped & ~0xFFF), (float)(p.clipped & 0xFFF)}, w));
+    count += by_sequence ? 1 : p.count;
+  }
+  __device__ __forceinline__ void reduce() {
+    for (int o = 16; o > 0; o >>= 1) {
+      policy = add(policy, shuffled(policy, o));
+      kl = add(kl, shuffled(kl, o));
+      clipped = add(clipped, shuffled(clipped, o));
+      count += __shfl_xor_sync(0xFFFFFFFFu, count, o);
+    }
+  }
+};
+
+// One CTA of kJoinThreads.
+__device__ void join(const Part* parts, int64_t batch, int64_t pieces, bool by_sequence,
+                     float kl_coef, float* stats, float* weight) {
+  __shared__ Total sh[kJoinThreads / 32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  // `width` neighbouring lanes to a sequence
+  int width = 1;
+  while (width < 32 && width < pieces) width *= 2;
+  const int groups = kJoinThreads / width, mine = threadIdx.x / width;
+  Total total = {};
+  for (int64_t b0 = 0; b0 < batch; b0 += groups) {
+    const int64_t b = b0 + mine;
+    Part s = {};
+    if (b < batch) {
+#pragma unroll 4
+      for (int64_t i = threadIdx.x % width; i < pieces; i += width)
+        s = add(s, parts[b * pieces + i]);
+    }
+    s = reduce(s, width);
+    if (b < batch && threadIdx.x % width == 0) {
+      total.take(s, by_sequence);
+      weight[b] = __int_as_float(s.count);      // for now
+    }
+  }
+  total.reduce();
+  if (lane == 0) sh[warp] = total;
+  __syncthreads();
+  total = sh[lane];
+  total.reduce();
+  const float all = total.count > 0 ? reciprocal(total.count) : 0.0f;
+  if (threadIdx.x == 0) {
+    const Two each[3] = {scaled(total.policy, all), scaled(total.kl, all),
+                         scaled(total.clipped, all)};
+    const Two loss = add(each[0], scaled(each[1], kl_coef));
+    stats[0] = loss.hi;
+    for (int k = 0; k < 3; ++k) stats[1 + k] = each[k].hi + each[k].lo;
+  }
+  // (each by the thread that wrote its count)
+  if (threadIdx.x % width == 0) {
+    for (int64_t b = mine; b < batch; b += groups) {
+      const int c = __float_as_int(weight[b]);
+      weight[b] = c == 0        ? 0.0f
+                  : by_sequence ? reciprocal((unsigned long long)c * total.count) : all;
+    }
+  }
+}
+static_assert(kJoinThreads / 32 == 32, "a lane to each warp's total");
 
 template <bool VEC>
 __global__ void __launch_bounds__(kCtaThreads)
@@ -160,76 +283,38 @@ policy_kernel(const Policy p, Part* parts) {
   if ((threadIdx.x & 31) == 0) parts[unit] = r;
 }
 
-// What the batch's sums come to: by_sequence, of the sequences' means, else of
-// all tokens.
-struct Total {
-  double policy = 0.0, kl = 0.0, clipped = 0.0;
-  long long count = 0;             // tokens, or sequences that have any
-  __device__ __forceinline__ void take(const Part& p, bool by_sequence) {
-    if (p.count == 0) return;
-    const double w = by_sequence ? 1.0 / p.count : 1.0;
-    policy += p.policy * w;
-    kl += p.kl * w;
-    clipped += p.clipped * w;
-    count += by_sequence ? 1 : p.count;
-  }
-};
-
 __global__ void __launch_bounds__(kJoinThreads)
 policy_join_kernel(const Part* parts, int64_t batch, int64_t pieces, bool by_sequence,
-                   double kl_coef, float* stats, float* weight) {
-  __shared__ double sh[3][kJoinThreads / 32];
-  __shared__ long long sh_count[kJoinThreads / 32];
+                   float kl_coef, float* stats, float* weight) {
   begin_after_previous();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  // `width` neighbouring lanes to a sequence
-  int width = 1;
-  while (width < 32 && width < pieces) width *= 2;
-  const int groups = kJoinThreads / width, mine = threadIdx.x / width;
-  Total total;
-  for (int64_t b0 = 0; b0 < batch; b0 += groups) {
-    const int64_t b = b0 + mine;
-    Part s = {0.0, 0.0, 0, 0};
-    if (b < batch)
-      for (int64_t i = threadIdx.x % width; i < pieces; i += width)
-        s = add(s, parts[b * pieces + i]);
-    s = reduce(s, width);
-    if (b < batch && threadIdx.x % width == 0) {
-      total.take(s, by_sequence);
-      weight[b] = __int_as_float(s.count);      // for now
-    }
+  join(parts, batch, pieces, by_sequence, kl_coef, stats, weight);
+}
+
+// At most kClusterUnits units.
+template <bool VEC>
+__global__ void __cluster_dims__(kClusterCtas, 1, 1) __launch_bounds__(kJoinThreads)
+policy_cluster_kernel(const Policy p, int64_t batch, bool by_sequence, float kl_coef,
+                      float* stats, float* weight) {
+  __shared__ Part parts[kClusterUnits];
+  begin_after_previous();
+  // (the first CTA has to be running before its memory is written)
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+  const int unit = (threadIdx.x >> 5) * kClusterCtas + (int)blockIdx.x;
+  Part r = {};
+  if (unit < p.units) r = part_of<VEC>(p, unit);
+  __syncwarp();
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  if (unit < p.units && (threadIdx.x & 31) == 0) {
+    const uint32_t to = cluster_addr(&parts[unit], 0);
+    const int words[kPartWords] = {__float_as_int(r.policy.hi), __float_as_int(r.policy.lo),
+                                   __float_as_int(r.kl.hi), __float_as_int(r.kl.lo), r.clipped,
+                                   r.count};
+#pragma unroll
+    for (int k = 0; k < kPartWords; ++k) cluster_store(to + 4 * k, words[k]);
   }
-  for (int o = 16; o > 0; o >>= 1) {
-    total.policy += __shfl_xor_sync(0xFFFFFFFFu, total.policy, o);
-    total.kl += __shfl_xor_sync(0xFFFFFFFFu, total.kl, o);
-    total.clipped += __shfl_xor_sync(0xFFFFFFFFu, total.clipped, o);
-    total.count += __shfl_xor_sync(0xFFFFFFFFu, total.count, o);
-  }
-  if (lane == 0) {
-    sh[0][warp] = total.policy;
-    sh[1][warp] = total.kl;
-    sh[2][warp] = total.clipped;
-    sh_count[warp] = total.count;
-  }
-  __syncthreads();
-  double sum[3] = {0.0, 0.0, 0.0};
-  long long count = 0;
-  for (int w = 0; w < kJoinThreads / 32; ++w) {
-    for (int k = 0; k < 3; ++k) sum[k] += sh[k][w];
-    count += sh_count[w];
-  }
-  const double all = count > 0 ? 1.0 / (double)count : 0.0;
-  if (threadIdx.x == 0) {
-    stats[0] = (float)((sum[0] + kl_coef * sum[1]) * all);
-    for (int k = 0; k < 3; ++k) stats[1 + k] = (float)(sum[k] * all);
-  }
-  // (each by the thread that wrote its count)
-  if (threadIdx.x % width == 0) {
-    for (int64_t b = mine; b < batch; b += groups) {
-      const int c = __float_as_int(weight[b]);
-      weight[b] = c == 0 ? 0.0f : (float)(by_sequence ? all / c : all);
-    }
-  }
+  __syncwarp();
+  cluster_sync();
+  if (blockIdx.x == 0) join(parts, batch, p.pieces, by_sequence, kl_coef, stats, weight);
 }
 
 template <bool VEC>
@@ -244,7 +329,10 @@ policy_backward_kernel(const Policy p, const float* dloss, const float* weight, 
                                const float (&ref)[N], const float (&a)[N], uint32_t m) {
     float d[N];
 #pragma unroll
+    for (int k = 0; k < N; ++k) d[k] = 0.0f;
+#pragma unroll
     for (int k = 0; k < N; ++k) {
+      if (m == 0) break;
       const Token t = token_of(p, lp[k], old[k], a[k]);
       float v = t.clipped ? 0.0f : -(t.ratio * a[k]);
       if (p.ref_logp != nullptr) {
@@ -266,7 +354,9 @@ Border border(double x) {
   return b;
 }
 
-Policy policy_of(const PolicyArgs& a) {
+// In pieces as small as they can be with at most `most` units (a warp's latency
+// goes with its piece).
+Policy policy_of(const PolicyArgs& a, int64_t most) {
   Policy p = {};
   p.logp = a.logp;
   p.old_logp = a.old_logp;
@@ -274,8 +364,11 @@ Policy policy_of(const PolicyArgs& a) {
   p.mask = a.mask;
   p.ref_logp = a.ref_logp;
   p.length = a.length;
-  p.pieces = (a.length + kPiece - 1) / kPiece;
-  p.units = a.batch * p.pieces;
+  for (p.piece = kLeastPiece;; p.piece *= 2) {
+    p.pieces = (a.length + p.piece - 1) / p.piece;
+    p.units = a.batch * p.pieces;
+    if (p.units <= most || p.piece == kMostPiece) break;
+  }
   p.per_token = a.per_token;
   p.low = border(-a.clip_low);
   p.high = border(a.clip_high);
@@ -294,31 +387,54 @@ bool vectors_ok(const PolicyArgs& a) {
 
 unsigned ctas(const Policy& p) { return (unsigned)((p.units + kCtaWarps - 1) / kCtaWarps); }
 
+// Forward: a cluster's units, of at most 256 tokens; else some for every SM, that
+// the joining CTA still takes a few to a thread of.
+constexpr int64_t kForwardUnits = 4096, kBackwardUnits = 16384;
+constexpr int kClusterPiece = 256;
+
+Policy forward_policy(const PolicyArgs& a, bool* cluster) {
+  const Policy p = policy_of(a, kClusterUnits);
+  *cluster = p.units <= kClusterUnits && p.piece <= kClusterPiece;
+  return *cluster ? p : policy_of(a, kForwardUnits);
+}
+
 }  // namespace
 
-size_t policy_scratch(const PolicyArgs& a) { return (size_t)policy_of(a).units * sizeof(Part); }
+size_t policy_scratch(const PolicyArgs& a) {
+  bool cluster;
+  const Policy p = forward_policy(a, &cluster);
+  return cluster ? 0 : (size_t)p.units * sizeof(Part);
+}
 
 cudaError_t launch_policy(const PolicyArgs& a, char* scratch, cudaStream_t stream,
                           LaunchMark mark) {
-  const Policy p = policy_of(a);
-  Part* parts = reinterpret_cast<Part*>(scratch);
-  cudaError_t e = cudaSuccess;
-  if (p.units > 0) {
-    if (mark) mark(kPolicyLossK, 0, stream);
-    e = launch(true, vectors_ok(a) ? policy_kernel<true> : policy_kernel<false>, ctas(p),
-               kCtaThreads, 0, stream, p, parts);
+  bool cluster;
+  const Policy p = forward_policy(a, &cluster);
+  const bool vec = vectors_ok(a);
+  const float kl = (float)a.kl_coef;
+  if (mark) mark(kPolicyLossK, 0, stream);
+  if (cluster) {
+    const cudaError_t e =
+        launch(false, vec ? policy_cluster_kernel<true> : policy_cluster_kernel<false>,
+               kClusterCtas, kJoinThreads, 0, stream, p, a.batch, a.by_sequence, kl, a.stats,
+               a.weight_out);
     if (mark) mark(kPolicyLossK, 1, stream);
+    return e;
   }
+  Part* parts = reinterpret_cast<Part*>(scratch);
+  cudaError_t e = launch(true, vec ? policy_kernel<true> : policy_kernel<false>, ctas(p),
+                         kCtaThreads, 0, stream, p, parts);
+  if (mark) mark(kPolicyLossK, 1, stream);
   if (e != cudaSuccess) return e;
   if (mark) mark(kPolicyJoinK, 0, stream);
   e = launch(true, policy_join_kernel, 1, kJoinThreads, 0, stream, (const Part*)parts, a.batch,
-             p.pieces, a.by_sequence, a.kl_coef, a.stats, a.weight_out);
+             p.pieces, a.by_sequence, kl, a.stats, a.weight_out);
   if (mark) mark(kPolicyJoinK, 1, stream);
   return e;
 }
 
 cudaError_t launch_policy_backward(const PolicyArgs& a, cudaStream_t stream, LaunchMark mark) {
-  const Policy p = policy_of(a);
+  const Policy p = policy_of(a, kBackwardUnits);
   if (mark) mark(kPolicyBackwardK, 0, stream);
   const cudaError_t e =
       launch(worth_early(a.batch * a.length),

@@ -12,7 +12,8 @@ from .api import (AdamWPlan, CastPlan, CastStepPlan, Fp8AdamW, ReducePlan,
                   fp8_reduce_scaled)
 from .ops import (act_load, act_save, embedding, embedding_backward, gelu,
                   gelu_backward, layer_norm, layer_norm_backward,
-                  linear_cross_entropy, linear_cross_entropy_backward, policy_loss,
+                  linear_cross_entropy, linear_cross_entropy_backward,
+                  linear_distillation, linear_distillation_backward, policy_loss,
                   policy_loss_backward)
 
 load()
@@ -25,4 +26,5 @@ __all__ = ["fp8_cast_scaled", "fp8_adamw_step", "fp8_reduce_scaled",
            "KERNELS", "timing_enable", "timing_read", "act_save", "act_load",
            "gelu", "gelu_backward", "layer_norm", "layer_norm_backward",
            "linear_cross_entropy", "linear_cross_entropy_backward", "embedding",
-           "embedding_backward", "policy_loss", "policy_loss_backward"]
+           "embedding_backward", "policy_loss", "policy_loss_backward",
+           "linear_distillation", "linear_distillation_backward"]

@@ -30,7 +30,8 @@ EXPORTS = ("fp8_cast_scaled", "fp8_adamw_step", "fp8_adam_step",
            "fp8_act_save", "fp8_act_load", "fp8_gelu", "fp8_gelu_backward",
            "fp8_layer_norm", "fp8_layer_norm_backward", "fp8_linear_xent",
            "fp8_linear_xent_backward", "fp8_embedding", "fp8_embedding_backward",
-           "fp8_policy_loss", "fp8_policy_loss_backward",
+           "fp8_policy_loss", "fp8_policy_loss_backward", "fp8_linear_distill",
+           "fp8_linear_distill_backward",
            "fp8opt_strerror",
            "fp8opt_last_error", "fp8opt_timing_enable", "fp8opt_timing_read",
            "fp8opt_release", "fp8opt_release_stream")
@@ -41,11 +42,12 @@ KERNELS = ("cast_amax", "cast_encode", "step_amax", "step_update", "step_w8",
            "layer_norm_params", "xent_logits", "xent_join", "xent_prepare",
            "xent_grads", "xent_dx", "embedding", "embedding_order",
            "embedding_sums", "embedding_join", "policy_loss", "policy_join",
-           "policy_backward")
+           "policy_backward", "xent_teacher")
 MAX_SHARDS = 64
 ACT_GROUP = 128
 GELU_ERF, GELU_TANH = 0, 1
 MEAN_TOKEN, MEAN_SEQUENCE = 0, 1
+MOST_TEACHER = 256
 
 
 class CastItem(C.Structure):
@@ -202,7 +204,11 @@ def load(path: str = LIB_PATH) -> C.CDLL:
             ("fp8_policy_loss", [p, p, p, p, p, i64, i64, i32, f64, f64, f64,
                                  i32, p, p, p]),
             ("fp8_policy_loss_backward", [p, p, p, p, p, p, p, i64, i64, i32,
-                                          f64, f64, f64, p, p])):
+                                          f64, f64, f64, p, p]),
+            ("fp8_linear_distill", [p, p, p, p, i64, i64, i64, i32, i32, i32,
+                                    C.c_float, p, p, p]),
+            ("fp8_linear_distill_backward", [p, p, p, p, p, p, i64, i64, i64, i32,
+                                             i32, i32, C.c_float, p, p, p])):
         fn = getattr(L, name)
         fn.restype, fn.argtypes = C.c_int, args
     L.fp8opt_strerror.restype = C.c_char_p

@@ -32,7 +32,7 @@ SOURCES = ["api.cu", "cast_kernels.cu", "step_kernels.cu", "fused_kernels.cu",
            "act_kernels.cu", "layer_norm_fwd.cu", "layer_norm_bwd.cu",
            "linear_xent.cu", "embedding.cu", "policy_loss.cu"]
 DEPS = ["fp8opt_internal.cuh", "ops_internal.cuh", "layer_norm.cuh",
-        "tensor_core.cuh", os.path.join("..", "..", "include", "fp8opt.h")]
+        "tensor_core.cuh", "teacher.cuh", os.path.join("..", "..", "include", "fp8opt.h")]
 
 NVCC = os.environ.get("NVCC", "nvcc")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

@@ -350,7 +350,7 @@ const char* const kKernelNames[kNumKernels] = {
     "gelu_backward", "layer_norm", "layer_norm_backward", "layer_norm_params",
     "xent_logits", "xent_join", "xent_prepare", "xent_grads", "xent_dx",
     "embedding", "embedding_order", "embedding_sums", "embedding_join", "policy_loss",
-    "policy_join", "policy_backward"};
+    "policy_join", "policy_backward", "xent_teacher"};
 
 struct Timing {
   bool on = false;

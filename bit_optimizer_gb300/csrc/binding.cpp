@@ -27,7 +27,8 @@ using at::ScalarType;
 // The C entry points, in the order of ops.py's list (the last one gives the text
 // of a call's error).
 enum { kActSave, kActLoad, kGelu, kGeluBackward, kNorm, kNormBackward, kXent, kXentBackward,
-       kEmbedding, kEmbeddingBackward, kPolicy, kPolicyBackward, kLastError, kEntries };
+       kEmbedding, kEmbeddingBackward, kPolicy, kPolicyBackward, kDistill, kDistillBackward,
+       kLastError, kEntries };
 void* g_fn[kEntries];
 PyObject* g_fail = nullptr;   // ops.py's function that raises for a status
 
@@ -381,15 +382,15 @@ PyObject* layer_norm_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
-// The linear layer of the cross entropy.
+// The linear layer of the cross entropy and of distillation.
 struct Linear {
   const Tensor *x, *w, *target;
   int64_t rows, dim, vocab, ignore;
   int dt;
 };
 
-Linear linear(Args& args, PyObject* x, PyObject* w, PyObject* target, PyObject* ignore) {
-  Linear l;
+Linear linear_layer(Args& args, PyObject* x, PyObject* w) {
+  Linear l = {};
   l.x = &args.tensor(x, "x");
   l.dt = dtype_of(*l.x, "x");
   if (l.dt == 0) refuse(PyExc_TypeError, "x must be bfloat16 or float16");
@@ -405,6 +406,11 @@ Linear linear(Args& args, PyObject* x, PyObject* w, PyObject* target, PyObject* 
   l.rows = l.x->size(0);
   l.dim = l.x->size(1);
   l.vocab = l.w->size(0);
+  return l;
+}
+
+Linear linear(Args& args, PyObject* x, PyObject* w, PyObject* target, PyObject* ignore) {
+  Linear l = linear_layer(args, x, w);
   l.target = &args.tensor(target, "target", ScalarType::Long, {l.rows});
   l.ignore = whole(ignore, "ignore_index");
   return l;
@@ -569,6 +575,65 @@ PyObject* policy_loss_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// The teacher's top logits of a linear layer's tokens.
+struct Top {
+  const Tensor *ids, *logits;
+  int k, dt;
+  float temperature;
+};
+
+Top teacher(Args& args, const Linear& l, PyObject* ids, PyObject* logits, PyObject* temperature) {
+  Top t;
+  t.ids = &args.tensor(ids, "ids");
+  if (t.ids->scalar_type() != ScalarType::Long)
+    refuse(PyExc_TypeError, std::string("ids must be Long, not ") +
+                                c10::toString(t.ids->scalar_type()));
+  if (t.ids->dim() != 2 || t.ids->size(0) != l.rows || t.ids->size(1) < 1 || t.ids->size(1) > 256)
+    refuse(PyExc_ValueError, "ids must have shape (" + std::to_string(l.rows) +
+                                 ", 1 to 256), not " + shape_text(t.ids->sizes()));
+  t.logits = &args.tensor(logits, "logits");
+  t.dt = dtype_of(*t.logits, "logits");
+  args.tensor(logits, "logits", t.logits->scalar_type(), t.ids->sizes());
+  t.k = (int)t.ids->size(1);
+  t.temperature = number(temperature, "temperature");
+  return t;
+}
+
+// linear_distillation(x, w, ids, logits, temperature, stream) -> loss, lse
+PyObject* distill(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return entry(n, 6, [&] {
+    Args args;
+    const Linear l = linear_layer(args, a[0], a[1]);
+    const Top t = teacher(args, l, a[2], a[3], a[4]);
+    OnStream on(a[5], args.device);
+    const Tensor loss = fresh({l.rows}, ScalarType::Float, args.device);
+    const Tensor lse = fresh({l.rows}, ScalarType::Float, args.device);
+    call(kDistill, l.x->data_ptr(), l.w->data_ptr(), t.ids->data_ptr(), t.logits->data_ptr(),
+         l.rows, l.dim, l.vocab, t.k, l.dt, t.dt, t.temperature, loss.data_ptr(), lse.data_ptr(),
+         on.handle);
+    return give(loss, lse);
+  });
+}
+
+// linear_distillation_backward(dloss, x, w, ids, logits, lse, temperature, stream)
+//   -> dx, dw
+PyObject* distill_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return entry(n, 8, [&] {
+    Args args;
+    const Linear l = linear_layer(args, a[1], a[2]);
+    const Top t = teacher(args, l, a[3], a[4], a[6]);
+    const Tensor& dloss = args.tensor(a[0], "dloss", ScalarType::Float, {l.rows});
+    const Tensor& lse = args.tensor(a[5], "lse", ScalarType::Float, {l.rows});
+    OnStream on(a[7], args.device);
+    const Tensor dx = fresh(l.x->sizes(), l.x->scalar_type(), args.device);
+    const Tensor dw = fresh(l.w->sizes(), l.w->scalar_type(), args.device);
+    call(kDistillBackward, dloss.data_ptr(), l.x->data_ptr(), l.w->data_ptr(), t.ids->data_ptr(),
+         t.logits->data_ptr(), lse.data_ptr(), l.rows, l.dim, l.vocab, t.k, l.dt, t.dt,
+         t.temperature, dx.data_ptr(), dw.data_ptr(), on.handle);
+    return give(dx, dw);
+  });
+}
+
 // bind(addresses of the C entry points, function that raises for a status)
 PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return entry(n, kEntries + 1, [&]() -> PyObject* {
@@ -591,7 +656,9 @@ PyMethodDef g_methods[] = {
     METHOD("linear_cross_entropy", xent),
     METHOD("linear_cross_entropy_backward", xent_backward), METHOD("embedding", embedding),
     METHOD("embedding_backward", embedding_backward), METHOD("policy_loss", policy_loss),
-    METHOD("policy_loss_backward", policy_loss_backward), {nullptr, nullptr, 0, nullptr}};
+    METHOD("policy_loss_backward", policy_loss_backward),
+    METHOD("linear_distillation", distill),
+    METHOD("linear_distillation_backward", distill_backward), {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "fp8opt_binding", nullptr, -1, g_methods,
                         nullptr, nullptr, nullptr, nullptr};

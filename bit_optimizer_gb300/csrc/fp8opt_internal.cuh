@@ -130,7 +130,7 @@ enum KernelId { kCastAmaxK = 0, kCastEncodeK, kStepAmaxK, kStepUpdateK,
                 kLayerNormBackwardK, kLayerNormParamsK, kXentLogitsK,
                 kXentJoinK, kXentPrepareK, kXentGradsK, kXentDxK,
                 kEmbeddingK, kEmbeddingOrderK, kEmbeddingSumsK, kEmbeddingJoinK,
-                kPolicyLossK, kPolicyJoinK, kPolicyBackwardK,
+                kPolicyLossK, kPolicyJoinK, kPolicyBackwardK, kXentTeacherK,
                 kNumKernels };
 
 // Called before (end = 0) and after (end = 1) each kernel launch when timing

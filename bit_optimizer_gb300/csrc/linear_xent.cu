@@ -45,6 +45,7 @@
 // rows are zero.  Rows that TMA cannot read (a row length that is not a
 // multiple of 8, unaligned tensors) are copied to a 16-byte pitch.
 #include "ops_internal.cuh"
+#include "teacher.cuh"
 #include "tensor_core.cuh"
 
 namespace fp8opt {
@@ -113,6 +114,8 @@ struct GemmOut {
   float* dx_sum;           // [split][token][dim_pitch]
   int64_t dim_pitch;
   void* dw;
+  Teacher teacher;         // with a teacher: lse is of z / temperature, and target says
+                           // whether a token counts
 };
 
 // One launch: up to three products that do not depend on one another, those
@@ -236,10 +239,11 @@ __device__ __forceinline__ void add_rows32(Turn& turn, float* out, int64_t pitch
 
 // exp(a + shift) and exp(b + shift) of two accumulators.  The difference is
 // taken before it is scaled to base 2: its rounding error does not grow with
-// the logits.
-__device__ __forceinline__ float2 exp_pair(uint32_t a, uint32_t b, float shift) {
+// the logits.  factor: log2(e), or with a teacher log2(e) / temperature.
+__device__ __forceinline__ float2 exp_pair(uint32_t a, uint32_t b, float shift,
+                                           float factor = kLog2eF) {
   const float2 d = mul2(add2(make_float2(__uint_as_float(a), __uint_as_float(b)), splat2(shift)),
-                        splat2(kLog2eF));
+                        splat2(factor));
   return make_float2(exp2_approx(d.x), exp2_approx(d.y));
 }
 
@@ -255,13 +259,22 @@ struct Strip {
 struct RowIn {
   long long target;
   float lse, dloss, top;
+  int entry, end;          // of the row's teacher's, in this tile
 };
 
-__device__ __forceinline__ RowIn row_in(const GemmShape& g, const GemmOut& o, int64_t row) {
-  RowIn in = {-1, 0.0f, 0.0f, 0.0f};
+template <bool TEACHER>
+__device__ __forceinline__ RowIn row_in(const GemmShape& g, const GemmOut& o, int64_t row,
+                                        int tile_n) {
+  RowIn in = {-1, 0.0f, 0.0f, 0.0f, 0, 0};
   if (g.mode == kStats || g.mode == kProbs) {
     if (row < o.tokens) {
-      in.target = o.target[row];
+      if (!TEACHER || g.mode == kProbs) in.target = o.target[row];
+      if (TEACHER) {
+        const uint16_t* s = o.teacher.start + row * (o.teacher.tiles + 1) + g.v0 / kTeacherTile +
+                            tile_n;
+        in.entry = s[0];
+        in.end = s[1];
+      }
       if (g.mode == kProbs) {
         in.lse = o.lse[row];
         in.dloss = o.dloss[row];
@@ -273,10 +286,10 @@ __device__ __forceinline__ RowIn row_in(const GemmShape& g, const GemmOut& o, in
 }
 
 // Two parts of a token's logits: maximum, and sum of exponentials above it.
-__device__ __forceinline__ float2 join_stats(float2 a, float2 b) {
+__device__ __forceinline__ float2 join_stats(float2 a, float2 b, float factor = kLog2eF) {
   const float top = fmaxf(a.x, b.x);
-  return make_float2(top, a.y * exp2_approx((a.x - top) * kLog2eF) +
-                              b.y * exp2_approx((b.x - top) * kLog2eF));
+  return make_float2(top, a.y * exp2_approx((a.x - top) * factor) +
+                              b.y * exp2_approx((b.x - top) * factor));
 }
 
 // A token's running maximum and sum of exponentials, and its target's logit.  The
@@ -287,7 +300,8 @@ struct Stats {
   float top = kLowest, sum = 0.0f, at_target = 0.0f;
   // 32 more logits, of which the first `valid` count; the target's is number
   // rel, if it is among them.
-  __device__ __forceinline__ void add(uint32_t (&r)[32], int valid, int rel) {
+  __device__ __forceinline__ void add(uint32_t (&r)[32], int valid, int rel,
+                                      float factor = kLog2eF) {
     if (valid < 32) {
 #pragma unroll
       for (int j = 0; j < 32; ++j)
@@ -302,28 +316,36 @@ struct Stats {
 #pragma unroll
     for (int j = 0; j < 32; ++j) m[j & 3] = fmaxf(m[j & 3], __uint_as_float(r[j]));
     m[0] = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
-    float2 s[2] = {make_float2(sum * exp2_approx((top - m[0]) * kLog2eF), 0.0f),
+    float2 s[2] = {make_float2(sum * exp2_approx((top - m[0]) * factor), 0.0f),
                    make_float2(0.0f, 0.0f)};
     top = m[0];
 #pragma unroll
     for (int j = 0; j < 32; j += 2)
-      s[j / 2 & 1] = add2(s[j / 2 & 1], exp_pair(r[j], r[j + 1], -top));
+      s[j / 2 & 1] = add2(s[j / 2 & 1], exp_pair(r[j], r[j + 1], -top, factor));
     s[0] = add2(s[0], s[1]);
     sum = s[0].x + s[0].y;
   }
 };
 
 // The strip's logits: maximum and sum of exponentials.
+template <bool TEACHER>
 __device__ __forceinline__ void stats_strip(const GemmOut& o, const Strip& t, const RowIn& in) {
   const long long target = in.target;
-  const int rel = target >= t.c0 && target < t.c0 + t.cols && target < o.vocab
+  const int rel = !TEACHER && target >= t.c0 && target < t.c0 + t.cols && target < o.vocab
                       ? (int)(target - t.c0) : -1;
   const int valid = (int)min((int64_t)t.cols, o.vocab - t.c0);   // may be <= 0
   Stats s;
   tmem_columns(t.tmem, t.cols, [&](int c, uint32_t (&r)[32], uint32_t (&q)[32]) {
-    s.add(r, valid - c, rel - c);
-    s.add(q, valid - c - 32, rel - c - 32);
+    s.add(r, valid - c, TEACHER ? -1 : rel - c, TEACHER ? o.teacher.factor : kLog2eF);
+    s.add(q, valid - c - 32, TEACHER ? -1 : rel - c - 32, TEACHER ? o.teacher.factor : kLog2eF);
   });
+  if constexpr (TEACHER) {
+    const int64_t row = t.row * o.teacher.k;
+    each_entry(o.teacher.words + row, in.entry, in.end, t.c0, t.cols, t.tmem,
+               [&](int first, int end, int, float z) {
+                 for (int i = first; i < end; ++i) o.teacher.z[row + i] = z;
+               });
+  }
   if (t.row < o.tokens) {
     o.partial[(int64_t)t.index * o.tokens + t.row] = make_float2(s.top, s.sum);
     if (rel >= 0) o.target_logit[t.row] = s.at_target;
@@ -337,6 +359,7 @@ __device__ __forceinline__ void stats_strip(const GemmOut& o, const Strip& t, co
 // from tile to tile, and a CTA writes its own once, at the end.
 struct SwappedStats {
   Stats s[2];
+  template <bool TEACHER>
   __device__ __forceinline__ void add(const GemmShape& g, const GemmOut& o, uint32_t tmem,
                                       int64_t v0, int half, Turn& turn) {
     const int lane = threadIdx.x & 31;
@@ -355,8 +378,25 @@ struct SwappedStats {
 #pragma unroll
       for (int j = 0; j < 32; ++j)
         r[j] = reinterpret_cast<const uint32_t*>(&turn.at(j, lane >> 2))[lane & 3];
-      __syncwarp();
       const int64_t token = c + lane;
+      if constexpr (TEACHER) {
+        if (token < o.tokens) {
+          const Teacher& t = o.teacher;
+          const uint16_t* start = t.start + token * (t.tiles + 1) + v0 / kTeacherTile;
+          const int end = valid > 0 ? start[1] : 0;
+          for (int i = valid > 0 ? start[0] : 0; i < end; ++i) {
+            const int64_t row = (int64_t)t.words[token * t.k + i] - v0;
+            if (row >= 32) break;
+            if (row >= 0)
+              t.z[token * t.k + i] = __uint_as_float(
+                  reinterpret_cast<const uint32_t*>(&turn.at((int)row, lane >> 2))[lane & 3]);
+          }
+        }
+        __syncwarp();
+        s[k].add(r, valid, -1, o.teacher.factor);
+        continue;
+      }
+      __syncwarp();
       const long long target = token < o.tokens ? o.target[token] : -1;
       const int rel = target >= v0 && target < v0 + 32 && target < o.vocab ? (int)(target - v0)
                                                                             : -1;
@@ -365,6 +405,7 @@ struct SwappedStats {
     }
   }
   // Every epilogue warp; turns: all warps' shared memory.
+  template <bool TEACHER>
   __device__ __forceinline__ void finish(const GemmOut& o, int warp, Turn* turns) {
     const int lane = threadIdx.x & 31;
     float2* const mine = reinterpret_cast<float2*>(&turns[warp]);
@@ -376,14 +417,16 @@ struct SwappedStats {
       if (token >= o.tokens) continue;
       float2 a = make_float2(kLowest, 0.0f);
       for (int w = 0; w < 4; ++w)
-        a = join_stats(a, reinterpret_cast<const float2*>(&turns[warp + w])[32 * k + lane]);
+        a = join_stats(a, reinterpret_cast<const float2*>(&turns[warp + w])[32 * k + lane],
+                       TEACHER ? o.teacher.factor : kLog2eF);
       o.partial[(int64_t)blockIdx.x * o.tokens + token] = a;
     }
   }
 };
 
-// The strip's logits turned into p.
-template <bool BF16>
+// The strip's logits turned into p.  With a teacher, the few columns with an entry
+// are written once more, less its share.
+template <bool BF16, bool TEACHER>
 __device__ __forceinline__ void probs_strip(const GemmShape& g, const GemmOut& o,
                                             const Strip& t, const RowIn& in, Turn& turn) {
   const bool live = t.row < o.tokens;
@@ -392,9 +435,9 @@ __device__ __forceinline__ void probs_strip(const GemmShape& g, const GemmOut& o
   if (live && in.target != o.ignore) {
     const float own = ldexpf(in.dloss, dloss_shift(in.dloss, in.top));
     k = (in.top == 0.0f ? own : __fdiv_rn(own, in.top)) * kProbScale;
-    shift = -in.lse;
+    shift = TEACHER ? -in.lse * o.teacher.temperature : -in.lse;
     const long long at = in.target - g.v0 - t.c0;
-    if (at >= 0 && at < t.cols) rel = (int)at;
+    if (!TEACHER && at >= 0 && at < t.cols) rel = (int)at;
     if (in.target < 0 || in.target >= o.vocab) k = __uint_as_float(0x7FC00000u);
   }
   const bool zero = k == 0.0f;      // an ignored token, whatever its logits are
@@ -406,13 +449,15 @@ __device__ __forceinline__ void probs_strip(const GemmShape& g, const GemmOut& o
     float v[64];
 #pragma unroll
     for (int j = 0; j < 32; j += 2) {
-      const float2 e = exp_pair(r[j], r[j + 1], shift), f = exp_pair(q[j], q[j + 1], shift);
+      const float factor = TEACHER ? o.teacher.factor : kLog2eF;
+      const float2 e = exp_pair(r[j], r[j + 1], shift, factor);
+      const float2 f = exp_pair(q[j], q[j + 1], shift, factor);
       v[j] = e.x;
       v[j + 1] = e.y;
       v[32 + j] = f.x;
       v[33 + j] = f.y;
     }
-    if (__any_sync(0xFFFFFFFFu, rel >= c && rel < c + 64)) {
+    if (!TEACHER && __any_sync(0xFFFFFFFFu, rel >= c && rel < c + 64)) {
 #pragma unroll
       for (int j = 0; j < 64; ++j)
         if (rel == c + j) v[j] -= 1.0f;
@@ -426,6 +471,17 @@ __device__ __forceinline__ void probs_strip(const GemmShape& g, const GemmOut& o
     }
     store_rows16<BF16>(turn, out + c, o.piece, rows, 64, v);
   });
+  if constexpr (TEACHER) {
+    const Teacher& h = o.teacher;
+    const int64_t row = t.row * h.k;
+    each_entry(h.words + row, in.entry, in.end, g.v0 + t.c0, t.cols, t.tmem,
+               [&](int first, int end, int c, float z) {
+                 float v = exp2_approx((z + shift) * h.factor);
+                 for (int i = first; i < end; ++i) v -= h.q[row + i];
+                 out[(t.row - row0) * o.piece + c] =
+                     (uint16_t)pack16<BF16>(zero ? 0.0f : v * k, 0.0f);
+               });
+  }
 }
 
 // This piece's part of dx, added to the earlier ones'.  `none`: the split has
@@ -540,7 +596,7 @@ struct TileReader {
   }
 };
 
-template <bool BF16>
+template <bool BF16, bool TEACHER>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
 gemm_kernel(const __grid_constant__ GemmArgs args) {
   extern __shared__ uint8_t dyn[];
@@ -731,8 +787,8 @@ gemm_kernel(const __grid_constant__ GemmArgs args) {
       *t = *next;
       if (t->work == kNoWork) return true;
       reader.done(bar);
-      *in = row_in(args.job[t->job].shape, args.out,
-                   (int64_t)t->m * kTileM + rank * kHalfM + (threadIdx.x & 127));
+      *in = row_in<TEACHER>(args.job[t->job].shape, args.out,
+                            (int64_t)t->m * kTileM + rank * kHalfM + (threadIdx.x & 127), t->n);
       return true;
     };
     Tile t;
@@ -750,11 +806,11 @@ gemm_kernel(const __grid_constant__ GemmArgs args) {
       Tile after;
       RowIn in_after;
       if (!(ok = read(&after, &in_after))) break;
-      if (g.mode == kStats) stats_strip(args.out, strip, in);
+      if (g.mode == kStats) stats_strip<TEACHER>(args.out, strip, in);
       else if (g.mode == kStatsSwapped)
-        swapped.add(g, args.out, tmem + buf * kTileN + ((uint32_t)(warp % 4) << 21),
+        swapped.add<TEACHER>(g, args.out, tmem + buf * kTileN + ((uint32_t)(warp % 4) << 21),
                     strip.row - (threadIdx.x & 31), half, turn);
-      else if (g.mode == kProbs) probs_strip<BF16>(g, args.out, strip, in, turn);
+      else if (g.mode == kProbs) probs_strip<BF16, TEACHER>(g, args.out, strip, in, turn);
       else if (g.mode == kDx) dx_strip(g, args.out, strip, t.split, work_blocks(t.work) == 0, turn);
       else dw_strip<BF16>(g, args.out, strip, in, turn);
       tcgen_fence_before();
@@ -767,7 +823,7 @@ gemm_kernel(const __grid_constant__ GemmArgs args) {
       t = after;
       in = in_after;
     }
-    if (args.job[0].shape.mode == kStatsSwapped) swapped.finish(args.out, warp, turns);
+    if (args.job[0].shape.mode == kStatsSwapped) swapped.finish<TEACHER>(args.out, warp, turns);
   }
   if (!ok) *args.error = 1;
   __syncwarp();
@@ -779,11 +835,14 @@ gemm_kernel(const __grid_constant__ GemmArgs args) {
 
 // Joins the column strips of 32 tokens, a token to each lane (neighbouring
 // tokens' statistics lie side by side): warp k takes strips k, k + 32, ... in
-// order, then the 32 warps' results are joined in order.
+// order, then the 32 warps' results are joined in order.  With a teacher, lse is of
+// z / temperature and a token's warp adds up its loss.
+template <bool TEACHER>
 __global__ void __launch_bounds__(1024, 2)
 xent_join_kernel(const float2* partial, int strips, int64_t tokens, int64_t vocab,
                  const long long* target, long long ignore, const float* target_logit,
-                 float* __restrict__ loss, float* __restrict__ lse) {
+                 const Teacher teacher, float* __restrict__ loss, float* __restrict__ lse) {
+  const float factor = TEACHER ? teacher.factor : kLog2eF;
   __shared__ float2 sh[32][33];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t row = (int64_t)blockIdx.x * 32 + lane;
@@ -797,7 +856,7 @@ xent_join_kernel(const float2* partial, int strips, int64_t tokens, int64_t voca
       p[k] = i + 32 * k < strips && row < tokens
                  ? __ldcg(partial + (int64_t)(i + 32 * k) * tokens + row) : none;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) s = join_stats(s, p[k]);
+    for (int k = 0; k < 8; ++k) s = join_stats(s, p[k], factor);
   }
   sh[warp][lane] = s;
   __syncthreads();
@@ -806,8 +865,19 @@ xent_join_kernel(const float2* partial, int strips, int64_t tokens, int64_t voca
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1)
     s = join_stats(s, make_float2(__shfl_xor_sync(0xFFFFFFFFu, s.x, o),
-                                  __shfl_xor_sync(0xFFFFFFFFu, s.y, o)));
+                                  __shfl_xor_sync(0xFFFFFFFFu, s.y, o)), factor);
   const int64_t mine = (int64_t)blockIdx.x * 32 + warp;
+  if constexpr (TEACHER) {
+    if (mine >= tokens) return;
+    const float l = __fdiv_rn(s.x, teacher.temperature) + logf(s.y);
+    const long long t = target[mine];
+    const float sum = teacher_loss(teacher, mine, l);
+    if (lane == 0) {
+      lse[mine] = l;
+      loss[mine] = t == ignore ? 0.0f : t < vocab ? sum : __uint_as_float(0x7FC00000u);
+    }
+    return;
+  }
   if (lane == 0 && mine < tokens) {
     const float l = s.x + logf(s.y);
     lse[mine] = l;
@@ -1010,8 +1080,9 @@ unsigned gemm_ctas(int64_t tiles, int sms) {
   return 2 * (unsigned)std::min(tiles, (int64_t)sms / 2);
 }
 
-cudaError_t launch_gemm(GemmArgs& g, bool bf16, int sms, cudaStream_t stream) {
-  auto kernel = bf16 ? gemm_kernel<true> : gemm_kernel<false>;
+cudaError_t launch_gemm(GemmArgs& g, bool bf16, bool teacher, int sms, cudaStream_t stream) {
+  auto kernel = teacher ? (bf16 ? gemm_kernel<true, true> : gemm_kernel<false, true>)
+                        : (bf16 ? gemm_kernel<true, false> : gemm_kernel<false, false>);
   const cudaError_t e =
       cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kGemmSmem);
   if (e != cudaSuccess) return e;
@@ -1105,6 +1176,52 @@ class Layout {
   size_t bytes_ = 0;
 };
 
+// With a teacher: what its kernel leaves for `tokens` tokens.
+struct TeacherScratch {
+  size_t words, q, z, start, state, dloss;
+};
+int teacher_tiles(const XentArgs& a) {
+  return (int)((a.vocab + kTeacherTile - 1) / kTeacherTile);
+}
+static_assert(kTeacherTile == kTileN && kTeacherTile == kTileM, "a tile's entries");
+TeacherScratch teacher_scratch(Layout& l, const XentArgs& a, int64_t tokens, bool forward) {
+  TeacherScratch s = {};
+  if (a.ids == nullptr) return s;
+  s.words = l.take(tokens * a.k * 4);
+  s.q = l.take(tokens * a.k * 4);
+  if (forward) s.z = l.take(tokens * a.k * 4);
+  s.start = l.take(tokens * (teacher_tiles(a) + 1) * 2);
+  s.state = l.take(tokens * 8);
+  if (!forward) s.dloss = l.take(tokens * 4);
+  return s;
+}
+
+// Makes the entries of the tokens from t0 on and returns what the other kernels
+// read of them.
+cudaError_t make_teacher(const XentArgs& a, int64_t t0, int64_t tokens, char* scratch,
+                         const TeacherScratch& s, bool forward, Teacher* t, cudaStream_t stream,
+                         LaunchMark mark) {
+  uint32_t* words = reinterpret_cast<uint32_t*>(scratch + s.words);
+  float* q = reinterpret_cast<float*>(scratch + s.q);
+  uint16_t* start = reinterpret_cast<uint16_t*>(scratch + s.start);
+  *t = {words, q, start, forward ? reinterpret_cast<float*>(scratch + s.z) : nullptr, a.k,
+        teacher_tiles(a), a.temperature, (float)(1.4426950408889634 / (double)a.temperature)};
+  const char* logits = static_cast<const char*>(a.logits) +
+                       t0 * a.k * (a.logit_dtype == kF32 ? 4 : 2);
+  if (mark) mark(kXentTeacherK, 0, stream);
+  const cudaError_t e =
+      launch(true, a.logit_dtype == kF32    ? teacher_kernel<kF32>
+                   : a.logit_dtype == kBF16 ? teacher_kernel<kBF16>
+                                            : teacher_kernel<kF16>,
+             (unsigned)((tokens + kTeacherWarps - 1) / kTeacherWarps), 32 * kTeacherWarps, 0,
+             stream, reinterpret_cast<const long long*>(a.ids) + t0 * a.k, (const void*)logits,
+             tokens, a.vocab, *t, words, q, start,
+             reinterpret_cast<long long*>(scratch + s.state), forward ? nullptr : a.dloss,
+             reinterpret_cast<float*>(scratch + s.dloss));
+  if (mark) mark(kXentTeacherK, 1, stream);
+  return e;
+}
+
 // Few tokens: the vocabulary's rows take the tiles' 256 rows and the tokens
 // their columns, as many as there are; a stage then holds little besides w,
 // which is all that has to be read.  24 x 768 x 50257: 19.9 us, 27.3 with the
@@ -1113,6 +1230,7 @@ constexpr int64_t kSwapTokens = 128;
 
 struct ForwardScratch {
   size_t x = 0, w = 0, partial = 0, logit = 0, bytes = 0;
+  TeacherScratch teacher;
   bool swapped = false;
   int64_t strips = 0;
 };
@@ -1128,6 +1246,7 @@ ForwardScratch forward_scratch(const XentArgs& a, int sms) {
                        : 2 * (up(a.vocab, kTileN) / kTileN);
   s.partial = l.take(s.strips * tokens * 8);
   s.logit = l.take(tokens * 4);
+  s.teacher = teacher_scratch(l, a, tokens, true);
   s.bytes = l.bytes();
   return s;
 }
@@ -1136,6 +1255,7 @@ struct BackwardScratch {
   size_t next = 0, x = 0, x_plain = 0, w = 0, top = 0, probs[2] = {0, 0}, dx = 0, bytes = 0;
   int64_t piece = 0, pieces = 0;
   int splits = 1;
+  TeacherScratch teacher;
 };
 BackwardScratch backward_scratch(const XentArgs& a, int sms) {
   BackwardScratch s;
@@ -1151,6 +1271,7 @@ BackwardScratch backward_scratch(const XentArgs& a, int sms) {
   if (!direct(a.w, a.dim)) s.w = l.take(a.vocab * pitch * 2);
   for (int i = 0; i < 2 && i < s.pieces; ++i) s.probs[i] = l.take(a.rows * s.piece * 2);
   s.dx = l.take(s.splits * a.rows * up(a.dim, width_of(a.dim)) * 4);
+  s.teacher = teacher_scratch(l, a, a.rows, false);
   s.bytes = l.bytes();
   return s;
 }
@@ -1192,6 +1313,12 @@ cudaError_t launch_xent_forward(const XentArgs& a, char* scratch, int* error, in
     g.out.dim = a.dim;
     g.out.target = reinterpret_cast<const long long*>(a.target) + t0;
     g.out.ignore = a.ignore;
+    if (a.ids != nullptr) {
+      e = make_teacher(a, t0, tokens, scratch, s.teacher, true, &g.out.teacher, stream, mark);
+      if (e != cudaSuccess) break;
+      g.out.target = reinterpret_cast<const long long*>(scratch + s.teacher.state);
+      g.out.ignore = kTeacherNone;
+    }
     g.out.partial = reinterpret_cast<float2*>(scratch + s.partial);
     g.out.target_logit = reinterpret_cast<float*>(scratch + s.logit);
     CUtensorMap& of_x = s.swapped ? g.job[0].b : g.job[0].a;
@@ -1202,14 +1329,14 @@ cudaError_t launch_xent_forward(const XentArgs& a, char* scratch, int* error, in
       e = make_map(&of_w, bf16, w, a.vocab, a.dim, pitch, s.swapped ? kHalfM : kTileN / 2);
     if (e != cudaSuccess) break;
     if (mark) mark(kXentLogitsK, 0, stream);
-    e = launch_gemm(g, bf16, sms, stream);
+    e = launch_gemm(g, bf16, a.ids != nullptr, sms, stream);
     if (mark) mark(kXentLogitsK, 1, stream);
     if (e != cudaSuccess) break;
     if (mark) mark(kXentJoinK, 0, stream);
-    e = launch(true, xent_join_kernel, (unsigned)((tokens + 31) / 32), 1024, 0, stream,
-                     (const float2*)g.out.partial, (int)s.strips, tokens, a.vocab, g.out.target,
-                     g.out.ignore, (const float*)g.out.target_logit, a.loss + t0,
-                     a.lse_out + t0);
+    e = launch(true, a.ids != nullptr ? xent_join_kernel<true> : xent_join_kernel<false>,
+               (unsigned)((tokens + 31) / 32), 1024, 0, stream, (const float2*)g.out.partial,
+               (int)s.strips, tokens, a.vocab, g.out.target, g.out.ignore,
+               (const float*)g.out.target_logit, g.out.teacher, a.loss + t0, a.lse_out + t0);
     if (mark) mark(kXentJoinK, 1, stream);
   }
   return e;
@@ -1223,6 +1350,17 @@ cudaError_t launch_xent_backward(const XentArgs& a, char* scratch, int* error, i
   const int64_t pitch = up(a.dim, 8);
   const int width = width_of(a.dim);
   const long long* target = reinterpret_cast<const long long*>(a.target);
+  int64_t ignore = a.ignore;
+  const float* dloss = a.dloss;
+  Teacher teacher = {};
+  cudaError_t e = cudaSuccess;
+  if (a.ids != nullptr) {
+    e = make_teacher(a, 0, a.rows, scratch, s.teacher, false, &teacher, stream, mark);
+    if (e != cudaSuccess) return e;
+    target = reinterpret_cast<const long long*>(scratch + s.teacher.state);
+    ignore = kTeacherNone;
+    dloss = reinterpret_cast<const float*>(scratch + s.teacher.dloss);
+  }
   // the logits' x, and dw's: zero for ignored tokens, scaled for a small dloss
   const bool x_direct = direct(a.x, a.dim);
   const char* x = x_direct ? static_cast<const char*>(a.x) : scratch + s.x_plain;
@@ -1230,11 +1368,12 @@ cudaError_t launch_xent_backward(const XentArgs& a, char* scratch, int* error, i
   const char* w = static_cast<const char*>(a.w);
   int* next = reinterpret_cast<int*>(scratch + s.next);
   float* top = reinterpret_cast<float*>(scratch + s.top);
-  cudaError_t e = cudaMemsetAsync(next, 0, (size_t)(s.pieces + 1) * 4, stream);
+  e = cudaMemsetAsync(next, 0, (size_t)(s.pieces + 1) * 4, stream);
   if (mark) mark(kXentPrepareK, 0, stream);
   if (e == cudaSuccess)
     e = copy_rows(a.x, a.rows, a.dim, pitch, bf16, scratch + s.x, sms, stream,
-                  {a.target, a.ignore, a.dloss, top, x_direct ? nullptr : scratch + s.x_plain});
+                  {reinterpret_cast<const int64_t*>(target), ignore, dloss, top,
+                   x_direct ? nullptr : scratch + s.x_plain});
   if (e == cudaSuccess && !direct(a.w, a.dim)) {
     e = copy_rows(a.w, a.vocab, a.dim, pitch, bf16, scratch + s.w, sms, stream);
     w = scratch + s.w;
@@ -1265,9 +1404,10 @@ cudaError_t launch_xent_backward(const XentArgs& a, char* scratch, int* error, i
   o.vocab = a.vocab;
   o.dim = a.dim;
   o.target = target;
-  o.ignore = a.ignore;
+  o.ignore = ignore;
+  o.teacher = teacher;
   o.lse = a.lse;
-  o.dloss = a.dloss;
+  o.dloss = dloss;
   o.top = top;
   o.piece = s.piece;
   o.dx_sum = reinterpret_cast<float*>(scratch + s.dx);
@@ -1297,7 +1437,7 @@ cudaError_t launch_xent_backward(const XentArgs& a, char* scratch, int* error, i
                           reinterpret_cast<uint16_t*>(scratch + s.probs[i & 1]), a_rows}};
     }
     if (mark) mark(kXentGradsK, 0, stream);
-    e = launch_gemm(g, bf16, sms, stream);
+    e = launch_gemm(g, bf16, a.ids != nullptr, sms, stream);
     if (mark) mark(kXentGradsK, 1, stream);
     if (e != cudaSuccess) return e;
   }
@@ -1305,7 +1445,7 @@ cudaError_t launch_xent_backward(const XentArgs& a, char* scratch, int* error, i
   e = launch(true, bf16 ? xent_dx_kernel<true> : xent_dx_kernel<false>,
                    (unsigned)std::min((a.rows * ((a.dim + 7) / 8) + 255) / 256, (int64_t)8 * sms), 256,
                    0, stream, (const float*)o.dx_sum, s.splits, a.rows, a.dim, o.dim_pitch, target,
-                   (long long)a.ignore, a.dloss, (const float*)top,
+                   (long long)ignore, dloss, (const float*)top,
                    static_cast<uint16_t*>(a.dx));
   if (mark) mark(kXentDxK, 1, stream);
   return e;

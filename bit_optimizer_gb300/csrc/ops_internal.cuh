@@ -113,6 +113,12 @@ struct XentArgs {
   const float* lse;
   void* dx;
   void* dw;
+  // Distillation (ids not NULL): k words of a teacher's for each token, and their
+  // logits, instead of target and ignore; lse is of z / temperature.
+  const int64_t* ids;
+  const void* logits;
+  int k, logit_dtype;
+  float temperature;
 };
 
 size_t xent_forward_scratch(const XentArgs& a, int sms);

@@ -394,3 +394,93 @@ extern "C" int fp8_policy_loss_backward(const float* dloss, const float* logp,
     return call.done(fn, launch_policy_backward(a, stream, call.mark));
   });
 }
+
+namespace fp8opt {
+namespace {
+
+int check_distill(const char* fn, const XentArgs& a, int64_t most_rows) {
+  const int st = check_xent(fn, a, most_rows);
+  if (st != FP8OPT_OK) return st;
+  if (a.k < 1 || a.k > FP8OPT_MOST_TEACHER) return bad(fn, "k outside [1, FP8OPT_MOST_TEACHER]");
+  if (!known(a.logit_dtype)) return unsupported(fn, "unknown dtype of the logits");
+  if (!(a.temperature >= 0x1p-20f && a.temperature <= 0x1p20f))
+    return bad(fn, "temperature outside [2^-20, 2^20]");
+  return FP8OPT_OK;
+}
+
+XentArgs distill_args(const void* x, const void* w, const int64_t* ids, const void* logits,
+                      int64_t rows, int64_t dim, int64_t vocab, int k, int dtype, int logit_dtype,
+                      float temperature) {
+  XentArgs a = {};
+  a.x = x;
+  a.w = w;
+  a.rows = rows;
+  a.dim = dim;
+  a.vocab = vocab;
+  a.dtype = dtype;
+  a.ids = ids;
+  a.logits = logits;
+  a.k = k;
+  a.logit_dtype = logit_dtype;
+  a.temperature = temperature;
+  return a;
+}
+
+}  // namespace
+}  // namespace fp8opt
+
+extern "C" int fp8_linear_distill(const void* x, const void* w, const int64_t* ids,
+                                  const void* logits, int64_t rows, int64_t dim, int64_t vocab,
+                                  int k, int dtype, int logit_dtype, float temperature,
+                                  float* loss, float* lse, void* stream_ptr) {
+  return entry([&] {
+    const char* fn = "fp8_linear_distill";
+    XentArgs a = distill_args(x, w, ids, logits, rows, dim, vocab, k, dtype, logit_dtype,
+                              temperature);
+    a.loss = loss;
+    a.lse_out = lse;
+    int st = check_distill(fn, a, kXentMost);
+    if (st != FP8OPT_OK || rows == 0) return st;
+    if (!x || !w || !ids || !logits || !loss || !lse) return bad(fn, "NULL pointer");
+    cudaStream_t stream = static_cast<cudaStream_t>(stream_ptr);
+    OpCall call;
+    int* error = nullptr;
+    if ((st = call.open(fn, stream, 0)) != FP8OPT_OK ||
+        (st = call.open(fn, stream, xent_forward_scratch(a, call.sms))) != FP8OPT_OK ||
+        (st = call.error_word(fn, stream, &error)) != FP8OPT_OK)
+      return st;
+    return call.done(fn, launch_xent_forward(a, call.scratch, error, call.sms, stream,
+                                             call.mark));
+  });
+}
+
+extern "C" int fp8_linear_distill_backward(const float* dloss, const void* x, const void* w,
+                                           const int64_t* ids, const void* logits,
+                                           const float* lse, int64_t rows, int64_t dim,
+                                           int64_t vocab, int k, int dtype, int logit_dtype,
+                                           float temperature, void* dx, void* dw,
+                                           void* stream_ptr) {
+  return entry([&] {
+    const char* fn = "fp8_linear_distill_backward";
+    XentArgs a = distill_args(x, w, ids, logits, rows, dim, vocab, k, dtype, logit_dtype,
+                              temperature);
+    a.dloss = dloss;
+    a.lse = lse;
+    a.dx = dx;
+    a.dw = dw;
+    int st = check_distill(fn, a, kXentMostSummed);
+    if (st != FP8OPT_OK) return st;
+    if (!dw || (rows > 0 && (!dloss || !x || !w || !ids || !logits || !lse || !dx)))
+      return bad(fn, "NULL pointer");
+    cudaStream_t stream = static_cast<cudaStream_t>(stream_ptr);
+    OpCall call;
+    int* error = nullptr;
+    if ((st = call.open(fn, stream, 0)) != FP8OPT_OK) return st;
+    const size_t bytes = rows > 0 ? xent_backward_scratch(a, call.sms) : 0;
+    if ((st = call.open(fn, stream, bytes)) != FP8OPT_OK ||
+        (st = call.error_word(fn, stream, &error)) != FP8OPT_OK)
+      return st;
+    return call.done(fn, launch_xent_backward(a, call.scratch, error, call.sms, stream,
+                                              call.mark));
+  });
+}

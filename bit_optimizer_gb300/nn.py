@@ -8,6 +8,7 @@ pass what the operator's 8-bit form keeps, and nothing else.
 * ``linear_cross_entropy``: the input, the weight and one float per token; no
   logits (the backward pass makes the probabilities again, two pieces of the
   vocabulary at a time).
+* ``linear_distillation``: the same, and the teacher's ids and logits.
 * ``embedding``: the ids.
 * ``policy_loss``: its inputs, and one float per sequence.
 
@@ -24,7 +25,7 @@ probabilities that the cross entropy gives:
     logp = -nn.linear_cross_entropy(x, wte, answer, reduction="none")
     loss, stats = nn.policy_loss(logp, old_logp, advantage, mask, ref_logp, kl_coef=0.04)
 
-Under torch.autocast the two linear layers cast their input and parameters to
+Under torch.autocast the linear layers cast their input and parameters to
 its dtype, as torch's do, so FP32 weights get FP32 gradients; ``layer_norm`` and
 ``gelu`` take what they are given, and their result has its type.  Under no_grad
 the checkpoints are written all the same, and freed.
@@ -37,8 +38,8 @@ from torch.autograd.function import once_differentiable
 
 from . import ops
 
-__all__ = ["layer_norm", "gelu", "linear", "linear_cross_entropy", "embedding",
-           "policy_loss"]
+__all__ = ["layer_norm", "gelu", "linear", "linear_cross_entropy",
+           "linear_distillation", "embedding", "policy_loss"]
 
 
 class _LayerNorm(Function):
@@ -117,6 +118,22 @@ class _LinearCrossEntropy(Function):
         return dx, dw, None, None
 
 
+class _LinearDistillation(Function):
+    @staticmethod
+    def forward(ctx, x, weight, ids, logits, temperature):
+        loss, lse = ops.linear_distillation(x, weight, ids, logits, temperature)
+        ctx.save_for_backward(x, weight, ids, logits, lse)
+        ctx.temperature = temperature
+        return loss
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dloss):
+        dx, dw = ops.linear_distillation_backward(dloss.contiguous(), *ctx.saved_tensors,
+                                                  ctx.temperature)
+        return dx, dw, None, None, None
+
+
 class _Embedding(Function):
     @staticmethod
     def forward(ctx, ids, weight, scale, padding_idx):
@@ -187,6 +204,26 @@ def linear_cross_entropy(x, weight, target, ignore_index: int = -100,
     if reduction == "sum":
         return loss.sum()
     return loss.sum() / (target != ignore_index).sum().clamp(min=1)
+
+
+def linear_distillation(x, weight, ids, logits, temperature: float = 1.0,
+                        reduction: str = "mean"):
+    """Divergence of x weight^T from a teacher's top logits (``ops.linear_distillation``).
+    x: (..., dim), ids and logits: (..., k); no gradient for the logits.  reduction:
+    "none" (one loss per token), "sum", or "mean" over the tokens that have an id
+    (0 when none has).  Soft targets' usual factor temperature ** 2 is the caller's."""
+    if reduction not in ("none", "sum", "mean"):
+        raise ValueError(f"reduction must be 'none', 'sum' or 'mean', not {reduction!r}")
+    x, weight = _autocast(x, weight)
+    k = ids.shape[-1]
+    loss = _LinearDistillation.apply(x.contiguous().view(-1, x.shape[-1]), weight,
+                                     ids.contiguous().view(-1, k), logits.contiguous().view(-1, k),
+                                     temperature)
+    if reduction == "none":
+        return loss.view(ids.shape[:-1])
+    if reduction == "sum":
+        return loss.sum()
+    return loss.sum() / (ids >= 0).any(-1).sum().clamp(min=1)
 
 
 def embedding(ids, weight, scale: float = 1.0, padding_idx=None):

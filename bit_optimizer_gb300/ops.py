@@ -1,7 +1,7 @@
 """The training operators around the optimizer: 8-bit activation checkpoints,
-GELU, layer norm, the cross entropy of a linear layer over a large vocabulary,
-the embedding and the clipped policy loss, forward and backward, as functions of
-CUDA tensors.
+GELU, layer norm, the cross entropy of a linear layer over a large vocabulary and
+its distillation from a teacher, the embedding and the clipped policy loss, forward
+and backward, as functions of CUDA tensors.
 
 Like the rest of the package this is argument checking and marshalling: every
 step runs in the library's kernels (include/fp8opt.h describes the arithmetic).
@@ -38,7 +38,8 @@ from ._lib import BF16, F16, F32
 __all__ = ["act_save", "act_load", "gelu", "gelu_backward", "layer_norm",
            "layer_norm_backward", "linear_cross_entropy",
            "linear_cross_entropy_backward", "embedding", "embedding_backward",
-           "policy_loss", "policy_loss_backward", "ACT_GROUP"]
+           "policy_loss", "policy_loss_backward", "linear_distillation",
+           "linear_distillation_backward", "ACT_GROUP"]
 
 ACT_GROUP = _lib.ACT_GROUP
 _REDUCTIONS = {"token": _lib.MEAN_TOKEN, "sequence": _lib.MEAN_SEQUENCE}
@@ -48,7 +49,8 @@ BINDING_PATH = os.path.join(_lib.HERE, "_build", "fp8opt_binding.so")
 _ENTRIES = ("fp8_act_save", "fp8_act_load", "fp8_gelu", "fp8_gelu_backward",
             "fp8_layer_norm", "fp8_layer_norm_backward", "fp8_linear_xent",
             "fp8_linear_xent_backward", "fp8_embedding", "fp8_embedding_backward",
-            "fp8_policy_loss", "fp8_policy_loss_backward", "fp8opt_last_error")
+            "fp8_policy_loss", "fp8_policy_loss_backward", "fp8_linear_distill",
+            "fp8_linear_distill_backward", "fp8opt_last_error")
 
 
 def _load_binding():
@@ -155,6 +157,27 @@ def linear_cross_entropy_backward(dloss: torch.Tensor, x: torch.Tensor, w: torch
     probabilities of two pieces of the vocabulary, in 16 bits (128 to 256 MiB each;
     for few tokens that is all of them)."""
     return _b.linear_cross_entropy_backward(dloss, x, w, target, lse, ignore_index, stream)
+
+
+def linear_distillation(x: torch.Tensor, w: torch.Tensor, ids: torch.Tensor,
+                        logits: torch.Tensor, temperature: float = 1.0, stream=None):
+    """(loss, lse), both float32, one per token: the divergence sum q (log q - log p)
+    of p = softmax(x w^T / temperature) from q = softmax(logits / temperature), a
+    teacher's top logits (tokens, up to 256) of the words ids (int64, the same shape;
+    negative: not given), and lse = log sum exp(x w^T / temperature).  A token without
+    entries has loss 0; an id outside the vocabulary gives NaN.  x: (tokens, dim), w:
+    (vocabulary, dim), bfloat16 or float16; logits: these or float32.  The student's
+    logits are never in memory."""
+    return _b.linear_distillation(x, w, ids, logits, temperature, stream)
+
+
+def linear_distillation_backward(dloss: torch.Tensor, x: torch.Tensor, w: torch.Tensor,
+                                 ids: torch.Tensor, logits: torch.Tensor, lse: torch.Tensor,
+                                 temperature: float = 1.0, stream=None):
+    """(dx, dw), in x's type, for the gradient dloss (float32, one per token) of
+    ``linear_distillation``'s loss; lse is that call's.  Scratch as
+    ``linear_cross_entropy_backward``'s."""
+    return _b.linear_distillation_backward(dloss, x, w, ids, logits, lse, temperature, stream)
 
 
 # --------------------------------------------------------------- embedding

@@ -718,6 +718,47 @@ FP8OPT_API int fp8_linear_xent_backward(const float *dloss, const void *x,
                                         int64_t ignore_index, void *dx,
                                         void *dw, void *stream);
 
+/* Most entries of a token's teacher. */
+#define FP8OPT_MOST_TEACHER 256
+
+/*
+ * fp8_linear_distill: distillation of the linear layer z = x w^T (as
+ * fp8_linear_xent's, without keeping the logits) from the top logits of a teacher,
+ * k words ids[i, j] (rows x k int64) and their logits (rows x k of type
+ * logit_dtype) for each token:
+ *   q[i] = softmax over the given entries of logits[i] / temperature,
+ *   lse[i] = log sum_v exp(z[i, v] / temperature),
+ *   loss[i] = sum_j q[i, j] (log q[i, j] - z[i, ids[i, j]] / temperature + lse[i]),
+ * the Kullback-Leibler divergence of the student's distribution from the
+ * teacher's.  An entry whose id is negative is not given; one whose logit is -inf
+ * counts nothing; a word given twice counts twice.  A token without an entry that
+ * counts has loss 0; an id that is not below vocab, or a logit that is NaN or
+ * +inf, gives a NaN loss.  loss, lse: rows fp32.
+ *
+ * fp8_linear_distill_backward: given dloss (rows fp32) and the forward pass's lse,
+ *   dz[i, v] = (exp(z[i, v] / temperature - lse[i]) - sum of q[i, j] over the
+ *              entries with ids[i, j] = v) * dloss[i] / temperature,
+ *   dx = dz w,  dw = dz^T x  (of type dtype, both overwritten),
+ * by pieces of the vocabulary and with the treatment of tokens that take no part
+ * as in fp8_linear_xent_backward, whose sizes, scratch and waits hold here too.
+ * Scratch besides: 8 bytes an entry (forward 12), 2 bytes for every 256 words of
+ * each token (forward of at most 65536 tokens at a time), 12 bytes a token.
+ *
+ * k in [1, FP8OPT_MOST_TEACHER]; temperature in [2^-20, 2^20].  No gradient for
+ * the teacher's logits.
+ */
+FP8OPT_API int fp8_linear_distill(const void *x, const void *w,
+                                  const int64_t *ids, const void *logits,
+                                  int64_t rows, int64_t dim, int64_t vocab,
+                                  int k, int dtype, int logit_dtype,
+                                  float temperature, float *loss, float *lse,
+                                  void *stream);
+FP8OPT_API int fp8_linear_distill_backward(
+    const float *dloss, const void *x, const void *w, const int64_t *ids,
+    const void *logits, const float *lse, int64_t rows, int64_t dim,
+    int64_t vocab, int k, int dtype, int logit_dtype, float temperature,
+    void *dx, void *dw, void *stream);
+
 /*
  * fp8_embedding: y[i] = scale * w[ids[i]], one rounding, w vocab x dim and y rows x
  * dim of type dtype, ids rows int64.  An id outside [0, vocab) gives a row of
@@ -798,7 +839,7 @@ FP8OPT_API const char *fp8opt_last_error(void);
  * "layer_norm_backward", "layer_norm_params", "xent_logits", "xent_join",
  * "xent_prepare", "xent_grads", "xent_dx", "embedding", "embedding_order",
  * "embedding_sums", "embedding_join", "policy_loss", "policy_join",
- * "policy_backward"), the launches recorded since enabling and their summed duration in milliseconds.  Returns
+ * "policy_backward", "xent_teacher"), the launches recorded since enabling and their summed duration in milliseconds.  Returns
  * FP8OPT_ERR_ARG for an unknown name or NULL outputs. */
 FP8OPT_API int fp8opt_timing_enable(int on);
 FP8OPT_API int fp8opt_timing_read(const char *kernel, int *launches,

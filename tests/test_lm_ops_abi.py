@@ -1,4 +1,4 @@
-"""The C entry points of the embedding and the policy loss refuse malformed calls
+"""The C entry points of the embedding, the policy loss and distillation refuse malformed calls
 before any CUDA call, and the binding refuses CPU tensors."""
 import math
 
@@ -71,13 +71,40 @@ def test_policy_loss(lib):
     assert grad(batch=0, dl=None, d=None) == grad(length=0, lp=None) == lib.OK
 
 
+def test_distillation(lib):
+    L = lib.load()
+
+    def loss(x=P, w=P, ids=P, logits=P, rows=4, dim=8, vocab=16, k=3, dt=1, ldt=0, t=1.0, out=P,
+             lse=P):
+        return L.fp8_linear_distill(x, w, ids, logits, rows, dim, vocab, k, dt, ldt, t, out, lse,
+                                    None)
+
+    def grad(x=P, w=P, ids=P, logits=P, rows=4, dim=8, vocab=16, k=3, dt=1, ldt=0, t=1.0, out=P,
+             lse=P, dl=P, dw=P):
+        return L.fp8_linear_distill_backward(dl, x, w, ids, logits, lse, rows, dim, vocab, k, dt,
+                                             ldt, t, out, dw, None)
+    for f in (loss, grad):
+        assert f(rows=-1) == f(dim=0) == f(vocab=0) == f(vocab=2 ** 31) == lib.ERR_ARG
+        assert f(k=0) == f(k=-1) == f(k=lib.MOST_TEACHER + 1) == lib.ERR_ARG
+        assert f(dt=0) == f(dt=3) == f(ldt=3) == f(ldt=-1) == lib.ERR_UNSUPPORTED
+        for t in (0.0, -1.0, math.nan, math.inf, 2.0 ** -21, 2.0 ** 21):
+            assert f(t=t) == lib.ERR_ARG and "temperature" in text(lib)
+        assert f(x=None) == f(w=None) == f(ids=None) == f(logits=None) == lib.ERR_ARG
+        assert f(out=None) == f(lse=None) == lib.ERR_ARG and "NULL" in text(lib)
+        assert f(dim=2 ** 30) == lib.ERR_ARG
+    assert grad(dl=None) == grad(dw=None) == lib.ERR_ARG
+    assert grad(rows=2 ** 30) == lib.ERR_ARG
+    assert loss(rows=0, x=None, ids=None, out=None) == lib.OK
+
+
 def test_binding_refuses_cpu_tensors():
     torch = pytest.importorskip("torch")
     import bit_optimizer_gb300 as bo
     ids, x = torch.zeros(4).long(), torch.zeros(4, 8)
     for call in (lambda: bo.embedding(ids, x), lambda: bo.embedding_backward(x, ids, 16),
                  lambda: bo.policy_loss(x, x, x[:, 0]),
-                 lambda: bo.policy_loss_backward(x[0, 0], x, x, x[:, 0], x[:, 0])):
+                 lambda: bo.policy_loss_backward(x[0, 0], x, x, x[:, 0], x[:, 0]),
+                 lambda: bo.linear_distillation(x.half(), x.half(), ids[:, None], x[:, :1])):
         with pytest.raises(TypeError):
             call()
     with pytest.raises(ValueError):
@@ -89,10 +116,10 @@ def test_constants_agree_with_the_header(lib, tmp_path):
     import subprocess
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     src = tmp_path / "c.c"
-    src.write_text('#include <stdio.h>\n#include "fp8opt.h"\nint main(void) { printf("%d %d", '
-                   'FP8OPT_MEAN_TOKEN, FP8OPT_MEAN_SEQUENCE); return 0; }\n')
+    src.write_text('#include <stdio.h>\n#include "fp8opt.h"\nint main(void) { printf("%d %d %d", '
+                   'FP8OPT_MEAN_TOKEN, FP8OPT_MEAN_SEQUENCE, FP8OPT_MOST_TEACHER); return 0; }\n')
     exe = tmp_path / "c"
     subprocess.run(["gcc", "-I", os.path.join(root, "include"), str(src), "-o", str(exe)],
                    check=True)
     got = subprocess.run([str(exe)], capture_output=True, text=True, check=True).stdout
-    assert got.split() == [str(lib.MEAN_TOKEN), str(lib.MEAN_SEQUENCE)]
+    assert got.split() == [str(lib.MEAN_TOKEN), str(lib.MEAN_SEQUENCE), str(lib.MOST_TEACHER)]

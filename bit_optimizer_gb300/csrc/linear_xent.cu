@@ -169,10 +169,15 @@ struct Turn {
 static_assert(sizeof(Turn) == kTurnBytes, "");
 
 // 64 results of each lane's row as 16-bit values, at out + row * pitch; rows
-// below `rows`, columns below `cols`.
-template <bool BF16>
+// below `rows`, columns below `cols`.  mend() may change the lane's own row of
+// `turn` before it is stored.
+struct AsItIs {
+  __device__ __forceinline__ void operator()() const {}
+};
+template <bool BF16, class Mend = AsItIs>
 __device__ __forceinline__ void store_rows16(Turn& turn, uint16_t* out, int64_t pitch, int rows,
-                                             int cols, const float (&v)[64]) {
+                                             int cols, const float (&v)[64],
+                                             const Mend& mend = Mend()) {
   const int lane = threadIdx.x & 31;
 #pragma unroll
   for (int j = 0; j < 8; ++j)
@@ -180,6 +185,7 @@ __device__ __forceinline__ void store_rows16(Turn& turn, uint16_t* out, int64_t 
         make_uint4(pack16<BF16>(v[8 * j], v[8 * j + 1]), pack16<BF16>(v[8 * j + 2], v[8 * j + 3]),
                    pack16<BF16>(v[8 * j + 4], v[8 * j + 5]),
                    pack16<BF16>(v[8 * j + 6], v[8 * j + 7]));
+  mend();
   __syncwarp();
   const int word = lane & 7, c = 8 * word, row0 = lane >> 3;
   uint16_t* p = out + row0 * pitch + c;
@@ -335,17 +341,16 @@ __device__ __forceinline__ void stats_strip(const GemmOut& o, const Strip& t, co
                       ? (int)(target - t.c0) : -1;
   const int valid = (int)min((int64_t)t.cols, o.vocab - t.c0);   // may be <= 0
   Stats s;
+  Entries entries(o.teacher.words + t.row * o.teacher.k, in.entry, in.end, t.c0);
   tmem_columns(t.tmem, t.cols, [&](int c, uint32_t (&r)[32], uint32_t (&q)[32]) {
+    if constexpr (TEACHER)
+      entries.take(c, [&](int j) { return __uint_as_float(j < 32 ? r[j & 31] : q[j & 31]); },
+                   [&](int first, int end, int, float z) {
+                     for (int i = first; i < end; ++i) o.teacher.z[t.row * o.teacher.k + i] = z;
+                   });
     s.add(r, valid - c, TEACHER ? -1 : rel - c, TEACHER ? o.teacher.factor : kLog2eF);
     s.add(q, valid - c - 32, TEACHER ? -1 : rel - c - 32, TEACHER ? o.teacher.factor : kLog2eF);
   });
-  if constexpr (TEACHER) {
-    const int64_t row = t.row * o.teacher.k;
-    each_entry(o.teacher.words + row, in.entry, in.end, t.c0, t.cols, t.tmem,
-               [&](int first, int end, int, float z) {
-                 for (int i = first; i < end; ++i) o.teacher.z[row + i] = z;
-               });
-  }
   if (t.row < o.tokens) {
     o.partial[(int64_t)t.index * o.tokens + t.row] = make_float2(s.top, s.sum);
     if (rel >= 0) o.target_logit[t.row] = s.at_target;
@@ -425,7 +430,7 @@ struct SwappedStats {
 };
 
 // The strip's logits turned into p.  With a teacher, the few columns with an entry
-// are written once more, less its share.
+// are rounded once more, less its share.
 template <bool BF16, bool TEACHER>
 __device__ __forceinline__ void probs_strip(const GemmShape& g, const GemmOut& o,
                                             const Strip& t, const RowIn& in, Turn& turn) {
@@ -445,6 +450,7 @@ __device__ __forceinline__ void probs_strip(const GemmShape& g, const GemmOut& o
   const int64_t row0 = t.row - (threadIdx.x & 31);
   uint16_t* const out = g.probs + row0 * o.piece + t.c0;
   const int rows = (int)min((int64_t)32, o.tokens - row0);
+  Entries entries(o.teacher.words + t.row * o.teacher.k, in.entry, in.end, g.v0 + t.c0);
   tmem_columns(t.tmem, t.cols, [&](int c, uint32_t (&r)[32], uint32_t (&q)[32]) {
     float v[64];
 #pragma unroll
@@ -462,26 +468,27 @@ __device__ __forceinline__ void probs_strip(const GemmShape& g, const GemmOut& o
       for (int j = 0; j < 64; ++j)
         if (rel == c + j) v[j] -= 1.0f;
     }
+    float s[64];
 #pragma unroll
-    for (int j = 0; j < 64; ++j) v[j] = zero ? 0.0f : v[j] * k;
+    for (int j = 0; j < 64; ++j) s[j] = zero ? 0.0f : v[j] * k;
     if (c + 64 > valid) {           // columns past the vocabulary's end are 0
 #pragma unroll
       for (int j = 0; j < 64; ++j)
-        if (c + j >= valid) v[j] = 0.0f;
+        if (c + j >= valid) s[j] = 0.0f;
     }
-    store_rows16<BF16>(turn, out + c, o.piece, rows, 64, v);
+    if constexpr (TEACHER) {
+      const int lane = threadIdx.x & 31;
+      store_rows16<BF16>(turn, out + c, o.piece, rows, 64, s, [&] {
+        entries.take(c, [&](int j) { return v[j]; }, [&](int first, int end, int i, float p) {
+          for (int j = first; j < end; ++j) p -= o.teacher.q[t.row * o.teacher.k + j];
+          reinterpret_cast<uint16_t*>(&turn.at(lane, i >> 3))[i & 7] =
+              (uint16_t)pack16<BF16>(zero ? 0.0f : p * k, 0.0f);
+        });
+      });
+    } else {
+      store_rows16<BF16>(turn, out + c, o.piece, rows, 64, s);
+    }
   });
-  if constexpr (TEACHER) {
-    const Teacher& h = o.teacher;
-    const int64_t row = t.row * h.k;
-    each_entry(h.words + row, in.entry, in.end, g.v0 + t.c0, t.cols, t.tmem,
-               [&](int first, int end, int c, float z) {
-                 float v = exp2_approx((z + shift) * h.factor);
-                 for (int i = first; i < end; ++i) v -= h.q[row + i];
-                 out[(t.row - row0) * o.piece + c] =
-                     (uint16_t)pack16<BF16>(zero ? 0.0f : v * k, 0.0f);
-               });
-  }
 }
 
 // This piece's part of dx, added to the earlier ones'.  `none`: the split has
@@ -1196,6 +1203,14 @@ TeacherScratch teacher_scratch(Layout& l, const XentArgs& a, int64_t tokens, boo
   return s;
 }
 
+template <int DT>
+auto teacher_of(int k) {
+  return k <= 32    ? teacher_kernel<DT, 1>
+         : k <= 64  ? teacher_kernel<DT, 2>
+         : k <= 128 ? teacher_kernel<DT, 4>
+                    : teacher_kernel<DT, 8>;
+}
+
 // Makes the entries of the tokens from t0 on and returns what the other kernels
 // read of them.
 cudaError_t make_teacher(const XentArgs& a, int64_t t0, int64_t tokens, char* scratch,
@@ -1210,9 +1225,9 @@ cudaError_t make_teacher(const XentArgs& a, int64_t t0, int64_t tokens, char* sc
                        t0 * a.k * (a.logit_dtype == kF32 ? 4 : 2);
   if (mark) mark(kXentTeacherK, 0, stream);
   const cudaError_t e =
-      launch(true, a.logit_dtype == kF32    ? teacher_kernel<kF32>
-                   : a.logit_dtype == kBF16 ? teacher_kernel<kBF16>
-                                            : teacher_kernel<kF16>,
+      launch(true, a.logit_dtype == kF32    ? teacher_of<kF32>(a.k)
+                   : a.logit_dtype == kBF16 ? teacher_of<kBF16>(a.k)
+                                            : teacher_of<kF16>(a.k),
              (unsigned)((tokens + kTeacherWarps - 1) / kTeacherWarps), 32 * kTeacherWarps, 0,
              stream, reinterpret_cast<const long long*>(a.ids) + t0 * a.k, (const void*)logits,
              tokens, a.vocab, *t, words, q, start,

@@ -6,8 +6,11 @@
 // the given ones, sorted by word; `start` says where in them each tile of
 // kTeacherTile words begins, so that a thread, whose row is a token, has its
 // tile's entries without a search.  On average a tile meets very few (64 of 50257
-// words: 0.33 of a row's 256), so the epilogues fetch their logits one column of
-// TMEM at a time instead of comparing every column with a list.
+// words: 0.33 of a row's 256), so a column that has one is picked out of the
+// thread's registers by the six bits of its place among 64 (63 selections for a
+// warp's 32 rows), instead of each column being compared with a list.  Read from
+// TMEM a column at a time, with the entries' loads behind one another, they cost
+// the gradients of 2048 x 768 x 50257 with 128 entries 90 us.
 #pragma once
 
 #include "ops_internal.cuh"
@@ -31,49 +34,51 @@ struct Teacher {
   float factor;              // log2(e) / temperature
 };
 
-// Entry `at` of a token's up to `end` as a column from c0 on (its word is not
-// below); kNoColumn behind the end.
+// A row's entries in the columns of a strip, in order.
 constexpr uint32_t kNoColumn = 0xFFFFFFFFu;
-__device__ __forceinline__ uint32_t column_of(const uint32_t* words, int at, int end, int64_t c0) {
-  return at < end ? (uint32_t)(words[at] - c0) : kNoColumn;
-}
-
-// One column of the warp's lanes.
-__device__ __forceinline__ float tmem_column(uint32_t addr) {
-  uint32_t r;
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];\n\t"
-      "tcgen05.wait::ld.sync.aligned;"
-      : "=r"(r)
-      : "r"(addr)
-      : "memory");
-  return __uint_as_float(r);
-}
-
-// Calls f(first entry, entry behind the last, column, logit) for every word of the
-// lane's token among the `cols` columns at `tmem`, which are the words from c0 on.
-// The whole warp calls it; each column with an entry is read once.
-template <class F>
-__device__ __forceinline__ void each_entry(const uint32_t* words, int at, int end, int64_t c0,
-                                           int cols, uint32_t tmem, F f) {
-  while (at < end && (int64_t)words[at] < c0) ++at;      // (of the tile's other half)
-  uint32_t column = column_of(words, at, end, c0);
-  for (;;) {
-    const uint32_t next = __reduce_min_sync(0xFFFFFFFFu, column);
-    if (next >= (uint32_t)cols) break;
-    const float z = tmem_column(tmem + next);
-    if (column == next) {
-      const int first = at;
-      do column = column_of(words, ++at, end, c0);
-      while (column == next);
-      f(first, at, (int)next, z);
-    }
-    __syncwarp();
+struct Entries {
+  const uint32_t* words;     // the token's
+  int at, end;
+  int64_t c0;                // the strip's first word
+  uint32_t column;           // of entry `at`, from c0 on; kNoColumn behind the last
+  __device__ __forceinline__ void find() {
+    column = at < end ? (uint32_t)(words[at] - c0) : kNoColumn;
   }
-}
+  __device__ __forceinline__ Entries(const uint32_t* w, int first, int last, int64_t c)
+      : words(w), at(first), end(last), c0(c) {
+    while (at < end && (int64_t)words[at] < c0) ++at;    // (of the tile's other half)
+    find();
+  }
+  // Calls f(first entry, entry behind the last, column - c, value) for each of the
+  // row's words among the columns [c, c + 64), whose values are get(0 .. 63).  The
+  // whole warp calls it, from left to right.
+  template <class G, class F>
+  __device__ __forceinline__ void take(uint32_t c, G get, F f) {
+    while (__any_sync(0xFFFFFFFFu, column - c < 64u)) {
+      const bool mine = column - c < 64u;
+      const uint32_t i = mine ? column - c : 0;
+      float v[32];
+#pragma unroll
+      for (int j = 0; j < 32; ++j) v[j] = i & 1 ? get(2 * j + 1) : get(2 * j);
+#pragma unroll
+      for (int bit = 1; bit < 6; ++bit) {
+#pragma unroll
+        for (int j = 0; j < 32 >> bit; ++j) v[j] = i >> bit & 1 ? v[2 * j + 1] : v[2 * j];
+      }
+      if (mine) {
+        const int first = at;
+        do {
+          ++at;
+          find();
+        } while (column - c == i);
+        f(first, at, (int)i, v[0]);
+      }
+    }
+  }
+};
 
-// Most entries of a token, and a CTA's warps, a token each.
-constexpr int kTeacherMost = 256, kTeacherWarps = 8;
+// A CTA's warps, a token each.
+constexpr int kTeacherWarps = 8;
 
 template <int DT>
 __device__ __forceinline__ float teacher_logit(const void* p, int64_t i) {
@@ -82,84 +87,104 @@ __device__ __forceinline__ float teacher_logit(const void* p, int64_t i) {
   return DT == kBF16 ? __uint_as_float(h << 16) : h2_to_f2(h).x;
 }
 
-// The entries of `tokens` tokens from their ids and logits.  Entries whose id is
-// negative are not given, and those whose share is 0 (of a logit of -inf) left
-// out.  Backward, dloss is divided by the temperature.
-template <int DT>
+// The entries of `tokens` tokens from their ids and logits, a warp to a token and
+// E of them to a lane.  Entries whose id is negative are not given, and those whose
+// share is 0 (of a logit of -inf) left out.  Backward, dloss is divided by the
+// temperature.
+template <int DT, int E>
 __global__ void __launch_bounds__(32 * kTeacherWarps)
 teacher_kernel(const long long* ids, const void* logits, int64_t tokens, int64_t vocab,
                const Teacher t, uint32_t* __restrict__ words, float* __restrict__ q,
                uint16_t* __restrict__ start, long long* __restrict__ state, const float* dloss,
                float* __restrict__ dloss_out) {
-  __shared__ uint32_t sh_id[kTeacherWarps][kTeacherMost], sh_word[kTeacherWarps][kTeacherMost];
-  __shared__ float sh_q[kTeacherWarps][kTeacherMost];
+  __shared__ uint4 sh_id[kTeacherWarps][8 * E];
+  __shared__ uint32_t sh_word[kTeacherWarps][32 * E];
   begin_after_previous();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t token = (int64_t)blockIdx.x * kTeacherWarps + warp;
   if (token >= tokens) return;
-  uint32_t* const id = sh_id[warp];
   uint32_t* const word = sh_word[warp];
-  float* const share = sh_q[warp];
   constexpr uint32_t kOut = 0x7FFFFFFFu;    // behind every word
   const float none = __uint_as_float(0xFF800000u);
+  uint32_t id[E];
+  float share[E], top = none;
   bool wrong = false;
-  float top = none;
-  for (int j = lane; j < t.k; j += 32) {
-    const long long i = ids[token * t.k + j];
-    const float l = teacher_logit<DT>(logits, token * t.k + j);
-    wrong |= i >= vocab;
-    id[j] = i >= 0 && i < vocab ? (uint32_t)i : kOut;
-    share[j] = id[j] != kOut ? l : none;
-    top = fmaxf(top, share[j]);
-    wrong |= share[j] != share[j];
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    const int j = lane + 32 * e;
+    const long long i = j < t.k ? ids[token * t.k + j] : -1;
+    const float l = j < t.k ? teacher_logit<DT>(logits, token * t.k + j) : none;
+    wrong |= i >= vocab || (i >= 0 && l != l);
+    id[e] = i >= 0 && i < vocab ? (uint32_t)i : kOut;
+    share[e] = id[e] != kOut ? l : none;
   }
+#pragma unroll
+  for (int e = 0; e < E; ++e) top = fmaxf(top, share[e]);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
   wrong = __any_sync(0xFFFFFFFFu, wrong || top == -none);
   const bool dead = !wrong && top == none;
-  __syncwarp();
   float sum = 0.0f;
-  if (!wrong && !dead) {
-    for (int j = lane; j < t.k; j += 32) {
-      share[j] = expf((share[j] - top) / t.temperature);
-      sum += share[j];
-    }
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    share[e] = dead ? 0.0f : expf((share[e] - top) / t.temperature);
+    sum += share[e];
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
   int count = 0;
-  if (!wrong && !dead) {
-    for (int j = lane; j < t.k; j += 32) {
-      share[j] = __fdiv_rn(share[j], sum);
-      if (share[j] == 0.0f) id[j] = kOut;
-      count += id[j] != kOut;
-    }
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    share[e] = __fdiv_rn(share[e], sum);
+    if (wrong || dead || share[e] == 0.0f) id[e] = kOut;
+    count += id[e] != kOut;
+    reinterpret_cast<uint32_t*>(sh_id[warp])[lane + 32 * e] = id[e];
   }
   count = __reduce_add_sync(0xFFFFFFFFu, count);
   __syncwarp();
   // an entry's place: the smaller words, and equal ones before it
-  if (count > 0) {
-    for (int j = lane; j < t.k; j += 32) {
-      const uint32_t mine = id[j];
-      if (mine == kOut) continue;
-      int at = 0;
+  int at[E] = {};
+#pragma unroll
+  for (int b = 0; b < E; ++b) {
 #pragma unroll 4
-      for (int i = 0; i < t.k; ++i) at += id[i] < mine + (i < j);
-      word[at] = mine;
-      words[token * t.k + at] = mine;
-      q[token * t.k + at] = share[j];
+    for (int i = 0; i < 8; ++i) {
+      const uint4 w = sh_id[warp][8 * b + i];
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        if (b == e) {
+          const int to = lane - 4 * i;      // equal ones count while they are before lane
+          at[e] += (w.x < id[e] + (0 < to)) + (w.y < id[e] + (1 < to)) +
+                   (w.z < id[e] + (2 < to)) + (w.w < id[e] + (3 < to));
+        } else {
+          const uint32_t limit = id[e] + (b < e ? 1 : 0);
+          at[e] += (w.x < limit) + (w.y < limit) + (w.z < limit) + (w.w < limit);
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    if (id[e] != kOut) {
+      word[at[e]] = id[e];
+      words[token * t.k + at[e]] = id[e];
+      q[token * t.k + at[e]] = share[e];
     }
   }
   __syncwarp();
-  for (int64_t tile = lane; tile <= t.tiles; tile += 32) {
-    const int64_t first = tile * kTeacherTile;
-    int lo = 0, hi = count;                 // the first entry of a word >= first
-    while (lo < hi) {
-      const int mid = (lo + hi) / 2;
-      if ((int64_t)word[mid] < first) lo = mid + 1;
-      else hi = mid;
+  // the number of words below each tile's first one, four tiles of a lane at a time
+  const int highest = count > 0 ? 1 << (31 - __clz(count)) : 0;
+  for (int64_t t0 = lane; t0 <= t.tiles; t0 += 4 * 32) {
+    int n[4] = {};
+    for (int step = highest; step > 0; step >>= 1) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (n[k] + step <= count && (int64_t)word[n[k] + step - 1] < (t0 + 32 * k) * kTeacherTile)
+          n[k] += step;
     }
-    start[token * (t.tiles + 1) + tile] = (uint16_t)lo;
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (t0 + 32 * k <= t.tiles)
+        start[token * (t.tiles + 1) + t0 + 32 * k] = (uint16_t)n[k];
   }
   if (lane == 0) {
     state[token] = wrong ? (long long)vocab : dead ? kTeacherNone : kTeacherLive;

@@ -211,8 +211,10 @@ embedding_rank_kernel(const long long* ids, int n, uint32_t vocab, long long pad
   }
 }
 
-// More tokens: a stable sort by eight bits of the key, in tiles of a CTA each (a
-// multiple of kSortStep tokens).  First the tiles' counts of each digit ...
+// More tokens: a stable sort by eight bits of the key a pass, in tiles of a CTA
+// each (a multiple of kSortStep tokens).  First the tiles' counts of each digit,
+// for the first pass; every pass then counts the next one's, where its tokens go
+// to (whole numbers: the order of the atomics does not matter).
 constexpr int kSortThreads = 1024, kSortWarps = kSortThreads / 32, kDigits = 256;
 constexpr int kRounds = 2, kSortStep = kRounds * kSortThreads;
 
@@ -225,6 +227,7 @@ struct SortPass {
   uint32_t vocab;
   long long padding;
   uint32_t* counts;          // [tile][digit]
+  uint32_t* next;            // the next pass's; NULL in the last one
   uint32_t* keys_out;
   uint32_t* tokens_out;
   __device__ __forceinline__ uint32_t key(int64_t i) const {
@@ -232,29 +235,35 @@ struct SortPass {
   }
 };
 
+// later: the counts of the `rest` later passes, set to zero.
 __global__ void __launch_bounds__(kSortThreads)
-embedding_count_kernel(SortPass s, Fill fill) {
+embedding_count_kernel(SortPass s, uint32_t* later, int rest, Fill fill) {
   __shared__ uint32_t count[kDigits];
   begin_after_previous();
   if ((int)blockIdx.x >= s.tiles) {
     fill_zeros(fill, blockIdx.x - s.tiles, gridDim.x - s.tiles);
     return;
   }
-  if (threadIdx.x < kDigits) count[threadIdx.x] = 0;
+  const int t = threadIdx.x;
+  if (t < kDigits) count[t] = 0;
   __syncthreads();
   const int64_t lo = blockIdx.x * s.tile, hi = min(lo + s.tile, s.n);
-  for (int64_t i = lo + threadIdx.x; i < hi; i += kSortThreads)
+#pragma unroll 2
+  for (int64_t i = lo + t; i < hi; i += kSortThreads)
     atomicAdd(&count[s.key(i) >> s.shift & (kDigits - 1)], 1u);
+  for (int p = 0; p < rest; ++p)
+    if (t < kDigits) later[((int64_t)p * s.tiles + blockIdx.x) * kDigits + t] = 0;
   __syncthreads();
-  if (threadIdx.x < kDigits)
-    s.counts[(int64_t)blockIdx.x * kDigits + threadIdx.x] = count[threadIdx.x];
+  if (t < kDigits) s.counts[(int64_t)blockIdx.x * kDigits + t] = count[t];
 }
 
-// ... then every token to its place: those of smaller digits, of its digit in
-// earlier tiles, in its tile's earlier warps and in its own warp come before it.
+// Every token to its place: those of smaller digits, of its digit in earlier
+// tiles, in its tile's earlier warps and in its own warp come before it.
 __global__ void __launch_bounds__(kSortThreads)
 embedding_place_kernel(SortPass s, Fill fill) {
+  constexpr int kGroups = kSortThreads / kDigits;
   __shared__ uint32_t base[kDigits], sums[kDigits / 32];
+  __shared__ uint32_t of_group[kGroups][2][kDigits];
   __shared__ uint32_t before[kSortWarps][kDigits];   // a warp's tokens, then where they start
   begin_after_previous();
   if ((int)blockIdx.x >= s.tiles) {
@@ -262,13 +271,39 @@ embedding_place_kernel(SortPass s, Fill fill) {
     return;
   }
   const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
-  if (t < kDigits) {
+  const int64_t lo = blockIdx.x * s.tile, hi = min(lo + s.tile, s.n);
+  // a warp's kRounds x 32 consecutive tokens
+  uint32_t key[kRounds], token[kRounds];
+  const auto read = [&](int64_t step) {
+#pragma unroll
+    for (int r = 0; r < kRounds; ++r) {
+      const int64_t i = step + warp * (kRounds * 32) + lane + 32 * r;
+      key[r] = i < hi ? s.key(i) : 0;
+      token[r] = i < hi && s.ids == nullptr ? s.tokens[i] : (uint32_t)i;
+    }
+  };
+  read(lo);
+  // of each digit, all tokens and those in earlier tiles; a quarter of the tiles to
+  // a group of threads
+  {
+    const int group = t / kDigits, d = t % kDigits;
     uint32_t all = 0, mine = 0;
 #pragma unroll 8
-    for (int k = 0; k < s.tiles; ++k) {
-      const uint32_t c = s.counts[(int64_t)k * kDigits + t];
+    for (int k = group; k < s.tiles; k += kGroups) {
+      const uint32_t c = s.counts[(int64_t)k * kDigits + d];
       all += c;
       mine += k < (int)blockIdx.x ? c : 0;
+    }
+    of_group[group][0][d] = all;
+    of_group[group][1][d] = mine;
+  }
+  __syncthreads();
+  if (t < kDigits) {
+    uint32_t all = 0, mine = 0;
+#pragma unroll
+    for (int g = 0; g < kGroups; ++g) {
+      all += of_group[g][0][t];
+      mine += of_group[g][1][t];
     }
     uint32_t up = all;     // of the digits up to this one, first within the warp
 #pragma unroll
@@ -282,17 +317,14 @@ embedding_place_kernel(SortPass s, Fill fill) {
   __syncthreads();
   if (t < kDigits)
     for (int w = 0; w < warp; ++w) base[t] += sums[w];
-  const int64_t lo = blockIdx.x * s.tile, hi = min(lo + s.tile, s.n);
   for (int64_t step = lo; step < hi; step += kSortStep) {
     for (int i = t; i < kSortWarps * kDigits; i += kSortThreads) (&before[0][0])[i] = 0;
     __syncthreads();
-    // a warp's kRounds x 32 consecutive tokens, in order
-    uint32_t key[kRounds], rank[kRounds];
+    uint32_t rank[kRounds];
     const int64_t i0 = step + warp * (kRounds * 32) + lane;
 #pragma unroll
     for (int r = 0; r < kRounds; ++r) {
       const bool in = i0 + 32 * r < hi;
-      key[r] = in ? s.key(i0 + 32 * r) : 0;
       const int digit = in ? (int)(key[r] >> s.shift & (kDigits - 1)) : kDigits;
       const unsigned same = __match_any_sync(0xFFFFFFFFu, digit);
       const unsigned earlier = same & ((1u << lane) - 1);
@@ -315,13 +347,17 @@ embedding_place_kernel(SortPass s, Fill fill) {
     __syncthreads();
 #pragma unroll
     for (int r = 0; r < kRounds; ++r) {
-      const int64_t i = i0 + 32 * r;
-      if (i < hi) {
+      const bool in = i0 + 32 * r < hi;
+      if (in) {
         const uint32_t at = before[warp][key[r] >> s.shift & (kDigits - 1)] + rank[r];
         s.keys_out[at] = key[r];
-        s.tokens_out[at] = s.ids != nullptr ? (uint32_t)i : s.tokens[i];
+        s.tokens_out[at] = token[r];
+        if (s.next != nullptr)
+          atomicAdd(&s.next[(int64_t)(at / (uint32_t)s.tile) * kDigits + (key[r] >> (s.shift + 8) & (kDigits - 1))],
+                    1u);
       }
     }
+    if (step + kSortStep < hi) read(step + kSortStep);
     __syncthreads();
   }
 }
@@ -571,7 +607,7 @@ Scratch backward_scratch(const EmbeddingArgs& a, int sms) {
     s.tile = blocks(blocks(a.rows, 2 * sms), kSortStep) * kSortStep;
     s.tiles = (int)blocks(a.rows, s.tile);
     for (int64_t v = a.vocab; v > 0; v >>= 8) ++s.passes;    // (keys go up to vocab)
-    s.counts = take((int64_t)s.tiles * kDigits * 4);
+    s.counts = take((int64_t)s.passes * s.tiles * kDigits * 4);
   }
   s.parts = take(blocks(a.rows, chunk_of(a, sms)) * 2 * a.dim * 4);
   return s;
@@ -618,23 +654,28 @@ cudaError_t backward(const EmbeddingArgs& a, char* scratch, int sms, cudaStream_
     s.tiles = l.tiles;
     s.vocab = (uint32_t)a.vocab;
     s.padding = a.padding;
+    s.ids = ids;
     s.counts = at(l.counts);
-    fill.parts = 2 * l.passes;
+    // two CTAs an SM, those that sort first
+    const int ctas = std::max(2 * sms, l.tiles + sms);
+    const int64_t pass = (int64_t)l.tiles * kDigits;
+    fill.parts = l.passes + 1;
+    e = launch(true, embedding_count_kernel, ctas, kSortThreads, 0, stream, s, s.counts + pass,
+               l.passes - 1, fill);
     for (int p = 0; e == cudaSuccess && p < l.passes; ++p) {
-      s.ids = p == 0 ? ids : nullptr;
       s.keys = at(l.keys[last]);
       s.tokens = at(l.tokens[last]);
-      if (p > 0) last ^= 1;
+      if (p > 0) {
+        s.ids = nullptr;
+        s.counts += pass;
+        s.shift += 8;
+        last ^= 1;
+      }
+      s.next = p + 1 < l.passes ? s.counts + pass : nullptr;
       s.keys_out = at(l.keys[last]);
       s.tokens_out = at(l.tokens[last]);
-      s.shift = 8 * p;
-      fill.part = 2 * p;
-      e = launch(true, embedding_count_kernel, l.tiles + fillers / 2, kSortThreads, 0, stream, s,
-                 fill);
-      fill.part = 2 * p + 1;
-      if (e == cudaSuccess)
-        e = launch(true, embedding_place_kernel, l.tiles + fillers / 2, kSortThreads, 0, stream,
-                   s, fill);
+      fill.part = p + 1;
+      e = launch(true, embedding_place_kernel, ctas, kSortThreads, 0, stream, s, fill);
     }
   }
   if (mark) mark(kEmbeddingOrderK, 1, stream);

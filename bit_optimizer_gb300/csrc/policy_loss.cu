@@ -40,8 +40,9 @@ struct Policy {
   const float* advantage;
   const uint8_t* mask;
   const float* ref_logp;
-  int64_t length, pieces, units;  // a unit: a piece of a sequence
-  int piece;
+  int64_t length, pieces, units;  // a unit: a piece of a sequence ...
+  int piece;                      // ... of so many tokens, of a warp, or (`wide`) of
+  bool wide;                      // each of a CTA's warps
   bool per_token;
   Border low, high;
   float kl_coef;
@@ -79,15 +80,14 @@ __device__ __forceinline__ Token token_of(const Policy& p, float logp, float old
 
 __device__ __forceinline__ bool counts(uint32_t m, int k) { return (m >> (8 * k) & 0xFFu) != 0; }
 
-// Calls f(first token, values, mask) for the lane's tokens of a unit; VEC: four at
-// a time, in 16-byte words.  Values of tokens that do not count are not read
-// where all of a call's do not.
+// Calls f(first token, values, mask) for the lane's tokens of a piece of sequence b,
+// from t0 on; VEC: four at a time, in 16-byte words.  Values of tokens that do not
+// count are not read where all of a call's do not.
 template <bool VEC, class F>
-__device__ __forceinline__ void each_token(const Policy& p, int64_t unit, F f) {
+__device__ __forceinline__ void each_token(const Policy& p, int64_t b, int64_t t0, F f) {
   const int lane = threadIdx.x & 31;
-  const int64_t b = unit / p.pieces, t0 = (unit - b * p.pieces) * p.piece;
   const int64_t base = b * p.length + t0;
-  const int n = (int)min((int64_t)p.piece, p.length - t0);
+  const int n = (int)min((int64_t)p.piece, p.length - t0);    // (may be below 0)
   const float a_all = p.per_token ? 0.0f : p.advantage[b];
   constexpr int N = VEC ? 4 : 1;
 #pragma unroll(VEC ? 2 : 4)
@@ -179,11 +179,11 @@ __device__ __forceinline__ Part reduce(Part p, int width) {
 }
 
 template <bool VEC>
-__device__ __forceinline__ Part part_of(const Policy& p, int64_t unit) {
+__device__ __forceinline__ Part part_of(const Policy& p, int64_t b, int64_t t0) {
   constexpr int N = VEC ? 4 : 1;
   float policy = 0.0f, kl = 0.0f;
   int clipped = 0, count = 0;
-  each_token<VEC>(p, unit, [&](int64_t, const float (&lp)[N], const float (&old)[N],
+  each_token<VEC>(p, b, t0, [&](int64_t, const float (&lp)[N], const float (&old)[N],
                                const float (&ref)[N], const float (&a)[N], uint32_t m) {
     if (m == 0) return;
 #pragma unroll
@@ -276,11 +276,20 @@ static_assert(kJoinThreads / 32 == 32, "a lane to each warp's total");
 template <bool VEC>
 __global__ void __launch_bounds__(kCtaThreads)
 policy_kernel(const Policy p, Part* parts) {
+  __shared__ Part sh[kCtaWarps];
   begin_after_previous();
-  const int64_t unit = (int64_t)blockIdx.x * kCtaWarps + (threadIdx.x >> 5);
-  if (unit >= p.units) return;
-  const Part r = part_of<VEC>(p, unit);
-  if ((threadIdx.x & 31) == 0) parts[unit] = r;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t unit = p.wide ? (int64_t)blockIdx.x : (int64_t)blockIdx.x * kCtaWarps + warp;
+  if (unit >= p.units) return;       // (all of a wide CTA's warps, or none)
+  const int64_t b = unit / p.pieces, i = unit - b * p.pieces;
+  Part r = part_of<VEC>(p, b, (p.wide ? i * kCtaWarps + warp : i) * p.piece);
+  if (p.wide) {
+    if (lane == 0) sh[warp] = r;
+    __syncthreads();
+    if (warp > 0) return;
+    r = reduce(sh[lane % kCtaWarps], kCtaWarps);
+  }
+  if (lane == 0) parts[unit] = r;
 }
 
 __global__ void __launch_bounds__(kJoinThreads)
@@ -301,7 +310,10 @@ policy_cluster_kernel(const Policy p, int64_t batch, bool by_sequence, float kl_
   asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
   const int unit = (threadIdx.x >> 5) * kClusterCtas + (int)blockIdx.x;
   Part r = {};
-  if (unit < p.units) r = part_of<VEC>(p, unit);
+  if (unit < p.units) {
+    const int64_t b = unit / p.pieces;
+    r = part_of<VEC>(p, b, (unit - b * p.pieces) * p.piece);
+  }
   __syncwarp();
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
   if (unit < p.units && (threadIdx.x & 31) == 0) {
@@ -324,8 +336,9 @@ policy_backward_kernel(const Policy p, const float* dloss, const float* weight, 
   const int64_t unit = (int64_t)blockIdx.x * kCtaWarps + (threadIdx.x >> 5);
   if (unit >= p.units) return;
   constexpr int N = VEC ? 4 : 1;
-  const float g = *dloss * weight[unit / p.pieces];
-  each_token<VEC>(p, unit, [&](int64_t at, const float (&lp)[N], const float (&old)[N],
+  const int64_t b = unit / p.pieces;
+  const float g = *dloss * weight[b];
+  each_token<VEC>(p, b, (unit - b * p.pieces) * p.piece, [&](int64_t at, const float (&lp)[N], const float (&old)[N],
                                const float (&ref)[N], const float (&a)[N], uint32_t m) {
     float d[N];
 #pragma unroll
@@ -354,9 +367,9 @@ Border border(double x) {
   return b;
 }
 
-// In pieces as small as they can be with at most `most` units (a warp's latency
+// In pieces as small as they can be with at most `most` warps (a warp's latency
 // goes with its piece).
-Policy policy_of(const PolicyArgs& a, int64_t most) {
+Policy policy_of(const PolicyArgs& a, int64_t most, bool wide = false) {
   Policy p = {};
   p.logp = a.logp;
   p.old_logp = a.old_logp;
@@ -364,10 +377,12 @@ Policy policy_of(const PolicyArgs& a, int64_t most) {
   p.mask = a.mask;
   p.ref_logp = a.ref_logp;
   p.length = a.length;
+  p.wide = wide;
+  const int64_t warps = wide ? kCtaWarps : 1;
   for (p.piece = kLeastPiece;; p.piece *= 2) {
-    p.pieces = (a.length + p.piece - 1) / p.piece;
+    p.pieces = (a.length + warps * p.piece - 1) / (warps * p.piece);
     p.units = a.batch * p.pieces;
-    if (p.units <= most || p.piece == kMostPiece) break;
+    if (p.units * warps <= most || p.piece == kMostPiece) break;
   }
   p.per_token = a.per_token;
   p.low = border(-a.clip_low);
@@ -385,17 +400,21 @@ bool vectors_ok(const PolicyArgs& a) {
   return a.length % 4 == 0 && (all & 15u) == 0 && (reinterpret_cast<uintptr_t>(a.mask) & 3u) == 0;
 }
 
-unsigned ctas(const Policy& p) { return (unsigned)((p.units + kCtaWarps - 1) / kCtaWarps); }
+unsigned ctas(const Policy& p) {
+  return (unsigned)(p.wide ? p.units : (p.units + kCtaWarps - 1) / kCtaWarps);
+}
 
-// Forward: a cluster's units, of at most 256 tokens; else some for every SM, that
-// the joining CTA still takes a few to a thread of.
-constexpr int64_t kForwardUnits = 4096, kBackwardUnits = 16384;
-constexpr int kClusterPiece = 256;
+// Forward: a cluster's units, of at most 256 tokens; else as many warps as are
+// resident (some 64 an SM, in one or two rounds), a CTA's joined at once where a
+// sequence is long enough for one: the CTA that joins the rest takes its time for
+// each of them.
+constexpr int64_t kWarps = 16384;
+constexpr int kClusterPiece = 256, kWideLength = 512;
 
 Policy forward_policy(const PolicyArgs& a, bool* cluster) {
   const Policy p = policy_of(a, kClusterUnits);
   *cluster = p.units <= kClusterUnits && p.piece <= kClusterPiece;
-  return *cluster ? p : policy_of(a, kForwardUnits);
+  return *cluster ? p : policy_of(a, kWarps, a.length > kWideLength);
 }
 
 }  // namespace
@@ -434,7 +453,7 @@ cudaError_t launch_policy(const PolicyArgs& a, char* scratch, cudaStream_t strea
 }
 
 cudaError_t launch_policy_backward(const PolicyArgs& a, cudaStream_t stream, LaunchMark mark) {
-  const Policy p = policy_of(a, kBackwardUnits);
+  const Policy p = policy_of(a, kWarps);
   if (mark) mark(kPolicyBackwardK, 0, stream);
   const cudaError_t e =
       launch(worth_early(a.batch * a.length),

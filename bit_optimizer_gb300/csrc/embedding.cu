@@ -3,16 +3,18 @@
 //
 // forward   Bound by memory: every thread has four 16-byte vectors of the
 //           result under way, each an id, its row's vector and a store.
-// backward  Three steps, each sum in the tokens' order, without float atomics:
-//           order   The tokens sorted by word, stably, while other CTAs fill dw
-//                   with zeros (which takes as long).  Few tokens: each finds its
-//                   place by comparing its key with all others, in one launch.
-//                   More: a radix sort of eight bits a pass.
-//           sums    A warp takes 32 consecutive tokens of the order and the
+// backward  Each sum is in the tokens' order, without float atomics.  Up to
+//           kFewTokens in one launch; else in three steps:
+//           order   The tokens sorted by word, stably.  Up to kRankTokens each
+//                   finds its place by comparing its key with all others; more, a
+//                   radix sort of eight bits a pass, while other CTAs fill dw with
+//                   zeros (which takes as long).
+//           sums    A warp takes 8 to 32 consecutive tokens of the order and the
 //                   columns that its lanes' 16-byte vectors cover, and adds rows
 //                   of one word in fp32.  A word whose tokens lie within the
 //                   chunk is written at once, a part of a word that goes on
-//                   beyond it to scratch.
+//                   beyond it to scratch.  After the short sort, other warps fill
+//                   the rows of words without tokens.
 //           join    The parts of such words, in order.
 // A frequent word's tokens are thereby spread over as many warps as any others.
 #include "ops_internal.cuh"
@@ -164,25 +166,24 @@ __device__ __forceinline__ void fill_zeros(const Fill& f, int64_t cta, int64_t c
   }
 }
 
-// Few tokens: the place of each is the number of smaller keys, and of equal ones
+// Some tokens: the place of each is the number of smaller keys, and of equal ones
 // before it.  A CTA places 32 tokens, its warps comparing them with a share of all
-// keys each; the CTAs from `sorters` on fill.
+// keys each.
 constexpr int64_t kRankTokens = 8192;
 
 __global__ void __launch_bounds__(kCtaThreads)
-embedding_rank_kernel(const long long* ids, int n, uint32_t vocab, long long padding, int sorters,
-                      uint32_t* __restrict__ keys, uint32_t* __restrict__ tokens, Fill fill) {
+embedding_rank_kernel(const long long* ids, int n, uint32_t vocab, long long padding,
+                      uint32_t* __restrict__ keys, uint32_t* __restrict__ tokens) {
   extern __shared__ uint4 all4[];
   __shared__ int smaller[kCtaWarps][32];
   begin_after_previous();
-  if ((int)blockIdx.x >= sorters) {
-    fill_zeros(fill, blockIdx.x - sorters, gridDim.x - sorters);
-    return;
-  }
   uint32_t* const all = reinterpret_cast<uint32_t*>(all4);
   const int share = ((n + kCtaWarps - 1) / kCtaWarps + 31) / 32 * 32;     // of a warp
-  for (int i = threadIdx.x; i < share * kCtaWarps; i += kCtaThreads)
-    all[i] = i < n ? key_of(ids[i], vocab, padding) : 0xFFFFFFFFu;
+#pragma unroll 8
+  for (int i = threadIdx.x; i < share * kCtaWarps; i += kCtaThreads) {
+    const long long id = ids[min(i, n - 1)];
+    all[i] = i < n ? key_of(id, vocab, padding) : 0xFFFFFFFFu;
+  }
   __syncthreads();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int first = blockIdx.x * 32, i = first + lane;
@@ -352,9 +353,10 @@ embedding_place_kernel(SortPass s, Fill fill) {
         const uint32_t at = before[warp][key[r] >> s.shift & (kDigits - 1)] + rank[r];
         s.keys_out[at] = key[r];
         s.tokens_out[at] = token[r];
-        if (s.next != nullptr)
-          atomicAdd(&s.next[(int64_t)(at / (uint32_t)s.tile) * kDigits + (key[r] >> (s.shift + 8) & (kDigits - 1))],
-                    1u);
+        if (s.next != nullptr) {
+          const uint32_t digit = key[r] >> (s.shift + 8) & (kDigits - 1);
+          atomicAdd(&s.next[(int64_t)(at / (uint32_t)s.tile) * kDigits + digit], 1u);
+        }
       }
     }
     if (step + kSortStep < hi) read(step + kSortStep);
@@ -376,20 +378,124 @@ struct Sums {
   uint32_t vocab;
   int64_t slices;              // of 32 lanes' columns
   int chunk;                   // tokens of a warp
+  int64_t sums;                // warps that add; those behind them fill
+  int group;                   // words of a filling warp; 0: dw is filled already
   const void* dy;
   float scale;
   float* parts;                // [chunk][2][dim]: the first word's, the last word's
   void* dw;
 };
 
-// A lane's columns: VEC, kPer in a row; else every 32nd.
+// A lane's columns of a slice: VEC, kPer in a row; else every 32nd from c on.
+template <int DT, bool VEC>
+struct Columns {
+  static constexpr int E = kPer<DT>, kStep = VEC ? 1 : 32;
+  int64_t c, dim;
+  __device__ __forceinline__ Columns(int64_t slice, int64_t d)
+      : c(slice * (32 * E) + (threadIdx.x & 31) * (VEC ? E : 1)), dim(d) {}
+  // What a row of p has there; anything behind its end, which is not stored.  The
+  // loads do not depend on whether the values count, so that many are under way.
+  struct Raw {
+    uint4 v;
+    float e[VEC ? 1 : E];
+  };
+  __device__ __forceinline__ Raw fetch(const void* p, int64_t row) const {
+    Raw r;
+    if constexpr (VEC) {
+      // (volatile: else the compiler moves each load behind the test of its count)
+      asm volatile("ld.global.cs.v4.u32 {%0, %1, %2, %3}, [%4];"
+                   : "=r"(r.v.x), "=r"(r.v.y), "=r"(r.v.z), "=r"(r.v.w)
+                   : "l"(static_cast<const char*>(p) +
+                         (row * dim + (c < dim ? c : 0)) * (16 / E)));
+    } else {
+#pragma unroll
+      for (int j = 0; j < E; ++j)
+        r.e[j] = load1<DT>(p, row * dim + (c + j * kStep < dim ? c + j * kStep : 0));
+    }
+    return r;
+  }
+  static __device__ __forceinline__ void add(const Raw& r, bool counts, float (&sum)[E]) {
+    float e[E];
+    if constexpr (VEC) {
+      unpack<DT>(r.v, e);
+    } else {
+#pragma unroll
+      for (int j = 0; j < E; ++j) e[j] = r.e[j];
+    }
+#pragma unroll
+    for (int j = 0; j < E; ++j) sum[j] += counts ? e[j] : 0.0f;
+  }
+  __device__ __forceinline__ void store(void* p, int64_t row, const float (&e)[E]) const {
+    if constexpr (VEC) {
+      if (c < dim)
+        *reinterpret_cast<uint4*>(static_cast<char*>(p) + (row * dim + c) * (16 / E)) =
+            pack<DT>(e);
+    } else {
+#pragma unroll
+      for (int j = 0; j < E; ++j)
+        if (c + j * kStep < dim) store1<DT>(p, row * dim + c + j * kStep, e[j]);
+    }
+  }
+};
+
+// Zeros in the rows of the words [v0, v0 + group) that have no token: their place
+// among the keys is searched for, a word to a lane.
+template <int DT, bool VEC>
+__device__ __forceinline__ void fill_absent(const Sums& s, int64_t v0) {
+  const int64_t v = v0 + (threadIdx.x & 31);
+  const bool mine = (threadIdx.x & 31) < s.group && v < (int64_t)s.vocab;
+  int64_t lo = 0, hi = s.n;                  // the first key >= v
+  while (lo < hi) {
+    const int64_t mid = (lo + hi) / 2;
+    if ((int64_t)s.keys[mid] < v) lo = mid + 1;
+    else hi = mid;
+  }
+  unsigned absent = __ballot_sync(0xFFFFFFFFu, mine && (lo == s.n || (int64_t)s.keys[lo] != v));
+  const float zero[kPer<DT>] = {};
+  for (; absent != 0; absent &= absent - 1) {
+    const int64_t row = v0 + __ffs(absent) - 1;
+    for (int64_t slice = 0; slice < s.slices; ++slice)
+      Columns<DT, VEC>(slice, s.dim).store(s.dw, row, zero);
+  }
+}
+
+// Adds `count` <= 32 rows of dy, the lanes' tokens in order, to sum; where `ends`
+// has a token's bit, put(its word) takes the sum, which starts again at 0.
+constexpr int kAhead = 8;      // rows under way
+
+template <int DT, bool VEC, class F>
+__device__ __forceinline__ void add_rows(const Columns<DT, VEC>& columns, const void* dy,
+                                         uint32_t word, uint32_t token, unsigned ends, int count,
+                                         float (&sum)[kPer<DT>], F put) {
+  for (int r = 0; r < count; r += kAhead) {
+    typename Columns<DT, VEC>::Raw raw[kAhead];
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k)     // (lanes without a token hold row 0's number)
+      raw[k] = columns.fetch(dy, __shfl_sync(0xFFFFFFFFu, token, r + k));
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      columns.add(raw[k], r + k < count, sum);
+      const uint32_t w = __shfl_sync(0xFFFFFFFFu, word, r + k);
+      if (ends >> (r + k) & 1u) {
+        put(w);
+#pragma unroll
+        for (int j = 0; j < kPer<DT>; ++j) sum[j] = 0.0f;
+      }
+    }
+  }
+}
+
 template <int DT, bool VEC>
 __global__ void __launch_bounds__(32 * kSumWarps)
 embedding_sums_kernel(const Sums s) {
   begin_after_previous();
-  constexpr int E = kPer<DT>, kAhead = 8;
+  constexpr int E = kPer<DT>;
   const int lane = threadIdx.x & 31;
   const int64_t unit = (int64_t)blockIdx.x * kSumWarps + (threadIdx.x >> 5);
+  if (unit >= s.sums) {
+    if (s.group > 0) fill_absent<DT, VEC>(s, (unit - s.sums) * s.group);
+    return;
+  }
   const int64_t chunk = unit / s.slices, slice = unit - chunk * s.slices;
   const int64_t first = chunk * s.chunk, at = first + lane;
   if (first >= s.n) return;
@@ -408,8 +514,9 @@ embedding_sums_kernel(const Sums s) {
   bool goes_on = before == __shfl_sync(0xFFFFFFFFu, key, 0);   // from the chunk before
   const int count = __popc(live);                              // (those without a part come last)
 
-  const int64_t c0 = slice * (32 * E) + (VEC ? lane * E : lane);
-  constexpr int kStep = VEC ? 1 : 32;
+  const Columns<DT, VEC> columns(slice, s.dim);
+  const int64_t c0 = columns.c;
+  constexpr int kStep = columns.kStep;
   float sum[E];
 #pragma unroll
   for (int j = 0; j < E; ++j) sum[j] = 0.0f;
@@ -422,59 +529,81 @@ embedding_sums_kernel(const Sums s) {
       float e[E];
 #pragma unroll
       for (int j = 0; j < E; ++j) e[j] = sum[j] * s.scale;
-      if constexpr (VEC) {
-        if (c0 < s.dim)
-          *reinterpret_cast<uint4*>(static_cast<char*>(s.dw) +
-                                    ((int64_t)word * s.dim + c0) * (16 / E)) = pack<DT>(e);
-      } else {
-#pragma unroll
-        for (int j = 0; j < E; ++j)
-          if (c0 + j * kStep < s.dim)
-            store1<DT>(s.dw, (int64_t)word * s.dim + c0 + j * kStep, e[j]);
-      }
+      columns.store(s.dw, word, e);
     }
-#pragma unroll
-    for (int j = 0; j < E; ++j) sum[j] = 0.0f;
   };
   float* const parts = s.parts + chunk * 2 * s.dim;
-  for (int r = 0; r < count; r += kAhead) {
-    uint4 raw[VEC ? kAhead : 1];
-    float val[VEC ? 1 : kAhead][E];
-#pragma unroll
-    for (int k = 0; k < kAhead; ++k) {
-      const int64_t row = __shfl_sync(0xFFFFFFFFu, token, r + k);
-      if constexpr (VEC) {
-        raw[k] = make_uint4(0, 0, 0, 0);
-        if (r + k < count && c0 < s.dim)
-          raw[k] = __ldcs(reinterpret_cast<const uint4*>(static_cast<const char*>(s.dy) +
-                                                         (row * s.dim + c0) * (16 / E)));
-      } else {
-#pragma unroll
-        for (int j = 0; j < E; ++j)
-          val[k][j] = r + k < count && c0 + j * kStep < s.dim
-                          ? load1<DT>(s.dy, row * s.dim + c0 + j * kStep) : 0.0f;
-      }
-    }
-#pragma unroll
-    for (int k = 0; k < kAhead; ++k) {
-      float e[E];
-      if constexpr (VEC) {
-        unpack<DT>(raw[k], e);
-      } else {
-#pragma unroll
-        for (int j = 0; j < E; ++j) e[j] = val[k][j];
-      }
-#pragma unroll
-      for (int j = 0; j < E; ++j) sum[j] += e[j];
-      const uint32_t word = __shfl_sync(0xFFFFFFFFu, key, r + k);
-      if (ends >> (r + k) & 1u) {
-        put(word, goes_on ? parts : nullptr);
-        goes_on = false;
-      }
-    }
-  }
+  add_rows<DT, VEC>(columns, s.dy, key, token, ends, count, sum, [&](uint32_t word) {
+    put(word, goes_on ? parts : nullptr);
+    goes_on = false;
+  });
   if (!(ends >> (count - 1) & 1u)) put(0, goes_on ? parts : parts + s.dim);
 }
+
+// Few tokens: one launch.  A warp takes `group` words and a slice of the columns,
+// looks for their tokens among all ids, puts them in order and adds their rows, and
+// writes zeros for the words without any.
+constexpr int kFewTokens = 256;
+
+template <int DT, bool VEC>
+__global__ void __launch_bounds__(32 * kSumWarps)
+embedding_few_kernel(const Sums s, const long long* ids, long long padding) {
+  __shared__ uint32_t keys[kFewTokens];
+  // a token's word, from the group's first on, and its number: found, then in order
+  __shared__ uint16_t found[kSumWarps][kFewTokens], ordered[kSumWarps][kFewTokens];
+  begin_after_previous();
+  constexpr int E = kPer<DT>, kBlocks = kFewTokens / 32;
+  const int n = (int)s.n, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  for (int i = threadIdx.x; i < kFewTokens; i += 32 * kSumWarps)
+    keys[i] = i < n ? key_of(ids[i], s.vocab, padding) : s.vocab;
+  __syncthreads();
+  const int64_t unit = (int64_t)blockIdx.x * kSumWarps + warp;
+  const int64_t g = unit / s.slices, v0 = g * s.group;
+  if (v0 >= (int64_t)s.vocab) return;
+  const Columns<DT, VEC> columns(unit - g * s.slices, s.dim);
+  const uint32_t words = (uint32_t)min((int64_t)s.group, (int64_t)s.vocab - v0);
+  int count = 0;
+  unsigned present = 0;
+#pragma unroll
+  for (int j = 0; j < kBlocks; ++j) {
+    const uint32_t word = keys[32 * j + lane] - (uint32_t)v0;
+    const bool mine = word < words;
+    const unsigned here = __ballot_sync(0xFFFFFFFFu, mine);
+    if (mine) {
+      const int at = count + __popc(here & ((1u << lane) - 1));
+      found[warp][at] = (uint16_t)(word << 8 | (32 * j + lane));
+      present |= 1u << word;
+    }
+    count += __popc(here);
+  }
+  present = __reduce_or_sync(0xFFFFFFFFu, present);
+  const float zero[E] = {};
+  for (uint32_t w = 0; w < words; ++w)
+    if (!(present >> w & 1u)) columns.store(s.dw, v0 + w, zero);
+  if (count == 0) return;
+  __syncwarp();
+  for (int i = lane; i < count; i += 32) {       // (all different)
+    const uint16_t mine = found[warp][i];
+    int at = 0;
+    for (int j = 0; j < count; ++j) at += found[warp][j] < mine;
+    ordered[warp][at] = mine;
+  }
+  __syncwarp();
+  float sum[E] = {};
+  for (int i = 0; i < count; i += 32) {
+    const uint32_t mine = i + lane < count ? ordered[warp][i + lane] : 0;
+    const uint32_t next = i + lane + 1 < count ? ordered[warp][i + lane + 1] >> 8 : 0xFFFFu;
+    const unsigned ends = __ballot_sync(0xFFFFFFFFu, i + lane < count && next != mine >> 8);
+    add_rows<DT, VEC>(columns, s.dy, mine >> 8, mine & 0xFFu, ends, min(count - i, 32), sum,
+                      [&](uint32_t word) {
+                        float e[E];
+#pragma unroll
+                        for (int j = 0; j < E; ++j) e[j] = sum[j] * s.scale;
+                        columns.store(s.dw, v0 + word, e);
+                      });
+  }
+}
+static_assert(kFewTokens == 256, "a token's number has eight bits");
 
 // The words that go on from one chunk to the next: a word's last part in the
 // chunk where it starts, then the first parts of the chunks that it reaches, in
@@ -508,14 +637,24 @@ embedding_join_kernel(const Sums s, bool vec) {
   begin_after_previous();
   const int64_t chunk = blockIdx.x, last = (chunk + 1) * s.chunk - 1;
   if (last + 1 >= s.n) return;
+  const int64_t chunks = (s.n + s.chunk - 1) / s.chunk;
+  // lanes 0 to 15: the last keys of the chunks before this one; 16 to 31: the
+  // first ones of those behind the next
+  static_assert(kFewParts == 16, "half a warp");
+  const int probe = threadIdx.x & 31;
+  const int64_t at = probe < 16 ? chunk - 1 - probe : chunk + 2 + probe - 16;
+  uint32_t there = s.vocab;
+  if (at >= 0 && at < chunks) there = s.keys[probe < 16 ? (at + 1) * s.chunk - 1 : at * s.chunk];
   const uint32_t key = s.keys[last], next = s.keys[last + 1];
   if (key == s.vocab || next != key) return;
+  const unsigned others = __ballot_sync(0xFFFFFFFFu, there != key);
   // the first and the last chunk of the word
-  const auto ends_before = [&](int64_t c) { return s.keys[(c + 1) * s.chunk - 1] == key; };
-  const auto starts_in = [&](int64_t c) { return s.keys[c * s.chunk] == key; };
-  const int64_t chunks = (s.n + s.chunk - 1) / s.chunk;
-  const int64_t from = -last_of(-chunk, 1, [&](int64_t c) { return ends_before(-c); });
-  const int64_t to = last_of(chunk + 1, chunks, starts_in);
+  int64_t from = chunk - (__ffs(others & 0xFFFFu | 0x10000u) - 1);
+  int64_t to = chunk + 1 + __ffs(others >> 16 | 0x10000u) - 1;
+  if (from == chunk - 16)
+    from = -last_of(-from, 1, [&](int64_t c) { return s.keys[(1 - c) * s.chunk - 1] == key; });
+  if (to == chunk + 17)
+    to = last_of(to, chunks, [&](int64_t c) { return s.keys[c * s.chunk] == key; });
   const int64_t count = to - from + 1;
   const auto part = [&](int64_t i, int64_t c) {
     const float* p = s.parts + ((from + i) * 2 + (i == 0 ? 1 : 0)) * s.dim + c;
@@ -577,6 +716,13 @@ bool vectors_ok(const void* a, const void* b, int64_t dim, int dtype) {
 
 int64_t blocks(int64_t n, int64_t per) { return (n + per - 1) / per; }
 
+// Words of a warp that fills, so that every SM has some 32 of them.
+int group_of(int64_t words, int sms) {
+  int group = 32;
+  while (group > 1 && blocks(words, group) < 32 * sms) group /= 2;
+  return group;
+}
+
 struct Scratch {
   size_t keys[2] = {0, 0}, tokens[2] = {0, 0}, counts = 0, parts = 0, bytes = 0;
   int64_t tile = 0;
@@ -599,6 +745,7 @@ Scratch backward_scratch(const EmbeddingArgs& a, int sms) {
     s.bytes += (size_t)((bytes + 255) / 256 * 256);
     return at;
   };
+  if (a.rows <= kFewTokens) return s;
   for (int i = 0; i < (a.rows <= kRankTokens ? 1 : 2); ++i) {
     s.keys[i] = take(a.rows * 4);
     s.tokens[i] = take(a.rows * 4);
@@ -636,58 +783,78 @@ cudaError_t backward(const EmbeddingArgs& a, char* scratch, int sms, cudaStream_
   const auto at = [&](size_t offset) { return reinterpret_cast<uint32_t*>(scratch + offset); };
   const int64_t size = element_size(DT);
   Fill fill = {static_cast<char*>(a.out), a.vocab * a.dim * size, (int)size, 0, 1};
-  const int fillers = 4 * sms;
   const long long* ids = reinterpret_cast<const long long*>(a.ids);
+  const bool vec = vectors_ok(a.in, a.out, a.dim, DT);
   cudaError_t e = cudaSuccess;
+  Sums s = {};
+  s.n = a.rows;
+  s.dim = a.dim;
+  s.vocab = (uint32_t)a.vocab;
+  s.slices = blocks(a.dim, 32 * kPer<DT>);
+  s.dy = a.in;
+  s.scale = a.scale;
+  s.dw = a.out;
+  if (a.rows <= kFewTokens) {
+    s.group = group_of(a.vocab * s.slices, sms);
+    if (mark) mark(kEmbeddingSumsK, 0, stream);
+    e = launch(worth_early(a.vocab * a.dim),
+               vec ? embedding_few_kernel<DT, true> : embedding_few_kernel<DT, false>,
+               (unsigned)blocks(blocks(a.vocab, s.group) * s.slices, kSumWarps), 32 * kSumWarps,
+               0, stream, s, ids, (long long)a.padding);
+    if (mark) mark(kEmbeddingSumsK, 1, stream);
+    return e;
+  }
   int last = 0;
   if (mark) mark(kEmbeddingOrderK, 0, stream);
   if (a.rows <= kRankTokens) {
-    const int n = (int)a.rows, sorters = (int)blocks(n, 32);
+    const int n = (int)a.rows;
     const size_t smem = (size_t)blocks(blocks(n, kCtaWarps), 32) * 32 * kCtaWarps * 4;
-    e = launch(true, embedding_rank_kernel, sorters + fillers, kCtaThreads, smem, stream, ids, n,
-               (uint32_t)a.vocab, (long long)a.padding, sorters, at(l.keys[0]), at(l.tokens[0]),
-               fill);
+    e = launch(true, embedding_rank_kernel, (unsigned)blocks(n, 32), kCtaThreads, smem, stream,
+               ids, n, (uint32_t)a.vocab, (long long)a.padding, at(l.keys[0]), at(l.tokens[0]));
+    s.group = group_of(a.vocab, sms);
   } else {
-    SortPass s = {};
-    s.n = a.rows;
-    s.tile = l.tile;
-    s.tiles = l.tiles;
-    s.vocab = (uint32_t)a.vocab;
-    s.padding = a.padding;
-    s.ids = ids;
-    s.counts = at(l.counts);
+    SortPass p = {};
+    p.n = a.rows;
+    p.tile = l.tile;
+    p.tiles = l.tiles;
+    p.vocab = (uint32_t)a.vocab;
+    p.padding = a.padding;
+    p.ids = ids;
+    p.counts = at(l.counts);
     // two CTAs an SM, those that sort first
     const int ctas = std::max(2 * sms, l.tiles + sms);
     const int64_t pass = (int64_t)l.tiles * kDigits;
     fill.parts = l.passes + 1;
-    e = launch(true, embedding_count_kernel, ctas, kSortThreads, 0, stream, s, s.counts + pass,
+    e = launch(true, embedding_count_kernel, ctas, kSortThreads, 0, stream, p, p.counts + pass,
                l.passes - 1, fill);
-    for (int p = 0; e == cudaSuccess && p < l.passes; ++p) {
-      s.keys = at(l.keys[last]);
-      s.tokens = at(l.tokens[last]);
-      if (p > 0) {
-        s.ids = nullptr;
-        s.counts += pass;
-        s.shift += 8;
+    for (int i = 0; e == cudaSuccess && i < l.passes; ++i) {
+      p.keys = at(l.keys[last]);
+      p.tokens = at(l.tokens[last]);
+      if (i > 0) {
+        p.ids = nullptr;
+        p.counts += pass;
+        p.shift += 8;
         last ^= 1;
       }
-      s.next = p + 1 < l.passes ? s.counts + pass : nullptr;
-      s.keys_out = at(l.keys[last]);
-      s.tokens_out = at(l.tokens[last]);
-      fill.part = p + 1;
-      e = launch(true, embedding_place_kernel, ctas, kSortThreads, 0, stream, s, fill);
+      p.next = i + 1 < l.passes ? p.counts + pass : nullptr;
+      p.keys_out = at(l.keys[last]);
+      p.tokens_out = at(l.tokens[last]);
+      fill.part = i + 1;
+      e = launch(true, embedding_place_kernel, ctas, kSortThreads, 0, stream, p, fill);
     }
   }
   if (mark) mark(kEmbeddingOrderK, 1, stream);
   if (e != cudaSuccess) return e;
-  const bool vec = vectors_ok(a.in, a.out, a.dim, DT);
-  Sums s = {at(l.keys[last]), at(l.tokens[last]), a.rows, a.dim, (uint32_t)a.vocab,
-            blocks(a.dim, 32 * kPer<DT>), chunk_of(a, sms), a.in, a.scale,
-            reinterpret_cast<float*>(scratch + l.parts), a.out};
+  s.keys = at(l.keys[last]);
+  s.tokens = at(l.tokens[last]);
+  s.chunk = chunk_of(a, sms);
+  s.parts = reinterpret_cast<float*>(scratch + l.parts);
   const int64_t chunks = blocks(a.rows, s.chunk);
+  s.sums = chunks * s.slices;
+  const int64_t fillers = s.group > 0 ? blocks(a.vocab, s.group) : 0;
   if (mark) mark(kEmbeddingSumsK, 0, stream);
   e = launch(true, vec ? embedding_sums_kernel<DT, true> : embedding_sums_kernel<DT, false>,
-             (unsigned)blocks(chunks * s.slices, kSumWarps), 32 * kSumWarps, 0, stream, s);
+             (unsigned)blocks(s.sums + fillers, kSumWarps), 32 * kSumWarps, 0, stream, s);
   if (mark) mark(kEmbeddingSumsK, 1, stream);
   if (e != cudaSuccess || chunks == 1) return e;
   if (mark) mark(kEmbeddingJoinK, 0, stream);

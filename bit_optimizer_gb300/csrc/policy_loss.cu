@@ -6,7 +6,7 @@
 //
 // Bound by memory for large batches, by launches for small ones.  A warp takes a
 // piece of one sequence and makes its sums; one CTA joins them in order.  Small
-// batches: a cluster of eight CTAs, whose warps leave their sums in the first
+// batches: a cluster of up to eight CTAs, whose warps leave their sums in the first
 // one's shared memory, in a single launch.  (A batch's terms cancel down to their
 // mean: sums over lanes and pieces are held in two floats, 48 bits.  The same in
 // fp64, which the GB300 has little of, took 37 us for 8 sequences and 73 for 512.)
@@ -90,38 +90,50 @@ __device__ __forceinline__ void each_token(const Policy& p, int64_t b, int64_t t
   const int n = (int)min((int64_t)p.piece, p.length - t0);    // (may be below 0)
   const float a_all = p.per_token ? 0.0f : p.advantage[b];
   constexpr int N = VEC ? 4 : 1;
-#pragma unroll(VEC ? 2 : 4)
-  for (int i = N * lane; i < n; i += 32 * N) {
-    const int64_t at = base + i;
-    float lp[N] = {}, old[N] = {}, ref[N] = {}, a[N];
-#pragma unroll
-    for (int k = 0; k < N; ++k) a[k] = a_all;
-    if constexpr (VEC) {
-      uint32_t m = 0x01010101u;
-      if (p.mask != nullptr) m = *reinterpret_cast<const uint32_t*>(p.mask + at);
-      const auto read = [&](float (&to)[N], const float* from) {
+  // the masks of kAhead rounds, then their values, then the rounds: two latencies
+  constexpr int kAhead = VEC ? 2 : 4;
+  for (int i0 = N * lane; i0 < n; i0 += kAhead * 32 * N) {
+    uint32_t m[kAhead];
+    float lp[kAhead][N], old[kAhead][N], ref[kAhead][N], a[kAhead][N];
+    const auto read = [&](float (&to)[N], const float* from, int64_t at) {
+      if constexpr (VEC) {
         const float4 v = *reinterpret_cast<const float4*>(from + at);
         to[0] = v.x;
         to[1] = v.y;
         to[2] = v.z;
         to[3] = v.w;
-      };
-      if (m != 0) {
-        read(lp, p.logp);
-        read(old, p.old_logp);
-        if (p.ref_logp != nullptr) read(ref, p.ref_logp);
-        if (p.per_token) read(a, p.advantage);
+      } else {
+        to[0] = from[at];
       }
-      f(at, lp, old, ref, a, m);
-    } else {
-      const uint32_t m = p.mask != nullptr ? (uint32_t)p.mask[at] : 1u;
-      if (m != 0) {
-        lp[0] = p.logp[at];
-        old[0] = p.old_logp[at];
-        if (p.ref_logp != nullptr) ref[0] = p.ref_logp[at];
-        if (p.per_token) a[0] = p.advantage[at];
+    };
+#pragma unroll
+    for (int r = 0; r < kAhead; ++r) {
+      const int i = i0 + r * 32 * N;
+      m[r] = i < n ? (VEC ? 0x01010101u : 1u) : 0u;
+      if (i < n && p.mask != nullptr) {
+        if constexpr (VEC) m[r] = *reinterpret_cast<const uint32_t*>(p.mask + base + i);
+        else m[r] = p.mask[base + i];
       }
-      f(at, lp, old, ref, a, m);
+    }
+#pragma unroll
+    for (int r = 0; r < kAhead; ++r) {
+      const int64_t at = base + i0 + r * 32 * N;
+#pragma unroll
+      for (int k = 0; k < N; ++k) {
+        lp[r][k] = old[r][k] = ref[r][k] = 0.0f;
+        a[r][k] = a_all;
+      }
+      if (m[r] != 0) {
+        read(lp[r], p.logp, at);
+        read(old[r], p.old_logp, at);
+        if (p.ref_logp != nullptr) read(ref[r], p.ref_logp, at);
+        if (p.per_token) read(a[r], p.advantage, at);
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < kAhead; ++r) {
+      const int i = i0 + r * 32 * N;
+      if (i < n) f(base + i, lp[r], old[r], ref[r], a[r], m[r]);
     }
   }
 }
@@ -199,8 +211,16 @@ __device__ __forceinline__ Part part_of(const Policy& p, int64_t b, int64_t t0) 
       }
     }
   });
-  return reduce({{policy, 0.0f}, {kl, 0.0f}, clipped, count}, 32);
+  // (a lane's at most 32 terms and the lanes' in fp32; from here on in two floats)
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    policy += __shfl_xor_sync(0xFFFFFFFFu, policy, o);
+    kl += __shfl_xor_sync(0xFFFFFFFFu, kl, o);
+  }
+  const unsigned n = __reduce_add_sync(0xFFFFFFFFu, (unsigned)clipped << 16 | (unsigned)count);
+  return {{policy, 0.0f}, {kl, 0.0f}, (int)(n >> 16), (int)(n & 0xFFFFu)};
 }
+static_assert(kMostPiece < 1 << 16, "a piece's counts");
 
 // What the batch's sums come to: by_sequence, of the sequences' means, else of
 // all tokens.
@@ -229,13 +249,17 @@ struct Total {
 __device__ void join(const Part* parts, int64_t batch, int64_t pieces, bool by_sequence,
                      float kl_coef, float* stats, float* weight) {
   __shared__ Total sh[kJoinThreads / 32];
+  __shared__ unsigned long long sh_count;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   // `width` neighbouring lanes to a sequence
   int width = 1;
   while (width < 32 && width < pieces) width *= 2;
   const int groups = kJoinThreads / width, mine = threadIdx.x / width;
   Total total = {};
-  for (int64_t b0 = 0; b0 < batch; b0 += groups) {
+  // (a warp without a sequence has nothing to add up: 32 warps' sums in two floats
+  // take longer than the memory)
+  const bool busy = warp * 32 / width < batch;
+  for (int64_t b0 = 0; busy && b0 < batch; b0 += groups) {
     const int64_t b = b0 + mine;
     Part s = {};
     if (b < batch) {
@@ -249,12 +273,17 @@ __device__ void join(const Part* parts, int64_t batch, int64_t pieces, bool by_s
       weight[b] = __int_as_float(s.count);      // for now
     }
   }
-  total.reduce();
+  if (busy) total.reduce();
   if (lane == 0) sh[warp] = total;
   __syncthreads();
-  total = sh[lane];
-  total.reduce();
-  const float all = total.count > 0 ? reciprocal(total.count) : 0.0f;
+  if (warp == 0) {
+    total = sh[lane];
+    if (batch * width > 32) total.reduce();
+    if (lane == 0) sh_count = total.count;
+  }
+  __syncthreads();
+  const unsigned long long count = sh_count;
+  const float all = count > 0 ? reciprocal(count) : 0.0f;
   if (threadIdx.x == 0) {
     const Two each[3] = {scaled(total.policy, all), scaled(total.kl, all),
                          scaled(total.clipped, all)};
@@ -267,7 +296,7 @@ __device__ void join(const Part* parts, int64_t batch, int64_t pieces, bool by_s
     for (int64_t b = mine; b < batch; b += groups) {
       const int c = __float_as_int(weight[b]);
       weight[b] = c == 0        ? 0.0f
-                  : by_sequence ? reciprocal((unsigned long long)c * total.count) : all;
+                  : by_sequence ? reciprocal((unsigned long long)c * count) : all;
     }
   }
 }
@@ -299,16 +328,16 @@ policy_join_kernel(const Part* parts, int64_t batch, int64_t pieces, bool by_seq
   join(parts, batch, pieces, by_sequence, kl_coef, stats, weight);
 }
 
-// At most kClusterUnits units.
+// One cluster of up to kClusterCtas CTAs, with at least as many warps as units.
 template <bool VEC>
-__global__ void __cluster_dims__(kClusterCtas, 1, 1) __launch_bounds__(kJoinThreads)
+__global__ void __launch_bounds__(kJoinThreads)
 policy_cluster_kernel(const Policy p, int64_t batch, bool by_sequence, float kl_coef,
                       float* stats, float* weight) {
   __shared__ Part parts[kClusterUnits];
   begin_after_previous();
   // (the first CTA has to be running before its memory is written)
   asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
-  const int unit = (threadIdx.x >> 5) * kClusterCtas + (int)blockIdx.x;
+  const int unit = (threadIdx.x >> 5) * (int)gridDim.x + (int)blockIdx.x;
   Part r = {};
   if (unit < p.units) {
     const int64_t b = unit / p.pieces;
@@ -338,7 +367,8 @@ policy_backward_kernel(const Policy p, const float* dloss, const float* weight, 
   constexpr int N = VEC ? 4 : 1;
   const int64_t b = unit / p.pieces;
   const float g = *dloss * weight[b];
-  each_token<VEC>(p, b, (unit - b * p.pieces) * p.piece, [&](int64_t at, const float (&lp)[N], const float (&old)[N],
+  const int64_t t0 = (unit - b * p.pieces) * p.piece;
+  each_token<VEC>(p, b, t0, [&](int64_t at, const float (&lp)[N], const float (&old)[N],
                                const float (&ref)[N], const float (&a)[N], uint32_t m) {
     float d[N];
 #pragma unroll
@@ -433,10 +463,20 @@ cudaError_t launch_policy(const PolicyArgs& a, char* scratch, cudaStream_t strea
   const float kl = (float)a.kl_coef;
   if (mark) mark(kPolicyLossK, 0, stream);
   if (cluster) {
-    const cudaError_t e =
-        launch(false, vec ? policy_cluster_kernel<true> : policy_cluster_kernel<false>,
-               kClusterCtas, kJoinThreads, 0, stream, p, a.batch, a.by_sequence, kl, a.stats,
-               a.weight_out);
+    unsigned ctas = 1;
+    while (ctas * (kJoinThreads / 32) < p.units) ctas *= 2;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = ctas;
+    cfg.blockDim = kJoinThreads;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim = {ctas, 1, 1};
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(
+        &cfg, vec ? policy_cluster_kernel<true> : policy_cluster_kernel<false>, p, a.batch,
+        a.by_sequence, kl, a.stats, a.weight_out);
     if (mark) mark(kPolicyLossK, 1, stream);
     return e;
   }

@@ -168,8 +168,11 @@ __device__ __forceinline__ void fill_zeros(const Fill& f, int64_t cta, int64_t c
 
 // Some tokens: the place of each is the number of smaller keys, and of equal ones
 // before it.  A CTA places 32 tokens, its warps comparing them with a share of all
-// keys each.
-constexpr int64_t kRankTokens = 8192;
+// keys each.  (4096 tokens over 50257 x 768, 5000 x 512: 25.2 and 16.4 us; sorted as
+// 8193 are: 28 and 23.  8192: 38 and 27.)  Launched early the CTAs start where the
+// previous kernel leaves room, many to an SM, which is right as long as they are
+// short: 512 tokens over 5000 x 512 8.7 us, 10.3 launched late; 4096 29.9 and 16.4.
+constexpr int64_t kRankTokens = 4096, kEarlyRank = 1024;
 
 __global__ void __launch_bounds__(kCtaThreads)
 embedding_rank_kernel(const long long* ids, int n, uint32_t vocab, long long padding,
@@ -809,7 +812,7 @@ cudaError_t backward(const EmbeddingArgs& a, char* scratch, int sms, cudaStream_
   if (a.rows <= kRankTokens) {
     const int n = (int)a.rows;
     const size_t smem = (size_t)blocks(blocks(n, kCtaWarps), 32) * 32 * kCtaWarps * 4;
-    e = launch(true, embedding_rank_kernel, (unsigned)blocks(n, 32), kCtaThreads, smem, stream,
+    e = launch(n <= kEarlyRank, embedding_rank_kernel, (unsigned)blocks(n, 32), kCtaThreads, smem, stream,
                ids, n, (uint32_t)a.vocab, (long long)a.padding, at(l.keys[0]), at(l.tokens[0]));
     s.group = group_of(a.vocab, sms);
   } else {

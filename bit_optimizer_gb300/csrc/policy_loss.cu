@@ -5,11 +5,12 @@
 // kl_coef (1 - exp(e)).
 //
 // Bound by memory for large batches, by launches for small ones.  A warp takes a
-// piece of one sequence and makes its sums; one CTA joins them in order.  Small
-// batches: a cluster of up to eight CTAs, whose warps leave their sums in the first
-// one's shared memory, in a single launch.  (A batch's terms cancel down to their
-// mean: sums over lanes and pieces are held in two floats, 48 bits.  The same in
-// fp64, which the GB300 has little of, took 37 us for 8 sequences and 73 for 512.)
+// piece of one sequence; a CTA adds up what its warps have of a sequence, and one
+// CTA joins the rest in order.  (A batch's terms cancel down to their mean: sums
+// over warps are held in two floats, 48 bits.  In fp64, which the GB300 has little
+// of, the join took 37 us for 8 sequences and 73 for 512.  Both kernels are launched
+// early, which makes them as fast as a single one for small batches: in one cluster
+// 8 x 512 took 8.2 us, 64 x 1023 10.3; 7.4 and 7.7.)
 //
 // Whether a token is clipped decides between its whole gradient and none, so it
 // is decided exactly: logp - old, as the fp32 difference and its rounding error,
@@ -17,17 +18,15 @@
 #include <cmath>
 
 #include "ops_internal.cuh"
-#include "tensor_core.cuh"
 
 namespace fp8opt {
 
 namespace {
 
 constexpr int kCtaThreads = 256, kCtaWarps = kCtaThreads / 32;
-// Tokens of a warp: a power of two, at most 32 of a lane.
+// Tokens of a warp: a multiple of 128, at most 32 of a lane.
 constexpr int kLeastPiece = 128, kMostPiece = 1024;
 constexpr int kJoinThreads = 1024;
-constexpr int kClusterCtas = 8, kClusterUnits = kClusterCtas * kJoinThreads / 32;
 
 struct Border {
   float hi, lo;                   // log of the border
@@ -40,9 +39,10 @@ struct Policy {
   const float* advantage;
   const uint8_t* mask;
   const float* ref_logp;
-  int64_t length, pieces, units;  // a unit: a piece of a sequence ...
-  int piece;                      // ... of so many tokens, of a warp, or (`wide`) of
-  bool wide;                      // each of a CTA's warps
+  // A sequence is `pieces` units, each `warps` neighbouring warps of a CTA with
+  // `piece` tokens each.
+  int64_t length, pieces, units;
+  int warps, piece;
   bool per_token;
   Border low, high;
   float kl_coef;
@@ -71,11 +71,26 @@ struct Token {
 };
 
 __device__ __forceinline__ Token token_of(const Policy& p, float logp, float old, float a) {
-  const float d = logp - old, back = d - logp;
-  const float err = (logp - (d - back)) + (-old - back);   // logp - old = d + err
-  const bool above = d > p.high.hi || (d == p.high.hi && err > p.high.lo);
-  const bool below = d < p.low.hi || (d == p.low.hi && err < p.low.lo);
+  const float d = logp - old;
+  bool above = d > p.high.hi, below = d < p.low.hi;
+  if (d == p.high.hi || d == p.low.hi) {      // then what d is off by decides
+    const float back = d - logp, err = (logp - (d - back)) + (-old - back);
+    above |= d == p.high.hi && err > p.high.lo;
+    below |= d == p.low.hi && err < p.low.lo;
+  }
   return {expf(d), (a > 0.0f && above) || (a < 0.0f && below)};
+}
+
+// The calling warp's unit, its sequence and the warp's first token of it.
+struct Place {
+  int64_t unit, b, t0;
+};
+
+__device__ __forceinline__ Place place_of(const Policy& p) {
+  const int warp = threadIdx.x >> 5;
+  const int64_t unit = (int64_t)blockIdx.x * (kCtaWarps / p.warps) + warp / p.warps;
+  const int64_t b = p.pieces == 1 ? unit : unit / p.pieces;
+  return {unit, b, ((unit - b * p.pieces) * p.warps + warp % p.warps) * p.piece};
 }
 
 __device__ __forceinline__ bool counts(uint32_t m, int k) { return (m >> (8 * k) & 0xFFu) != 0; }
@@ -90,10 +105,22 @@ __device__ __forceinline__ void each_token(const Policy& p, int64_t b, int64_t t
   const int n = (int)min((int64_t)p.piece, p.length - t0);    // (may be below 0)
   const float a_all = p.per_token ? 0.0f : p.advantage[b];
   constexpr int N = VEC ? 4 : 1;
-  // the masks of kAhead rounds, then their values, then the rounds: two latencies
+  // the masks of kAhead rounds, and while these are added the next ones'
   constexpr int kAhead = VEC ? 2 : 4;
+  const auto masks = [&](int i0, uint32_t (&m)[kAhead]) {
+#pragma unroll
+    for (int r = 0; r < kAhead; ++r) {
+      const int i = i0 + r * 32 * N;
+      m[r] = i < n ? (VEC ? 0x01010101u : 1u) : 0u;
+      if (i < n && p.mask != nullptr) {
+        if constexpr (VEC) m[r] = *reinterpret_cast<const uint32_t*>(p.mask + base + i);
+        else m[r] = p.mask[base + i];
+      }
+    }
+  };
+  uint32_t m[kAhead];
+  masks(N * lane, m);
   for (int i0 = N * lane; i0 < n; i0 += kAhead * 32 * N) {
-    uint32_t m[kAhead];
     float lp[kAhead][N], old[kAhead][N], ref[kAhead][N], a[kAhead][N];
     const auto read = [&](float (&to)[N], const float* from, int64_t at) {
       if constexpr (VEC) {
@@ -106,15 +133,6 @@ __device__ __forceinline__ void each_token(const Policy& p, int64_t b, int64_t t
         to[0] = from[at];
       }
     };
-#pragma unroll
-    for (int r = 0; r < kAhead; ++r) {
-      const int i = i0 + r * 32 * N;
-      m[r] = i < n ? (VEC ? 0x01010101u : 1u) : 0u;
-      if (i < n && p.mask != nullptr) {
-        if constexpr (VEC) m[r] = *reinterpret_cast<const uint32_t*>(p.mask + base + i);
-        else m[r] = p.mask[base + i];
-      }
-    }
 #pragma unroll
     for (int r = 0; r < kAhead; ++r) {
       const int64_t at = base + i0 + r * 32 * N;
@@ -130,10 +148,13 @@ __device__ __forceinline__ void each_token(const Policy& p, int64_t b, int64_t t
         if (p.per_token) read(a[r], p.advantage, at);
       }
     }
+    uint32_t next[kAhead];
+    masks(i0 + kAhead * 32 * N, next);
 #pragma unroll
     for (int r = 0; r < kAhead; ++r) {
       const int i = i0 + r * 32 * N;
       if (i < n) f(base + i, lp[r], old[r], ref[r], a[r], m[r]);
+      m[r] = next[r];
     }
   }
 }
@@ -245,11 +266,12 @@ struct Total {
   }
 };
 
-// One CTA of kJoinThreads.
-__device__ void join(const Part* parts, int64_t batch, int64_t pieces, bool by_sequence,
-                     float kl_coef, float* stats, float* weight) {
+__global__ void __launch_bounds__(kJoinThreads)
+policy_join_kernel(const Part* parts, int64_t batch, int64_t pieces, bool by_sequence,
+                   float kl_coef, float* stats, float* weight) {
   __shared__ Total sh[kJoinThreads / 32];
   __shared__ unsigned long long sh_count;
+  begin_after_previous();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   // `width` neighbouring lanes to a sequence
   int width = 1;
@@ -308,67 +330,27 @@ policy_kernel(const Policy p, Part* parts) {
   __shared__ Part sh[kCtaWarps];
   begin_after_previous();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t unit = p.wide ? (int64_t)blockIdx.x : (int64_t)blockIdx.x * kCtaWarps + warp;
-  if (unit >= p.units) return;       // (all of a wide CTA's warps, or none)
-  const int64_t b = unit / p.pieces, i = unit - b * p.pieces;
-  Part r = part_of<VEC>(p, b, (p.wide ? i * kCtaWarps + warp : i) * p.piece);
-  if (p.wide) {
+  const Place at = place_of(p);
+  if (at.unit < p.units) {
+    const Part r = part_of<VEC>(p, at.b, at.t0);
     if (lane == 0) sh[warp] = r;
-    __syncthreads();
-    if (warp > 0) return;
-    r = reduce(sh[lane % kCtaWarps], kCtaWarps);
   }
-  if (lane == 0) parts[unit] = r;
-}
-
-__global__ void __launch_bounds__(kJoinThreads)
-policy_join_kernel(const Part* parts, int64_t batch, int64_t pieces, bool by_sequence,
-                   float kl_coef, float* stats, float* weight) {
-  begin_after_previous();
-  join(parts, batch, pieces, by_sequence, kl_coef, stats, weight);
-}
-
-// One cluster of up to kClusterCtas CTAs, with at least as many warps as units.
-template <bool VEC>
-__global__ void __launch_bounds__(kJoinThreads)
-policy_cluster_kernel(const Policy p, int64_t batch, bool by_sequence, float kl_coef,
-                      float* stats, float* weight) {
-  __shared__ Part parts[kClusterUnits];
-  begin_after_previous();
-  // (the first CTA has to be running before its memory is written)
-  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
-  const int unit = (threadIdx.x >> 5) * (int)gridDim.x + (int)blockIdx.x;
-  Part r = {};
-  if (unit < p.units) {
-    const int64_t b = unit / p.pieces;
-    r = part_of<VEC>(p, b, (unit - b * p.pieces) * p.piece);
-  }
-  __syncwarp();
-  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-  if (unit < p.units && (threadIdx.x & 31) == 0) {
-    const uint32_t to = cluster_addr(&parts[unit], 0);
-    const int words[kPartWords] = {__float_as_int(r.policy.hi), __float_as_int(r.policy.lo),
-                                   __float_as_int(r.kl.hi), __float_as_int(r.kl.lo), r.clipped,
-                                   r.count};
-#pragma unroll
-    for (int k = 0; k < kPartWords; ++k) cluster_store(to + 4 * k, words[k]);
-  }
-  __syncwarp();
-  cluster_sync();
-  if (blockIdx.x == 0) join(parts, batch, p.pieces, by_sequence, kl_coef, stats, weight);
+  __syncthreads();
+  // (a unit's first warp goes on)
+  if (at.unit >= p.units || warp % p.warps != 0) return;
+  const Part r = reduce(sh[warp + lane % p.warps], p.warps);
+  if (lane == 0) parts[at.unit] = r;
 }
 
 template <bool VEC>
 __global__ void __launch_bounds__(kCtaThreads)
 policy_backward_kernel(const Policy p, const float* dloss, const float* weight, float* dlogp) {
   begin_after_previous();
-  const int64_t unit = (int64_t)blockIdx.x * kCtaWarps + (threadIdx.x >> 5);
-  if (unit >= p.units) return;
+  const Place place = place_of(p);
+  if (place.unit >= p.units) return;
   constexpr int N = VEC ? 4 : 1;
-  const int64_t b = unit / p.pieces;
-  const float g = *dloss * weight[b];
-  const int64_t t0 = (unit - b * p.pieces) * p.piece;
-  each_token<VEC>(p, b, t0, [&](int64_t at, const float (&lp)[N], const float (&old)[N],
+  const float g = *dloss * weight[place.b];
+  each_token<VEC>(p, place.b, place.t0, [&](int64_t at, const float (&lp)[N], const float (&old)[N],
                                const float (&ref)[N], const float (&a)[N], uint32_t m) {
     float d[N];
 #pragma unroll
@@ -397,9 +379,11 @@ Border border(double x) {
   return b;
 }
 
-// In pieces as small as they can be with at most `most` warps (a warp's latency
-// goes with its piece).
-Policy policy_of(const PolicyArgs& a, int64_t most, bool wide = false) {
+// The pieces are as large as they can be while there are kWarps of them (27 an SM):
+// fewer sums to join.  512 x 8192: 18.6 us, 20.4 with twice as many.
+constexpr int64_t kWarps = 4096;
+
+Policy policy_of(const PolicyArgs& a) {
   Policy p = {};
   p.logp = a.logp;
   p.old_logp = a.old_logp;
@@ -407,12 +391,14 @@ Policy policy_of(const PolicyArgs& a, int64_t most, bool wide = false) {
   p.mask = a.mask;
   p.ref_logp = a.ref_logp;
   p.length = a.length;
-  p.wide = wide;
-  const int64_t warps = wide ? kCtaWarps : 1;
-  for (p.piece = kLeastPiece;; p.piece *= 2) {
-    p.pieces = (a.length + warps * p.piece - 1) / (warps * p.piece);
+  const auto up = [](int64_t x, int64_t m) { return (x + m - 1) / m; };
+  for (int most = kMostPiece;; most /= 2) {
+    p.warps = 1;
+    while (p.warps < kCtaWarps && (int64_t)p.warps * most < a.length) p.warps *= 2;
+    p.pieces = up(a.length, (int64_t)p.warps * most);
     p.units = a.batch * p.pieces;
-    if (p.units * warps <= most || p.piece == kMostPiece) break;
+    p.piece = p.pieces > 0 ? (int)(up(up(a.length, p.warps * p.pieces), 128) * 128) : most;
+    if (p.units * p.warps >= kWarps || most == kLeastPiece) break;
   }
   p.per_token = a.per_token;
   p.low = border(-a.clip_low);
@@ -431,69 +417,35 @@ bool vectors_ok(const PolicyArgs& a) {
 }
 
 unsigned ctas(const Policy& p) {
-  return (unsigned)(p.wide ? p.units : (p.units + kCtaWarps - 1) / kCtaWarps);
-}
-
-// Forward: a cluster's units, of at most 256 tokens; else as many warps as are
-// resident (some 64 an SM, in one or two rounds), a CTA's joined at once where a
-// sequence is long enough for one: the CTA that joins the rest takes its time for
-// each of them.
-constexpr int64_t kWarps = 16384;
-constexpr int kClusterPiece = 256, kWideLength = 512;
-
-Policy forward_policy(const PolicyArgs& a, bool* cluster) {
-  const Policy p = policy_of(a, kClusterUnits);
-  *cluster = p.units <= kClusterUnits && p.piece <= kClusterPiece;
-  return *cluster ? p : policy_of(a, kWarps, a.length > kWideLength);
+  const int units = kCtaWarps / p.warps;
+  return (unsigned)((p.units + units - 1) / units);
 }
 
 }  // namespace
 
-size_t policy_scratch(const PolicyArgs& a) {
-  bool cluster;
-  const Policy p = forward_policy(a, &cluster);
-  return cluster ? 0 : (size_t)p.units * sizeof(Part);
-}
+size_t policy_scratch(const PolicyArgs& a) { return (size_t)policy_of(a).units * sizeof(Part); }
 
 cudaError_t launch_policy(const PolicyArgs& a, char* scratch, cudaStream_t stream,
                           LaunchMark mark) {
-  bool cluster;
-  const Policy p = forward_policy(a, &cluster);
-  const bool vec = vectors_ok(a);
-  const float kl = (float)a.kl_coef;
-  if (mark) mark(kPolicyLossK, 0, stream);
-  if (cluster) {
-    unsigned ctas = 1;
-    while (ctas * (kJoinThreads / 32) < p.units) ctas *= 2;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = ctas;
-    cfg.blockDim = kJoinThreads;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim = {ctas, 1, 1};
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(
-        &cfg, vec ? policy_cluster_kernel<true> : policy_cluster_kernel<false>, p, a.batch,
-        a.by_sequence, kl, a.stats, a.weight_out);
-    if (mark) mark(kPolicyLossK, 1, stream);
-    return e;
-  }
+  const Policy p = policy_of(a);
   Part* parts = reinterpret_cast<Part*>(scratch);
-  cudaError_t e = launch(true, vec ? policy_kernel<true> : policy_kernel<false>, ctas(p),
-                         kCtaThreads, 0, stream, p, parts);
-  if (mark) mark(kPolicyLossK, 1, stream);
+  cudaError_t e = cudaSuccess;
+  if (p.units > 0) {
+    if (mark) mark(kPolicyLossK, 0, stream);
+    e = launch(true, vectors_ok(a) ? policy_kernel<true> : policy_kernel<false>, ctas(p),
+               kCtaThreads, 0, stream, p, parts);
+    if (mark) mark(kPolicyLossK, 1, stream);
+  }
   if (e != cudaSuccess) return e;
   if (mark) mark(kPolicyJoinK, 0, stream);
   e = launch(true, policy_join_kernel, 1, kJoinThreads, 0, stream, (const Part*)parts, a.batch,
-             p.pieces, a.by_sequence, kl, a.stats, a.weight_out);
+             p.pieces, a.by_sequence, (float)a.kl_coef, a.stats, a.weight_out);
   if (mark) mark(kPolicyJoinK, 1, stream);
   return e;
 }
 
 cudaError_t launch_policy_backward(const PolicyArgs& a, cudaStream_t stream, LaunchMark mark) {
-  const Policy p = policy_of(a, kWarps);
+  const Policy p = policy_of(a);
   if (mark) mark(kPolicyBackwardK, 0, stream);
   const cudaError_t e =
       launch(worth_early(a.batch * a.length),

@@ -216,11 +216,12 @@ embedding_rank_kernel(const long long* ids, int n, uint32_t vocab, long long pad
 }
 
 // More tokens: a stable sort by eight bits of the key a pass, in tiles of a CTA
-// each (a multiple of kSortStep tokens).  First the tiles' counts of each digit,
+// each (a multiple of kSortStep tokens: 65536 tokens 59.6 us, with twice the step
+// 62.4).  First the tiles' counts of each digit,
 // for the first pass; every pass then counts the next one's, where its tokens go
 // to (whole numbers: the order of the atomics does not matter).
 constexpr int kSortThreads = 1024, kSortWarps = kSortThreads / 32, kDigits = 256;
-constexpr int kRounds = 2, kSortStep = kRounds * kSortThreads;
+constexpr int kRounds = 1, kSortStep = kRounds * kSortThreads;
 
 struct SortPass {
   const long long* ids;      // the first pass's input; else NULL
@@ -352,14 +353,23 @@ embedding_place_kernel(SortPass s, Fill fill) {
 #pragma unroll
     for (int r = 0; r < kRounds; ++r) {
       const bool in = i0 + 32 * r < hi;
+      const uint32_t at =
+          in ? before[warp][key[r] >> s.shift & (kDigits - 1)] + rank[r] : 0;
       if (in) {
-        const uint32_t at = before[warp][key[r] >> s.shift & (kDigits - 1)] + rank[r];
         s.keys_out[at] = key[r];
         s.tokens_out[at] = token[r];
-        if (s.next != nullptr) {
-          const uint32_t digit = key[r] >> (s.shift + 8) & (kDigits - 1);
-          atomicAdd(&s.next[(int64_t)(at / (uint32_t)s.tile) * kDigits + digit], 1u);
-        }
+      }
+      if (s.next != nullptr) {
+        // one atomic for a word's tokens in the warp, where they go to one tile:
+        // a frequent word's meet at one address
+        const uint32_t to = at / (uint32_t)s.tile;
+        const unsigned same = __match_any_sync(0xFFFFFFFFu, in ? key[r] : ~0u);
+        const int first = __ffs(same) - 1;
+        const bool one = __shfl_sync(0xFFFFFFFFu, to, first) ==
+                         __shfl_sync(0xFFFFFFFFu, to, 31 - __clz(same));
+        if (in && (!one || lane == first))
+          atomicAdd(&s.next[(int64_t)to * kDigits + (key[r] >> (s.shift + 8) & (kDigits - 1))],
+                    one ? __popc(same) : 1u);
       }
     }
     if (step + kSortStep < hi) read(step + kSortStep);
@@ -613,9 +623,10 @@ static_assert(kFewTokens == 256, "a token's number has eight bits");
 // order.  A CTA for every chunk, with the word that goes on behind it.  Up to
 // kFewParts parts: the CTA where the word starts adds them, a thread to four
 // columns.  More: all CTAs that the word goes on behind take 32 columns each in
-// turn, 32 ranges of parts side by side.
-constexpr int kJoinThreads = 256, kFewParts = 16, kJoinColumns = 32;
-constexpr int kJoinLanes = kJoinColumns / 4, kJoinRanges = kJoinThreads / kJoinLanes;
+// turn, ranges of parts side by side.
+// Narrow tables have CTAs of fewer threads: most end at once, and more are resident.
+constexpr int kFewParts = 16, kJoinColumns = 32, kJoinLanes = kJoinColumns / 4;
+constexpr int kNarrow = 256;      // columns
 
 // The last number in [lo, hi) for which f holds, which holds for lo and, if for
 // any number, for all smaller ones.  A whole warp; 32 probes a round, neighbours
@@ -633,9 +644,10 @@ __device__ __forceinline__ int64_t last_of(int64_t lo, int64_t hi, F f) {
   return lo;
 }
 
-template <int DT>
+template <int DT, int kJoinThreads>
 __global__ void __launch_bounds__(kJoinThreads)
 embedding_join_kernel(const Sums s, bool vec) {
+  constexpr int kJoinRanges = kJoinThreads / kJoinLanes;
   __shared__ float4 sh[kJoinRanges][kJoinLanes];
   begin_after_previous();
   const int64_t chunk = blockIdx.x, last = (chunk + 1) * s.chunk - 1;
@@ -861,8 +873,9 @@ cudaError_t backward(const EmbeddingArgs& a, char* scratch, int sms, cudaStream_
   if (mark) mark(kEmbeddingSumsK, 1, stream);
   if (e != cudaSuccess || chunks == 1) return e;
   if (mark) mark(kEmbeddingJoinK, 0, stream);
-  e = launch(true, embedding_join_kernel<DT>, (unsigned)chunks, kJoinThreads, 0, stream, s,
-             a.dim % 4 == 0);
+  const bool narrow = a.dim <= kNarrow;
+  e = launch(true, narrow ? embedding_join_kernel<DT, 64> : embedding_join_kernel<DT, 256>,
+             (unsigned)chunks, narrow ? 64 : 256, 0, stream, s, a.dim % 4 == 0);
   if (mark) mark(kEmbeddingJoinK, 1, stream);
   return e;
 }

@@ -855,6 +855,8 @@ xent_join_kernel(const float2* partial, int strips, int64_t tokens, int64_t voca
   const int64_t row = (int64_t)blockIdx.x * 32 + lane;
   const float2 none = make_float2(kLowest, 0.0f);
   begin_after_previous();
+  const int64_t mine = (int64_t)blockIdx.x * 32 + warp;
+  TeacherLoss of_teacher(teacher, mine, TEACHER && mine < tokens);
   float2 s = none;
   for (int i = warp; i < strips; i += 8 * 32) {
     float2 p[8];
@@ -873,12 +875,11 @@ xent_join_kernel(const float2* partial, int strips, int64_t tokens, int64_t voca
   for (int o = 16; o > 0; o >>= 1)
     s = join_stats(s, make_float2(__shfl_xor_sync(0xFFFFFFFFu, s.x, o),
                                   __shfl_xor_sync(0xFFFFFFFFu, s.y, o)), factor);
-  const int64_t mine = (int64_t)blockIdx.x * 32 + warp;
   if constexpr (TEACHER) {
     if (mine >= tokens) return;
     const float l = __fdiv_rn(s.x, teacher.temperature) + logf(s.y);
     const long long t = target[mine];
-    const float sum = teacher_loss(teacher, mine, l);
+    const float sum = of_teacher(teacher, mine, l);
     if (lane == 0) {
       lse[mine] = l;
       loss[mine] = t == ignore ? 0.0f : t < vocab ? sum : __uint_as_float(0x7FC00000u);
@@ -1203,14 +1204,6 @@ TeacherScratch teacher_scratch(Layout& l, const XentArgs& a, int64_t tokens, boo
   return s;
 }
 
-template <int DT>
-auto teacher_of(int k) {
-  return k <= 32    ? teacher_kernel<DT, 1>
-         : k <= 64  ? teacher_kernel<DT, 2>
-         : k <= 128 ? teacher_kernel<DT, 4>
-                    : teacher_kernel<DT, 8>;
-}
-
 // Makes the entries of the tokens from t0 on and returns what the other kernels
 // read of them.
 cudaError_t make_teacher(const XentArgs& a, int64_t t0, int64_t tokens, char* scratch,
@@ -1223,14 +1216,13 @@ cudaError_t make_teacher(const XentArgs& a, int64_t t0, int64_t tokens, char* sc
         teacher_tiles(a), a.temperature, (float)(1.4426950408889634 / (double)a.temperature)};
   const char* logits = static_cast<const char*>(a.logits) +
                        t0 * a.k * (a.logit_dtype == kF32 ? 4 : 2);
+  int group = 1;
+  while (32 * group < a.k) group *= 2;
   if (mark) mark(kXentTeacherK, 0, stream);
   const cudaError_t e =
-      launch(true, a.logit_dtype == kF32    ? teacher_of<kF32>(a.k)
-                   : a.logit_dtype == kBF16 ? teacher_of<kBF16>(a.k)
-                                            : teacher_of<kF16>(a.k),
-             (unsigned)((tokens + kTeacherWarps - 1) / kTeacherWarps), 32 * kTeacherWarps, 0,
-             stream, reinterpret_cast<const long long*>(a.ids) + t0 * a.k, (const void*)logits,
-             tokens, a.vocab, *t, words, q, start,
+      launch(true, teacher_kernel, (unsigned)((tokens * group + kTeacherWarps - 1) / kTeacherWarps),
+             32 * kTeacherWarps, 0, stream, reinterpret_cast<const long long*>(a.ids) + t0 * a.k,
+             (const void*)logits, a.logit_dtype, tokens, a.vocab, group, *t, words, q, start,
              reinterpret_cast<long long*>(scratch + s.state), forward ? nullptr : a.dloss,
              reinterpret_cast<float*>(scratch + s.dloss));
   if (mark) mark(kXentTeacherK, 1, stream);

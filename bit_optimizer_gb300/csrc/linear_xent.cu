@@ -265,19 +265,20 @@ struct Strip {
 struct RowIn {
   long long target;
   float lse, dloss, top;
-  int entry, end;          // of the row's teacher's, in this tile
+  int entry, end;          // of the row's teacher's, in this strip
 };
 
+// strip: the thread's columns, in strips of the whole product.
 template <bool TEACHER>
 __device__ __forceinline__ RowIn row_in(const GemmShape& g, const GemmOut& o, int64_t row,
-                                        int tile_n) {
+                                        int strip) {
   RowIn in = {-1, 0.0f, 0.0f, 0.0f, 0, 0};
   if (g.mode == kStats || g.mode == kProbs) {
     if (row < o.tokens) {
       if (!TEACHER || g.mode == kProbs) in.target = o.target[row];
       if (TEACHER) {
-        const uint16_t* s = o.teacher.start + row * (o.teacher.tiles + 1) + g.v0 / kTeacherTile +
-                            tile_n;
+        const uint16_t* s = o.teacher.start + row * (o.teacher.strips + 1) +
+                            g.v0 / kTeacherStrip + strip;
         in.entry = s[0];
         in.end = s[1];
       }
@@ -341,11 +342,11 @@ __device__ __forceinline__ void stats_strip(const GemmOut& o, const Strip& t, co
                       ? (int)(target - t.c0) : -1;
   const int valid = (int)min((int64_t)t.cols, o.vocab - t.c0);   // may be <= 0
   Stats s;
-  Entries entries(o.teacher.words + t.row * o.teacher.k, in.entry, in.end, t.c0);
+  Entries<false> entries(o.teacher, t.row, in.entry, in.end, t.c0);
   tmem_columns(t.tmem, t.cols, [&](int c, uint32_t (&r)[32], uint32_t (&q)[32]) {
     if constexpr (TEACHER)
       entries.take(c, [&](int j) { return __uint_as_float(j < 32 ? r[j & 31] : q[j & 31]); },
-                   [&](int first, int end, int, float z) {
+                   [&](int first, int end, float, int, float z) {
                      for (int i = first; i < end; ++i) o.teacher.z[t.row * o.teacher.k + i] = z;
                    });
     s.add(r, valid - c, TEACHER ? -1 : rel - c, TEACHER ? o.teacher.factor : kLog2eF);
@@ -387,7 +388,7 @@ struct SwappedStats {
       if constexpr (TEACHER) {
         if (token < o.tokens) {
           const Teacher& t = o.teacher;
-          const uint16_t* start = t.start + token * (t.tiles + 1) + v0 / kTeacherTile;
+          const uint16_t* start = t.start + token * (t.strips + 1) + v0 / kTeacherStrip;
           const int end = valid > 0 ? start[1] : 0;
           for (int i = valid > 0 ? start[0] : 0; i < end; ++i) {
             const int64_t row = (int64_t)t.words[token * t.k + i] - v0;
@@ -450,7 +451,7 @@ __device__ __forceinline__ void probs_strip(const GemmShape& g, const GemmOut& o
   const int64_t row0 = t.row - (threadIdx.x & 31);
   uint16_t* const out = g.probs + row0 * o.piece + t.c0;
   const int rows = (int)min((int64_t)32, o.tokens - row0);
-  Entries entries(o.teacher.words + t.row * o.teacher.k, in.entry, in.end, g.v0 + t.c0);
+  Entries<true> entries(o.teacher, t.row, in.entry, in.end, g.v0 + t.c0);
   tmem_columns(t.tmem, t.cols, [&](int c, uint32_t (&r)[32], uint32_t (&q)[32]) {
     float v[64];
 #pragma unroll
@@ -479,10 +480,9 @@ __device__ __forceinline__ void probs_strip(const GemmShape& g, const GemmOut& o
     if constexpr (TEACHER) {
       const int lane = threadIdx.x & 31;
       store_rows16<BF16>(turn, out + c, o.piece, rows, 64, s, [&] {
-        entries.take(c, [&](int j) { return v[j]; }, [&](int first, int end, int i, float p) {
-          for (int j = first; j < end; ++j) p -= o.teacher.q[t.row * o.teacher.k + j];
+        entries.take(c, [&](int j) { return v[j]; }, [&](int, int, float share, int i, float p) {
           reinterpret_cast<uint16_t*>(&turn.at(lane, i >> 3))[i & 7] =
-              (uint16_t)pack16<BF16>(zero ? 0.0f : p * k, 0.0f);
+              (uint16_t)pack16<BF16>(zero ? 0.0f : (p - share) * k, 0.0f);
         });
       });
     } else {
@@ -795,7 +795,8 @@ gemm_kernel(const __grid_constant__ GemmArgs args) {
       if (t->work == kNoWork) return true;
       reader.done(bar);
       *in = row_in<TEACHER>(args.job[t->job].shape, args.out,
-                            (int64_t)t->m * kTileM + rank * kHalfM + (threadIdx.x & 127), t->n);
+                            (int64_t)t->m * kTileM + rank * kHalfM + (threadIdx.x & 127),
+                            2 * t->n + warp / 4);
       return true;
     };
     Tile t;
@@ -1188,17 +1189,17 @@ class Layout {
 struct TeacherScratch {
   size_t words, q, z, start, state, dloss;
 };
-int teacher_tiles(const XentArgs& a) {
-  return (int)((a.vocab + kTeacherTile - 1) / kTeacherTile);
+int teacher_strips(const XentArgs& a) {
+  return (int)(up(a.vocab, kTileN) / kTeacherStrip);
 }
-static_assert(kTeacherTile == kTileN && kTeacherTile == kTileM, "a tile's entries");
+static_assert(kTeacherStrip == kTileN / 2, "an epilogue thread's columns");
 TeacherScratch teacher_scratch(Layout& l, const XentArgs& a, int64_t tokens, bool forward) {
   TeacherScratch s = {};
   if (a.ids == nullptr) return s;
   s.words = l.take(tokens * a.k * 4);
   s.q = l.take(tokens * a.k * 4);
   if (forward) s.z = l.take(tokens * a.k * 4);
-  s.start = l.take(tokens * (teacher_tiles(a) + 1) * 2);
+  s.start = l.take(tokens * (teacher_strips(a) + 1) * 2);
   s.state = l.take(tokens * 8);
   if (!forward) s.dloss = l.take(tokens * 4);
   return s;
@@ -1213,7 +1214,7 @@ cudaError_t make_teacher(const XentArgs& a, int64_t t0, int64_t tokens, char* sc
   float* q = reinterpret_cast<float*>(scratch + s.q);
   uint16_t* start = reinterpret_cast<uint16_t*>(scratch + s.start);
   *t = {words, q, start, forward ? reinterpret_cast<float*>(scratch + s.z) : nullptr, a.k,
-        teacher_tiles(a), a.temperature, (float)(1.4426950408889634 / (double)a.temperature)};
+        teacher_strips(a), a.temperature, (float)(1.4426950408889634 / (double)a.temperature)};
   const char* logits = static_cast<const char*>(a.logits) +
                        t0 * a.k * (a.logit_dtype == kF32 ? 4 : 2);
   int group = 1;

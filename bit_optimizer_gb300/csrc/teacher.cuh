@@ -3,10 +3,10 @@
 // tiles' epilogues, which meet them in the order of the vocabulary.
 //
 // The entries of a token are its words with their share q of the softmax over
-// the given ones, sorted by word; `start` says where in them each tile of
-// kTeacherTile words begins, so that a thread, whose row is a token, has its
-// tile's entries without a search.  On average a tile meets very few (64 of 50257
-// words: 0.33 of a row's 256), so a column that has one is picked out of the
+// the given ones, sorted by word; `start` says where in them each strip of
+// kTeacherStrip words begins, so that a thread, whose row is a token, has its
+// strip's entries without a search.  On average a strip meets very few (64 of 50257
+// words: 0.16 of a row's 128), so a column that has one is picked out of the
 // thread's registers by the six bits of its place among 64 (63 selections for a
 // warp's 32 rows), instead of each column being compared with a list.  Read from
 // TMEM a column at a time, with the entries' loads behind one another, they cost
@@ -18,7 +18,7 @@
 namespace fp8opt {
 namespace {
 
-constexpr int kTeacherTile = 256;
+constexpr int kTeacherStrip = 128;
 
 // What a token's target stands for in the kernels that the cross entropy shares:
 // one that counts, one without entries (ignored), one whose loss is NaN (vocab).
@@ -27,31 +27,41 @@ constexpr long long kTeacherLive = 0, kTeacherNone = -1;
 struct Teacher {
   const uint32_t* words;     // [token][k], sorted
   const float* q;            // [token][k]
-  const uint16_t* start;     // [token][tiles + 1]
+  const uint16_t* start;     // [token][strips + 1]
   float* z;                  // [token][k]: the words' logits (forward)
-  int k, tiles;
+  int k, strips;
   float temperature;
   float factor;              // log2(e) / temperature
 };
 
-// A row's entries in the columns of a strip, in order.
+// A row's entries in the columns of a strip, in order: the one that comes next and
+// the one behind it, which is read while the first is waited for.
 constexpr uint32_t kNoColumn = 0xFFFFFFFFu;
+template <bool SHARES>
 struct Entries {
   const uint32_t* words;     // the token's
-  int at, end;
+  const float* q;
+  int at, end;               // the entry that comes next, behind the strip's last
   int64_t c0;                // the strip's first word
-  uint32_t column;           // of entry `at`, from c0 on; kNoColumn behind the last
-  __device__ __forceinline__ void find() {
-    column = at < end ? (uint32_t)(words[at] - c0) : kNoColumn;
+  uint32_t column, column1;  // from c0 on; kNoColumn behind the last
+  float share, share1;
+  __device__ __forceinline__ void read(int i, uint32_t* column, float* share) const {
+    *column = kNoColumn;
+    if (i < end) {
+      *column = (uint32_t)(words[i] - c0);
+      if (SHARES) *share = q[i];
+    }
   }
-  __device__ __forceinline__ Entries(const uint32_t* w, int first, int last, int64_t c)
-      : words(w), at(first), end(last), c0(c) {
-    while (at < end && (int64_t)words[at] < c0) ++at;    // (of the tile's other half)
-    find();
+  __device__ __forceinline__ Entries(const Teacher& t, int64_t token, int first, int last,
+                                     int64_t c)
+      : words(t.words + token * t.k), q(t.q + token * t.k), at(first), end(last), c0(c),
+        share(0.0f), share1(0.0f) {
+    read(at, &column, &share);
+    read(at + 1, &column1, &share1);
   }
-  // Calls f(first entry, entry behind the last, column - c, value) for each of the
-  // row's words among the columns [c, c + 64), whose values are get(0 .. 63).  The
-  // whole warp calls it, from left to right.
+  // Calls f(first entry, entry behind the last, their shares' sum, column - c, value)
+  // for each of the row's words among the columns [c, c + 64), whose values are
+  // get(0 .. 63).  The whole warp calls it, from left to right.
   template <class G, class F>
   __device__ __forceinline__ void take(uint32_t c, G get, F f) {
     while (__any_sync(0xFFFFFFFFu, column - c < 64u)) {
@@ -67,11 +77,15 @@ struct Entries {
       }
       if (mine) {
         const int first = at;
+        float sum = 0.0f;
         do {
+          if (SHARES) sum += share;
+          column = column1;
+          share = share1;
           ++at;
-          find();
+          read(at + 1, &column1, &share1);
         } while (column - c == i);
-        f(first, at, (int)i, v[0]);
+        f(first, at, sum, (int)i, v[0]);
       }
     }
   }
@@ -157,27 +171,31 @@ teacher_kernel(const long long* ids, const void* logits, int logit_dtype, int64_
   const int mine = __popc(__ballot_sync(0xFFFFFFFFu, id != kOut));
   if (lane == 0) sh_count[warp] = mine;
   // sorted by word, a bitonic network: entry j to thread j, shuffles within a warp
-  for (int k = 2; k <= 32 * group; k *= 2) {
-    for (int d = k / 2; d > 0; d /= 2) {
-      uint32_t other;
-      float other_share;
-      if (d < 32) {
-        other = __shfl_xor_sync(0xFFFFFFFFu, id, d);
-        other_share = __shfl_xor_sync(0xFFFFFFFFu, share, d);
-      } else {
-        __syncthreads();
-        sh_word[threadIdx.x] = id;
-        sh_share[threadIdx.x] = share;
-        __syncthreads();
-        other = sh_word[threadIdx.x ^ d];
-        other_share = sh_share[threadIdx.x ^ d];
-      }
-      const bool least = ((j & k) == 0) == ((j & d) == 0);
-      if (least ? other < id : other > id) {
-        id = other;
-        share = other_share;
-      }
+  const auto exchange = [&](int k, int d, uint32_t other, float other_share) {
+    const bool least = ((j & k) == 0) == ((j & d) == 0);
+    if (least ? other < id : other > id) {
+      id = other;
+      share = other_share;
     }
+  };
+  const auto shuffles = [&](int k, int most) {
+#pragma unroll
+    for (int d = 16; d > 0; d /= 2)
+      if (d <= most)
+        exchange(k, d, __shfl_xor_sync(0xFFFFFFFFu, id, d),
+                 __shfl_xor_sync(0xFFFFFFFFu, share, d));
+  };
+#pragma unroll
+  for (int k = 2; k <= 32; k *= 2) shuffles(k, k / 2);
+  for (int k = 64; k <= 32 * group; k *= 2) {
+    for (int d = k / 2; d >= 32; d /= 2) {
+      __syncthreads();
+      sh_word[threadIdx.x] = id;
+      sh_share[threadIdx.x] = share;
+      __syncthreads();
+      exchange(k, d, sh_word[threadIdx.x ^ d], sh_share[threadIdx.x ^ d]);
+    }
+    shuffles(k, 16);
   }
   __syncthreads();
   uint32_t* const word = sh_word + 32 * first;
@@ -190,13 +208,13 @@ teacher_kernel(const long long* ids, const void* logits, int logit_dtype, int64_
   }
   __syncthreads();
   if (!live) return;
-  // the number of words below each tile's first one
+  // the number of words below each strip's first one
   const int highest = count > 0 ? 1 << (31 - __clz(count)) : 0;
-  for (int64_t tile = j; tile <= t.tiles; tile += 32 * group) {
+  for (int64_t strip = j; strip <= t.strips; strip += 32 * group) {
     int n = 0;
     for (int step = highest; step > 0; step >>= 1)
-      if (n + step <= count && (int64_t)word[n + step - 1] < tile * kTeacherTile) n += step;
-    start[token * (t.tiles + 1) + tile] = (uint16_t)n;
+      if (n + step <= count && (int64_t)word[n + step - 1] < strip * kTeacherStrip) n += step;
+    start[token * (t.strips + 1) + strip] = (uint16_t)n;
   }
   if (j == 0) {
     state[token] = wrong ? (long long)vocab : dead ? kTeacherNone : kTeacherLive;
@@ -212,7 +230,7 @@ struct TeacherLoss {
   __device__ __forceinline__ TeacherLoss(const Teacher& t, int64_t token, bool any) {
     const int lane = threadIdx.x & 31;
     if (!any) return;
-    count = t.start[token * (t.tiles + 1) + t.tiles];
+    count = t.start[token * (t.strips + 1) + t.strips];
     if (lane < t.k) {      // (what is behind `count` was never written, and is not used)
       q = t.q[token * t.k + lane];
       z = __ldcg(t.z + token * t.k + lane);

@@ -741,7 +741,7 @@ FP8OPT_API int fp8_linear_xent_backward(const float *dloss, const void *x,
  *   dx = dz w,  dw = dz^T x  (of type dtype, both overwritten),
  * by pieces of the vocabulary and with the treatment of tokens that take no part
  * as in fp8_linear_xent_backward, whose sizes, scratch and waits hold here too.
- * Scratch besides: 8 bytes an entry (forward 12), 2 bytes for every 256 words of
+ * Scratch besides: 8 bytes an entry (forward 12), 2 bytes for every 128 words of
  * each token (forward of at most 65536 tokens at a time), 12 bytes a token.
  *
  * k in [1, FP8OPT_MOST_TEACHER]; temperature in [2^-20, 2^20].  No gradient for

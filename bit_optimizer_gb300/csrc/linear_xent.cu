@@ -344,13 +344,14 @@ __device__ __forceinline__ void stats_strip(const GemmOut& o, const Strip& t, co
   Stats s;
   Entries<false> entries(o.teacher, t.row, in.entry, in.end, t.c0);
   tmem_columns(t.tmem, t.cols, [&](int c, uint32_t (&r)[32], uint32_t (&q)[32]) {
+    s.add(r, valid - c, TEACHER ? -1 : rel - c, TEACHER ? o.teacher.factor : kLog2eF);
+    s.add(q, valid - c - 32, TEACHER ? -1 : rel - c - 32, TEACHER ? o.teacher.factor : kLog2eF);
+    // (after the exponentials, which take as long as the first entries' loads)
     if constexpr (TEACHER)
       entries.take(c, [&](int j) { return __uint_as_float(j < 32 ? r[j & 31] : q[j & 31]); },
                    [&](int first, int end, float, int, float z) {
                      for (int i = first; i < end; ++i) o.teacher.z[t.row * o.teacher.k + i] = z;
                    });
-    s.add(r, valid - c, TEACHER ? -1 : rel - c, TEACHER ? o.teacher.factor : kLog2eF);
-    s.add(q, valid - c - 32, TEACHER ? -1 : rel - c - 32, TEACHER ? o.teacher.factor : kLog2eF);
   });
   if (t.row < o.tokens) {
     o.partial[(int64_t)t.index * o.tokens + t.row] = make_float2(s.top, s.sum);
@@ -386,7 +387,7 @@ struct SwappedStats {
         r[j] = reinterpret_cast<const uint32_t*>(&turn.at(j, lane >> 2))[lane & 3];
       const int64_t token = c + lane;
       if constexpr (TEACHER) {
-        if (token < o.tokens) {
+        if (token < o.tokens && o.teacher.words != nullptr) {
           const Teacher& t = o.teacher;
           const uint16_t* start = t.start + token * (t.strips + 1) + v0 / kTeacherStrip;
           const int end = valid > 0 ? start[1] : 0;
@@ -896,6 +897,106 @@ xent_join_kernel(const float2* partial, int strips, int64_t tokens, int64_t voca
   }
 }
 
+// Distillation of few tokens with few entries: the statistics of a token joined and
+// its loss, without entries in order or a search for them in the tiles.  A CTA
+// takes a token, a warp an entry: its logit is x w^T again, from rows of w that the
+// product has left in L2.
+template <bool BF16>
+__global__ void __launch_bounds__(1024)
+xent_few_kernel(const float2* partial, int strips, int64_t tokens, int64_t vocab, const char* x,
+                const char* w, int64_t pitch, const long long* ids, const void* logits,
+                int logit_dtype, const Teacher t, float* __restrict__ loss,
+                float* __restrict__ lse) {
+  __shared__ long long sh_id[kTeacherMost];
+  __shared__ float sh_logit[kTeacherMost], sh_z[kTeacherMost];
+  __shared__ float2 sh[32];
+  begin_after_previous();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t token = blockIdx.x;
+  float2 s = make_float2(kLowest, 0.0f);
+  if ((int)threadIdx.x < strips) s = __ldcg(partial + threadIdx.x * tokens + token);
+  for (int i = threadIdx.x + 1024; i < strips; i += 1024)
+    s = join_stats(s, __ldcg(partial + (int64_t)i * tokens + token), t.factor);
+  if ((int)threadIdx.x < t.k) {
+    const int64_t at = token * t.k + threadIdx.x;
+    sh_id[threadIdx.x] = ids[at];
+    sh_logit[threadIdx.x] = logit_dtype == kF32    ? teacher_logit<kF32>(logits, at)
+                            : logit_dtype == kBF16 ? teacher_logit<kBF16>(logits, at)
+                                                   : teacher_logit<kF16>(logits, at);
+  }
+  __syncthreads();
+  const uint4* const a = reinterpret_cast<const uint4*>(x + token * pitch * 2);
+  for (int j = warp; j < t.k; j += 32) {
+    const long long id = sh_id[j];
+    if (id < 0 || id >= vocab) continue;
+    const uint4* const b = reinterpret_cast<const uint4*>(w + id * pitch * 2);
+    float2 z = make_float2(0.0f, 0.0f);
+#pragma unroll 4
+    for (int64_t c = lane; c < pitch / 8; c += 32) {
+      const uint4 u = a[c], v = b[c];
+      const uint32_t p[4] = {u.x, u.y, u.z, u.w}, q[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float2 f = BF16 ? make_float2(__uint_as_float(p[k] << 16),
+                                            __uint_as_float(p[k] & 0xFFFF0000u)) : h2_to_f2(p[k]);
+        const float2 g = BF16 ? make_float2(__uint_as_float(q[k] << 16),
+                                            __uint_as_float(q[k] & 0xFFFF0000u)) : h2_to_f2(q[k]);
+        z = make_float2(fmaf(f.x, g.x, z.x), fmaf(f.y, g.y, z.y));
+      }
+    }
+    z.x += z.y;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) z.x += __shfl_xor_sync(0xFFFFFFFFu, z.x, o);
+    if (lane == 0) sh_z[j] = z.x;
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1)
+    s = join_stats(s, make_float2(__shfl_xor_sync(0xFFFFFFFFu, s.x, o),
+                                  __shfl_xor_sync(0xFFFFFFFFu, s.y, o)), t.factor);
+  if (lane == 0) sh[warp] = s;
+  __syncthreads();
+  if (warp > 0) return;
+  s = sh[lane];
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1)
+    s = join_stats(s, make_float2(__shfl_xor_sync(0xFFFFFFFFu, s.x, o),
+                                  __shfl_xor_sync(0xFFFFFFFFu, s.y, o)), t.factor);
+  const float l = __fdiv_rn(s.x, t.temperature) + logf(s.y);
+  // (teacher_kernel's steps)
+  const float none = __uint_as_float(0xFF800000u);
+  float top = none;
+  bool wrong = false;
+  for (int j = lane; j < t.k; j += 32) {
+    const bool given = sh_id[j] >= 0;
+    wrong |= given && (sh_id[j] >= vocab || sh_logit[j] != sh_logit[j]);
+    if (!given) sh_logit[j] = none;
+    top = fmaxf(top, sh_logit[j]);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+  wrong = __any_sync(0xFFFFFFFFu, wrong || top == -none);
+  const bool dead = !wrong && top == none;
+  float sum = 0.0f, of = 0.0f;
+  if (!wrong && !dead) {
+    for (int j = lane; j < t.k; j += 32) {
+      sh_logit[j] = expf((sh_logit[j] - top) / t.temperature);
+      sum += sh_logit[j];
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+    for (int j = lane; j < t.k; j += 32) {
+      const float q = __fdiv_rn(sh_logit[j], sum);
+      if (q != 0.0f) of += q * (logf(q) - (__fdiv_rn(sh_z[j], t.temperature) - l));
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) of += __shfl_xor_sync(0xFFFFFFFFu, of, o);
+  }
+  if (lane == 0) {
+    lse[token] = l;
+    loss[token] = wrong ? __uint_as_float(0x7FC00000u) : of;
+  }
+}
+
 // Threads and CTAs an SM of the copying kernel: every CTA looks through all tokens'
 // dloss, so few large ones (65000 x 1024: 265 us with eight of 256 threads, 103;
 // 2048 x 768: 10.1 and 8.5).
@@ -1205,16 +1306,20 @@ TeacherScratch teacher_scratch(Layout& l, const XentArgs& a, int64_t tokens, boo
   return s;
 }
 
+float teacher_factor(const XentArgs& a) {
+  return (float)(1.4426950408889634 / (double)a.temperature);
+}
+
 // Makes the entries of the tokens from t0 on and returns what the other kernels
-// read of them.
+// read of them; and `n_zeros` zeros.
 cudaError_t make_teacher(const XentArgs& a, int64_t t0, int64_t tokens, char* scratch,
                          const TeacherScratch& s, bool forward, Teacher* t, cudaStream_t stream,
-                         LaunchMark mark) {
+                         LaunchMark mark, int* zeros = nullptr, int n_zeros = 0) {
   uint32_t* words = reinterpret_cast<uint32_t*>(scratch + s.words);
   float* q = reinterpret_cast<float*>(scratch + s.q);
   uint16_t* start = reinterpret_cast<uint16_t*>(scratch + s.start);
   *t = {words, q, start, forward ? reinterpret_cast<float*>(scratch + s.z) : nullptr, a.k,
-        teacher_strips(a), a.temperature, (float)(1.4426950408889634 / (double)a.temperature)};
+        teacher_strips(a), a.temperature, teacher_factor(a)};
   const char* logits = static_cast<const char*>(a.logits) +
                        t0 * a.k * (a.logit_dtype == kF32 ? 4 : 2);
   int group = 1;
@@ -1225,7 +1330,7 @@ cudaError_t make_teacher(const XentArgs& a, int64_t t0, int64_t tokens, char* sc
              32 * kTeacherWarps, 0, stream, reinterpret_cast<const long long*>(a.ids) + t0 * a.k,
              (const void*)logits, a.logit_dtype, tokens, a.vocab, group, *t, words, q, start,
              reinterpret_cast<long long*>(scratch + s.state), forward ? nullptr : a.dloss,
-             reinterpret_cast<float*>(scratch + s.dloss));
+             reinterpret_cast<float*>(scratch + s.dloss), zeros, n_zeros);
   if (mark) mark(kXentTeacherK, 1, stream);
   return e;
 }
@@ -1235,11 +1340,15 @@ cudaError_t make_teacher(const XentArgs& a, int64_t t0, int64_t tokens, char* sc
 // which is all that has to be read.  24 x 768 x 50257: 19.9 us, 27.3 with the
 // tokens as rows (mostly past x's end); 128 x 768 x 200000: 56 us against 75.
 constexpr int64_t kSwapTokens = 128;
+// What xent_few_kernel reads of w again: rows in all, and elements for a token (a
+// warp reads the rows of its entries one after another).
+constexpr int64_t kFewEntries = 4096, kFewElements = 65536;
 
 struct ForwardScratch {
   size_t x = 0, w = 0, partial = 0, logit = 0, bytes = 0;
   TeacherScratch teacher;
   bool swapped = false;
+  bool few = false;        // xent_few_kernel's
   int64_t strips = 0;
 };
 ForwardScratch forward_scratch(const XentArgs& a, int sms) {
@@ -1254,7 +1363,9 @@ ForwardScratch forward_scratch(const XentArgs& a, int sms) {
                        : 2 * (up(a.vocab, kTileN) / kTileN);
   s.partial = l.take(s.strips * tokens * 8);
   s.logit = l.take(tokens * 4);
-  s.teacher = teacher_scratch(l, a, tokens, true);
+  s.few = a.ids != nullptr && s.swapped && a.rows * a.k <= kFewEntries &&
+          a.k * pitch <= kFewElements;
+  if (!s.few) s.teacher = teacher_scratch(l, a, tokens, true);
   s.bytes = l.bytes();
   return s;
 }
@@ -1321,7 +1432,11 @@ cudaError_t launch_xent_forward(const XentArgs& a, char* scratch, int* error, in
     g.out.dim = a.dim;
     g.out.target = reinterpret_cast<const long long*>(a.target) + t0;
     g.out.ignore = a.ignore;
-    if (a.ids != nullptr) {
+    if (s.few) {
+      g.out.teacher.k = a.k;
+      g.out.teacher.temperature = a.temperature;
+      g.out.teacher.factor = teacher_factor(a);
+    } else if (a.ids != nullptr) {
       e = make_teacher(a, t0, tokens, scratch, s.teacher, true, &g.out.teacher, stream, mark);
       if (e != cudaSuccess) break;
       g.out.target = reinterpret_cast<const long long*>(scratch + s.teacher.state);
@@ -1341,7 +1456,12 @@ cudaError_t launch_xent_forward(const XentArgs& a, char* scratch, int* error, in
     if (mark) mark(kXentLogitsK, 1, stream);
     if (e != cudaSuccess) break;
     if (mark) mark(kXentJoinK, 0, stream);
-    e = launch(true, a.ids != nullptr ? xent_join_kernel<true> : xent_join_kernel<false>,
+    if (s.few)
+      e = launch(true, bf16 ? xent_few_kernel<true> : xent_few_kernel<false>, (unsigned)tokens,
+                 1024, 0, stream, (const float2*)g.out.partial, (int)s.strips, tokens, a.vocab, x,
+                 w, pitch, reinterpret_cast<const long long*>(a.ids), a.logits, a.logit_dtype,
+                 g.out.teacher, a.loss, a.lse_out);
+    else e = launch(true, a.ids != nullptr ? xent_join_kernel<true> : xent_join_kernel<false>,
                (unsigned)((tokens + 31) / 32), 1024, 0, stream, (const float2*)g.out.partial,
                (int)s.strips, tokens, a.vocab, g.out.target, g.out.ignore,
                (const float*)g.out.target_logit, g.out.teacher, a.loss + t0, a.lse_out + t0);
@@ -1363,7 +1483,8 @@ cudaError_t launch_xent_backward(const XentArgs& a, char* scratch, int* error, i
   Teacher teacher = {};
   cudaError_t e = cudaSuccess;
   if (a.ids != nullptr) {
-    e = make_teacher(a, 0, a.rows, scratch, s.teacher, false, &teacher, stream, mark);
+    e = make_teacher(a, 0, a.rows, scratch, s.teacher, false, &teacher, stream, mark,
+                     reinterpret_cast<int*>(scratch + s.next), (int)s.pieces + 1);
     if (e != cudaSuccess) return e;
     target = reinterpret_cast<const long long*>(scratch + s.teacher.state);
     ignore = kTeacherNone;
@@ -1376,7 +1497,8 @@ cudaError_t launch_xent_backward(const XentArgs& a, char* scratch, int* error, i
   const char* w = static_cast<const char*>(a.w);
   int* next = reinterpret_cast<int*>(scratch + s.next);
   float* top = reinterpret_cast<float*>(scratch + s.top);
-  e = cudaMemsetAsync(next, 0, (size_t)(s.pieces + 1) * 4, stream);
+  // (with a teacher, its kernel has done so)
+  if (a.ids == nullptr) e = cudaMemsetAsync(next, 0, (size_t)(s.pieces + 1) * 4, stream);
   if (mark) mark(kXentPrepareK, 0, stream);
   if (e == cudaSuccess)
     e = copy_rows(a.x, a.rows, a.dim, pitch, bf16, scratch + s.x, sms, stream,

@@ -91,8 +91,9 @@ struct Entries {
   }
 };
 
-// Of a CTA.
-constexpr int kTeacherWarps = 8;
+// Most entries of a token, and a CTA's warps.
+constexpr int kTeacherMost = 256, kTeacherWarps = 8;
+static_assert(kTeacherMost == 32 * kTeacherWarps, "a thread to an entry");
 
 template <int DT>
 __device__ __forceinline__ float teacher_logit(const void* p, int64_t i) {
@@ -104,7 +105,7 @@ __device__ __forceinline__ float teacher_logit(const void* p, int64_t i) {
 // The entries of `tokens` tokens from their ids and logits, a thread to an entry and
 // `group` warps (1, 2, 4 or 8) to a token.  Entries whose id is negative are not
 // given, and those whose share is 0 (of a logit of -inf) left out.  Backward, dloss
-// is divided by the temperature.
+// is divided by the temperature.  `zeros`: words to set to zero besides.
 //
 // Bound by latency: with a warp to a token a single one of 197 entries took 19 us.
 // Many tokens of many entries: 2279 of 217, 28 us by counting each entry's smaller
@@ -114,7 +115,7 @@ teacher_kernel(const long long* ids, const void* logits, int logit_dtype, int64_
                int64_t vocab, int group, const Teacher t, uint32_t* __restrict__ words,
                float* __restrict__ q, uint16_t* __restrict__ start,
                long long* __restrict__ state, const float* dloss,
-               float* __restrict__ dloss_out) {
+               float* __restrict__ dloss_out, int* __restrict__ zeros, int n_zeros) {
   __shared__ uint32_t sh_word[32 * kTeacherWarps];
   __shared__ float sh_share[32 * kTeacherWarps];
   __shared__ float sh_top[kTeacherWarps], sh_sum[kTeacherWarps];
@@ -124,6 +125,8 @@ teacher_kernel(const long long* ids, const void* logits, int logit_dtype, int64_
   const int sub = warp % group, first = warp - sub;      // of the token's warps
   const int64_t token = (int64_t)blockIdx.x * (kTeacherWarps / group) + warp / group;
   const bool live = token < tokens;
+  if (blockIdx.x == 0)
+    for (int i = threadIdx.x; i < n_zeros; i += 32 * kTeacherWarps) zeros[i] = 0;
   const int j = 32 * sub + lane;
   constexpr uint32_t kOut = 0x7FFFFFFFu;    // behind every word
   const float none = __uint_as_float(0xFF800000u);

@@ -27,11 +27,11 @@ constexpr int kCtaThreads = 256, kCtaWarps = kCtaThreads / 32;
 
 // --------------------------------------------------------------- elements
 
+// An element as it was loaded.
 template <int DT>
-__device__ __forceinline__ float load1(const void* p, int64_t i) {
-  if (DT == kF32) return static_cast<const float*>(p)[i];
-  const uint32_t h = static_cast<const uint16_t*>(p)[i];
-  return DT == kBF16 ? __uint_as_float(h << 16) : h2_to_f2(h).x;
+__device__ __forceinline__ float value(uint32_t v) {
+  if (DT == kF32) return __uint_as_float(v);
+  return DT == kBF16 ? __uint_as_float(v << 16) : h2_to_f2(v).x;
 }
 
 // Elements of a lane's 16-byte vector.
@@ -105,27 +105,42 @@ embedding_kernel(const long long* ids, const uint4* w, int64_t rows, int64_t vec
   }
 }
 
-// Rows that start anywhere: a warp takes kRowPart elements of a row.
+// Rows that start anywhere: a warp takes kRowPart elements of a row.  parts: of a
+// row.  (The loads do not depend on whether the id or the column exists, so that
+// all are under way.)
 constexpr int kRowPart = 512;
 template <int DT>
 __global__ void __launch_bounds__(kCtaThreads)
 embedding_any_kernel(const long long* ids, const void* w, int64_t rows, int64_t dim,
-                     int64_t vocab, float scale, void* y) {
+                     int64_t vocab, unsigned parts, float scale, void* y) {
   begin_after_previous();
-  const int64_t parts = (dim + kRowPart - 1) / kRowPart;
-  const int64_t unit = (int64_t)blockIdx.x * kCtaWarps + (threadIdx.x >> 5);
-  const int64_t row = unit / parts, c0 = (unit - row * parts) * kRowPart + (threadIdx.x & 31);
+  const unsigned unit = blockIdx.x * kCtaWarps + (threadIdx.x >> 5);
+  const unsigned row = unit / parts;
+  const int64_t c0 = (int64_t)(unit - row * parts) * kRowPart + (threadIdx.x & 31);
   if (row >= rows) return;
   const long long id = ids[row];
   const bool known = id >= 0 && id < vocab;
-  float e[kRowPart / 32];
+  const int n = (int)min((int64_t)kRowPart, dim - c0);       // of the lane's columns, 32 apart
+  constexpr int kSize = DT == kF32 ? 4 : 2;
+  const char* const from = static_cast<const char*>(w) + ((known ? id : 0) * dim + c0) * kSize;
+  char* const to = static_cast<char*>(y) + ((int64_t)row * dim + c0) * kSize;
+  if (n <= 0) return;
+  uint32_t v[kRowPart / 32];
 #pragma unroll
-  for (int k = 0; k < kRowPart / 32; ++k)
-    e[k] = known && c0 + 32 * k < dim ? load1<DT>(w, id * dim + c0 + 32 * k) * scale
-                                      : __uint_as_float(0x7FC00000u);
+  for (int k = 0; k < kRowPart / 32; ++k) {
+    const char* const p = from + (32 * k < n ? 32 * k * kSize : 0);
+    if (kSize == 4) asm volatile("ld.global.b32 %0, [%1];" : "=r"(v[k]) : "l"(p));
+    else {
+      uint16_t h;
+      asm volatile("ld.global.b16 %0, [%1];" : "=h"(h) : "l"(p));
+      v[k] = h;
+    }
+  }
 #pragma unroll
-  for (int k = 0; k < kRowPart / 32; ++k)
-    if (c0 + 32 * k < dim) store1<DT>(y, row * dim + c0 + 32 * k, e[k]);
+  for (int k = 0; k < kRowPart / 32; ++k) {
+    if (32 * k < n)
+      store1<DT>(to, 32 * k, known ? value<DT>(v[k]) * scale : __uint_as_float(0x7FC00000u));
+  }
 }
 
 // ------------------------------------------------------------------ order
@@ -389,9 +404,9 @@ struct Sums {
   const uint32_t* tokens;
   int64_t n, dim;
   uint32_t vocab;
-  int64_t slices;              // of 32 lanes' columns
+  unsigned slices;             // of 32 lanes' columns
   int chunk;                   // tokens of a warp
-  int64_t sums;                // warps that add; those behind them fill
+  unsigned sums;               // warps that add; those behind them fill
   int group;                   // words of a filling warp; 0: dw is filled already
   const void* dy;
   float scale;
@@ -407,33 +422,41 @@ struct Columns {
   __device__ __forceinline__ Columns(int64_t slice, int64_t d)
       : c(slice * (32 * E) + (threadIdx.x & 31) * (VEC ? E : 1)), dim(d) {}
   // What a row of p has there; anything behind its end, which is not stored.  The
-  // loads do not depend on whether the values count, so that many are under way.
+  // loads do not depend on whether the values count, so that many are under way
+  // (volatile: else the compiler moves each behind the test of its count).
   struct Raw {
-    uint4 v;
-    float e[VEC ? 1 : E];
+    uint32_t v[VEC ? 4 : E];
   };
   __device__ __forceinline__ Raw fetch(const void* p, int64_t row) const {
+    constexpr int kSize = 16 / E;
     Raw r;
+    const char* const from = static_cast<const char*>(p) + (row * dim + (c < dim ? c : 0)) * kSize;
     if constexpr (VEC) {
-      // (volatile: else the compiler moves each load behind the test of its count)
       asm volatile("ld.global.cs.v4.u32 {%0, %1, %2, %3}, [%4];"
-                   : "=r"(r.v.x), "=r"(r.v.y), "=r"(r.v.z), "=r"(r.v.w)
-                   : "l"(static_cast<const char*>(p) +
-                         (row * dim + (c < dim ? c : 0)) * (16 / E)));
+                   : "=r"(r.v[0]), "=r"(r.v[1]), "=r"(r.v[2]), "=r"(r.v[3])
+                   : "l"(from));
     } else {
 #pragma unroll
-      for (int j = 0; j < E; ++j)
-        r.e[j] = load1<DT>(p, row * dim + (c + j * kStep < dim ? c + j * kStep : 0));
+      for (int j = 0; j < E; ++j) {
+        const char* const at = from + (c + j * kStep < dim ? j * kStep * kSize : 0);
+        if constexpr (kSize == 4) {
+          asm volatile("ld.global.b32 %0, [%1];" : "=r"(r.v[j]) : "l"(at));
+        } else {
+          uint16_t h;
+          asm volatile("ld.global.b16 %0, [%1];" : "=h"(h) : "l"(at));
+          r.v[j] = h;
+        }
+      }
     }
     return r;
   }
   static __device__ __forceinline__ void add(const Raw& r, bool counts, float (&sum)[E]) {
     float e[E];
     if constexpr (VEC) {
-      unpack<DT>(r.v, e);
+      unpack<DT>(make_uint4(r.v[0], r.v[1], r.v[2], r.v[3]), e);
     } else {
 #pragma unroll
-      for (int j = 0; j < E; ++j) e[j] = r.e[j];
+      for (int j = 0; j < E; ++j) e[j] = value<DT>(r.v[j]);
     }
 #pragma unroll
     for (int j = 0; j < E; ++j) sum[j] += counts ? e[j] : 0.0f;
@@ -467,7 +490,7 @@ __device__ __forceinline__ void fill_absent(const Sums& s, int64_t v0) {
   const float zero[kPer<DT>] = {};
   for (; absent != 0; absent &= absent - 1) {
     const int64_t row = v0 + __ffs(absent) - 1;
-    for (int64_t slice = 0; slice < s.slices; ++slice)
+    for (unsigned slice = 0; slice < s.slices; ++slice)
       Columns<DT, VEC>(slice, s.dim).store(s.dw, row, zero);
   }
 }
@@ -504,12 +527,12 @@ embedding_sums_kernel(const Sums s) {
   begin_after_previous();
   constexpr int E = kPer<DT>;
   const int lane = threadIdx.x & 31;
-  const int64_t unit = (int64_t)blockIdx.x * kSumWarps + (threadIdx.x >> 5);
+  const unsigned unit = blockIdx.x * kSumWarps + (threadIdx.x >> 5);
   if (unit >= s.sums) {
-    if (s.group > 0) fill_absent<DT, VEC>(s, (unit - s.sums) * s.group);
+    if (s.group > 0) fill_absent<DT, VEC>(s, (int64_t)(unit - s.sums) * s.group);
     return;
   }
-  const int64_t chunk = unit / s.slices, slice = unit - chunk * s.slices;
+  const int64_t chunk = unit / s.slices, slice = unit - (unsigned)chunk * s.slices;
   const int64_t first = chunk * s.chunk, at = first + lane;
   if (first >= s.n) return;
   const uint32_t none = s.vocab;
@@ -570,8 +593,8 @@ embedding_few_kernel(const Sums s, const long long* ids, long long padding) {
   for (int i = threadIdx.x; i < kFewTokens; i += 32 * kSumWarps)
     keys[i] = i < n ? key_of(ids[i], s.vocab, padding) : s.vocab;
   __syncthreads();
-  const int64_t unit = (int64_t)blockIdx.x * kSumWarps + warp;
-  const int64_t g = unit / s.slices, v0 = g * s.group;
+  const unsigned unit = blockIdx.x * kSumWarps + warp, g = unit / s.slices;
+  const int64_t v0 = (int64_t)g * s.group;
   if (v0 >= (int64_t)s.vocab) return;
   const Columns<DT, VEC> columns(unit - g * s.slices, s.dim);
   const uint32_t words = (uint32_t)min((int64_t)s.group, (int64_t)s.vocab - v0);
@@ -788,7 +811,8 @@ cudaError_t forward(const EmbeddingArgs& a, cudaStream_t stream) {
   }
   return launch(early, embedding_any_kernel<DT>,
                 (unsigned)blocks(a.rows * blocks(a.dim, kRowPart), kCtaWarps), kCtaThreads, 0,
-                stream, ids, a.in, a.rows, a.dim, a.vocab, a.scale, a.out);
+                stream, ids, a.in, a.rows, a.dim, a.vocab, (unsigned)blocks(a.dim, kRowPart),
+                a.scale, a.out);
 }
 
 template <int DT>
@@ -805,12 +829,12 @@ cudaError_t backward(const EmbeddingArgs& a, char* scratch, int sms, cudaStream_
   s.n = a.rows;
   s.dim = a.dim;
   s.vocab = (uint32_t)a.vocab;
-  s.slices = blocks(a.dim, 32 * kPer<DT>);
+  s.slices = (unsigned)blocks(a.dim, 32 * kPer<DT>);
   s.dy = a.in;
   s.scale = a.scale;
   s.dw = a.out;
   if (a.rows <= kFewTokens) {
-    s.group = group_of(a.vocab * s.slices, sms);
+    s.group = group_of(a.vocab * (int64_t)s.slices, sms);
     if (mark) mark(kEmbeddingSumsK, 0, stream);
     e = launch(worth_early(a.vocab * a.dim),
                vec ? embedding_few_kernel<DT, true> : embedding_few_kernel<DT, false>,
@@ -865,11 +889,11 @@ cudaError_t backward(const EmbeddingArgs& a, char* scratch, int sms, cudaStream_
   s.chunk = chunk_of(a, sms);
   s.parts = reinterpret_cast<float*>(scratch + l.parts);
   const int64_t chunks = blocks(a.rows, s.chunk);
-  s.sums = chunks * s.slices;
+  s.sums = (unsigned)(chunks * s.slices);
   const int64_t fillers = s.group > 0 ? blocks(a.vocab, s.group) : 0;
   if (mark) mark(kEmbeddingSumsK, 0, stream);
   e = launch(true, vec ? embedding_sums_kernel<DT, true> : embedding_sums_kernel<DT, false>,
-             (unsigned)blocks(s.sums + fillers, kSumWarps), 32 * kSumWarps, 0, stream, s);
+             (unsigned)blocks((int64_t)s.sums + fillers, kSumWarps), 32 * kSumWarps, 0, stream, s);
   if (mark) mark(kEmbeddingSumsK, 1, stream);
   if (e != cudaSuccess || chunks == 1) return e;
   if (mark) mark(kEmbeddingJoinK, 0, stream);

@@ -41,8 +41,9 @@ struct Policy {
   const float* ref_logp;
   // A sequence is `pieces` units, each `warps` neighbouring warps of a CTA with
   // `piece` tokens each.
-  int64_t length, pieces, units;
-  int warps, piece;
+  int64_t length;
+  unsigned pieces, units, warps;
+  int piece;
   bool per_token;
   Border low, high;
   float kl_coef;
@@ -83,14 +84,15 @@ __device__ __forceinline__ Token token_of(const Policy& p, float logp, float old
 
 // The calling warp's unit, its sequence and the warp's first token of it.
 struct Place {
-  int64_t unit, b, t0;
+  unsigned unit;
+  int64_t b, t0;
 };
 
 __device__ __forceinline__ Place place_of(const Policy& p) {
-  const int warp = threadIdx.x >> 5;
-  const int64_t unit = (int64_t)blockIdx.x * (kCtaWarps / p.warps) + warp / p.warps;
-  const int64_t b = p.pieces == 1 ? unit : unit / p.pieces;
-  return {unit, b, ((unit - b * p.pieces) * p.warps + warp % p.warps) * p.piece};
+  const unsigned warp = threadIdx.x >> 5;
+  const unsigned unit = blockIdx.x * (kCtaWarps / p.warps) + warp / p.warps, b = unit / p.pieces;
+  return {unit, (int64_t)b,
+          ((int64_t)(unit - b * p.pieces) * p.warps + warp % p.warps) * p.piece};
 }
 
 __device__ __forceinline__ bool counts(uint32_t m, int k) { return (m >> (8 * k) & 0xFFu) != 0; }
@@ -395,10 +397,10 @@ Policy policy_of(const PolicyArgs& a) {
   for (int most = kMostPiece;; most /= 2) {
     p.warps = 1;
     while (p.warps < kCtaWarps && (int64_t)p.warps * most < a.length) p.warps *= 2;
-    p.pieces = up(a.length, (int64_t)p.warps * most);
-    p.units = a.batch * p.pieces;
-    p.piece = p.pieces > 0 ? (int)(up(up(a.length, p.warps * p.pieces), 128) * 128) : most;
-    if (p.units * p.warps >= kWarps || most == kLeastPiece) break;
+    p.pieces = (unsigned)up(a.length, (int64_t)p.warps * most);
+    p.units = (unsigned)(a.batch * p.pieces);
+    p.piece = p.pieces > 0 ? (int)(up(up(a.length, (int64_t)p.warps * p.pieces), 128) * 128) : most;
+    if ((int64_t)p.units * p.warps >= kWarps || most == kLeastPiece) break;
   }
   p.per_token = a.per_token;
   p.low = border(-a.clip_low);
@@ -417,8 +419,8 @@ bool vectors_ok(const PolicyArgs& a) {
 }
 
 unsigned ctas(const Policy& p) {
-  const int units = kCtaWarps / p.warps;
-  return (unsigned)((p.units + units - 1) / units);
+  const unsigned units = kCtaWarps / p.warps;
+  return (p.units + units - 1) / units;
 }
 
 }  // namespace
@@ -439,7 +441,7 @@ cudaError_t launch_policy(const PolicyArgs& a, char* scratch, cudaStream_t strea
   if (e != cudaSuccess) return e;
   if (mark) mark(kPolicyJoinK, 0, stream);
   e = launch(true, policy_join_kernel, 1, kJoinThreads, 0, stream, (const Part*)parts, a.batch,
-             p.pieces, a.by_sequence, (float)a.kl_coef, a.stats, a.weight_out);
+             (int64_t)p.pieces, a.by_sequence, (float)a.kl_coef, a.stats, a.weight_out);
   if (mark) mark(kPolicyJoinK, 1, stream);
   return e;
 }

@@ -285,7 +285,7 @@ namespace fp8opt {
 namespace {
 
 int check_embedding(const char* fn, const EmbeddingArgs& a) {
-  if (a.rows < 0 || a.rows > kXentMost || a.dim < 1 || a.dim > kMaxElems || a.vocab < 1 ||
+  if (a.rows < 0 || a.rows > kXentMost || a.dim < 1 || a.dim > kXentMost || a.vocab < 1 ||
       a.vocab > kXentMost || a.rows > kMaxElems / a.dim || a.vocab > kMaxElems / a.dim)
     return bad(fn, "rows < 0, dim < 1, vocab < 1, or a size above its maximum");
   if (!known(a.dtype)) return unsupported(fn, "unknown dtype");

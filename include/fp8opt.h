@@ -768,8 +768,8 @@ FP8OPT_API int fp8_linear_distill_backward(
  * padding_idx gets no gradient (any number outside [0, vocab): none is left
  * out), and an id outside [0, vocab) takes no part.  rows = 0 gives dw 0.  The
  * tokens are sorted by word and a word's rows added in their order, in fp32.
- * Scratch: 16 bytes a token and dim / 4 a token.  rows and vocab below 2^31,
- * dim >= 1, scale finite.
+ * Scratch: 16 bytes a token, and dim / 4 (few tokens: dim) a token.  rows, vocab
+ * and dim below 2^31, dim and vocab >= 1, scale finite.
  */
 FP8OPT_API int fp8_embedding(const int64_t *ids, const void *w, int64_t rows,
                              int64_t dim, int64_t vocab, int dtype,
@@ -798,7 +798,8 @@ FP8OPT_API int fp8_embedding_backward(const void *dy, const int64_t *ids,
  * tokens that are clipped (r A is above the clipped term); all 0 where no token
  * counts.  weight (batch fp32): what a token of each sequence weighs in the mean
  * (0 for a sequence without any).  Whether a token is clipped follows from the
- * exact difference logp - old_logp; sums over more than 1024 tokens are fp64.
+ * exact difference logp - old_logp; sums over more than 1024 tokens are held in two
+ * fp32 numbers each (48 bits).
  *
  * fp8_policy_loss_backward: dlogp (batch x length fp32) = *dloss * weight *
  * dl / dlogp, dl / dlogp = -r A (0 where clipped) + kl_coef (1 - exp(e)); 0 where

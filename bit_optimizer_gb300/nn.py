@@ -29,6 +29,10 @@ Under torch.autocast the linear layers cast their input and parameters to
 its dtype, as torch's do, so FP32 weights get FP32 gradients; ``layer_norm`` and
 ``gelu`` take what they are given, and their result has its type.  Under no_grad
 the checkpoints are written all the same, and freed.
+
+A step with its backward pass can be captured into a CUDA graph once it has run on
+the stream, as long as no eager graph of the same leaves lives: torch's engine would
+order the capturing stream against the one that graph used, and the capture fails.
 """
 from __future__ import annotations
 

@@ -647,7 +647,8 @@ static_assert(kFewTokens == 256, "a token's number has eight bits");
 // kFewParts parts: the CTA where the word starts adds them, a thread to four
 // columns.  More: all CTAs that the word goes on behind take 32 columns each in
 // turn, ranges of parts side by side.
-// Narrow tables have CTAs of fewer threads: most end at once, and more are resident.
+// CTAs of 128 threads, of 64 for narrow tables: most end at once, and more are
+// resident (131072 tokens over 50257 x 512: 60.4 us, with 256 threads 65.5).
 constexpr int kFewParts = 16, kJoinColumns = 32, kJoinLanes = kJoinColumns / 4;
 constexpr int kNarrow = 256;      // columns
 
@@ -898,8 +899,8 @@ cudaError_t backward(const EmbeddingArgs& a, char* scratch, int sms, cudaStream_
   if (e != cudaSuccess || chunks == 1) return e;
   if (mark) mark(kEmbeddingJoinK, 0, stream);
   const bool narrow = a.dim <= kNarrow;
-  e = launch(true, narrow ? embedding_join_kernel<DT, 64> : embedding_join_kernel<DT, 256>,
-             (unsigned)chunks, narrow ? 64 : 256, 0, stream, s, a.dim % 4 == 0);
+  e = launch(true, narrow ? embedding_join_kernel<DT, 64> : embedding_join_kernel<DT, 128>,
+             (unsigned)chunks, narrow ? 64 : 128, 0, stream, s, a.dim % 4 == 0);
   if (mark) mark(kEmbeddingJoinK, 1, stream);
   return e;
 }

@@ -201,23 +201,27 @@ teacher_kernel(const long long* ids, const void* logits, int logit_dtype, int64_
     shuffles(k, 16);
   }
   __syncthreads();
-  uint32_t* const word = sh_word + 32 * first;
+  uint32_t* const strip_of = sh_word + 32 * first;
   int count = 0;
   for (int w = first; w < first + group; ++w) count += sh_count[w];
-  word[j] = id;
+  strip_of[j] = id / kTeacherStrip;
   if (j < count) {
     words[token * t.k + j] = id;
     q[token * t.k + j] = share;
   }
   __syncthreads();
   if (!live) return;
-  // the number of words below each strip's first one
-  const int highest = count > 0 ? 1 << (31 - __clz(count)) : 0;
-  for (int64_t strip = j; strip <= t.strips; strip += 32 * group) {
-    int n = 0;
-    for (int step = highest; step > 0; step >>= 1)
-      if (n + step <= count && (int64_t)word[n + step - 1] < strip * kTeacherStrip) n += step;
-    start[token * (t.strips + 1) + strip] = (uint16_t)n;
+  // the number of entries before each strip: a thread has neighbouring strips, looks
+  // for the first one's and goes on from there (8191 tokens of 64 entries, 393
+  // strips: 24 us with a search for each)
+  const int per = (t.strips + 32 * group) / (32 * group), s0 = j * per;
+  int n = 0;
+  for (int step = count > 0 ? 1 << (31 - __clz(count)) : 0; step > 0; step >>= 1)
+    if (n + step <= count && strip_of[n + step - 1] < (uint32_t)s0) n += step;
+  uint16_t* const out = start + token * (t.strips + 1);
+  for (int s = s0; s < min(s0 + per, t.strips + 1); ++s) {
+    while (n < count && strip_of[n] < (uint32_t)s) ++n;
+    out[s] = (uint16_t)n;
   }
   if (j == 0) {
     state[token] = wrong ? (long long)vocab : dead ? kTeacherNone : kTeacherLive;

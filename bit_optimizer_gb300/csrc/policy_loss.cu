@@ -8,8 +8,10 @@
 // piece of one sequence; a CTA adds up what its warps have of a sequence, and one
 // CTA joins the rest in order.  (A batch's terms cancel down to their mean: sums
 // over warps are held in two floats, 48 bits.  In fp64, which the GB300 has little
-// of, the join took 37 us for 8 sequences and 73 for 512.  Both kernels are launched
-// early, which makes them as fast as a single one for small batches: in one cluster
+// of, the join took 37 us for 8 sequences and 73 for 512.)  512 x 8192 tokens, half
+// of them masked: 16 us, the gradient 10.4 to 11.6 us; the values of masked tokens
+// are not read, and what is left is the latency of mask, values and join.  (Both
+// forward kernels are launched early, which makes them as fast as a single one for small batches: in one cluster
 // 8 x 512 took 8.2 us, 64 x 1023 10.3; 7.4 and 7.7.)
 //
 // Whether a token is clipped decides between its whole gradient and none, so it
@@ -382,7 +384,7 @@ Border border(double x) {
 }
 
 // The pieces are as large as they can be while there are kWarps of them (27 an SM):
-// fewer sums to join.  512 x 8192: 18.6 us, 20.4 with twice as many.
+// fewer sums to join.  512 x 8192: 15.9 us, 17.3 with twice as many.
 constexpr int64_t kWarps = 4096;
 
 Policy policy_of(const PolicyArgs& a) {

@@ -107,9 +107,9 @@ __device__ __forceinline__ float teacher_logit(const void* p, int64_t i) {
 // given, and those whose share is 0 (of a logit of -inf) left out.  Backward, dloss
 // is divided by the temperature.  `zeros`: words to set to zero besides.
 //
-// Bound by latency: with a warp to a token a single one of 197 entries took 19 us.
-// Many tokens of many entries: 2279 of 217, 28 us by counting each entry's smaller
-// words.
+// Bound by latency for few tokens (6 of 197 entries: 7 us; with a warp to a token
+// 19), by the sort's instructions for many (8191 of 64 entries: 19 us with cold
+// caches; 2279 of 217: 21, by counting each entry's smaller words 28).
 __global__ void __launch_bounds__(32 * kTeacherWarps)
 teacher_kernel(const long long* ids, const void* logits, int logit_dtype, int64_t tokens,
                int64_t vocab, int group, const Teacher t, uint32_t* __restrict__ words,

@@ -1,6 +1,6 @@
 """Trains a small language model on one GPU with the package's operators and
-optimizer: FP16 weights, layer norm, GELU and linear layers that keep 8-bit
-activations, the vocabulary's cross entropy without logits in memory, and
+optimizer: FP16 weights, the embedding, layer norm, GELU and linear layers that keep
+8-bit activations, the vocabulary's cross entropy without logits in memory, and
 Fp8AdamW on the gradients, with a loss scale.
 
     python examples/train_lm.py [--steps 200] [--tokens 4096] [--vocab 5003]
@@ -43,7 +43,7 @@ class Model:
         return [self.wte, *(p for b in self.blocks for p in b.values()), self.lnf_w, self.lnf_b]
 
     def loss(self, tokens, target):
-        x = torch.nn.functional.embedding(tokens, self.wte)
+        x = nn.embedding(tokens, self.wte)
         for b in self.blocks:
             h = nn.gelu(nn.linear(nn.layer_norm(x, b["ln_w"], b["ln_b"]), b["fc_w"], b["fc_b"]))
             x = x + nn.linear(h, b["out_w"], b["out_b"])

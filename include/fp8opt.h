@@ -701,9 +701,9 @@ FP8OPT_API int fp8_layer_norm_backward(
  *
  * The kernels wait for their copies and products with a limit of about two
  * seconds.  Should one run out (it does not on a working device), the call's
- * results are not complete, and the first fp8_linear_xent or
- * fp8_linear_xent_backward issued on the device after that kernel has ended
- * returns FP8OPT_ERR_CUDA and launches nothing.  Calls issued earlier, other
+ * results are not complete, and the first call of fp8_linear_xent,
+ * fp8_linear_distill or their backward passes issued on the device after that
+ * kernel has ended returns FP8OPT_ERR_CUDA and launches nothing.  Calls issued earlier, other
  * calls and replays of a captured graph do not look.
  */
 FP8OPT_API int fp8_linear_xent(const void *x, const void *w,

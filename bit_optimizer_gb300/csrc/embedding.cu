@@ -190,10 +190,13 @@ __device__ __forceinline__ void fill_zeros(const Fill& f, int64_t cta, int64_t c
 // Some tokens: the place of each is the number of smaller keys, and of equal ones
 // before it.  A CTA places 32 tokens, its warps comparing them with a share of all
 // keys each.  (4096 tokens over 50257 x 768, 5000 x 512: 25.2 and 16.4 us; by the
-// radix sort 8192 take 25 and 20, by this one 38 and 27.)  Launched early the CTAs start where the
-// previous kernel leaves room, many to an SM, which is right as long as they are
-// short: 512 tokens over 5000 x 512 8.7 us, 10.3 launched late; 4096 29.9 and 16.4.
-constexpr int64_t kRankTokens = 4096, kEarlyRank = 1024;
+// radix sort 8192 take 25 and 20, by this one 38 and 27.)  CTAs that are launched
+// early start where the previous kernel leaves room, many to an SM; kRankSmem bytes
+// of shared memory, more than half of it, keep them to one each (4096 tokens over
+// 5000 x 512: 14.8 us; launched late 16.4, early without it 29.9).
+constexpr int64_t kRankTokens = 4096;
+constexpr int kRankSmem = 200 << 10;
+static_assert(kRankTokens * 4 <= kRankSmem - 4096, "the keys");
 
 __global__ void __launch_bounds__(kCtaThreads)
 embedding_rank_kernel(const long long* ids, int n, uint32_t vocab, long long padding,
@@ -238,9 +241,9 @@ embedding_rank_kernel(const long long* ids, int n, uint32_t vocab, long long pad
 
 // More tokens: a stable sort by eight bits of the key a pass, in tiles of a CTA
 // each (a multiple of kSortStep tokens: 65536 tokens 59.6 us, with twice the step
-// 62.4).  First the tiles' counts of each digit,
-// for the first pass; every pass then counts the next one's, where its tokens go
-// to (whole numbers: the order of the atomics does not matter).
+// 62.4).  First the tiles' counts of each digit, for the first pass; every pass then
+// counts the next one's, where its tokens go to (whole numbers: the order of the
+// atomics does not matter).
 constexpr int kSortThreads = 1024, kSortWarps = kSortThreads / 32, kDigits = 256;
 constexpr int kRounds = 1, kSortStep = kRounds * kSortThreads;
 
@@ -652,9 +655,9 @@ static_assert(kFewTokens == 256, "a token's number has eight bits");
 // order.  A CTA for every chunk, with the word that goes on behind it.  Up to
 // kFewParts parts: the CTA where the word starts adds them, a thread to four
 // columns.  More: all CTAs that the word goes on behind take 32 columns each in
-// turn, ranges of parts side by side.
-// CTAs of 128 threads, of 64 for narrow tables: most end at once, and more are
-// resident (131072 tokens over 50257 x 512: 60.4 us, with 256 threads 65.5).
+// turn, ranges of parts side by side.  CTAs of 128 threads, of 64 for narrow tables:
+// most end at once, and more are resident (131072 tokens over 50257 x 512: 60.4 us,
+// with 256 threads 65.5).
 constexpr int kFewParts = 16, kJoinColumns = 32, kJoinLanes = kJoinColumns / 4;
 constexpr int kNarrow = 256;      // columns
 
@@ -854,9 +857,12 @@ cudaError_t backward(const EmbeddingArgs& a, char* scratch, int sms, cudaStream_
   if (mark) mark(kEmbeddingOrderK, 0, stream);
   if (a.rows <= kRankTokens) {
     const int n = (int)a.rows;
-    const size_t smem = (size_t)blocks(blocks(n, kCtaWarps), 32) * 32 * kCtaWarps * 4;
-    e = launch(n <= kEarlyRank, embedding_rank_kernel, (unsigned)blocks(n, 32), kCtaThreads, smem, stream,
-               ids, n, (uint32_t)a.vocab, (long long)a.padding, at(l.keys[0]), at(l.tokens[0]));
+    e = cudaFuncSetAttribute(embedding_rank_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             kRankSmem);
+    if (e == cudaSuccess)
+      e = launch(true, embedding_rank_kernel, (unsigned)blocks(n, 32), kCtaThreads, kRankSmem,
+                 stream, ids, n, (uint32_t)a.vocab, (long long)a.padding, at(l.keys[0]),
+                 at(l.tokens[0]));
     s.group = group_of(a.vocab, sms);
   } else {
     SortPass p = {};

@@ -10,9 +10,9 @@
 // over warps are held in two floats, 48 bits.  In fp64, which the GB300 has little
 // of, the join took 37 us for 8 sequences and 73 for 512.)  512 x 8192 tokens, half
 // of them masked: 16 us, the gradient 10.4 to 11.6 us; the values of masked tokens
-// are not read, and what is left is the latency of mask, values and join.  (Both
-// forward kernels are launched early, which makes them as fast as a single one for small batches: in one cluster
-// 8 x 512 took 8.2 us, 64 x 1023 10.3; 7.4 and 7.7.)
+// are not read, and what is left is the latency of mask, values and join.  Both
+// forward kernels are launched early, which makes them as fast as a single one for
+// small batches (in one cluster 8 x 512 took 8.2 us, 64 x 1023 10.3; 7.4 and 7.7).
 //
 // Whether a token is clipped decides between its whole gradient and none, so it
 // is decided exactly: logp - old, as the fp32 difference and its rounding error,

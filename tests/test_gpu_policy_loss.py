@@ -280,3 +280,21 @@ def test_refusals():
         bo.policy_loss(lp, old, adv, clip_low=1.5)
     with pytest.raises(ValueError):
         bo.policy_loss_backward(adv, lp, old, adv, adv)
+
+
+def test_offsets_past_32_bits():
+    """2.4e9 tokens, of which the last sequence's last ones differ."""
+    batch, length = 3, 800_000_003
+    lp = torch.zeros(batch, length, device="cuda")
+    old = torch.zeros(batch, length, device="cuda")
+    old[2, -3:] = torch.tensor([0.1, -0.1, 1.0], device="cuda")
+    adv = torch.tensor([1.0, -2.0, 4.0], device="cuda")
+    stats, weight = bo.policy_loss(lp, old, adv)
+    # -(1 - 2 + 4) / 3 but for three tokens of 2.4e9; the same number of tokens each
+    assert abs(stats[0].item() + 1.0) < 1e-6 and stats[3] == 0
+    assert ((weight.double() * (batch * length) - 1).abs() <= 2.0 ** -23).all()
+    d = bo.policy_loss_backward(torch.ones((), device="cuda"), lp, old, adv, weight)
+    scaled = d[:, -4:].double() * (batch * length)
+    want = -adv.double()[:, None] * torch.exp(-old[:, -4:].double())
+    assert ((scaled - want).abs() <= 1e-6 * want.abs()).all()
+    assert d[0, 0] == -weight[0] and d[1, 0] == 2 * weight[1]

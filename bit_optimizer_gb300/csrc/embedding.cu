@@ -18,10 +18,10 @@
 //                   the rows of words without tokens.
 //           join    The parts of such words, in order.
 // A frequent word's tokens are thereby spread over as many warps as any others.
-// 65536 x 1024 BF16 over 50257 words: 58 to 61 us, of which the sort takes 12 alone
+// 65536 x 1024 BF16 over 50257 words: 57 to 58 us, of which the sort takes 12 alone
 // and 22 with the zeros, the sums some 30 (170 MB), the join 8; bound by memory but
 // for the sort's and the join's latencies.  Fewer tokens are bound by those and by
-// the zeros: 2047 x 768, 22.5 us (77 MB of zeros alone 12).  Zeros for the highest
+// the zeros: 2047 x 768, 21.5 us (77 MB of zeros alone 12).  Zeros for the highest
 // words beside the sort and for the rest beside the sums gained nothing.
 #include "ops_internal.cuh"
 

@@ -215,3 +215,34 @@ def test_a_captured_step():
             assert torch.equal(a, b)
     del g, out
     bo.release_stream(s)
+
+
+def test_under_autocast():
+    """FP32 weights get FP32 gradients; distillation's product is autocast's type."""
+    args, params = inputs(7), [p.detach().float().requires_grad_(True) for p in parameters()]
+    tokens, _, ids, logits = args[:4]
+    wte = params[0]
+    with torch.autocast("cuda", dtype=torch.bfloat16):
+        h = nn.embedding(tokens, wte, 4.0)
+        loss = nn.linear_distillation(h, wte, ids, logits.float(), 2.0)
+    d, = torch.autograd.grad(loss, wte)
+    assert h.dtype == d.dtype == torch.float32
+    full = wte.detach().double().requires_grad_(True)
+    z = (4 * full[tokens]) @ full.T / 2
+    logq = torch.log_softmax(logits.double() / 2, -1)
+    each = (logq.exp() * (logq - torch.log_softmax(z, -1).gather(-1, ids.clamp(min=0)))).sum(-1)
+    live = (ids >= 0).any(-1)
+    want = (each * live).sum() / live.sum()
+    ref, = torch.autograd.grad(want, full)
+    # 16-bit inputs, p - q and results: some 2^-8 each
+    assert abs(loss.item() - want.item()) < 1e-2 * want.item()
+    assert (d.double() - ref).norm() < 2.0 ** -6 * ref.norm()
+
+
+def test_one_token_without_a_dimension():
+    w = randn(30, 64, seed=1)
+    ids = torch.tensor(7, device="cuda")
+    y = bo.embedding(ids, w)
+    assert torch.equal(y, w[7])
+    dw = bo.embedding_backward(y, ids, 30, 2.0)
+    assert torch.equal(dw[7], 2 * w[7]) and dw.count_nonzero() == dw[7].count_nonzero()

@@ -886,11 +886,11 @@ xent_join_kernel(const float2* partial, int strips, int64_t tokens, int64_t voca
                                   __shfl_xor_sync(0xFFFFFFFFu, s.y, o)), factor);
   if constexpr (TEACHER) {
     if (mine >= tokens) return;
-    const float l = __fdiv_rn(s.x, teacher.temperature) + logf(s.y);
+    const float log_sum = logf(s.y);
     const long long t = target[mine];
-    const float sum = of_teacher(teacher, mine, l);
+    const float sum = of_teacher(teacher, mine, s.x, log_sum);
     if (lane == 0) {
-      lse[mine] = l;
+      lse[mine] = __fdiv_rn(s.x, teacher.temperature) + log_sum;
       loss[mine] = t == ignore ? 0.0f : t < vocab ? sum : __uint_as_float(0x7FC00000u);
     }
     return;
@@ -968,8 +968,8 @@ xent_few_kernel(const float2* partial, int strips, int64_t tokens, int64_t vocab
   for (int o = 16; o > 0; o >>= 1)
     s = join_stats(s, make_float2(__shfl_xor_sync(0xFFFFFFFFu, s.x, o),
                                   __shfl_xor_sync(0xFFFFFFFFu, s.y, o)), t.factor);
-  const float l = __fdiv_rn(s.x, t.temperature) + logf(s.y);
-  // (teacher_kernel's steps)
+  const float log_sum = logf(s.y);
+  // (teacher_kernel's and TeacherLoss' steps)
   const float none = __uint_as_float(0xFF800000u);
   float top = none;
   bool wrong = false;
@@ -993,13 +993,13 @@ xent_few_kernel(const float2* partial, int strips, int64_t tokens, int64_t vocab
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
     for (int j = lane; j < t.k; j += 32) {
       const float q = __fdiv_rn(sh_logit[j], sum);
-      if (q != 0.0f) of += q * (logf(q) - (__fdiv_rn(sh_z[j], t.temperature) - l));
+      if (q != 0.0f) of += q * (logf(q) - (__fdiv_rn(sh_z[j] - s.x, t.temperature) - log_sum));
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) of += __shfl_xor_sync(0xFFFFFFFFu, of, o);
   }
   if (lane == 0) {
-    lse[token] = l;
+    lse[token] = __fdiv_rn(s.x, t.temperature) + log_sum;
     loss[token] = wrong ? __uint_as_float(0x7FC00000u) : of;
   }
 }

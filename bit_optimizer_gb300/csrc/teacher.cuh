@@ -229,8 +229,12 @@ teacher_kernel(const long long* ids, const void* logits, int logit_dtype, int64_
   }
 }
 
-// A token's loss from its entries' logits and its lse; a whole warp.  The first 32
-// entries are read when it is made.
+// A token's loss from its entries' logits, the row's largest logit and the log of its
+// sum of exponentials above that; a whole warp.  (lse, which adds the two up, is
+// rounded to its own size, and z / t to its: with differences from the largest logit
+// the loss of 64 entries at logits around 28 and t = 0.05 is off by 1.4e-7 on average
+// instead of 7.6e-6, at t = 1 by 1.5e-7 instead of 9.4e-7.)  The first 32 entries are
+// read when it is made.
 struct TeacherLoss {
   int count = 0;
   float q = 0.0f, z = 0.0f;
@@ -243,14 +247,15 @@ struct TeacherLoss {
       z = __ldcg(t.z + token * t.k + lane);
     }
   }
-  __device__ __forceinline__ float operator()(const Teacher& t, int64_t token, float lse) {
+  __device__ __forceinline__ float operator()(const Teacher& t, int64_t token, float top,
+                                              float log_sum) {
     float sum = 0.0f;
     for (int j = threadIdx.x & 31; j < count; j += 32) {
       if (j >= 32) {
         q = t.q[token * t.k + j];
         z = __ldcg(t.z + token * t.k + j);
       }
-      sum += q * (logf(q) - (__fdiv_rn(z, t.temperature) - lse));
+      sum += q * (logf(q) - (__fdiv_rn(z - top, t.temperature) - log_sum));
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);

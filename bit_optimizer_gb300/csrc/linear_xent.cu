@@ -306,6 +306,59 @@ __device__ __forceinline__ float2 join_stats(float2 a, float2 b, float factor = 
                               b.y * exp2_approx((b.x - top) * factor));
 }
 
+// Up to so many entries of few tokens (the vocabulary's rows as the tiles' rows) are
+// not sorted: each CTA lists those whose words are rows of its own tiles, some in a
+// hundred, while its first tile is copied, and the epilogues look through the list.
+// The list lies where the stages' halves of B, of at most kSwapTokens / 2 rows, end,
+// whose room sets the limit.  768 x 50257 with 32 entries: 24 tokens 24.2 us, sorted
+// first 28.4; 128 tokens 25.9 and 32.6 (the cross entropy 21.5 and 24.1).  The entries'
+// logits have to be the product's: the tensor cores' sums are some 2^-22 of the
+// logits off all the same way, which the loss's differences cancel (summed again from
+// w's rows, 24 tokens' losses at logits of 29 and t = 0.5 were off by 1.1e-5 on
+// average, now 1.3e-7).
+constexpr int64_t kSwapTokens = 128, kFewEntries = 4096;
+struct FewEntries {
+  uint8_t* stages;
+  static constexpr int kSpare = kStageB / 2, kEach = kSpare / 8;      // of a stage: bytes, entries
+  static_assert(kSwapTokens / 2 * kBlockK * 2 <= kStageB - kSpare, "B's rows");
+  static_assert(kFewEntries <= (kGemmStages - 1) * kEach, "the list, and its count");
+  __device__ __forceinline__ uint8_t* spare(int stage) const {
+    return stages + stage * (kStageA + kStageB) + kStageB - kSpare + kStageA;
+  }
+  __device__ __forceinline__ int* count() const {
+    return reinterpret_cast<int*>(spare(kGemmStages - 1));
+  }
+  // a word, and the entry's number among all tokens'
+  __device__ __forceinline__ uint2* entry(int i) const {
+    return reinterpret_cast<uint2*>(spare(i / kEach)) + i % kEach;
+  }
+  // Every epilogue thread; a pair's tiles are every gridDim / 2-th.  (The order of the
+  // list does not matter: each entry's logit is stored once.)
+  __device__ __forceinline__ void list(const GemmOut& o, uint32_t rank) const {
+    constexpr int kThreads = 32 * kEpilogueWarps, kAhead = 8;
+    const Teacher& t = o.teacher;
+    const int total = (int)o.tokens * t.k;
+    const uint32_t pairs = gridDim.x / 2, pair = blockIdx.x / 2;
+    if (threadIdx.x == 0) *count() = 0;
+    asm volatile("bar.sync 1, 256;" ::: "memory");
+    for (int i0 = threadIdx.x; i0 < total; i0 += kAhead * kThreads) {
+      long long id[kAhead];
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k)
+        id[k] = i0 + k * kThreads < total ? t.ids[i0 + k * kThreads] : -1;
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        const uint32_t word = (uint32_t)id[k];
+        if (id[k] >= 0 && id[k] < o.vocab && word / kHalfM % 2 == rank &&
+            word / kTileM % pairs == pair)
+          *entry(atomicAdd(count(), 1)) = make_uint2(word, (uint32_t)(i0 + k * kThreads));
+      }
+    }
+    asm volatile("bar.sync 1, 256;" ::: "memory");
+  }
+};
+static_assert(kEpilogueWarps == 8, "256 threads of barrier 1");
+
 // A token's running maximum and sum of exponentials, and its target's logit.  The
 // maximum starts at fp32's lowest number, which is above no logit but -inf and
 // makes its exponential 0 (from -inf the difference of two would be NaN).
@@ -375,7 +428,7 @@ struct SwappedStats {
   Stats s[2];
   template <bool TEACHER>
   __device__ __forceinline__ void add(const GemmShape& g, const GemmOut& o, uint32_t tmem,
-                                      int64_t v0, int half, Turn& turn) {
+                                      int64_t v0, int half, Turn& turn, uint8_t* stages) {
     const int lane = threadIdx.x & 31;
     const int valid = (int)min((int64_t)32, max(o.vocab - v0, (int64_t)0));
 #pragma unroll
@@ -394,8 +447,19 @@ struct SwappedStats {
         r[j] = reinterpret_cast<const uint32_t*>(&turn.at(j, lane >> 2))[lane & 3];
       const int64_t token = c + lane;
       if constexpr (TEACHER) {
-        if (token < o.tokens && o.teacher.words != nullptr) {
-          const Teacher& t = o.teacher;
+        const Teacher& t = o.teacher;
+        if (t.ids != nullptr) {
+          const FewEntries few = {stages};
+          const int end = *few.count();
+          for (int i = lane; i < end; i += 32) {
+            const uint2 entry = *few.entry(i);
+            const uint32_t row = entry.x - (uint32_t)v0;
+            const int of = (int)entry.y / t.k - c;
+            if (row < (uint32_t)valid && of >= 0 && of < 32)
+              t.z[entry.y] = __uint_as_float(
+                  reinterpret_cast<const uint32_t*>(&turn.at((int)row, of >> 2))[of & 3]);
+          }
+        } else if (token < o.tokens) {
           const uint16_t* start = t.start + token * (t.strips + 1) + v0 / kTeacherStrip;
           const int end = valid > 0 ? start[1] : 0;
           for (int i = valid > 0 ? start[0] : 0; i < end; ++i) {
@@ -793,6 +857,8 @@ gemm_kernel(const __grid_constant__ GemmArgs args) {
     Turn* const turns = reinterpret_cast<Turn*>(stages + kGemmStages * (kStageA + kStageB));
     Turn& turn = turns[warp];
     SwappedStats swapped;
+    if constexpr (TEACHER)
+      if (args.out.teacher.ids != nullptr) FewEntries{stages}.list(args.out, rank);
     int buf = 0, phase = 0;
     // A tile's row inputs are asked for one tile ahead, so that their latency
     // lies under the tile before.
@@ -825,7 +891,7 @@ gemm_kernel(const __grid_constant__ GemmArgs args) {
       if (g.mode == kStats) stats_strip<TEACHER>(args.out, strip, in);
       else if (g.mode == kStatsSwapped)
         swapped.add<TEACHER>(g, args.out, tmem + buf * kTileN + ((uint32_t)(warp % 4) << 21),
-                    strip.row - (threadIdx.x & 31), half, turn);
+                    strip.row - (threadIdx.x & 31), half, turn, stages);
       else if (g.mode == kProbs) probs_strip<BF16, TEACHER>(g, args.out, strip, in, turn);
       else if (g.mode == kDx) dx_strip(g, args.out, strip, t.split, work_blocks(t.work) == 0, turn);
       else dw_strip<BF16>(g, args.out, strip, in, turn);
@@ -905,100 +971,79 @@ xent_join_kernel(const float2* partial, int strips, int64_t tokens, int64_t voca
 }
 
 // Distillation of few tokens with few entries: the statistics of a token joined and
-// its loss, without entries in order or a search for them in the tiles.  A CTA
-// takes a token, a warp an entry: its logit is x w^T again, from rows of w that the
-// product has left in L2.
-template <bool BF16>
-__global__ void __launch_bounds__(1024)
-xent_few_kernel(const float2* partial, int strips, int64_t tokens, int64_t vocab, const char* x,
-                const char* w, int64_t pitch, const long long* ids, const void* logits,
-                int logit_dtype, const Teacher t, float* __restrict__ loss,
+// its loss from its entries' logits, which the product's epilogues have picked without
+// an order of the entries.  A CTA takes a token, a thread an entry.
+constexpr int kFewWarps = kTeacherMost / 32;
+__global__ void __launch_bounds__(32 * kFewWarps)
+xent_few_kernel(const float2* partial, int strips, int64_t tokens, int64_t vocab,
+                const void* logits, int logit_dtype, const Teacher t, float* __restrict__ loss,
                 float* __restrict__ lse) {
-  __shared__ long long sh_id[kTeacherMost];
-  __shared__ float sh_logit[kTeacherMost], sh_z[kTeacherMost];
-  __shared__ float2 sh[32];
+  __shared__ float2 sh[kFewWarps];
+  __shared__ float sh_top[kFewWarps], sh_sum[kFewWarps], sh_of[kFewWarps];
+  __shared__ int sh_wrong[kFewWarps];
   begin_after_previous();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t token = blockIdx.x;
-  float2 s = make_float2(kLowest, 0.0f);
-  if ((int)threadIdx.x < strips) s = __ldcg(partial + threadIdx.x * tokens + token);
-  for (int i = threadIdx.x + 1024; i < strips; i += 1024)
-    s = join_stats(s, __ldcg(partial + (int64_t)i * tokens + token), t.factor);
-  if ((int)threadIdx.x < t.k) {
-    const int64_t at = token * t.k + threadIdx.x;
-    sh_id[threadIdx.x] = ids[at];
-    sh_logit[threadIdx.x] = logit_dtype == kF32    ? teacher_logit<kF32>(logits, at)
-                            : logit_dtype == kBF16 ? teacher_logit<kBF16>(logits, at)
-                                                   : teacher_logit<kF16>(logits, at);
-  }
-  __syncthreads();
-  const uint4* const a = reinterpret_cast<const uint4*>(x + token * pitch * 2);
-  for (int j = warp; j < t.k; j += 32) {
-    const long long id = sh_id[j];
-    if (id < 0 || id >= vocab) continue;
-    const uint4* const b = reinterpret_cast<const uint4*>(w + id * pitch * 2);
-    float2 z = make_float2(0.0f, 0.0f);
-#pragma unroll 4
-    for (int64_t c = lane; c < pitch / 8; c += 32) {
-      const uint4 u = a[c], v = b[c];
-      const uint32_t p[4] = {u.x, u.y, u.z, u.w}, q[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const float2 f = BF16 ? make_float2(__uint_as_float(p[k] << 16),
-                                            __uint_as_float(p[k] & 0xFFFF0000u)) : h2_to_f2(p[k]);
-        const float2 g = BF16 ? make_float2(__uint_as_float(q[k] << 16),
-                                            __uint_as_float(q[k] & 0xFFFF0000u)) : h2_to_f2(q[k]);
-        z = make_float2(fmaf(f.x, g.x, z.x), fmaf(f.y, g.y, z.y));
-      }
-    }
-    z.x += z.y;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) z.x += __shfl_xor_sync(0xFFFFFFFFu, z.x, o);
-    if (lane == 0) sh_z[j] = z.x;
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1)
-    s = join_stats(s, make_float2(__shfl_xor_sync(0xFFFFFFFFu, s.x, o),
-                                  __shfl_xor_sync(0xFFFFFFFFu, s.y, o)), t.factor);
-  if (lane == 0) sh[warp] = s;
-  __syncthreads();
-  if (warp > 0) return;
-  s = sh[lane];
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1)
-    s = join_stats(s, make_float2(__shfl_xor_sync(0xFFFFFFFFu, s.x, o),
-                                  __shfl_xor_sync(0xFFFFFFFFu, s.y, o)), t.factor);
-  const float log_sum = logf(s.y);
   // (teacher_kernel's and TeacherLoss' steps)
   const float none = __uint_as_float(0xFF800000u);
-  float top = none;
-  bool wrong = false;
-  for (int j = lane; j < t.k; j += 32) {
-    const bool given = sh_id[j] >= 0;
-    wrong |= given && (sh_id[j] >= vocab || sh_logit[j] != sh_logit[j]);
-    if (!given) sh_logit[j] = none;
-    top = fmaxf(top, sh_logit[j]);
+  long long id = -1;
+  float share = none, z = 0.0f;
+  if ((int)threadIdx.x < t.k) {
+    const int64_t at = token * t.k + threadIdx.x;
+    id = t.ids[at];
+    z = __ldcg(t.z + at);         // (of a word of the vocabulary; else not used)
+    share = logit_dtype == kF32    ? teacher_logit<kF32>(logits, at)
+            : logit_dtype == kBF16 ? teacher_logit<kBF16>(logits, at)
+                                   : teacher_logit<kF16>(logits, at);
   }
+  float2 s = make_float2(kLowest, 0.0f);
+  for (int i = threadIdx.x; i < strips; i += 32 * kFewWarps)
+    s = join_stats(s, __ldcg(partial + (int64_t)i * tokens + token), t.factor);
+  bool wrong = id >= vocab || (id >= 0 && share != share);
+  if (id < 0) share = none;
+  float top = share;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-  wrong = __any_sync(0xFFFFFFFFu, wrong || top == -none);
-  const bool dead = !wrong && top == none;
-  float sum = 0.0f, of = 0.0f;
-  if (!wrong && !dead) {
-    for (int j = lane; j < t.k; j += 32) {
-      sh_logit[j] = expf((sh_logit[j] - top) / t.temperature);
-      sum += sh_logit[j];
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
-    for (int j = lane; j < t.k; j += 32) {
-      const float q = __fdiv_rn(sh_logit[j], sum);
-      if (q != 0.0f) of += q * (logf(q) - (__fdiv_rn(sh_z[j] - s.x, t.temperature) - log_sum));
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) of += __shfl_xor_sync(0xFFFFFFFFu, of, o);
+  for (int o = 16; o > 0; o >>= 1) {
+    s = join_stats(s, make_float2(__shfl_xor_sync(0xFFFFFFFFu, s.x, o),
+                                  __shfl_xor_sync(0xFFFFFFFFu, s.y, o)), t.factor);
+    top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
   }
+  wrong = __any_sync(0xFFFFFFFFu, wrong);
   if (lane == 0) {
+    sh[warp] = s;
+    sh_top[warp] = top;
+    sh_wrong[warp] = wrong;
+  }
+  __syncthreads();
+  s = sh[0];
+  top = sh_top[0];
+  wrong = sh_wrong[0] != 0;
+  for (int w = 1; w < kFewWarps; ++w) {
+    s = join_stats(s, sh[w], t.factor);
+    top = fmaxf(top, sh_top[w]);
+    wrong |= sh_wrong[w] != 0;
+  }
+  wrong |= top == -none;
+  const bool dead = !wrong && top == none;
+  const float log_sum = logf(s.y);
+  share = wrong || dead ? 0.0f : expf((share - top) / t.temperature);
+  float sum = share;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+  if (lane == 0) sh_sum[warp] = sum;
+  __syncthreads();
+  sum = 0.0f;
+  for (int w = 0; w < kFewWarps; ++w) sum += sh_sum[w];
+  const float q = share > 0.0f ? __fdiv_rn(share, sum) : 0.0f;
+  float of = 0.0f;
+  if (q != 0.0f) of = q * (logf(q) - (__fdiv_rn(z - s.x, t.temperature) - log_sum));
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) of += __shfl_xor_sync(0xFFFFFFFFu, of, o);
+  if (lane == 0) sh_of[warp] = of;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    of = 0.0f;
+    for (int w = 0; w < kFewWarps; ++w) of += sh_of[w];
     lse[token] = __fdiv_rn(s.x, t.temperature) + log_sum;
     loss[token] = wrong ? __uint_as_float(0x7FC00000u) : of;
   }
@@ -1342,14 +1387,10 @@ cudaError_t make_teacher(const XentArgs& a, int64_t t0, int64_t tokens, char* sc
   return e;
 }
 
-// Few tokens: the vocabulary's rows take the tiles' 256 rows and the tokens
-// their columns, as many as there are; a stage then holds little besides w,
+// Few tokens (kSwapTokens): the vocabulary's rows take the tiles' 256 rows and the
+// tokens their columns, as many as there are; a stage then holds little besides w,
 // which is all that has to be read.  24 x 768 x 50257: 19.9 us, 27.3 with the
 // tokens as rows (mostly past x's end); 128 x 768 x 200000: 56 us against 75.
-constexpr int64_t kSwapTokens = 128;
-// What xent_few_kernel reads of w again: rows in all, and elements for a token (a
-// warp reads the rows of its entries one after another).
-constexpr int64_t kFewEntries = 4096, kFewElements = 65536;
 
 struct ForwardScratch {
   size_t x = 0, w = 0, partial = 0, logit = 0, bytes = 0;
@@ -1370,9 +1411,9 @@ ForwardScratch forward_scratch(const XentArgs& a, int sms) {
                        : 2 * (up(a.vocab, kTileN) / kTileN);
   s.partial = l.take(s.strips * tokens * 8);
   s.logit = l.take(tokens * 4);
-  s.few = a.ids != nullptr && s.swapped && a.rows * a.k <= kFewEntries &&
-          a.k * pitch <= kFewElements;
-  if (!s.few) s.teacher = teacher_scratch(l, a, tokens, true);
+  s.few = a.ids != nullptr && s.swapped && a.rows * a.k <= kFewEntries;
+  if (s.few) s.teacher.z = l.take(tokens * a.k * 4);
+  else s.teacher = teacher_scratch(l, a, tokens, true);
   s.bytes = l.bytes();
   return s;
 }
@@ -1440,9 +1481,12 @@ cudaError_t launch_xent_forward(const XentArgs& a, char* scratch, int* error, in
     g.out.target = reinterpret_cast<const long long*>(a.target) + t0;
     g.out.ignore = a.ignore;
     if (s.few) {
-      g.out.teacher.k = a.k;
-      g.out.teacher.temperature = a.temperature;
-      g.out.teacher.factor = teacher_factor(a);
+      Teacher& t = g.out.teacher;
+      t.z = reinterpret_cast<float*>(scratch + s.teacher.z);
+      t.k = a.k;
+      t.temperature = a.temperature;
+      t.factor = teacher_factor(a);
+      t.ids = reinterpret_cast<const long long*>(a.ids);
     } else if (a.ids != nullptr) {
       e = make_teacher(a, t0, tokens, scratch, s.teacher, true, &g.out.teacher, stream, mark);
       if (e != cudaSuccess) break;
@@ -1464,10 +1508,9 @@ cudaError_t launch_xent_forward(const XentArgs& a, char* scratch, int* error, in
     if (e != cudaSuccess) break;
     if (mark) mark(kXentJoinK, 0, stream);
     if (s.few)
-      e = launch(true, bf16 ? xent_few_kernel<true> : xent_few_kernel<false>, (unsigned)tokens,
-                 1024, 0, stream, (const float2*)g.out.partial, (int)s.strips, tokens, a.vocab, x,
-                 w, pitch, reinterpret_cast<const long long*>(a.ids), a.logits, a.logit_dtype,
-                 g.out.teacher, a.loss, a.lse_out);
+      e = launch(true, xent_few_kernel, (unsigned)tokens, 32 * kFewWarps, 0, stream,
+                 (const float2*)g.out.partial, (int)s.strips, tokens, a.vocab, a.logits,
+                 a.logit_dtype, g.out.teacher, a.loss, a.lse_out);
     else e = launch(true, a.ids != nullptr ? xent_join_kernel<true> : xent_join_kernel<false>,
                (unsigned)((tokens + 31) / 32), 1024, 0, stream, (const float2*)g.out.partial,
                (int)s.strips, tokens, a.vocab, g.out.target, g.out.ignore,

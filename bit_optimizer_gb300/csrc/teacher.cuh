@@ -32,6 +32,8 @@ struct Teacher {
   int k, strips;
   float temperature;
   float factor;              // log2(e) / temperature
+  const long long* ids;      // few tokens: the entries as they are given (z goes by
+                             // them too); words, q and start are NULL then
 };
 
 // A row's entries in the columns of a strip, in order: the one that comes next and

@@ -176,22 +176,23 @@ __device__ __forceinline__ Two add(Two a, Two b) {
   return {hi, e - (hi - s)};
 }
 
-__device__ __forceinline__ Two scaled(Two a, float k) {
-  if (nonfinite(a.hi)) return {a.hi * k, 0.0f};
-  const float hi = a.hi * k;
-  return {hi, fmaf(a.hi, k, -hi) + a.lo * k};
+__device__ __forceinline__ Two scaled(Two a, Two k) {
+  const float hi = a.hi * k.hi;
+  if (nonfinite(hi)) return {hi, 0.0f};
+  return {hi, fmaf(a.hi, k.hi, -hi) + (a.lo * k.hi + a.hi * k.lo)};
 }
 
 __device__ __forceinline__ Two shuffled(Two a, int o) {
   return {__shfl_xor_sync(0xFFFFFFFFu, a.hi, o), __shfl_xor_sync(0xFFFFFFFFu, a.lo, o)};
 }
 
-// 1 / x.
-__device__ __forceinline__ float reciprocal(unsigned long long x) {
+// 1 / x.  (In one float, means of sequences that cancel keep 2^-25 of theirs.)
+__device__ __forceinline__ Two reciprocal(unsigned long long x) {
   const float hi = __ull2float_rn(x);
   const float lo = (float)(long long)(x - (unsigned long long)hi);
-  const float q = 1.0f / hi;
-  return q + q * (fmaf(-q, hi, 1.0f) - q * lo);
+  const float q = 1.0f / hi, e = q * (fmaf(-q, hi, 1.0f) - q * lo);
+  const float r = q + e;
+  return {r, e - (r - q)};
 }
 
 // A unit's sums.
@@ -254,7 +255,7 @@ struct Total {
   unsigned long long count;        // tokens, or sequences that have any
   __device__ __forceinline__ void take(const Part& p, bool by_sequence) {
     if (p.count == 0) return;
-    const float w = by_sequence ? reciprocal(p.count) : 1.0f;
+    const Two w = by_sequence ? reciprocal(p.count) : Two{1.0f, 0.0f};
     policy = add(policy, scaled(p.policy, w));
     kl = add(kl, scaled(p.kl, w));
     clipped = add(clipped, scaled({(float)(p.clipped & ~0xFFF), (float)(p.clipped & 0xFFF)}, w));
@@ -309,11 +310,11 @@ policy_join_kernel(const Part* parts, int64_t batch, int64_t pieces, bool by_seq
   }
   __syncthreads();
   const unsigned long long count = sh_count;
-  const float all = count > 0 ? reciprocal(count) : 0.0f;
+  const Two all = count > 0 ? reciprocal(count) : Two{0.0f, 0.0f};
   if (threadIdx.x == 0) {
     const Two each[3] = {scaled(total.policy, all), scaled(total.kl, all),
                          scaled(total.clipped, all)};
-    const Two loss = add(each[0], scaled(each[1], kl_coef));
+    const Two loss = add(each[0], scaled(each[1], {kl_coef, 0.0f}));
     stats[0] = loss.hi;
     for (int k = 0; k < 3; ++k) stats[1 + k] = each[k].hi + each[k].lo;
   }
@@ -322,7 +323,7 @@ policy_join_kernel(const Part* parts, int64_t batch, int64_t pieces, bool by_seq
     for (int64_t b = mine; b < batch; b += groups) {
       const int c = __float_as_int(weight[b]);
       weight[b] = c == 0        ? 0.0f
-                  : by_sequence ? reciprocal((unsigned long long)c * count) : all;
+                  : by_sequence ? reciprocal((unsigned long long)c * count).hi : all.hi;
     }
   }
 }

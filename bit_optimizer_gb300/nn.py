@@ -213,11 +213,16 @@ def linear_cross_entropy(x, weight, target, ignore_index: int = -100,
 def linear_distillation(x, weight, ids, logits, temperature: float = 1.0,
                         reduction: str = "mean"):
     """Divergence of x weight^T from a teacher's top logits (``ops.linear_distillation``).
-    x: (..., dim), ids and logits: (..., k); no gradient for the logits.  reduction:
-    "none" (one loss per token), "sum", or "mean" over the tokens that have an id
-    (0 when none has).  Soft targets' usual factor temperature ** 2 is the caller's."""
+    x: (..., dim), ids and logits: (..., k) with x's leading dimensions; no gradient
+    for the logits.  reduction: "none" (one loss per token), "sum", or "mean" over the
+    tokens that have an id (0 when none has).  Soft targets' usual factor temperature ** 2 is the caller's."""
     if reduction not in ("none", "sum", "mean"):
         raise ValueError(f"reduction must be 'none', 'sum' or 'mean', not {reduction!r}")
+    if (x.dim() < 1 or ids.dim() != x.dim() or ids.shape[:-1] != x.shape[:-1]
+            or logits.shape != ids.shape or ids.shape[-1] < 1):
+        raise ValueError("ids and logits must have one shape, of x's leading dimensions and at "
+                         f"least one entry, not {tuple(ids.shape)} and {tuple(logits.shape)} "
+                         f"for x of {tuple(x.shape)}")
     x, weight = _autocast(x, weight)
     k = ids.shape[-1]
     loss = _LinearDistillation.apply(x.contiguous().view(-1, x.shape[-1]), weight,

@@ -795,6 +795,7 @@ struct Scratch {
 
 // The largest chunk with which every SM still has kSumUnits warps.
 constexpr int64_t kSumUnits = 16;
+static_assert(kFewTokens > kMostChunk, "the chunked path always has several chunks");
 int chunk_of(const EmbeddingArgs& a, int sms) {
   const int64_t slices = blocks(a.dim, 32 * (a.dtype == kF32 ? kPer<kF32> : kPer<kF16>));
   int chunk = kMostChunk;
@@ -925,7 +926,7 @@ cudaError_t backward(const EmbeddingArgs& a, char* scratch, int sms, cudaStream_
   e = launch(true, vec ? embedding_sums_kernel<DT, true> : embedding_sums_kernel<DT, false>,
              (unsigned)blocks((int64_t)s.sums + fillers, warps), 32 * warps, 0, stream, s);
   if (mark) mark(kEmbeddingSumsK, 1, stream);
-  if (e != cudaSuccess || chunks == 1) return e;
+  if (e != cudaSuccess) return e;
   if (mark) mark(kEmbeddingJoinK, 0, stream);
   const bool narrow = a.dim <= kNarrow;
   e = launch(true, narrow ? embedding_join_kernel<DT, 64> : embedding_join_kernel<DT, 128>,

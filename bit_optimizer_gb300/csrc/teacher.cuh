@@ -214,7 +214,7 @@ teacher_kernel(const long long* ids, const void* logits, int logit_dtype, int64_
   __syncthreads();
   if (!live) return;
   // the number of entries before each strip: a thread has neighbouring strips, looks
-  // for the first one's and goes on from there (8191 tokens of 64 entries, 393
+  // for the first one's and goes on from there (8191 tokens of 64 entries, 394
   // strips: 24 us with a search for each)
   const int per = (t.strips + 32 * group) / (32 * group), s0 = j * per;
   int n = 0;

@@ -406,8 +406,11 @@ embedding_place_kernel(SortPass s, Fill fill) {
 // Tokens of a warp, at most one to a lane: 32, or where that makes few warps, 16
 // or 8 (whose rows are all under way at once).
 constexpr int kMostChunk = 32, kLeastChunk = 8;
-// Warps of a CTA, and where the chunks are the largest (65536 tokens x 1024: 58.1 us,
-// with four 62.0; 2047 x 768: 22.8 and 21.8).
+// Warps of a CTA, and where the chunks are the largest.  With eight and four at the
+// largest: 65536 x 1024 58.1 and 62.2 us, 131072 x 768 74.3 and 77.8, 16381 x 2048 59.3
+// and 64.2, but 16381 x 2047 76.9 and 73.4.  Below them it hardly matters (2047 x 768
+// 21.8 both, 4096 x 768 26.0 and 26.6, 16384 x 768 31.4 and 31.1), but for the one launch
+// of few tokens (256 x 768: 16.3 and 15.9; 100 x 769: 18.1 and 17.0).
 constexpr int kSumWarps = 4, kMostSumWarps = 8;
 
 struct Sums {

@@ -43,9 +43,10 @@
 // With a teacher (teacher.cuh) the loss is the divergence from its top words
 // instead of one target's: the same products, whose epilogues pick a token's few
 // words out of their strips: forward their logits, which the join adds up, backward
-// p - q, rounded as p is.  8191 x 1024 x 50257 with 64 words: 467 us forward in
-// calls in a row, 1.65 ms backward, as the cross entropy; where a strip meets many
-// words that is what bounds it (2279 x 192 x 20888 with 217: 74 us, 29).
+// p - q, rounded as p is.  8191 x 1024 x 50257 with 64 words: 467 to 495 us
+// forward in calls in a row, 1.65 to 1.81 ms backward, as the cross entropy; where a
+// strip meets many words that is what bounds it (2279 x 192 x 20888 with 217: 75 us,
+// 29).
 //
 // Tokens whose target is `ignore` have no loss and give no gradient whatever
 // is in their row of x: their p is 0 and dw reads a copy of x in which such

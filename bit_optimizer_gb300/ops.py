@@ -175,8 +175,9 @@ def linear_distillation_backward(dloss: torch.Tensor, x: torch.Tensor, w: torch.
                                  ids: torch.Tensor, logits: torch.Tensor, lse: torch.Tensor,
                                  temperature: float = 1.0, stream=None):
     """(dx, dw), in x's type, for the gradient dloss (float32, one per token) of
-    ``linear_distillation``'s loss; lse is that call's.  Scratch as
-    ``linear_cross_entropy_backward``'s."""
+    ``linear_distillation``'s loss; lse is that call's, and being float32 leaves the
+    student's probabilities off by 2^-23 |lse| of themselves (low temperatures: lse is
+    about the largest logit over it).  Scratch as ``linear_cross_entropy_backward``'s."""
     return _b.linear_distillation_backward(dloss, x, w, ids, logits, lse, temperature, stream)
 
 

@@ -742,7 +742,15 @@ FP8OPT_API int fp8_linear_xent_backward(const float *dloss, const void *x,
  * by pieces of the vocabulary and with the treatment of tokens that take no part
  * as in fp8_linear_xent_backward, whose sizes, scratch and waits hold here too.
  * Scratch besides: 8 bytes an entry (forward 12), 2 bytes for every 128 words of
- * each token (forward of at most 65536 tokens at a time), 12 bytes a token.
+ * each token (forward of at most 65536 tokens at a time), 12 bytes a token;
+ * forward of up to 128 tokens with up to 4096 entries in all, 4 bytes an entry.
+ *
+ * The loss is computed from differences to the token's largest logit: its error
+ * does not grow with the logits' common part.  The gradients' p is exp of a
+ * difference from lse, an fp32 number: p is off by about 2^-23 |lse| of itself, and
+ * by what the logits' own fp32 sums are off by over temperature.  At a low
+ * temperature lse is about the largest logit over it, so that |lse| of 10^4 leaves p
+ * three digits (and |lse| of 10^7 none), as many as bf16 results hold.
  *
  * k in [1, FP8OPT_MOST_TEACHER]; temperature in [2^-20, 2^20].  No gradient for
  * the teacher's logits.
@@ -768,8 +776,9 @@ FP8OPT_API int fp8_linear_distill_backward(
  * padding_idx gets no gradient (any number outside [0, vocab): none is left
  * out), and an id outside [0, vocab) takes no part.  rows = 0 gives dw 0.  The
  * tokens are sorted by word and a word's rows added in their order, in fp32.
- * Scratch: 16 bytes a token, and dim / 4 (few tokens: dim) a token.  rows, vocab
- * and dim below 2^31, dim and vocab >= 1, scale finite.
+ * Scratch: none for up to 256 tokens; else 16 bytes a token (up to 4096: 8), dim / 4
+ * (where that makes few warps: dim / 2 or dim) a token, and from 4097 tokens on up to
+ * 1.3 MB.  rows, vocab and dim below 2^31, dim and vocab >= 1, scale finite.
  */
 FP8OPT_API int fp8_embedding(const int64_t *ids, const void *w, int64_t rows,
                              int64_t dim, int64_t vocab, int dtype,
@@ -798,8 +807,9 @@ FP8OPT_API int fp8_embedding_backward(const void *dy, const int64_t *ids,
  * tokens that are clipped (r A is above the clipped term); all 0 where no token
  * counts.  weight (batch fp32): what a token of each sequence weighs in the mean
  * (0 for a sequence without any).  Whether a token is clipped follows from the
- * exact difference logp - old_logp; sums over more than 1024 tokens are held in two
- * fp32 numbers each (48 bits).
+ * exact difference logp - old_logp; up to 1024 tokens of a sequence are added in
+ * fp32, and these sums, and the means of sequences, in two fp32 numbers each (48
+ * bits).
  *
  * fp8_policy_loss_backward: dlogp (batch x length fp32) = *dloss * weight *
  * dl / dlogp, dl / dlogp = -r A (0 where clipped) + kl_coef (1 - exp(e)); 0 where
@@ -840,8 +850,9 @@ FP8OPT_API const char *fp8opt_last_error(void);
  * "layer_norm_backward", "layer_norm_params", "xent_logits", "xent_join",
  * "xent_prepare", "xent_grads", "xent_dx", "embedding", "embedding_order",
  * "embedding_sums", "embedding_join", "policy_loss", "policy_join",
- * "policy_backward", "xent_teacher"), the launches recorded since enabling and their summed duration in milliseconds.  Returns
- * FP8OPT_ERR_ARG for an unknown name or NULL outputs. */
+ * "policy_backward", "xent_teacher"), the launches recorded since enabling and
+ * their summed duration in milliseconds.  Returns FP8OPT_ERR_ARG for an unknown
+ * name or NULL outputs. */
 FP8OPT_API int fp8opt_timing_enable(int on);
 FP8OPT_API int fp8opt_timing_read(const char *kernel, int *launches,
                                   double *total_ms);

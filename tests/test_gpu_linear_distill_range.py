@@ -86,3 +86,41 @@ def test_minus_infinity_and_overflow(bo):
         want = math.log(48) - math.log(2)
         assert ((loss[keep] - want).abs() <= 2.0 ** -18).all()
         assert ((lse - math.log(48)).abs() <= 2.0 ** -18).all()
+
+
+@pytest.mark.parametrize("t,offset", [(1.0, 2048), (2.5, 2048), (0.05, 0), (0.05, 256)])
+def test_gradients(bo, t, offset):
+    """p is exp of a difference from the given lse: off by 2^-23 |lse| of itself (lse t,
+    rounded), 6 u |d| + 2^-21 (factor, product, exponential), and q by (2 |a| + 10) u; one
+    rounding of dz to 16 bits, at random, 4 h sqrt(sum dz^2 w^2); fp32 sums of `rows` or
+    `vocab` products; and the result's own rounding."""
+    g = torch.Generator().manual_seed(offset)
+    rows, dim, vocab, k = 200, 64, 1000, 40
+    x, w = eighths((rows, dim), g), eighths((vocab, dim), g)
+    x[:, 0], w[:, 0] = offset / 64, 64 if offset else 0
+    x, w = x.half().cuda(), w.half().cuda()
+    t = float(torch.tensor(t).float())
+    z = x.double() @ w.double().T
+    zk, ids = torch.topk(z, k, 1)
+    noise = 0.3 * torch.randn(rows, k, generator=g).double().cuda()
+    logits = (zk - zk.amax(1, keepdim=True) + t * noise).float()
+    dloss = (torch.rand(rows, generator=g) + 0.5).cuda() / rows
+    _, lse = bo.linear_distillation(x, w, ids, logits, t)
+    dx, dw = bo.linear_distillation_backward(dloss, x, w, ids, logits, lse, t)
+    d = z / t - lse.double()[:, None]
+    p, y = torch.exp(d), logits.double() / t
+    q = torch.softmax(y, 1)
+    arg = (y - y.amax(1, keepdim=True)).abs()
+    r, r_off = (torch.zeros_like(p).scatter_add_(1, ids, v)
+                for v in (q, q * (2 * arg + 10) * U))
+    up = dloss.double()[:, None] / t
+    dz = (p - r) * up
+    off = (p * (2.0 ** -23 * lse.double().abs()[:, None] + 6 * U * d.abs() + 2.0 ** -21)
+           + r_off) * up
+    size, h = (p + r) * up, 2.0 ** -11
+    for got, a, e, s, b in ((dx, dz, off, size, w.double()), (dw, dz.T, off.T, size.T, x.double())):
+        ref = a @ b
+        tol = 4 * h * (a.square() @ b.square()).sqrt()
+        tol += e @ b.abs() + 4 * U * math.sqrt(a.shape[1]) * (s @ b.abs())
+        tol += h * (ref.abs() + tol) + 2.0 ** -25
+        assert ((got.double() - ref).abs() <= tol).all(), ((got.double() - ref).abs() / tol).max()

@@ -312,7 +312,8 @@ __device__ __forceinline__ float2 join_stats(float2 a, float2 b, float factor = 
 // hundred, while its first tile is copied, and the epilogues look through the list.
 // The list lies where the stages' halves of B, of at most kSwapTokens / 2 rows, end,
 // whose room sets the limit.  768 x 50257 with 32 entries: 24 tokens 24.2 us, sorted
-// first 28.4; 128 tokens 25.9 and 32.6 (the cross entropy 21.5 and 24.1).  The entries'
+// first 28.4; 128 tokens 25.8 and 32.6 (the cross entropy 21.5 and 24.1), 29 where all
+// their words are below 500, 50 below 100, which lie in one CTA's list.  The entries'
 // logits have to be the product's: the tensor cores' sums are some 2^-22 of the
 // logits off all the same way, which the loss's differences cancel (summed again from
 // w's rows, 24 tokens' losses at logits of 29 and t = 0.5 were off by 1.1e-5 on
@@ -321,15 +322,17 @@ constexpr int64_t kSwapTokens = 128, kFewEntries = 4096;
 struct FewEntries {
   uint8_t* stages;
   static constexpr int kSpare = kStageB / 2, kEach = kSpare / 8;      // of a stage: bytes, entries
+  static_assert(kFewEntries <= 1 << 16 && kSwapTokens <= 1 << 16, "16 bits each");
   static_assert(kSwapTokens / 2 * kBlockK * 2 <= kStageB - kSpare, "B's rows");
-  static_assert(kFewEntries <= (kGemmStages - 1) * kEach, "the list, and its count");
+  // (the list, the rest of its last round's reads, and its count)
+  static_assert(kFewEntries + 4 * 32 <= (kGemmStages - 1) * kEach, "spare room");
   __device__ __forceinline__ uint8_t* spare(int stage) const {
     return stages + stage * (kStageA + kStageB) + kStageB - kSpare + kStageA;
   }
   __device__ __forceinline__ int* count() const {
     return reinterpret_cast<int*>(spare(kGemmStages - 1));
   }
-  // a word, and the entry's number among all tokens'
+  // a word, and the entry's token << 16 | its number among all tokens'
   __device__ __forceinline__ uint2* entry(int i) const {
     return reinterpret_cast<uint2*>(spare(i / kEach)) + i % kEach;
   }
@@ -351,8 +354,10 @@ struct FewEntries {
       for (int k = 0; k < kAhead; ++k) {
         const uint32_t word = (uint32_t)id[k];
         if (id[k] >= 0 && id[k] < o.vocab && word / kHalfM % 2 == rank &&
-            word / kTileM % pairs == pair)
-          *entry(atomicAdd(count(), 1)) = make_uint2(word, (uint32_t)(i0 + k * kThreads));
+            word / kTileM % pairs == pair) {
+          const uint32_t e = i0 + k * kThreads;
+          *entry(atomicAdd(count(), 1)) = make_uint2(word, e / (uint32_t)t.k << 16 | e);
+        }
       }
     }
     asm volatile("bar.sync 1, 256;" ::: "memory");
@@ -450,15 +455,22 @@ struct SwappedStats {
       if constexpr (TEACHER) {
         const Teacher& t = o.teacher;
         if (t.ids != nullptr) {
+          // (four entries of a lane under way)
           const FewEntries few = {stages};
           const int end = *few.count();
-          for (int i = lane; i < end; i += 32) {
-            const uint2 entry = *few.entry(i);
-            const uint32_t row = entry.x - (uint32_t)v0;
-            const int of = (int)entry.y / t.k - c;
-            if (row < (uint32_t)valid && of >= 0 && of < 32)
-              t.z[entry.y] = __uint_as_float(
-                  reinterpret_cast<const uint32_t*>(&turn.at((int)row, of >> 2))[of & 3]);
+          for (int i0 = 2 * lane; i0 < end; i0 += 4 * 32) {
+            const uint4 v[2] = {*reinterpret_cast<const uint4*>(few.entry(i0)),
+                                *reinterpret_cast<const uint4*>(few.entry(i0 + 2 * 32))};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const uint32_t row = (j & 1 ? v[j / 2].z : v[j / 2].x) - (uint32_t)v0;
+              const uint32_t token_e = j & 1 ? v[j / 2].w : v[j / 2].y;
+              if (i0 + j / 2 * 64 + (j & 1) >= end || row >= (uint32_t)valid) continue;
+              const uint32_t of = (token_e >> 16) - (uint32_t)c;
+              if (of < 32)
+                t.z[token_e & 0xFFFFu] = __uint_as_float(
+                    reinterpret_cast<const uint32_t*>(&turn.at((int)row, of >> 2))[of & 3]);
+            }
           }
         } else if (token < o.tokens) {
           const uint16_t* start = t.start + token * (t.strips + 1) + v0 / kTeacherStrip;
